@@ -350,6 +350,37 @@ BEAM_API beam_status beam_moe_combine_boundary_nvfp4(beam_stream_t stream, uint1
                                             const beam_launch_opts* opts);
 
 /*
+ * The dense and MoE boundaries with y leaving as 8-bit integers with one scale
+ * per token, the activations of an 8-bit product (beam_matmul_int8). The pages
+ * name no such format; this is symmetric per-token quantisation, an addition of
+ * this library. y is computed as in the BF16 calls (rounded to BF16), then, for
+ * each row t:
+ *   amax = max_j |y_j|,  y_scale[t] = RN32(amax / 127)
+ *   q_j  = rint(RN32(y_j * RN32(127 / amax)))   in [-127, 127], ties to even
+ * (for amax < 2^-100, y and amax are first multiplied by 2^64, which is exact).
+ *   y_int8  [T, D] int8; y_scale [T] FP32; both 16-byte aligned
+ *   D a multiple of 8, as in the BF16 calls; no BF16 y is written.
+ *   route_scale as in beam_moe_combine_boundary_scaled (1 when topk_w carries it)
+ * Other arguments and errors as beam_boundary_fused_ex / beam_moe_combine_boundary_ex;
+ * opts may be NULL; options of the shared-memory ring (stages > 0, the wait
+ * timeout hook) give BEAM_ERR_ARG. y_int8 and y_scale overlap neither each other
+ * nor any other operand.
+ * A row of zeros gets codes 0 and scale 0. A row that holds an infinity or a NaN
+ * gets codes 0 and the scale inf or NaN, so a product with that row is NaN.
+ */
+BEAM_API beam_status beam_boundary_fused_int8(beam_stream_t stream, uint16_t* h, const uint16_t* x,
+                                     const uint16_t* post_w, const uint16_t* pre_w, int n,
+                                     float eps, int64_t T, int D, int8_t* y_int8, float* y_scale,
+                                     const beam_launch_opts* opts);
+
+BEAM_API beam_status beam_moe_combine_boundary_int8(beam_stream_t stream, uint16_t* h,
+                                           const uint16_t* expert_out, const float* topk_w,
+                                           float route_scale, const uint16_t* post_w,
+                                           const uint16_t* pre_w, int n, float eps, int64_t T,
+                                           int D, int8_t* y_int8, float* y_scale,
+                                           const beam_launch_opts* opts);
+
+/*
  * The dense and MoE boundaries on a batch that lives in host memory. Any
  * operand may be page-locked host memory (cudaHostAlloc, cudaHostRegister),
  * device memory of the current device, or managed memory; pageable host memory

@@ -17,7 +17,8 @@ from ._lib import LaunchOpts  # noqa: F401
 
 __all__ = ["boundary_fused", "moe_combine_boundary", "boundary_fused_host",
            "moe_combine_boundary_host", "boundary_fused_nvfp4",
-           "moe_combine_boundary_nvfp4", "moe_route", "router_sigmoid", "qk_norm", "sync_status",
+           "moe_combine_boundary_nvfp4", "boundary_fused_int8", "moe_combine_boundary_int8",
+           "moe_route", "router_sigmoid", "qk_norm", "sync_status",
            "exact_sum_count",
            "version", "BeamError", "LaunchOpts", "library"]
 
@@ -291,6 +292,70 @@ def moe_combine_boundary_nvfp4(h, expert_out, topk_w, post_w, pre_w, n: int, eps
     if st != 0:
         raise BeamError(st, "beam_moe_combine_boundary_nvfp4")
     return q, sf
+
+
+def _int8_out(h, q, scale):
+    import torch
+    T, D = h.shape
+    if q is None:
+        q = torch.empty((T, D), dtype=torch.int8, device=h.device)
+    if scale is None:
+        scale = torch.empty(T, dtype=torch.float32, device=h.device)
+    _check(q, "y_int8", torch.int8, 2)
+    _check(scale, "y_scale", torch.float32, 1)
+    _shape(q, "y_int8", (T, D))
+    _shape(scale, "y_scale", (T,))
+    return q, scale
+
+
+def boundary_fused_int8(h, x, post_w, pre_w, n: int, eps: float = 1e-6, y_int8=None, y_scale=None,
+                        stream=None, opts=None):
+    """Dense boundary with y as int8 and one FP32 scale per token; updates h in place,
+    returns (y_int8 [T, D] int8, y_scale [T] float32), the operands of ``matmul_int8``."""
+    import torch
+    for t, name in ((h, "h"), (x, "x")):
+        _check(t, name, torch.bfloat16, 2)
+    _check(post_w, "post_w", torch.bfloat16, 1)
+    _check(pre_w, "pre_w", torch.bfloat16, 1)
+    T, D = h.shape
+    if x.shape != h.shape or post_w.shape[0] != D or pre_w.shape[0] != D:
+        raise ValueError("shape mismatch: h, x [T, D]; post_w, pre_w [D]")
+    q, scale = _int8_out(h, y_int8, y_scale)
+    _on_current_device(h=h, x=x, post_w=post_w, pre_w=pre_w, y_int8=q, y_scale=scale)
+    st = _lib.load().beam_boundary_fused_int8(_stream_ptr(stream), h.data_ptr(), x.data_ptr(),
+                                              post_w.data_ptr(), pre_w.data_ptr(), int(n),
+                                              float(eps), T, D, q.data_ptr(), scale.data_ptr(),
+                                              _opts(opts))
+    if st != 0:
+        raise BeamError(st, "beam_boundary_fused_int8")
+    return q, scale
+
+
+def moe_combine_boundary_int8(h, expert_out, topk_w, post_w, pre_w, n: int, eps: float = 1e-6,
+                              y_int8=None, y_scale=None, stream=None, opts=None,
+                              route_scale: float = 1.0):
+    """MoE boundary with y as int8 and one FP32 scale per token; updates h in place, returns
+    (y_int8, y_scale). ``route_scale`` multiplies the combined sum (1: topk_w carries it)."""
+    import torch
+    _check(h, "h", torch.bfloat16, 2)
+    _check(expert_out, "expert_out", torch.bfloat16, 3)
+    _check(topk_w, "topk_w", torch.float32, 2)
+    _check(post_w, "post_w", torch.bfloat16, 1)
+    _check(pre_w, "pre_w", torch.bfloat16, 1)
+    T, D = h.shape
+    if (expert_out.shape != (T, _lib.BEAM_MOE_TOPK, D) or topk_w.shape != (T, _lib.BEAM_MOE_TOPK)
+            or post_w.shape[0] != D or pre_w.shape[0] != D):
+        raise ValueError("shape mismatch: h [T, D]; expert_out [T, 8, D]; topk_w [T, 8]")
+    q, scale = _int8_out(h, y_int8, y_scale)
+    _on_current_device(h=h, expert_out=expert_out, topk_w=topk_w, post_w=post_w, pre_w=pre_w,
+                       y_int8=q, y_scale=scale)
+    st = _lib.load().beam_moe_combine_boundary_int8(
+        _stream_ptr(stream), h.data_ptr(), expert_out.data_ptr(), topk_w.data_ptr(),
+        float(route_scale), post_w.data_ptr(), pre_w.data_ptr(), int(n), float(eps), T, D,
+        q.data_ptr(), scale.data_ptr(), _opts(opts))
+    if st != 0:
+        raise BeamError(st, "beam_moe_combine_boundary_int8")
+    return q, scale
 
 
 def moe_route(logits, bias, n_group: int = 8, topk_group: int = 4, topk: int = 8,

@@ -52,6 +52,10 @@ SIGNATURES = {
                                           _vp, _vp]),
     "beam_moe_combine_boundary_nvfp4": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _f32, _i64, _i32,
                                                 _f32, _vp, _vp, _vp]),
+    "beam_boundary_fused_int8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _f32, _i64, _i32, _vp, _vp,
+                                         _OPTS]),
+    "beam_moe_combine_boundary_int8": (_i32, [_vp, _vp, _vp, _vp, _f32, _vp, _vp, _i32, _f32, _i64,
+                                               _i32, _vp, _vp, _OPTS]),
     "beam_boundary_fused_host": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _f32, _i64, _i32, _vp]),
     "beam_moe_combine_boundary_host": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _f32, _i64, _i32,
                                                _vp]),

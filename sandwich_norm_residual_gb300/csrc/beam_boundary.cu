@@ -47,8 +47,8 @@ struct DeviceInfo {
     int sms = 0;
     long long l2_bytes = 0;
     int smem_optin = 0;                       // max dynamic + static shared memory per CTA
-    KernelFn lim_fn[64] = {};                 // kernels whose dynamic smem limit was raised
-    int lim_val[64] = {};
+    KernelFn lim_fn[96] = {};                 // kernels whose dynamic smem limit was raised
+    int lim_val[96] = {};
     int lim_n = 0;
     OccKey occ_key[128] = {};
     int occ_val[128] = {};
@@ -62,48 +62,59 @@ DeviceInfo g_dev[kMaxDevices];
 // memory) exist for these vectors-per-thread values
 bool has_full(int vpt) { return vpt >= 2 && vpt <= 5; }
 
-template <int V, int KIND, bool FULL, bool QUANT>
+template <int V, int KIND, bool FULL, int OUT>
 KernelFn pick() {
     if constexpr (KIND == kDenseRing) return beam::boundary_ring_kernel<V, FULL>;
-    else return beam::boundary_kernel<V, KIND == kMoeRegs, FULL, QUANT>;
+    else if constexpr (OUT == beam::kOutInt8) return beam::boundary_int8_kernel<V, KIND == kMoeRegs, FULL>;
+    else return beam::boundary_kernel<V, KIND == kMoeRegs, FULL, OUT == beam::kOutNvfp4>;
 }
 
-template <int KIND, bool QUANT>
+template <int KIND, int OUT>
 KernelFn kernel_for(int vpt, bool full) {
     if (full) {
         switch (vpt) {
-        case 2: return pick<2, KIND, true, QUANT>();
-        case 3: return pick<3, KIND, true, QUANT>();
-        case 4: return pick<4, KIND, true, QUANT>();
-        case 5: return pick<5, KIND, true, QUANT>();
+        case 2: return pick<2, KIND, true, OUT>();
+        case 3: return pick<3, KIND, true, OUT>();
+        case 4: return pick<4, KIND, true, OUT>();
+        case 5: return pick<5, KIND, true, OUT>();
         default: return nullptr;
         }
     }
     switch (vpt) {
-    case 1: return pick<1, KIND, false, QUANT>();
-    case 2: return pick<2, KIND, false, QUANT>();
-    case 3: return pick<3, KIND, false, QUANT>();
-    case 4: return pick<4, KIND, false, QUANT>();
-    case 5: return pick<5, KIND, false, QUANT>();
-    case 6: return pick<6, KIND, false, QUANT>();
-    case 7: return pick<7, KIND, false, QUANT>();
-    case 8: return pick<8, KIND, false, QUANT>();
+    case 1: return pick<1, KIND, false, OUT>();
+    case 2: return pick<2, KIND, false, OUT>();
+    case 3: return pick<3, KIND, false, OUT>();
+    case 4: return pick<4, KIND, false, OUT>();
+    case 5: return pick<5, KIND, false, OUT>();
+    case 6: return pick<6, KIND, false, OUT>();
+    case 7: return pick<7, KIND, false, OUT>();
+    case 8: return pick<8, KIND, false, OUT>();
     default: return nullptr;
     }
 }
 
-KernelFn kernel_for_kind(int kind, int vpt, bool full, bool quant = false) {
-    if (quant) return kind == kMoeRegs ? kernel_for<kMoeRegs, true>(vpt, full) : kernel_for<kDenseRegs, true>(vpt, full);
-    return kind == kDenseRing ? kernel_for<kDenseRing, false>(vpt, full)
-           : kind == kMoeRegs ? kernel_for<kMoeRegs, false>(vpt, full)
-                              : kernel_for<kDenseRegs, false>(vpt, full);
+template <int OUT>
+KernelFn register_kernel(int kind, int vpt, bool full) {
+    return kind == kMoeRegs ? kernel_for<kMoeRegs, OUT>(vpt, full) : kernel_for<kDenseRegs, OUT>(vpt, full);
 }
 
-// NVFP4 destination of y (NULL: y is written as BF16)
+KernelFn kernel_for_kind(int kind, int vpt, bool full, int out) {
+    if (kind == kDenseRing) return kernel_for<kDenseRing, beam::kOutBf16>(vpt, full);
+    switch (out) {
+    case beam::kOutNvfp4: return register_kernel<beam::kOutNvfp4>(kind, vpt, full);
+    case beam::kOutInt8: return register_kernel<beam::kOutInt8>(kind, vpt, full);
+    default: return register_kernel<beam::kOutBf16>(kind, vpt, full);
+    }
+}
+
+// Where y goes when it does not leave as BF16
 struct QuantOut {
+    int kind;  // kOutNvfp4: q, sf, gs; kOutInt8: yi, yis
     uint8_t* q;
     uint8_t* sf;
     float gs;
+    int8_t* yi;
+    float* yis;
 };
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -209,7 +220,7 @@ beam_status smem_limit(DeviceInfo* d, KernelFn fn, int* out) {
         cudaGetLastError();
         return BEAM_ERR_CUDA;
     }
-    if (d->lim_n < 64) {
+    if (d->lim_n < 96) {
         d->lim_fn[d->lim_n] = fn;
         d->lim_val[d->lim_n++] = limit;
     }
@@ -275,6 +286,7 @@ beam_status launch(bool moe, beam_stream_t stream, uint16_t* h, const uint16_t* 
     const bool full = has_full(vpt) && nt * vpt == nvec;
     const int wbytes = full ? 4 * D : 0;
     const int slot_bytes = 4 * D;
+    const int out = quant ? quant->kind : beam::kOutBf16;
     int kind = moe ? kMoeRegs : kDenseRing;
     int stages = 0;
     KernelFn fn = nullptr;
@@ -282,12 +294,12 @@ beam_status launch(bool moe, beam_stream_t stream, uint16_t* h, const uint16_t* 
     if (!moe) {
         // dense rows go through the shared-memory ring when at least two slots fit
         int want = (opts && opts->stages) ? opts->stages : kAutoStages;
-        if (quant) want = -1;  // the NVFP4 output exists only in the register kernels
+        if (quant) want = -1;  // the ring kernels write y as BF16 only
         if (want == -1 && opts && !opts->stages && (opts->flags & BEAM_OPT_TEST_WAIT_TIMEOUT)) want = kTestStages;
         if (want == -1) {
             kind = kDenseRegs;
         } else {
-            fn = kernel_for_kind(kDenseRing, vpt, full);
+            fn = kernel_for_kind(kDenseRing, vpt, full, out);
             if (!fn) return BEAM_ERR_SHAPE;
             st = smem_limit(info, fn, &limit);
             if (st != BEAM_OK) return st;
@@ -305,12 +317,12 @@ beam_status launch(bool moe, beam_stream_t stream, uint16_t* h, const uint16_t* 
         }
     }
     if (kind != kDenseRing) {
-        fn = kernel_for_kind(kind, vpt, full, quant != nullptr);
+        fn = kernel_for_kind(kind, vpt, full, out);
         if (!fn) return BEAM_ERR_SHAPE;
         st = smem_limit(info, fn, &limit);
         if (st != BEAM_OK) return st;
         if (wbytes > limit) {  // weights do not fit: the generic kernel reads them from global memory
-            fn = kernel_for_kind(kind, vpt, false, quant != nullptr);
+            fn = kernel_for_kind(kind, vpt, false, out);
             if (!fn) return BEAM_ERR_SHAPE;
         }
     }
@@ -361,6 +373,8 @@ beam_status launch(bool moe, beam_stream_t stream, uint16_t* h, const uint16_t* 
     p.yq = quant ? quant->q : nullptr;
     p.ysf = quant ? quant->sf : nullptr;
     p.y_gs = quant ? quant->gs : 0.0f;
+    p.yi = quant ? quant->yi : nullptr;
+    p.yis = quant ? quant->yis : nullptr;
 
     void* args[] = {&p};
     cudaError_t err;
@@ -500,7 +514,7 @@ beam_status beam_boundary_fused_nvfp4(beam_stream_t stream, uint16_t* h, const u
         return BEAM_ERR_ALIAS;
     if ((const void*)x != (const void*)h && overlaps(h, rows, x, rows)) return BEAM_ERR_ALIAS;
     if (overlaps(h, rows, post_w, vec) || overlaps(h, rows, pre_w, vec)) return BEAM_ERR_ALIAS;
-    const QuantOut qo{y_fp4, y_scale, y_global_scale};
+    const QuantOut qo{beam::kOutNvfp4, y_fp4, y_scale, y_global_scale, nullptr, nullptr};
     return launch(false, stream, h, x, nullptr, nullptr, post_w, pre_w, n, eps, T, D, nullptr, opts, 1.0f, &qo);
 }
 
@@ -522,9 +536,62 @@ beam_status beam_moe_combine_boundary_nvfp4(beam_stream_t stream, uint16_t* h, c
     if (overlaps(h, rows, expert_out, erows) || overlaps(h, rows, topk_w, wbytes) || overlaps(h, rows, post_w, vec) ||
         overlaps(h, rows, pre_w, vec))
         return BEAM_ERR_ALIAS;
-    const QuantOut qo{y_fp4, y_scale, y_global_scale};
+    const QuantOut qo{beam::kOutNvfp4, y_fp4, y_scale, y_global_scale, nullptr, nullptr};
     return launch(true, stream, h, nullptr, expert_out, topk_w, post_w, pre_w, n, eps, T, D, nullptr, opts, 1.0f,
                   &qo);
+}
+
+// y's int8 buffers: both given, aligned, apart from each other and from every other operand
+static beam_status check_int8(int64_t T, int D, const int8_t* q, const float* scale, const beam_launch_opts* opts,
+                              std::initializer_list<std::pair<const void*, size_t>> others) {
+    // the register kernels alone write int8: no ring options
+    if (opts && (opts->stages > 0 || (opts->flags & BEAM_OPT_TEST_WAIT_TIMEOUT))) return BEAM_ERR_ARG;
+    if (T == 0) return BEAM_OK;
+    if (!q || !scale) return BEAM_ERR_NULL;
+    for (const auto& o : others)
+        if (!o.first) return BEAM_ERR_NULL;
+    if (!aligned16(q) || !aligned16(scale)) return BEAM_ERR_ALIGN;
+    for (const auto& o : others)
+        if (!aligned16(o.first)) return BEAM_ERR_ALIGN;
+    const size_t qb = (size_t)T * (size_t)D, sb = (size_t)T * 4u;
+    if (overlaps(q, qb, scale, sb)) return BEAM_ERR_ALIAS;
+    for (const auto& o : others)
+        if (overlaps(q, qb, o.first, o.second) || overlaps(scale, sb, o.first, o.second)) return BEAM_ERR_ALIAS;
+    return BEAM_OK;
+}
+
+beam_status beam_boundary_fused_int8(beam_stream_t stream, uint16_t* h, const uint16_t* x, const uint16_t* post_w,
+                                     const uint16_t* pre_w, int n, float eps, int64_t T, int D, int8_t* y_int8,
+                                     float* y_scale, const beam_launch_opts* opts) {
+    beam_status st = check_common(n, eps, T, D, opts);
+    if (st != BEAM_OK) return st;
+    const size_t rows = (size_t)T * (size_t)D * 2u, vec = (size_t)D * 2u;
+    st = check_int8(T, D, y_int8, y_scale, opts, {{h, rows}, {x, rows}, {post_w, vec}, {pre_w, vec}});
+    if (st != BEAM_OK || T == 0) return st;
+    if ((const void*)x != (const void*)h && overlaps(h, rows, x, rows)) return BEAM_ERR_ALIAS;
+    if (overlaps(h, rows, post_w, vec) || overlaps(h, rows, pre_w, vec)) return BEAM_ERR_ALIAS;
+    const QuantOut qo{beam::kOutInt8, nullptr, nullptr, 0.0f, y_int8, y_scale};
+    return launch(false, stream, h, x, nullptr, nullptr, post_w, pre_w, n, eps, T, D, nullptr, opts, 1.0f, &qo);
+}
+
+beam_status beam_moe_combine_boundary_int8(beam_stream_t stream, uint16_t* h, const uint16_t* expert_out,
+                                           const float* topk_w, float route_scale, const uint16_t* post_w,
+                                           const uint16_t* pre_w, int n, float eps, int64_t T, int D,
+                                           int8_t* y_int8, float* y_scale, const beam_launch_opts* opts) {
+    beam_status st = check_common(n, eps, T, D, opts);
+    if (st != BEAM_OK) return st;
+    if (!std::isfinite(route_scale)) return BEAM_ERR_ARG;
+    const size_t rows = (size_t)T * (size_t)D * 2u, vec = (size_t)D * 2u;
+    const size_t erows = rows * BEAM_MOE_TOPK, wbytes = (size_t)T * BEAM_MOE_TOPK * 4u;
+    st = check_int8(T, D, y_int8, y_scale, opts,
+                    {{h, rows}, {expert_out, erows}, {topk_w, wbytes}, {post_w, vec}, {pre_w, vec}});
+    if (st != BEAM_OK || T == 0) return st;
+    if (overlaps(h, rows, expert_out, erows) || overlaps(h, rows, topk_w, wbytes) || overlaps(h, rows, post_w, vec) ||
+        overlaps(h, rows, pre_w, vec))
+        return BEAM_ERR_ALIAS;
+    const QuantOut qo{beam::kOutInt8, nullptr, nullptr, 0.0f, y_int8, y_scale};
+    return launch(true, stream, h, nullptr, expert_out, topk_w, post_w, pre_w, n, eps, T, D, nullptr, opts,
+                  route_scale, &qo);
 }
 
 beam_status beam_boundary_fused(beam_stream_t stream, uint16_t* h, const uint16_t* x, const uint16_t* post_w,

@@ -45,6 +45,8 @@ struct BoundaryParams {
     uint8_t* yq;            // NVFP4 y: [T, D/2] E2M1 codes, element 2i in the low nibble
     uint8_t* ysf;           // NVFP4 y: [T, D/16] E4M3 block scales
     float y_gs;             // NVFP4 y: global scale
+    int8_t* yi;             // [T, D] int8 codes of y (y as int8)
+    float* yis;             // [T] their scales
 };
 
 constexpr unsigned kFlagForceExact = 1u;
@@ -85,6 +87,10 @@ __device__ __forceinline__ void st_stream(void* p, uint4 v) {
 __device__ __forceinline__ void st_stream_u32(void* p, uint32_t v) {
     asm volatile("st.global.L2::cache_hint.u32 [%0], %1, %2;" :: "l"(p), "r"(v), "l"(l2_evict_first()) : "memory");
 }
+__device__ __forceinline__ void st_stream_u64(void* p, uint2 v) {
+    asm volatile("st.global.L2::cache_hint.v2.u32 [%0], {%1, %2}, %3;"
+                 :: "l"(p), "r"(v.x), "r"(v.y), "l"(l2_evict_first()) : "memory");
+}
 __device__ __forceinline__ void st_stream_u8(void* p, uint32_t v) {
     asm volatile("st.global.L2::cache_hint.u8 [%0], %1, %2;" :: "l"(p), "r"(v), "l"(l2_evict_first()) : "memory");
 }
@@ -114,7 +120,11 @@ struct RedScratch {
     float2 part[kMaxThreads];
     float4 result;      // (rounded sum, 1 if certified else 0, its RMS factor, unused)
     float inv_sf[128];  // NVFP4: RN32(y_global_scale / sf) for every E4M3 code sf, 0 for sf = 0
+    uint32_t amax[16];  // int8: every warp's largest |y| (BF16 bits)
 };
+
+// How y leaves
+enum OutKind { kOutBf16 = 0, kOutNvfp4 = 1, kOutInt8 = 2 };
 
 // r = 1 / sqrt(S/D + eps), each operation rounded to nearest
 __device__ __forceinline__ float rms_factor(float S, int D, float eps) {
@@ -239,12 +249,90 @@ __device__ __forceinline__ float div6_bf16(float a) {
 }
 
 // h is read and later overwritten by the same thread; this form also keeps
-// the read ahead of any later store (the NVFP4 MoE path parks x in the h row)
+// the read ahead of any later store (the MoE paths that write y in fewer bits park x
+// in the h row)
 __device__ __forceinline__ uint4 ld_stream_rw_ordered(const void* p) {
     uint4 r;
     asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
                  : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p), "l"(l2_evict_first()) : "memory");
     return r;
+}
+
+// the larger of each half, as unsigned 16-bit numbers
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// The row's largest |y| as BF16 bits, from the y vectors that every thread of
+// the block holds (zeros in unused slots). Sign-free BF16 bits order like the
+// numbers they stand for, infinity above every finite value and NaN above
+// that, so one integer maximum finds it and keeps a NaN. One barrier; the next
+// row's reductions keep its scratch from being overwritten too early.
+template <int VPT>
+__device__ __forceinline__ float block_amax(const uint4 (&yv)[VPT], RedScratch* rs) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) m = max_u16x2(m, word(yv[i], q) & 0x7FFF7FFFu);
+    m = __reduce_max_sync(0xFFFFFFFFu, max(m >> 16, m & 0xFFFFu));
+    if ((threadIdx.x & 31) == 0) rs->amax[threadIdx.x >> 5] = m;
+    __syncthreads();
+    const int nw = blockDim.x >> 5;
+    for (int w = 0; w < nw; ++w) m = max(m, rs->amax[w]);
+    return __uint_as_float(m << 16);
+}
+
+// Eight BF16 values -> eight int8 codes rint(RN32(v * inv)), |v * inv| <= 127.
+// Adding 1.5 * 2^23 rounds to an integer (nearest even) and leaves its two's
+// complement in the low byte; scalar adds, which never fuse with the product.
+__device__ __forceinline__ uint2 bf8_to_int8(const uint4& v, float2 inv) {
+    constexpr float kMagic = 0x1.8p+23f;
+    uint32_t r[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const float2 a = mul2_rn(bf2_to_f2(word(v, 2 * p)), inv), b = mul2_rn(bf2_to_f2(word(v, 2 * p + 1)), inv);
+        const uint32_t lo = __byte_perm(__float_as_uint(__fadd_rn(a.x, kMagic)), __float_as_uint(__fadd_rn(a.y, kMagic)), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(__fadd_rn(b.x, kMagic)), __float_as_uint(__fadd_rn(b.y, kMagic)), 0x0040);
+        r[p] = __byte_perm(lo, hi, 0x5410);
+    }
+    return make_uint2(r[0], r[1]);
+}
+
+// y as int8 with one scale for the row: scale = RN32(amax / 127), codes
+// rint(RN32(y * RN32(127 / amax))). A row of zeros gets codes 0 and scale 0; a
+// row that holds a NaN or an infinity gets codes 0 and that scale, so that
+// every product with the row is NaN. Below 2^-100 the row is first brought up
+// by 2^64 (exact), where 127 / amax does not overflow.
+// One more block reduction than the BF16 output, over values that are in
+// registers already; it saves D bytes of the 8 D that a dense row moves.
+template <int VPT, bool FULL>
+__device__ __forceinline__ void store_row_int8(const BoundaryParams& p, long long row, uint4 (&yv)[VPT],
+                                               RedScratch* rs) {
+    const int tid = threadIdx.x, nt = blockDim.x;
+    float amax = block_amax<VPT>(yv, rs);
+    if (tid == 0) p.yis[row] = __fdiv_rn(amax, 127.0f);
+    const bool live = amax > 0.0f && amax < INFINITY;
+    if (live && amax < 0x1p-100f) {
+        const float2 up = make_float2(0x1p+64f, 0x1p+64f);
+        amax *= 0x1p+64f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) set_word(yv[i], q, f2_to_bf2(mul2_rn(bf2_to_f2(word(yv[i], q)), up)));
+    }
+    const float inv = __fdiv_rn(127.0f, amax);
+    const float2 iv = make_float2(inv, inv);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int vi = tid + i * nt;
+        if (FULL || vi < p.nvec) {
+            const uint2 c = live ? bf8_to_int8(yv[i], iv) : make_uint2(0u, 0u);
+            st_stream_u64(p.yi + (size_t)row * (size_t)p.D + (size_t)vi * 8, c);
+        }
+    }
 }
 
 // Norm weights staged once per CTA in shared memory by FULL kernels, as BF16
@@ -273,7 +361,7 @@ __device__ __forceinline__ void load_weights(const uint16_t* g, const uint4* ws,
 // `after_s1` runs on every thread right after the post-norm reduction's
 // barrier, when every thread has consumed its inputs of this row. FULL: the
 // row is exactly NT * VPT vectors (no bounds checks) and ws holds the weights.
-template <int VPT, bool MOE, bool FULL, bool QUANT, class AfterS1>
+template <int VPT, bool MOE, bool FULL, int OUT, class AfterS1>
 __device__ __forceinline__ void finish_row(const BoundaryParams& p, long long row, uint4 (&xv)[VPT],
                                            uint4 (&hv)[VPT], RedScratch* rs, ExactScratch* sc,
                                            const uint4* ws, AfterS1 after_s1) {
@@ -299,9 +387,9 @@ __device__ __forceinline__ void finish_row(const BoundaryParams& p, long long ro
         // or, for MoE, the combined x parked in this y row
         const uint16_t* srow = p.x + base;
         if (MOE) {
-            // park x in this row of y, or, when y leaves as NVFP4, in the row of
-            // h (already in registers; h' overwrites it later)
-            uint16_t* park = QUANT ? p.h + base : p.y + base;
+            // park x in this row of y, or, when y leaves in fewer bits, in the row
+            // of h (already in registers; h' overwrites it later)
+            uint16_t* park = OUT != kOutBf16 ? p.h + base : p.y + base;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int vi = tid + i * nt;
@@ -350,7 +438,7 @@ __device__ __forceinline__ void finish_row(const BoundaryParams& p, long long ro
     }
     const float2 r2v = make_float2(r2, r2);
 
-    // ---- y = bf16((h' r2) pre_w), stored as BF16 or quantised to NVFP4
+    // ---- y = bf16((h' r2) pre_w), stored as BF16 or quantised to NVFP4 or int8
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int vi = tid + i * nt;
@@ -362,9 +450,10 @@ __device__ __forceinline__ void finish_row(const BoundaryParams& p, long long ro
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 set_word(yv, q, f2_to_bf2(mul2_rn(mul2_rn(bf2_to_f2(word(hv[i], q)), r2v), qw[q])));
-            if (!QUANT) st_stream(p.y + base + (size_t)vi * 8, yv);
+            if (OUT == kOutBf16) st_stream(p.y + base + (size_t)vi * 8, yv);
         }
-        if (QUANT) {
+        if (OUT == kOutInt8) xv[i] = yv;  // x is spent: its registers hold y for the row's maximum
+        if (OUT == kOutNvfp4) {
             // a block of 16 is this vector and its neighbour, held by lane ^ 1
             float am = 0.0f;
 #pragma unroll
@@ -389,6 +478,7 @@ __device__ __forceinline__ void finish_row(const BoundaryParams& p, long long ro
             }
         }
     }
+    if (OUT == kOutInt8) store_row_int8<VPT, FULL>(p, row, xv, rs);
 }
 
 struct NoOp {
@@ -397,8 +487,8 @@ struct NoOp {
 
 // Loads straight to registers (dense x or the MoE combine), optionally asking
 // L2 for the inputs of this CTA's row `prefetch_rows` ahead.
-template <int VPT, bool MOE, bool FULL, bool QUANT>
-__global__ void __launch_bounds__(kMaxThreads) boundary_kernel(const BoundaryParams p) {
+template <int VPT, bool MOE, bool FULL, int OUT>
+__device__ __forceinline__ void boundary_rows(const BoundaryParams& p) {
     extern __shared__ __align__(16) uint4 ws_dyn[];
     __shared__ RedScratch rs;
     __shared__ ExactScratch sc;
@@ -409,7 +499,7 @@ __global__ void __launch_bounds__(kMaxThreads) boundary_kernel(const BoundaryPar
     // overlaps the previous kernel on the stream (the caller guarantees that
     // kernel does not write the weights)
     pdl_trigger();
-    if (QUANT) {
+    if (OUT == kOutNvfp4) {
         // inverse block scales, read after the first row reduction's barrier
         for (int i = tid; i < 128; i += nt) {
             const float sf = e4m3_to_f32((uint32_t)i);
@@ -472,11 +562,22 @@ __global__ void __launch_bounds__(kMaxThreads) boundary_kernel(const BoundaryPar
         for (int i = 0; i < VPT; ++i) {
             const int vi = tid + i * nt;
             const uint16_t* hp = p.h + base + (size_t)vi * 8;
-            hv[i] = (FULL || vi < p.nvec) ? ((MOE && QUANT) ? ld_stream_rw_ordered(hp) : ld_stream_rw(hp))
+            hv[i] = (FULL || vi < p.nvec) ? ((MOE && OUT != kOutBf16) ? ld_stream_rw_ordered(hp) : ld_stream_rw(hp))
                                          : make_uint4(0, 0, 0, 0);
         }
-        finish_row<VPT, MOE, FULL, QUANT>(p, row, xv, hv, &rs, &sc, ws, NoOp{});
+        finish_row<VPT, MOE, FULL, OUT>(p, row, xv, hv, &rs, &sc, ws, NoOp{});
     }
+}
+
+template <int VPT, bool MOE, bool FULL, bool QUANT>
+__global__ void __launch_bounds__(kMaxThreads) boundary_kernel(const BoundaryParams p) {
+    boundary_rows<VPT, MOE, FULL, QUANT ? kOutNvfp4 : kOutBf16>(p);
+}
+
+// the same rows with y as int8
+template <int VPT, bool MOE, bool FULL>
+__global__ void __launch_bounds__(kMaxThreads) boundary_int8_kernel(const BoundaryParams p) {
+    boundary_rows<VPT, MOE, FULL, kOutInt8>(p);
 }
 
 // Dense boundary fed by a ring of `stages` shared-memory slots per CTA. Slot s
@@ -548,7 +649,7 @@ __global__ void __launch_bounds__(kMaxThreads) boundary_ring_kernel(const Bounda
             xv[j] = (FULL || vi < p.nvec) ? xs[vi] : make_uint4(0, 0, 0, 0);
             hv[j] = (FULL || vi < p.nvec) ? hs[vi] : make_uint4(0, 0, 0, 0);
         }
-        finish_row<VPT, false, FULL, false>(p, blockIdx.x + i * G, xv, hv, &rs, &sc, ws, [&]() {
+        finish_row<VPT, false, FULL, kOutBf16>(p, blockIdx.x + i * G, xv, hv, &rs, &sc, ws, [&]() {
             if (tid == 0 && i + S < n_iter) issue(i + S);
         });
     }

@@ -1,0 +1,78 @@
+"""Refusals of the int8 calls, in the C ABI (before any CUDA call) and in the binding: no GPU."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+import torch
+
+import sandwich_norm_residual_gb300 as snr
+from sandwich_norm_residual_gb300 import _lib, build
+
+A = 0x7F0000000000  # fake device addresses: never dereferenced
+D = 5120
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return _lib.load()
+
+
+def test_boundary_int8_argument_errors(lib):
+    H, X, PW, QW, Q, S = (A + (i << 32) for i in range(6))
+    E, W = A + (6 << 32), A + (7 << 32)
+
+    def dense(T=4, d=D, n=2, eps=1e-6, h=H, x=X, q=Q, s=S, opts=None):
+        return lib.beam_boundary_fused_int8(None, h, x, PW, QW, n, eps, T, d, q, s, opts)
+
+    def moe(T=4, d=D, h=H, e=E, w=W, rs=1.0, q=Q, s=S, opts=None):
+        return lib.beam_moe_combine_boundary_int8(None, h, e, w, rs, PW, QW, 2, 1e-6, T, d, q, s, opts)
+
+    for call in (dense, moe):
+        assert call(d=12) == _lib.BEAM_ERR_SHAPE
+        assert call(T=-1) == _lib.BEAM_ERR_SHAPE
+        assert call(T=0, h=None, q=None, s=None) == _lib.BEAM_OK
+        assert call(h=None) == _lib.BEAM_ERR_NULL
+        assert call(q=None) == _lib.BEAM_ERR_NULL
+        assert call(s=None) == _lib.BEAM_ERR_NULL
+        assert call(q=Q + 8) == _lib.BEAM_ERR_ALIGN
+        assert call(s=S + 4) == _lib.BEAM_ERR_ALIGN
+        assert call(s=Q + 4 * D - 16) == _lib.BEAM_ERR_ALIAS  # scales over the codes
+        assert call(q=H + 64) == _lib.BEAM_ERR_ALIAS          # codes inside h
+        assert call(s=PW + 16) == _lib.BEAM_ERR_ALIAS         # scales inside a weight
+        ring = _lib.LaunchOpts(stages=2)
+        assert call(opts=ctypes.byref(ring)) == _lib.BEAM_ERR_ARG
+        hook = _lib.LaunchOpts(flags=_lib.BEAM_OPT_TEST_WAIT_TIMEOUT)
+        assert call(opts=ctypes.byref(hook)) == _lib.BEAM_ERR_ARG
+        assert call() in (_lib.BEAM_ERR_CUDA, _lib.BEAM_ERR_DEVICE)
+    assert dense(n=0) == _lib.BEAM_ERR_ARG
+    assert dense(eps=float("nan")) == _lib.BEAM_ERR_ARG
+    assert dense(q=X + 64) == _lib.BEAM_ERR_ALIAS
+    assert dense(x=H + 2 * D) == _lib.BEAM_ERR_ALIAS          # x partly over h
+    assert dense(x=H) in (_lib.BEAM_ERR_CUDA, _lib.BEAM_ERR_DEVICE)  # x may be h itself
+    assert moe(rs=float("inf")) == _lib.BEAM_ERR_ARG
+    assert moe(h=E + 4096) == _lib.BEAM_ERR_ALIAS
+    assert moe(q=W) == _lib.BEAM_ERR_ALIAS
+
+
+def bf(*shape, device="cpu"):
+    return torch.zeros(shape, dtype=torch.bfloat16, device=device)
+
+
+def test_binding_checks_the_int8_boundaries():
+    T, d = 4, 64
+    h, x, w = bf(T, d), bf(T, d), bf(d)
+    with pytest.raises(ValueError, match="y_int8 must have shape"):
+        snr.boundary_fused_int8(h, x, w, w, 2, y_int8=torch.zeros((T, d // 2), dtype=torch.int8))
+    with pytest.raises(ValueError, match="y_scale must have shape"):
+        snr.boundary_fused_int8(h, x, w, w, 2, y_scale=torch.zeros(T + 1))
+    with pytest.raises(TypeError, match="y_int8 must be"):
+        snr.boundary_fused_int8(h, x, w, w, 2, y_int8=torch.zeros((T, d), dtype=torch.uint8))
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        snr.boundary_fused_int8(h, x, w, w, 2)
+    e, tw = bf(T, 8, d), torch.zeros((T, 8))
+    with pytest.raises(ValueError, match="shape mismatch"):
+        snr.moe_combine_boundary_int8(h, e[:3].contiguous(), tw, w, w, 2)
+    with pytest.raises(ValueError, match="one device"):
+        snr.moe_combine_boundary_int8(h, e, tw.to("meta"), w, w, 2)
