@@ -250,6 +250,39 @@ BEAM_API beam_status beam_qk_norm_ex(beam_stream_t stream, uint16_t* q, uint16_t
                                      int n_q_heads, int n_kv_heads, int head_dim, float eps,
                                      int mode, uint32_t flags);
 
+/* Output types and the largest inner size of beam_matmul_int8. */
+#define BEAM_OUT_BF16 0
+#define BEAM_OUT_FP32 1
+#define BEAM_MATMUL_MAX_K 65536
+
+/*
+ * Product of 8-bit integers with a scale for each token and each channel: the
+ * projection that reads an int8 boundary's y (beam_boundary_fused_int8). An
+ * addition of this library; the pages name no 8-bit integer product.
+ *   out[m, n] = RN( RN32( RN32( (float)acc * a_scale[m] ) * w_scale[n] ) ),
+ *   acc = sum_k a[m, k] * w[n, k]
+ * The last rounding is to BF16, or nothing when out is FP32.
+ * acc is the integer sum, exact as long as no partial sum of its terms leaves
+ * +-2^24 (so always for K <= 1024); where one does, acc carries FP32 rounding
+ * of its partial sums.
+ *   a       [M, K] int8 tokens (all 256 codes); 16-byte aligned
+ *   a_scale [M] FP32; w_scale [N] FP32; 4-byte aligned
+ *   w       [N, K] int8 channels (one row per output channel); 16-byte aligned
+ *   K       a multiple of 16, 16 <= K <= BEAM_MATMUL_MAX_K
+ *   M, N    0 launches nothing; M at most 2^31 - 1
+ *   out     [M, N], BF16 for BEAM_OUT_BF16, FP32 for BEAM_OUT_FP32; aligned to
+ *           its element, overlapping no other operand
+ * A scale that is infinite or NaN makes its row's or channel's products with
+ * acc = 0 NaN (0 * inf), as the FP32 products above say.
+ * flags: BEAM_OPT_PDL launches with programmatic stream serialisation: the
+ * kernel reads w before the previous kernel on the stream has completed (that
+ * kernel must not write w), and everything else after. Any other flag gives
+ * BEAM_ERR_ARG.
+ */
+BEAM_API beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, const float* a_scale,
+                                      const int8_t* w, const float* w_scale, int64_t M, int N,
+                                      int K, int out_type, void* out, uint32_t flags);
+
 /*
  * Synchronises `stream`, then reads and clears the current device's status
  * word. Returns BEAM_OK; BEAM_ERR_TIMEOUT if a kernel's bounded wait gave up

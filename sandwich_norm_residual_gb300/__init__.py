@@ -18,7 +18,7 @@ from ._lib import LaunchOpts  # noqa: F401
 __all__ = ["boundary_fused", "moe_combine_boundary", "boundary_fused_host",
            "moe_combine_boundary_host", "boundary_fused_nvfp4",
            "moe_combine_boundary_nvfp4", "boundary_fused_int8", "moe_combine_boundary_int8",
-           "moe_route", "router_sigmoid", "qk_norm", "sync_status",
+           "matmul_int8", "moe_route", "router_sigmoid", "qk_norm", "sync_status",
            "exact_sum_count",
            "version", "BeamError", "LaunchOpts", "library"]
 
@@ -356,6 +356,41 @@ def moe_combine_boundary_int8(h, expert_out, topk_w, post_w, pre_w, n: int, eps:
     if st != 0:
         raise BeamError(st, "beam_moe_combine_boundary_int8")
     return q, scale
+
+
+def matmul_int8(a, a_scale, w, w_scale, out_dtype=None, out=None, stream=None, pdl: bool = False):
+    """Product of int8 tokens and int8 channels, scaled per token and channel.
+
+    a: [M, K] int8 and a_scale: [M] float32, as an int8 boundary writes them; w: [N, K] int8
+    and w_scale: [N] float32. K must be a multiple of 16.
+    Returns [M, N] in out_dtype: bfloat16 (the default) or float32.
+    pdl: launch with programmatic dependent launch (BEAM_OPT_PDL); the kernel before on the
+    stream must not write w.
+    """
+    import torch
+    _check(a, "a", torch.int8, 2)
+    _check(a_scale, "a_scale", torch.float32, 1)
+    _check(w, "w", torch.int8, 2)
+    _check(w_scale, "w_scale", torch.float32, 1)
+    (M, K), N = a.shape, w.shape[0]
+    if w.shape[1] != K or a_scale.shape[0] != M or w_scale.shape[0] != N:
+        raise ValueError("shape mismatch: a [M, K]; a_scale [M]; w [N, K]; w_scale [N]")
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out_dtype must be bfloat16 or float32 (got {out_dtype})")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    _check(out, "out", out_dtype, 2)
+    _shape(out, "out", (M, N))
+    _on_current_device(a=a, a_scale=a_scale, w=w, w_scale=w_scale, out=out)
+    st = _lib.load().beam_matmul_int8(
+        _stream_ptr(stream), a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), M, N, K,
+        _lib.BEAM_OUT_FP32 if out_dtype == torch.float32 else _lib.BEAM_OUT_BF16, out.data_ptr(),
+        _lib.BEAM_OPT_PDL if pdl else 0)
+    if st != 0:
+        raise BeamError(st, "beam_matmul_int8")
+    return out
 
 
 def moe_route(logits, bias, n_group: int = 8, topk_group: int = 4, topk: int = 8,

@@ -9,13 +9,15 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbeamboundary.so")
-SOURCES = [os.path.join(CSRC, "beam_boundary.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("beam_boundary.cu", "matmul_int8.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
     os.path.join(INCLUDE, "beam_boundary.h")]
 
@@ -56,14 +58,21 @@ def up_to_date() -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
+    def run(cmd: list[str]) -> None:
+        r = subprocess.run([nvcc()] + flags(verbose) + cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("nvcc failed building libbeamboundary.so")
+        if verbose:
+            sys.stderr.write(r.stdout + r.stderr)
+
     tmp = f"{LIB}.{os.getpid()}.tmp"
-    cmd = [nvcc()] + flags(verbose) + SOURCES + ["-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("nvcc failed building libbeamboundary.so")
-    if verbose:
-        sys.stderr.write(r.stdout + r.stderr)
+    with tempfile.TemporaryDirectory() as d:
+        # the sources compile side by side; with -c the -shared among the flags has no effect
+        objs = [os.path.join(d, os.path.basename(s) + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(len(SOURCES)) as ex:
+            list(ex.map(lambda so: run(["-c", so[0], "-o", so[1]]), zip(SOURCES, objs)))
+        run(objs + ["-o", tmp])
     os.replace(tmp, LIB)
     return LIB
 

@@ -15,6 +15,7 @@
 #include <utility>
 
 #include "boundary_kernels.cuh"
+#include "device.h"
 #include "route.cuh"
 #include "qk_norm.cuh"
 
@@ -43,6 +44,7 @@ struct DeviceInfo {
     bool checked = false;
     bool ok = false;
     int ordinal = 0;
+    unsigned int* status_word = nullptr;      // device address of g_status_word
     bool pageable_access = false;             // kernels may read pageable host memory
     int sms = 0;
     long long l2_bytes = 0;
@@ -187,6 +189,12 @@ beam_status current_device(DeviceInfo** info) {
             return BEAM_ERR_CUDA;
         }
         d.ok = (major == 10 && minor == 3);
+        void* word = nullptr;
+        if (d.ok && cudaGetSymbolAddress(&word, beam::g_status_word) != cudaSuccess) {
+            cudaGetLastError();
+            return BEAM_ERR_CUDA;
+        }
+        d.status_word = static_cast<unsigned int*>(word);
         d.ordinal = dev;
         d.l2_bytes = l2;
         d.pageable_access = pageable != 0;
@@ -443,6 +451,13 @@ beam_status host_addresses(P*&... ptrs) {
 }
 
 }  // namespace
+
+beam_status beam::device(Device* out) {
+    DeviceInfo* info = nullptr;
+    const beam_status st = current_device(&info);
+    if (st == BEAM_OK) *out = Device{info->ordinal, info->sms, info->status_word};
+    return st;
+}
 
 extern "C" {
 

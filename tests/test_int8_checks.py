@@ -76,3 +76,55 @@ def test_binding_checks_the_int8_boundaries():
         snr.moe_combine_boundary_int8(h, e[:3].contiguous(), tw, w, w, 2)
     with pytest.raises(ValueError, match="one device"):
         snr.moe_combine_boundary_int8(h, e, tw.to("meta"), w, w, 2)
+
+
+def test_matmul_argument_errors(lib):
+    AA, AS, W, WS, O = (A + (i << 33) for i in range(5))
+
+    def mm(M=4, N=40, K=64, a=AA, sa=AS, w=W, sw=WS, ty=0, o=O, flags=0):
+        return lib.beam_matmul_int8(None, a, sa, w, sw, M, N, K, ty, o, flags)
+
+    assert mm(M=-1) == _lib.BEAM_ERR_SHAPE
+    assert mm(M=1 << 31) == _lib.BEAM_ERR_SHAPE
+    assert mm(N=-1) == _lib.BEAM_ERR_SHAPE
+    for K in (0, 8, 24, -16, _lib.BEAM_MATMUL_MAX_K + 16):
+        assert mm(K=K) == _lib.BEAM_ERR_SHAPE
+    assert mm(ty=2) == _lib.BEAM_ERR_ARG
+    assert mm(flags=_lib.BEAM_OPT_FORCE_EXACT_SUM) == _lib.BEAM_ERR_ARG
+    assert mm(M=0, a=None) == _lib.BEAM_OK
+    assert mm(N=0, w=None) == _lib.BEAM_OK
+    for name in ("a", "sa", "w", "sw", "o"):
+        assert mm(**{name: None}) == _lib.BEAM_ERR_NULL
+    assert mm(a=AA + 8) == _lib.BEAM_ERR_ALIGN
+    assert mm(w=W + 4) == _lib.BEAM_ERR_ALIGN
+    assert mm(sa=AS + 2) == _lib.BEAM_ERR_ALIGN
+    assert mm(o=O + 1) == _lib.BEAM_ERR_ALIGN
+    assert mm(o=O + 2, ty=1) == _lib.BEAM_ERR_ALIGN
+    assert mm(o=AA + 64) == _lib.BEAM_ERR_ALIAS
+    assert mm(o=W - 2) == _lib.BEAM_ERR_ALIAS
+    assert mm(o=AS + 4) == _lib.BEAM_ERR_ALIAS
+    assert mm(o=WS) == _lib.BEAM_ERR_ALIAS
+    for flags in (0, _lib.BEAM_OPT_PDL):
+        assert mm(o=O + 2, flags=flags) in (_lib.BEAM_ERR_CUDA, _lib.BEAM_ERR_DEVICE)
+
+
+def test_binding_checks_the_product():
+    a, sa, w, sw = torch.zeros((4, 64), dtype=torch.int8), torch.zeros(4), torch.zeros((6, 64), dtype=torch.int8), \
+        torch.zeros(6)
+    for bad in ((a, sa, w[:, :32].contiguous(), sw), (a, sa[:3], w, sw), (a, sa, w, sw[:5])):
+        with pytest.raises(ValueError, match="shape mismatch"):
+            snr.matmul_int8(*bad)
+    with pytest.raises(TypeError, match="a must be"):
+        snr.matmul_int8(a.to(torch.uint8), sa, w, sw)
+    with pytest.raises(ValueError, match="contiguous"):
+        snr.matmul_int8(a, sa, torch.zeros((64, 6), dtype=torch.int8).t(), sw)
+    with pytest.raises(TypeError, match="out_dtype"):
+        snr.matmul_int8(a, sa, w, sw, out_dtype=torch.float16)
+    with pytest.raises(ValueError, match="out must have shape"):
+        snr.matmul_int8(a, sa, w, sw, out=torch.zeros((4, 7), dtype=torch.bfloat16))
+    with pytest.raises(TypeError, match="out must be"):
+        snr.matmul_int8(a, sa, w, sw, out_dtype=torch.float32, out=torch.zeros((4, 6), dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="one device"):
+        snr.matmul_int8(a, sa, w.to("meta"), sw)
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        snr.matmul_int8(a, sa, w, sw)
