@@ -208,6 +208,62 @@ BEAM_API beam_status beam_router_sigmoid(beam_stream_t stream, const float* z, f
  */
 BEAM_API beam_status beam_router_sigmoid_fast(beam_stream_t stream, const float* z, float* s, int64_t count);
 
+/* Most experts of beam_moe_balance_loss. */
+#define BEAM_BALANCE_MAX_EXPERTS 512
+
+/*
+ * Balance loss of the router in front of the MoE combine, with the per-expert
+ * counts (which also drive the correction bias that beam_moe_route adds). The
+ * pages say that Beam routes as DeepSeek-V3 does, which trains with this
+ * sequence-wise loss; the pages print no formula. For the n tokens of a
+ * sequence, with s = sigmoid(logits), p_t = s_t / sum_e s_te:
+ *   counts_e = how often expert e stands in the tokens' topk_idx
+ *   loss     = alpha * sum_e f_e P_e,  f_e = E / (topk n) counts_e,
+ *              P_e = (1/n) sum_t p_te
+ * FP32 sigmoids (a few ulp, not the correctly rounded ones of
+ * beam_router_sigmoid) and rows, 64-bit sums over tokens and experts, one
+ * rounding of the loss. Every run gives the same bits.
+ *   logits      [T, E] FP32, E a multiple of 4, at most BEAM_BALANCE_MAX_EXPERTS;
+ *               16-byte aligned
+ *   topk_idx    [T, topk] int32 in [0, E), topk in [1, BEAM_ROUTE_MAX_TOPK]
+ *   seq_offsets [S + 1] int32, non-decreasing, within [0, T]: sequence i holds the
+ *               tokens seq_offsets[i] .. seq_offsets[i + 1] - 1; or NULL for one
+ *               sequence of T tokens (S = 1). Tokens of no sequence (padding) are
+ *               not read. An empty sequence has loss 0 and counts 0.
+ *   loss [S] FP32; counts [S, E] int32, 16-byte aligned; every element written
+ *   workspace   device memory for this call alone, 16-byte aligned, of at least
+ *               beam_moe_balance_workspace(T, E, S) bytes; need not be cleared
+ * 4-byte aligned where nothing else is said. Outputs and workspace overlap
+ * neither each other nor an input. T at most 2^31 - 1.
+ * A token whose sigmoids are all 0 has p = 0. A NaN logit makes its sequence's
+ * loss NaN. An expert id outside [0, E) is not counted; offsets that decrease or
+ * leave [0, T] make losses and counts unspecified (no address outside the
+ * operands is touched); for both, beam_sync_status then returns BEAM_ERR_ARG.
+ */
+BEAM_API beam_status beam_moe_balance_loss(beam_stream_t stream, const float* logits,
+                                           const int32_t* topk_idx, const int32_t* seq_offsets,
+                                           int64_t T, int E, int topk, int64_t S, float alpha,
+                                           float* loss, int32_t* counts, void* workspace,
+                                           int64_t workspace_bytes);
+
+/* Bytes of workspace of beam_moe_balance_loss, -1 for a bad shape. */
+BEAM_API int64_t beam_moe_balance_workspace(int64_t T, int E, int64_t S);
+
+/*
+ * Gradient of sum_i dloss_i * loss_i for the logits (the counts are constants):
+ *   dlogits_te = dloss alpha E / (topk n^2) s_te (1 - s_te) / (sum_i s_ti)
+ *                * (counts_e - sum_i counts_i p_ti)
+ *   dloss [S] FP32; counts as beam_moe_balance_loss wrote them; logits,
+ *   seq_offsets, alpha and topk the same as there
+ *   dlogits [T, E] FP32, 16-byte aligned, overlapping no input; every element is
+ *   written, 0 for a token of no sequence and for one whose sigmoids are all 0
+ */
+BEAM_API beam_status beam_moe_balance_loss_backward(beam_stream_t stream, const float* dloss,
+                                                    const float* logits, const int32_t* counts,
+                                                    const int32_t* seq_offsets, int64_t T, int E,
+                                                    int topk, int64_t S, float alpha,
+                                                    float* dlogits);
+
 /* Head dimension and modes of beam_qk_norm. */
 #define BEAM_QK_HEAD_DIM 128
 #define BEAM_QK_ROPE 0
@@ -287,7 +343,7 @@ BEAM_API beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, con
  * Synchronises `stream`, then reads and clears the current device's status
  * word. Returns BEAM_OK; BEAM_ERR_TIMEOUT if a kernel's bounded wait gave up
  * since the last read; BEAM_ERR_ARG if beam_qk_norm met a position out of
- * range; or BEAM_ERR_CUDA if the synchronisation failed. The word is shared
+ * range, or beam_moe_balance_loss an expert or offset out of range; or BEAM_ERR_CUDA if the synchronisation failed. The word is shared
  * by all streams and threads using the device.
  */
 BEAM_API beam_status beam_sync_status(beam_stream_t stream);

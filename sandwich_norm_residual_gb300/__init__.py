@@ -18,7 +18,8 @@ from ._lib import LaunchOpts  # noqa: F401
 __all__ = ["boundary_fused", "moe_combine_boundary", "boundary_fused_host",
            "moe_combine_boundary_host", "boundary_fused_nvfp4",
            "moe_combine_boundary_nvfp4", "boundary_fused_int8", "moe_combine_boundary_int8",
-           "matmul_int8", "moe_route", "router_sigmoid", "qk_norm", "sync_status",
+           "matmul_int8", "moe_route", "moe_balance_loss", "moe_balance_loss_backward",
+           "router_sigmoid", "qk_norm", "sync_status",
            "exact_sum_count",
            "version", "BeamError", "LaunchOpts", "library"]
 
@@ -422,6 +423,86 @@ def moe_route(logits, bias, n_group: int = 8, topk_group: int = 4, topk: int = 8
     if st != 0:
         raise BeamError(st, "beam_moe_route_ex")
     return idx, w
+
+
+def _sequences(seq_offsets, **operands):
+    """(pointer, S) of the sequence offsets, which join the operands of the device check."""
+    import torch
+    S, ptr = 1, None
+    if seq_offsets is not None:
+        _check(seq_offsets, "seq_offsets", torch.int32, 1)
+        S = seq_offsets.shape[0] - 1
+        if S < 1:
+            raise ValueError("seq_offsets must have at least two entries")
+        operands["seq_offsets"] = seq_offsets
+        ptr = seq_offsets.data_ptr()
+    return ptr, S, operands
+
+
+def moe_balance_loss(logits, topk_idx, alpha: float, seq_offsets=None, loss=None, counts=None,
+                     stream=None):
+    """Sequence-wise balance loss of the router, with the per-expert counts.
+
+    logits: [T, E] float32; topk_idx: [T, topk] int32, as ``moe_route`` gives them;
+    seq_offsets: [S + 1] int32 first tokens of the sequences and the end of the last (None: one
+    sequence); tokens outside are padding and not read.
+    Returns (loss float32 [S], counts int32 [S, E]).
+    """
+    import torch
+    _check(logits, "logits", torch.float32, 2)
+    _check(topk_idx, "topk_idx", torch.int32, 2)
+    T, E = logits.shape
+    if topk_idx.shape[0] != T:
+        raise ValueError("shape mismatch: logits [T, E]; topk_idx [T, topk]")
+    off, S, ops = _sequences(seq_offsets, logits=logits, topk_idx=topk_idx)
+    if loss is None:
+        loss = torch.empty(S, dtype=torch.float32, device=logits.device)
+    if counts is None:
+        counts = torch.empty((S, E), dtype=torch.int32, device=logits.device)
+    _check(loss, "loss", torch.float32, 1)
+    _check(counts, "counts", torch.int32, 2)
+    _shape(loss, "loss", (S,))
+    _shape(counts, "counts", (S, E))
+    _on_current_device(loss=loss, counts=counts, **ops)
+    lib = _lib.load()
+    ws_bytes = max(0, lib.beam_moe_balance_workspace(T, E, S))
+    # from the pool of the stream that uses it, so that no other stream takes it over too early
+    with torch.cuda.stream(stream):
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=logits.device)
+    st = lib.beam_moe_balance_loss(_stream_ptr(stream), logits.data_ptr(), topk_idx.data_ptr(), off, T, E,
+                                   topk_idx.shape[1], S, float(alpha), loss.data_ptr(),
+                                   counts.data_ptr(), ws.data_ptr(), ws_bytes)
+    if st != 0:
+        raise BeamError(st, "beam_moe_balance_loss")
+    return loss, counts
+
+
+def moe_balance_loss_backward(dloss, logits, counts, topk: int, alpha: float, seq_offsets=None,
+                              dlogits=None, stream=None):
+    """Gradient of ``(dloss * loss).sum()`` for the logits of ``moe_balance_loss``.
+
+    dloss: [S] float32; counts: [S, E] int32 as ``moe_balance_loss`` returned them; the other
+    arguments as there. Returns dlogits float32 [T, E] (0 for padding).
+    """
+    import torch
+    _check(dloss, "dloss", torch.float32, 1)
+    _check(logits, "logits", torch.float32, 2)
+    _check(counts, "counts", torch.int32, 2)
+    T, E = logits.shape
+    off, S, ops = _sequences(seq_offsets, dloss=dloss, logits=logits, counts=counts)
+    _shape(dloss, "dloss", (S,))
+    _shape(counts, "counts", (S, E))
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    _check(dlogits, "dlogits", torch.float32, 2)
+    _shape(dlogits, "dlogits", (T, E))
+    _on_current_device(dlogits=dlogits, **ops)
+    st = _lib.load().beam_moe_balance_loss_backward(_stream_ptr(stream), dloss.data_ptr(), logits.data_ptr(),
+                                                    counts.data_ptr(), off, T, E, int(topk), S,
+                                                    float(alpha), dlogits.data_ptr())
+    if st != 0:
+        raise BeamError(st, "beam_moe_balance_loss_backward")
+    return dlogits
 
 
 def router_sigmoid(z, out=None, stream=None, fast: bool = False):

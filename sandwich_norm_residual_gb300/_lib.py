@@ -24,6 +24,7 @@ BEAM_ROUTE_MAX_TOPK = 16
 BEAM_QK_HEAD_DIM = 128
 BEAM_QK_ROPE = 0
 BEAM_QK_SSMAX = 1
+BEAM_BALANCE_MAX_EXPERTS = 512
 BEAM_OUT_BF16 = 0
 BEAM_OUT_FP32 = 1
 BEAM_MATMUL_MAX_K = 65536
@@ -71,6 +72,11 @@ SIGNATURES = {
     "beam_qk_norm_ex": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _i32,
                                 _f32, _i32, _u32]),
     "beam_matmul_int8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _u32]),
+    "beam_moe_balance_loss": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i64, _f32, _vp, _vp, _vp,
+                                     _i64]),
+    "beam_moe_balance_workspace": (_i64, [_i64, _i32, _i64]),
+    "beam_moe_balance_loss_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i64, _f32,
+                                              _vp]),
     "beam_sync_status": (_i32, [_vp]),
     "beam_exact_sum_count": (_i32, [_vp, ctypes.POINTER(ctypes.c_uint64), _i32]),
     "beam_status_string": (ctypes.c_char_p, [_i32]),

@@ -17,7 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbeamboundary.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("beam_boundary.cu", "matmul_int8.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("beam_boundary.cu", "matmul_int8.cu", "balance.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
     os.path.join(INCLUDE, "beam_boundary.h")]
 

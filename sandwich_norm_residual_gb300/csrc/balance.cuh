@@ -1,0 +1,292 @@
+// Balance loss of a sigmoid router, its per-expert counts, and its gradient.
+//
+// For the tokens t of a sequence of length n (E experts, K choices a token):
+//   s = sigmoid(z_t), p = s / sum_e s, Q_e = sum_t p_e, c_e = choices of expert e
+//   loss = alpha E / (K n^2) sum_e c_e Q_e
+//   dloss/dz_te = alpha E / (K n^2) s_e (1 - s_e) / (sum s) (c_e - sum_i c_i p_i)
+// Both passes are bound by the logits' way from (and the gradient's way to)
+// HBM: 4 E bytes a token read forward, 4 E read and 4 E written backward. One
+// warp holds a token's row in registers (4 experts a lane for every 128), so
+// the row is read once and its sums are shuffles.
+//
+// Sequences are ragged, so the split goes by tokens: block b takes the tokens
+// [b C, (b + 1) C) and writes one record (Q and c) for every sequence it meets,
+// at index b + s. Along the staircase of (block, sequence) pairs that overlap,
+// b + s grows, so no two pairs share a record, nothing needs to be zeroed, there
+// are no floating-point atomics and the result is the same in every run. A
+// second kernel adds a sequence's records in order, in 64 bits.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "tma.cuh"
+
+namespace beam {
+
+constexpr int kBalanceThreads = 512;
+constexpr int kBalanceWarps = kBalanceThreads / 32;
+constexpr int kBalanceBlocks = 304;  // at most two blocks on each of 152 SMs
+constexpr int kBalanceFinalThreads = 1024;
+constexpr int kBalanceFinalSums = 4 * kBalanceFinalThreads;  // 4 experts a thread
+
+struct BalanceParams {
+    const float* logits;    // [T, E]
+    const int32_t* idx;     // [T, K]
+    const int32_t* off;     // [S + 1], or NULL: one sequence of T tokens
+    long long T;
+    int E, K, S;
+    int chunk;              // tokens a block
+    int blocks;
+    float* rec_q;           // [blocks + S, E]
+    int32_t* rec_c;         // [blocks + S, E]
+    double factor;          // alpha E / K
+    float* loss;            // [S]
+    int32_t* counts;        // [S, E] (written forward, read backward)
+    const float* dloss;     // [S]
+    float* dlogits;         // [T, E]
+    unsigned int* status;
+};
+
+__device__ __forceinline__ long long seq_begin(const BalanceParams& p, int s) {
+    return p.off ? (long long)__ldg(p.off + s) : 0;
+}
+__device__ __forceinline__ long long seq_end(const BalanceParams& p, int s) {
+    return p.off ? (long long)__ldg(p.off + s + 1) : p.T;
+}
+
+// the first sequence that ends behind token t (S: none does)
+__device__ __forceinline__ int find_seq(const BalanceParams& p, long long t) {
+    int lo = 0, hi = p.S;
+    while (lo < hi) {
+        const int mid = lo + (hi - lo) / 2;
+        if (seq_end(p, mid) > t) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+// Calls body(s, lo, hi) for every sequence s and its tokens [lo, hi) within
+// [t0, t1), and gap(lo, hi) for tokens of no sequence. Every call advances s,
+// so it ends whatever the offsets hold.
+template <class Body, class Gap>
+__device__ __forceinline__ void for_sequences(const BalanceParams& p, long long t0, long long t1, Body body, Gap gap) {
+    long long t = t0;
+    for (int s = find_seq(p, t0); s < p.S && t < t1; ++s) {
+        const long long b = min(max(seq_begin(p, s), t), t1), e = min(max(seq_end(p, s), b), t1);
+        if (b > t) gap(t, b);
+        if (e > b) body(s, b, e);
+        t = e;
+    }
+    if (t < t1) gap(t, t1);
+}
+
+// s = sigmoid(z) and e = exp(-z), each within a few units of 2^-24 of its value
+__device__ __forceinline__ float sigmoid_e(float z, float* e_out) {
+    const float e = expf(-z);
+    *e_out = e;
+    return __fdividef(1.0f, 1.0f + e);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// V float4 a lane: experts 128 v + 4 lane + i. Slots behind E hold logits of
+// -inf, whose sigmoid is 0.
+template <int V>
+__device__ __forceinline__ void load_row(const BalanceParams& p, long long t, int lane, float4 (&z)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = 128 * v + 4 * lane;
+        if (e < p.E) {
+            const float* a = p.logits + (size_t)t * (size_t)p.E + e;
+            asm volatile("ld.global.nc.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(z[v].x), "=f"(z[v].y), "=f"(z[v].z), "=f"(z[v].w) : "l"(a));
+        } else {
+            z[v] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        }
+    }
+}
+
+// 1 / sum, or 0 when every sigmoid of the token is 0 (NaN stays)
+__device__ __forceinline__ float inverse_or_zero(float sum) { return sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum); }
+
+template <int V>
+__global__ void __launch_bounds__(kBalanceThreads) balance_records_kernel(const BalanceParams p) {
+    __shared__ float sq[kBalanceWarps][V * 128];
+    __shared__ int sc[V * 128];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_trigger();
+    const long long t0 = (long long)blockIdx.x * p.chunk, t1 = min(t0 + p.chunk, p.T);
+    for_sequences(p, t0, t1, [&](int s, long long lo, long long hi) {
+        for (int e = tid; e < V * 128; e += kBalanceThreads) sc[e] = 0;
+        __syncthreads();
+        // choices: K a token, counted in shared memory
+        for (long long i = lo * p.K + tid; i < hi * p.K; i += kBalanceThreads) {
+            const int e = __ldg(p.idx + i);
+            if ((unsigned)e < (unsigned)p.E) atomicAdd(&sc[e], 1);
+            else atomicOr(p.status, 2u);
+        }
+        float4 q[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) q[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 nx[V];
+        if (lo + warp < hi) load_row<V>(p, lo + warp, lane, nx);
+        for (long long t = lo + warp; t < hi; t += kBalanceWarps) {
+            float4 z[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) z[v] = nx[v];
+            if (t + kBalanceWarps < hi) load_row<V>(p, t + kBalanceWarps, lane, nx);
+            float sum = 0.f, unused;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                z[v].x = sigmoid_e(z[v].x, &unused);
+                z[v].y = sigmoid_e(z[v].y, &unused);
+                z[v].z = sigmoid_e(z[v].z, &unused);
+                z[v].w = sigmoid_e(z[v].w, &unused);
+                sum += (z[v].x + z[v].y) + (z[v].z + z[v].w);
+            }
+            const float inv = inverse_or_zero(warp_sum(sum));
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                q[v].x = __fmaf_rn(z[v].x, inv, q[v].x);
+                q[v].y = __fmaf_rn(z[v].y, inv, q[v].y);
+                q[v].z = __fmaf_rn(z[v].z, inv, q[v].z);
+                q[v].w = __fmaf_rn(z[v].w, inv, q[v].w);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) *reinterpret_cast<float4*>(&sq[warp][128 * v + 4 * lane]) = q[v];
+        __syncthreads();
+        const size_t rec = ((size_t)blockIdx.x + (size_t)s) * (size_t)p.E;
+        for (int e = tid; e < p.E; e += kBalanceThreads) {
+            float a = 0.f;
+#pragma unroll
+            for (int w = 0; w < kBalanceWarps; ++w) a += sq[w][e];
+            p.rec_q[rec + e] = a;
+            p.rec_c[rec + e] = sc[e];
+        }
+        __syncthreads();
+    }, [](long long, long long) {});
+}
+
+// One block a sequence: its records added in order (groups of threads take
+// every G-th record, then the groups in order), the counts and the loss.
+__global__ void __launch_bounds__(kBalanceFinalThreads) balance_loss_kernel(const BalanceParams p) {
+    __shared__ double sq[kBalanceFinalSums];  // [groups][E]
+    __shared__ double part[kBalanceFinalThreads / 32];
+    const int tid = threadIdx.x, s = blockIdx.x, quads = p.E / 4;
+    pdl_wait();
+    const long long b = seq_begin(p, s), e = seq_end(p, s);
+    if (tid == 0 && (b < 0 || e < b || e > p.T)) atomicOr(p.status, 2u);
+    const long long lo = max(b, 0ll), hi = min(e, p.T);
+    const long long n = hi > lo ? hi - lo : 0;
+    const int first = n ? (int)(lo / p.chunk) : 0, last = n ? (int)((hi - 1) / p.chunk) : -1;
+    const int groups = kBalanceFinalThreads / quads;
+    const int g = tid / quads, quad = tid % quads;
+    double q[4] = {0, 0, 0, 0};
+    long long c[4] = {0, 0, 0, 0};
+    if (g < groups) {
+#pragma unroll 4
+        for (int r = first + g; r <= last; r += groups) {
+            const size_t at = ((size_t)r + (size_t)s) * (size_t)p.E + 4 * quad;
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(p.rec_q + at));
+            const int4 k = __ldcg(reinterpret_cast<const int4*>(p.rec_c + at));
+            q[0] += f.x, q[1] += f.y, q[2] += f.z, q[3] += f.w;
+            c[0] += k.x, c[1] += k.y, c[2] += k.z, c[3] += k.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sq[g * p.E + 4 * quad + i] = q[i];
+    }
+    __syncthreads();
+    double mine = 0;
+    if (tid < p.E)
+        for (int k = 0; k < groups; ++k) mine += sq[k * p.E + tid];
+    __syncthreads();
+    long long* scn = reinterpret_cast<long long*>(sq);
+    if (g < groups) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) scn[g * p.E + 4 * quad + i] = c[i];
+    }
+    __syncthreads();
+    double term = 0;
+    if (tid < p.E) {
+        long long count = 0;
+        for (int k = 0; k < groups; ++k) count += scn[k * p.E + tid];
+        p.counts[(size_t)s * (size_t)p.E + tid] = (int32_t)count;
+        term = (double)count * mine;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) term += __shfl_xor_sync(0xFFFFFFFFu, term, o);
+    if ((tid & 31) == 0) part[tid >> 5] = term;
+    __syncthreads();
+    if (tid == 0) {
+        double sum = 0;
+        for (int w = 0; w < kBalanceFinalThreads / 32; ++w) sum += part[w];
+        p.loss[s] = n ? (float)(p.factor / ((double)n * (double)n) * sum) : 0.0f;
+    }
+}
+
+template <int V>
+__global__ void __launch_bounds__(kBalanceThreads) balance_grad_kernel(const BalanceParams p) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long t0 = (long long)blockIdx.x * p.chunk, t1 = min(t0 + p.chunk, p.T);
+    for_sequences(p, t0, t1, [&](int s, long long lo, long long hi) {
+        const double n = (double)(min(seq_end(p, s), p.T) - max(seq_begin(p, s), 0ll));
+        const float g = (float)((double)__ldg(p.dloss + s) * p.factor / (n * n));
+        float4 c[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = 128 * v + 4 * lane;
+            const int4 k = e < p.E ? __ldg(reinterpret_cast<const int4*>(p.counts + (size_t)s * (size_t)p.E + e))
+                                   : make_int4(0, 0, 0, 0);
+            c[v] = make_float4((float)k.x, (float)k.y, (float)k.z, (float)k.w);
+        }
+        float4 nx[V];
+        if (lo + warp < hi) load_row<V>(p, lo + warp, lane, nx);
+        for (long long t = lo + warp; t < hi; t += kBalanceWarps) {
+            float4 z[V], d[V];  // d: s (1 - s)
+#pragma unroll
+            for (int v = 0; v < V; ++v) z[v] = nx[v];
+            if (t + kBalanceWarps < hi) load_row<V>(p, t + kBalanceWarps, lane, nx);
+            float sum = 0.f, mix = 0.f;
+            // 1 - s is e s, which keeps its digits where s is near 1; where z < 0
+            // (e may be infinite there) 1 - s itself loses none
+            auto one = [&](float& zi, float& di, float ci) {
+                float e;
+                const float s1 = sigmoid_e(zi, &e);
+                di = s1 * (zi < 0.0f ? 1.0f - s1 : e * s1);
+                sum += s1;
+                mix = __fmaf_rn(ci, s1, mix);
+            };
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                one(z[v].x, d[v].x, c[v].x);
+                one(z[v].y, d[v].y, c[v].y);
+                one(z[v].z, d[v].z, c[v].z);
+                one(z[v].w, d[v].w, c[v].w);
+            }
+            const float inv = inverse_or_zero(warp_sum(sum));
+            const float mean = warp_sum(mix) * inv, f = g * inv;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int e = 128 * v + 4 * lane;
+                if (e < p.E)
+                    __stcs(reinterpret_cast<float4*>(p.dlogits + (size_t)t * (size_t)p.E + e),
+                           make_float4(d[v].x * f * (c[v].x - mean), d[v].y * f * (c[v].y - mean),
+                                       d[v].z * f * (c[v].z - mean), d[v].w * f * (c[v].w - mean)));
+            }
+        }
+    }, [&](long long lo, long long hi) {
+        // tokens of no sequence: no gradient
+        for (long long t = lo + warp; t < hi; t += kBalanceWarps)
+            for (int e = 4 * lane; e < p.E; e += 128)
+                __stcs(reinterpret_cast<float4*>(p.dlogits + (size_t)t * (size_t)p.E + e),
+                       make_float4(0.f, 0.f, 0.f, 0.f));
+    });
+}
+
+}  // namespace beam
