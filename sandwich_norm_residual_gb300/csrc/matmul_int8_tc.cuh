@@ -1,0 +1,295 @@
+// The 8-bit integer product on the tensor cores.
+//
+// GB300's tcgen05 has no integer kind, and its legacy integer path is slow. But
+// every int8 is an FP16 number, a product of two is an integer of at most 2^14,
+// and FP32 accumulators hold integers below 2^24 exactly: so the FP16 kind at
+// its full rate gives the integer product. What has to be added is the widening
+// on the way from shared memory to the operands:
+//   - 128 channels are the rows of A. A lives in tensor memory, which the
+//     widening warps write directly (thread = channel row = lane), so widened
+//     channels never pass through shared memory;
+//   - tokens are the rows of B. B has to come from shared memory; its warps read
+//     the int8 tile, widen it and write the 128-byte swizzle that the matrix
+//     instruction reads.
+// TMA brings both int8 tiles, 128 k a step, into a ring; one thread issues the
+// matrix instructions; accumulators (channels in the lanes, tokens in the
+// columns) are read back, scaled and stored, 32 consecutive channels a warp.
+//
+// int8 -> FP16: with the sign bit flipped a byte is v + 128, and the FP16 with
+// the bits 0x6400 | byte is 1024 + (v + 128): one subtraction of 1152, exact.
+#pragma once
+
+#include "matmul_int8.cuh"
+#include "umma.cuh"
+
+namespace beam {
+
+constexpr int kStepK = 128;                         // k of one ring slot and of one operand slot
+constexpr int kTileN = 128;                         // channels of a CTA: the lanes of tensor memory
+constexpr int kStepCols = kStepK / 2;               // columns of A for a step (two FP16 a column)
+constexpr uint32_t kABytes = kTileN * kStepK;       // int8 channels of a step
+constexpr uint64_t kMatmulWaitNs = 2000000000ull;   // every wait gives up after 2 s
+
+struct MatmulTcParams {
+    MatmulParams p;
+    int m_tiles, n_tiles;
+    int splits;               // CTAs of a cluster, each with a part of k
+    uint64_t wait_ns;
+    unsigned int* status;
+};
+
+// four int8 -> four FP16
+__device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = v ^ 0x80808080u;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
+}
+
+// One step of channels: row `row` (this thread's lane) of the int8 tile, 128
+// bytes in the TMA's swizzle, to 64 columns of tensor memory at `at`. The 8
+// lanes of a shared-memory phase read 8 different 16-byte chunks.
+__device__ __forceinline__ void widen_channels(const unsigned char* tile, int row, uint32_t at) {
+    const unsigned char* r = tile + row * 128;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4*>(r + (((half * 4 + c) ^ (row & 7)) << 4));
+            widen4(v.x, w[8 * c + 0], w[8 * c + 1]);
+            widen4(v.y, w[8 * c + 2], w[8 * c + 3]);
+            widen4(v.z, w[8 * c + 4], w[8 * c + 5]);
+            widen4(v.w, w[8 * c + 6], w[8 * c + 7]);
+        }
+        tmem_st32(at + 32 * half, w);
+    }
+}
+
+// One step of ROWS tokens, by 128 threads: int8 tile -> two FP16 tiles of 64 k,
+// ROWS * 128 bytes each. Eight threads take a row, 16 bytes each; a chunk of 16
+// int8 becomes two chunks of 8 FP16, and the threads of the second tile write
+// theirs in the other order, so that a phase's 8 stores meet 8 different chunks.
+template <int ROWS>
+__device__ __forceinline__ void widen_tokens(const unsigned char* tile, unsigned char* op, int t) {
+    const int c = t & 7, sub = c >> 2, f = 2 * (c & 3);
+#pragma unroll
+    for (int i = 0; i < ROWS / 16; ++i) {
+        const int row = i * 16 + (t >> 3), x = row & 7;
+        const uint4 v = *reinterpret_cast<const uint4*>(tile + row * 128 + ((c ^ x) << 4));
+        uint4 a, b;
+        widen4(v.x, a.x, a.y);
+        widen4(v.y, a.z, a.w);
+        widen4(v.z, b.x, b.y);
+        widen4(v.w, b.z, b.w);
+        unsigned char* o = op + sub * (ROWS * 128) + row * 128;
+        const int fa = (f ^ x) << 4, fb = ((f + 1) ^ x) << 4;
+        *reinterpret_cast<uint4*>(o + (sub ? fb : fa)) = sub ? b : a;
+        *reinterpret_cast<uint4*>(o + (sub ? fa : fb)) = sub ? a : b;
+    }
+}
+
+// all lanes: whether every lane's wait ended
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t ns) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, ns));
+}
+
+template <int NT>
+struct TileConfig {  // NT tokens a CTA
+    static constexpr int kSlots = NT == 16 ? 5 : NT == 32 ? 4 : NT == 64 ? 3 : 4;  // int8 ring
+    static constexpr int kOps = NT <= 64 ? 2 : 3;                                // widened slots
+    static constexpr int kCtas = NT <= 64 ? 2 : 1;                               // CTAs an SM
+    static constexpr int kAcc = NT < 32 ? 32 : NT;                               // accumulator columns
+    static constexpr int kCols = kAcc + kOps * kStepCols <= 256 ? 256 : 512;     // allocated
+    static constexpr uint32_t kSlotBytes = kABytes + NT * kStepK;
+    static constexpr uint32_t kOpBytes = NT * kStepK * 2;
+    static constexpr uint32_t kSmem = kSlots * kSlotBytes + kOps * kOpBytes + 1024;  // and alignment
+};
+
+// A tile of 128 channels by NT tokens, one CTA, or a cluster of `splits` CTAs
+// that share its k. Ten warps: 0-3 widen channels and read the result back,
+// 4-7 widen tokens, 8 loads, 9 multiplies. For few tokens the way of the
+// weights from HBM bounds it; two CTAs an SM then keep about 150 KB of weights
+// in flight on each. Split along k, the CTAs' integer partial sums meet in
+// shared memory: CTA r adds and stores its share of the columns.
+template <int NT, bool F32>
+__global__ void __launch_bounds__(320, TileConfig<NT>::kCtas)
+    matmul_int8_tile_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
+                            const MatmulTcParams q) {
+    using C = TileConfig<NT>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) uint64_t raw_full[C::kSlots], raw_empty[C::kSlots], op_full[C::kOps], op_empty[C::kOps],
+        acc_full;
+    __shared__ uint32_t tmem_slot;
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    unsigned char* ops = smem + C::kSlots * C::kSlotBytes;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int split = q.splits > 1 ? (int)cluster_rank() : 0;
+    const int tile = blockIdx.x / q.splits;
+    const int n0 = (tile / q.m_tiles) * kTileN;
+    const long long m0 = (long long)(tile % q.m_tiles) * NT;
+    const int steps = (q.p.K + kStepK - 1) / kStepK;
+    const int first = (int)((long long)steps * split / q.splits);
+    const int count = (int)((long long)steps * (split + 1) / q.splits) - first;
+
+    if (tid == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(&raw_full[i], 1);
+            mbar_init(&raw_empty[i], 8);
+        }
+        for (int i = 0; i < C::kOps; ++i) {
+            mbar_init(&op_full[i], 8);
+            mbar_init(&op_empty[i], 1);
+        }
+        mbar_init(&acc_full, 1);
+        mbar_fence_init();
+    }
+    if (warp == 9) tmem_alloc<1>(&tmem_slot, C::kCols);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    // only now: a CTA that the trigger lets in allocates tensor memory too, and
+    // must not take the columns that a CTA of this grid still waits for
+    pdl_trigger();
+    const uint32_t acc = tmem_slot, acols = acc + C::kAcc;
+    bool ok = true;
+
+    if (warp == 8) {
+        if (lane == 0) {
+            const uint64_t pol_w = q.m_tiles == 1 ? l2_evict_first() : l2_evict_normal(), pol_a = l2_evict_normal();
+            auto load_w = [&](int i, int s) {
+                mbar_arrive_expect_tx(&raw_full[s], C::kSlotBytes);
+                tma_load_2d(smem + s * C::kSlotBytes, &wmap, (first + i) * kStepK, n0, &raw_full[s], pol_w);
+            };
+            auto load_a = [&](int i, int s) {
+                tma_load_2d(smem + s * C::kSlotBytes + kABytes, &amap, (first + i) * kStepK, (int)m0, &raw_full[s], pol_a);
+            };
+            // the weights do not depend on the kernel before: the first slots' are
+            // asked for ahead of the wait for it
+            const int head = count < C::kSlots ? count : C::kSlots;
+            for (int i = 0; i < head; ++i) load_w(i, i);
+            pdl_wait();
+            for (int i = 0; i < head; ++i) load_a(i, i);
+            int issued = head;
+            for (int i = head; i < count; ++i) {
+                const int s = i % C::kSlots;
+                if (!mbar_wait_bounded(&raw_empty[s], (uint32_t)(i / C::kSlots - 1) & 1, q.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                load_w(i, s);
+                load_a(i, s);
+                issued = i + 1;
+            }
+            if (!ok)  // copies in flight must land before the shared memory goes
+                for (int i = issued > C::kSlots ? issued - C::kSlots : 0; i < issued; ++i)
+                    mbar_wait_bounded(&raw_full[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = UmmaF16<kTileN, NT>::kDesc;
+            for (int i = 0; i < count; ++i) {
+                const int o = i % C::kOps;
+                if (!mbar_wait_bounded(&op_full[o], (uint32_t)(i / C::kOps) & 1, q.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                tmem_fence_after();
+                const uint32_t b = smem_u32(ops + o * C::kOpBytes);
+#pragma unroll
+                for (int k = 0; k < kStepK / 16; ++k)
+                    umma_f16<1>(acc, acols + o * kStepCols + k * 8,
+                                umma_smem_desc(b + (k / 4) * (NT * 128) + (k % 4) * 32), idesc, i > 0 || k > 0);
+                umma_commit<1>(&op_empty[o]);
+            }
+            umma_commit<1>(&acc_full);
+            if (!ok) mbar_wait_bounded(&acc_full, 0, q.wait_ns);
+        }
+    } else {
+        const uint32_t lanes = acols + ((uint32_t)(warp * 32) << 16);
+        for (int i = 0; i < count; ++i) {
+            const int s = i % C::kSlots, o = i % C::kOps;
+            ok = warp_wait(&raw_full[s], (uint32_t)(i / C::kSlots) & 1, q.wait_ns) &&
+                 (i < C::kOps || warp_wait(&op_empty[o], (uint32_t)(i / C::kOps - 1) & 1, q.wait_ns));
+            if (!ok) break;
+            const unsigned char* slot = smem + s * C::kSlotBytes;
+            if (warp < 4) {
+                tmem_fence_after();
+                widen_channels(slot, tid, lanes + o * kStepCols);
+                tmem_wait_st();
+                tmem_fence_before();
+            } else {
+                widen_tokens<NT>(slot + kABytes, ops + o * C::kOpBytes, tid - 128);
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&op_full[o]);
+                mbar_arrive(&raw_empty[s]);
+            }
+        }
+    }
+
+    __syncwarp();
+
+    // accumulators: lane = channel n0 + tid, column = token m0 + c
+    const long long left = q.p.M - m0;
+    const int cols = left < NT ? (int)left : NT;
+    int* part = reinterpret_cast<int*>(smem);  // [NT][128] of the ring, which is idle by then
+    if (warp < 4) {
+        ok = warp_wait(&acc_full, 0, q.wait_ns) && ok;
+        if (ok) {
+            tmem_fence_after();
+            pdl_wait();
+            const int n = n0 + tid;
+            const float ws = n < q.p.N ? __ldg(q.p.w_scale + n) : 0.0f;
+            for (int c0 = 0; c0 < cols; c0 += 16) {
+                float v[16];
+                tmem_ld16(acc + ((uint32_t)(warp * 32) << 16) + c0, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    if (q.splits > 1) {
+                        part[(c0 + c) * kTileN + tid] = __float2int_rn(v[c]);
+                    } else if (c0 + c < cols && n < q.p.N) {
+                        const long long m = m0 + c0 + c;
+                        store_out<F32>(q.p.out, (size_t)m * (size_t)q.p.N + (size_t)n,
+                                       __fmul_rn(__fmul_rn(v[c], __ldg(q.p.a_scale + m)), ws));
+                    }
+                }
+            }
+            tmem_fence_before();
+        }
+    }
+    if (!ok) atomicOr(q.status, 1u);
+    __syncthreads();
+    // the columns go back before the cluster meets: no CTA holds tensor memory
+    // while it waits for another one, which may still wait for some
+    if (warp == 9) {
+        tmem_fence_after();
+        tmem_dealloc<1>(acc, C::kCols);
+    }
+    if (q.splits > 1) {
+        __syncwarp();
+        cluster_sync();  // every CTA's partial sums are written
+        const int lo = cols * split / q.splits, hi = cols * (split + 1) / q.splits;
+        pdl_wait();
+        if (tid < 256) {
+            const int r = tid & 127, n = n0 + r;
+            const float ws = n < q.p.N ? __ldg(q.p.w_scale + n) : 0.0f;
+            for (int c = lo + (tid >> 7); c < hi; c += 2) {
+                int sum = 0;
+                for (int i = 0; i < q.splits; ++i)
+                    sum += ld_cluster_s32(cluster_addr(part + c * kTileN + r, (uint32_t)i));
+                if (n < q.p.N) {
+                    const long long m = m0 + c;
+                    store_out<F32>(q.p.out, (size_t)m * (size_t)q.p.N + (size_t)n,
+                                   __fmul_rn(__fmul_rn((float)sum, __ldg(q.p.a_scale + m)), ws));
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // nobody leaves while others read its sums
+    }
+}
+
+}  // namespace beam
