@@ -16,7 +16,8 @@
 // columns) are read back, scaled and stored, 32 consecutive channels a warp.
 //
 // int8 -> FP16: with the sign bit flipped a byte is v + 128, and the FP16 with
-// the bits 0x6400 | byte is 1024 + (v + 128): one subtraction of 1152, exact.
+// the bits 0x6400 | byte is 1024 + (v + 128): one subtraction of 1152 (0x6480),
+// exact.
 #pragma once
 
 #include "matmul_int8.cuh"
@@ -38,59 +39,73 @@ struct MatmulTcParams {
     unsigned int* status;
 };
 
-// four int8 -> four FP16
-__device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
-    const uint32_t u = v ^ 0x80808080u;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(0x64806480u));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
+// four int8 -> four FP16, in the order 0, 2, 1, 3: what a sum over k does not
+// see, as channels and tokens go through the same. The exclusive or sets the
+// exponent and flips the sign bit at once.
+__device__ __forceinline__ void widen4(uint32_t v, uint32_t& even, uint32_t& odd) {
+    constexpr uint32_t kMask = 0x00FF00FFu, kOne = 0x64806480u;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(even) : "r"((v & kMask) ^ kOne), "r"(kOne));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(odd) : "r"(((v >> 8) & kMask) ^ kOne), "r"(kOne));
 }
 
 // One step of channels: row `row` (this thread's lane) of the int8 tile, 128
-// bytes in the TMA's swizzle, to 64 columns of tensor memory at `at`. The 8
-// lanes of a shared-memory phase read 8 different 16-byte chunks.
-__device__ __forceinline__ void widen_channels(const unsigned char* tile, int row, uint32_t at) {
-    const unsigned char* r = tile + row * 128;
+// bytes in the TMA's swizzle. The 8 lanes of a shared-memory phase read 8
+// different 16-byte chunks.
+__device__ __forceinline__ void load_channels(const unsigned char* tile, int row, uint4 (&v)[8]) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const uint4*>(tile + row * 128 + ((c ^ (row & 7)) << 4));
+}
+
+// ... to 64 columns of tensor memory at `at`
+__device__ __forceinline__ void widen_channels(const uint4 (&v)[8], uint32_t at) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         uint32_t w[32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const uint4 v = *reinterpret_cast<const uint4*>(r + (((half * 4 + c) ^ (row & 7)) << 4));
-            widen4(v.x, w[8 * c + 0], w[8 * c + 1]);
-            widen4(v.y, w[8 * c + 2], w[8 * c + 3]);
-            widen4(v.z, w[8 * c + 4], w[8 * c + 5]);
-            widen4(v.w, w[8 * c + 6], w[8 * c + 7]);
+            const uint4 x = v[4 * half + c];
+            widen4(x.x, w[8 * c + 0], w[8 * c + 1]);
+            widen4(x.y, w[8 * c + 2], w[8 * c + 3]);
+            widen4(x.z, w[8 * c + 4], w[8 * c + 5]);
+            widen4(x.w, w[8 * c + 6], w[8 * c + 7]);
         }
         tmem_st32(at + 32 * half, w);
     }
 }
 
-// One step of ROWS tokens, by 128 threads: int8 tile -> two FP16 tiles of 64 k,
-// ROWS * 128 bytes each. Eight threads take a row, 16 bytes each; a chunk of 16
-// int8 becomes two chunks of 8 FP16, and the threads of the second tile write
-// theirs in the other order, so that a phase's 8 stores meet 8 different chunks.
+// One step of ROWS tokens, by 128 threads: eight threads take a row, 16 bytes each
 template <int ROWS>
-__device__ __forceinline__ void widen_tokens(const unsigned char* tile, unsigned char* op, int t) {
-    const int c = t & 7, sub = c >> 2, f = 2 * (c & 3);
+__device__ __forceinline__ void load_tokens(const unsigned char* tile, int t, uint4 (&v)[ROWS / 16]) {
 #pragma unroll
     for (int i = 0; i < ROWS / 16; ++i) {
-        const int row = i * 16 + (t >> 3), x = row & 7;
-        const uint4 v = *reinterpret_cast<const uint4*>(tile + row * 128 + ((c ^ x) << 4));
+        const int row = i * 16 + (t >> 3);
+        v[i] = *reinterpret_cast<const uint4*>(tile + row * 128 + (((t & 7) ^ (row & 7)) << 4));
+    }
+}
+
+// ... to two FP16 tiles of 64 k, ROWS * 128 bytes each. A chunk of 16 int8
+// becomes two chunks of 8 FP16, and the threads of the second tile write theirs
+// in the other order, so that a phase's 8 stores meet 8 different chunks.
+template <int ROWS>
+__device__ __forceinline__ void widen_tokens(const uint4 (&v)[ROWS / 16], unsigned char* op, int t) {
+    const int c = t & 7, sub = c >> 2, f = 2 * (c & 3), x = (t >> 3) & 7;  // row % 8: rows are 16 apart
+    unsigned char* o = op + sub * (ROWS * 128) + (t >> 3) * 128;
+    const int first = ((f + sub) ^ x) << 4, second = ((f + 1 - sub) ^ x) << 4;
+#pragma unroll
+    for (int i = 0; i < ROWS / 16; ++i) {
         uint4 a, b;
-        widen4(v.x, a.x, a.y);
-        widen4(v.y, a.z, a.w);
-        widen4(v.z, b.x, b.y);
-        widen4(v.w, b.z, b.w);
-        unsigned char* o = op + sub * (ROWS * 128) + row * 128;
-        const int fa = (f ^ x) << 4, fb = ((f + 1) ^ x) << 4;
-        *reinterpret_cast<uint4*>(o + (sub ? fb : fa)) = sub ? b : a;
-        *reinterpret_cast<uint4*>(o + (sub ? fa : fb)) = sub ? a : b;
+        widen4(v[i].x, a.x, a.y);
+        widen4(v[i].y, a.z, a.w);
+        widen4(v[i].z, b.x, b.y);
+        widen4(v[i].w, b.z, b.w);
+        *reinterpret_cast<uint4*>(o + i * 2048 + first) = sub ? b : a;
+        *reinterpret_cast<uint4*>(o + i * 2048 + second) = sub ? a : b;
     }
 }
 
 // all lanes: whether every lane's wait ended
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t ns) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, ns));
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, ns));
 }
 
 template <int NT>
@@ -120,6 +135,7 @@ __global__ void __launch_bounds__(320, TileConfig<NT>::kCtas)
     __shared__ __align__(8) uint64_t raw_full[C::kSlots], raw_empty[C::kSlots], op_full[C::kOps], op_empty[C::kOps],
         acc_full;
     __shared__ uint32_t tmem_slot;
+    __shared__ float a_scale[NT], w_scale[kTileN];
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char* ops = smem + C::kSlots * C::kSlotBytes;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -152,9 +168,12 @@ __global__ void __launch_bounds__(320, TileConfig<NT>::kCtas)
     pdl_trigger();
     const uint32_t acc = tmem_slot, acols = acc + C::kAcc;
     bool ok = true;
+    float ws = 0.0f;
 
     if (warp == 8) {
         if (lane == 0) {
+            tma_prefetch_map(&wmap);
+            tma_prefetch_map(&amap);
             const uint64_t pol_w = q.m_tiles == 1 ? l2_evict_first() : l2_evict_normal(), pol_a = l2_evict_normal();
             auto load_w = [&](int i, int s) {
                 mbar_arrive_expect_tx(&raw_full[s], C::kSlotBytes);
@@ -172,7 +191,7 @@ __global__ void __launch_bounds__(320, TileConfig<NT>::kCtas)
             int issued = head;
             for (int i = head; i < count; ++i) {
                 const int s = i % C::kSlots;
-                if (!mbar_wait_bounded(&raw_empty[s], (uint32_t)(i / C::kSlots - 1) & 1, q.wait_ns)) {
+                if (!mbar_wait(&raw_empty[s], (uint32_t)(i / C::kSlots - 1) & 1, q.wait_ns)) {
                     ok = false;
                     break;
                 }
@@ -182,14 +201,14 @@ __global__ void __launch_bounds__(320, TileConfig<NT>::kCtas)
             }
             if (!ok)  // copies in flight must land before the shared memory goes
                 for (int i = issued > C::kSlots ? issued - C::kSlots : 0; i < issued; ++i)
-                    mbar_wait_bounded(&raw_full[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
+                    mbar_wait(&raw_full[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
         }
     } else if (warp == 9) {
         if (lane == 0) {
             constexpr uint32_t idesc = UmmaF16<kTileN, NT>::kDesc;
             for (int i = 0; i < count; ++i) {
                 const int o = i % C::kOps;
-                if (!mbar_wait_bounded(&op_full[o], (uint32_t)(i / C::kOps) & 1, q.wait_ns)) {
+                if (!mbar_wait(&op_full[o], (uint32_t)(i / C::kOps) & 1, q.wait_ns)) {
                     ok = false;
                     break;
                 }
@@ -202,33 +221,43 @@ __global__ void __launch_bounds__(320, TileConfig<NT>::kCtas)
                 umma_commit<1>(&op_empty[o]);
             }
             umma_commit<1>(&acc_full);
-            if (!ok) mbar_wait_bounded(&acc_full, 0, q.wait_ns);
+            if (!ok) mbar_wait(&acc_full, 0, q.wait_ns);
         }
     } else {
         const uint32_t lanes = acols + ((uint32_t)(warp * 32) << 16);
+        // the scales wait in shared memory (tokens) and a register (channel)
+        pdl_wait();
+        if (warp < 4) {
+            if (n0 + tid < q.p.N) ws = __ldg(q.p.w_scale + n0 + tid);
+            w_scale[tid] = ws;
+        } else if (tid - 128 < NT && m0 + tid - 128 < q.p.M) {
+            a_scale[tid - 128] = __ldg(q.p.a_scale + m0 + tid - 128);
+        }
         for (int i = 0; i < count; ++i) {
             const int s = i % C::kSlots, o = i % C::kOps;
-            ok = warp_wait(&raw_full[s], (uint32_t)(i / C::kSlots) & 1, q.wait_ns) &&
-                 (i < C::kOps || warp_wait(&op_empty[o], (uint32_t)(i / C::kOps - 1) & 1, q.wait_ns));
-            if (!ok) break;
             const unsigned char* slot = smem + s * C::kSlotBytes;
+            uint4 v[8];  // tokens: NT / 16 of them
+            ok = warp_wait(&raw_full[s], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
+            if (!ok) break;
+            if (warp < 4) load_channels(slot, tid, v);
+            else load_tokens<NT>(slot + kABytes, tid - 128, reinterpret_cast<uint4(&)[NT / 16]>(v));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&raw_empty[s]);
+            ok = i < C::kOps || warp_wait(&op_empty[o], (uint32_t)(i / C::kOps - 1) & 1, q.wait_ns);
+            if (!ok) break;
             if (warp < 4) {
                 tmem_fence_after();
-                widen_channels(slot, tid, lanes + o * kStepCols);
+                widen_channels(v, lanes + o * kStepCols);
                 tmem_wait_st();
                 tmem_fence_before();
             } else {
-                widen_tokens<NT>(slot + kABytes, ops + o * C::kOpBytes, tid - 128);
+                widen_tokens<NT>(reinterpret_cast<uint4(&)[NT / 16]>(v), ops + o * C::kOpBytes, tid - 128);
                 fence_proxy_async_smem();
             }
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&op_full[o]);
-                mbar_arrive(&raw_empty[s]);
-            }
+            if (lane == 0) mbar_arrive(&op_full[o]);
         }
     }
-
     __syncwarp();
 
     // accumulators: lane = channel n0 + tid, column = token m0 + c
@@ -239,22 +268,21 @@ __global__ void __launch_bounds__(320, TileConfig<NT>::kCtas)
         ok = warp_wait(&acc_full, 0, q.wait_ns) && ok;
         if (ok) {
             tmem_fence_after();
-            pdl_wait();
             const int n = n0 + tid;
-            const float ws = n < q.p.N ? __ldg(q.p.w_scale + n) : 0.0f;
             for (int c0 = 0; c0 < cols; c0 += 16) {
                 float v[16];
                 tmem_ld16(acc + ((uint32_t)(warp * 32) << 16) + c0, v);
                 tmem_wait_ld();
+                if (q.splits > 1) {
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    if (q.splits > 1) {
-                        part[(c0 + c) * kTileN + tid] = __float2int_rn(v[c]);
-                    } else if (c0 + c < cols && n < q.p.N) {
-                        const long long m = m0 + c0 + c;
-                        store_out<F32>(q.p.out, (size_t)m * (size_t)q.p.N + (size_t)n,
-                                       __fmul_rn(__fmul_rn(v[c], __ldg(q.p.a_scale + m)), ws));
-                    }
+                    for (int c = 0; c < 16; ++c) part[(c0 + c) * kTileN + tid] = __float2int_rn(v[c]);
+                } else if (n < q.p.N) {
+                    const size_t at = (size_t)(m0 + c0) * (size_t)q.p.N + (size_t)n;
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        if (c0 + c < cols)
+                            store_out<F32>(q.p.out, at + (size_t)c * (size_t)q.p.N,
+                                           __fmul_rn(__fmul_rn(v[c], a_scale[c0 + c]), ws));
                 }
             }
             tmem_fence_before();
@@ -272,10 +300,8 @@ __global__ void __launch_bounds__(320, TileConfig<NT>::kCtas)
         __syncwarp();
         cluster_sync();  // every CTA's partial sums are written
         const int lo = cols * split / q.splits, hi = cols * (split + 1) / q.splits;
-        pdl_wait();
         if (tid < 256) {
             const int r = tid & 127, n = n0 + r;
-            const float ws = n < q.p.N ? __ldg(q.p.w_scale + n) : 0.0f;
             for (int c = lo + (tid >> 7); c < hi; c += 2) {
                 int sum = 0;
                 for (int i = 0; i < q.splits; ++i)
@@ -283,7 +309,7 @@ __global__ void __launch_bounds__(320, TileConfig<NT>::kCtas)
                 if (n < q.p.N) {
                     const long long m = m0 + c;
                     store_out<F32>(q.p.out, (size_t)m * (size_t)q.p.N + (size_t)n,
-                                   __fmul_rn(__fmul_rn((float)sum, __ldg(q.p.a_scale + m)), ws));
+                                   __fmul_rn(__fmul_rn((float)sum, a_scale[c]), w_scale[r]));
                 }
             }
         }
