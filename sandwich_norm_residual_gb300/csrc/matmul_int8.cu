@@ -122,7 +122,7 @@ beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, cudaStre
     q.wait_ns = beam::kMatmulWaitNs;
     q.status = dev.status_word;
     void* args[] = {&wmap, &amap, &q};
-    return launch(fn, dim3((unsigned)(tiles * q.splits)), dim3(320), args, C::kSmem, stream, pdl, q.splits);
+    return launch(fn, dim3((unsigned)(tiles * q.splits)), dim3(C::kThreads), args, C::kSmem, stream, pdl, q.splits);
 }
 
 template <bool F32>

@@ -73,24 +73,33 @@ __device__ __forceinline__ void widen_channels(const uint4 (&v)[8], uint32_t at)
     }
 }
 
-// One step of ROWS tokens, by 128 threads: eight threads take a row, 16 bytes each
-template <int ROWS>
-__device__ __forceinline__ void load_tokens(const unsigned char* tile, int t, uint4 (&v)[ROWS / 16]) {
-#pragma unroll
-    for (int i = 0; i < ROWS / 16; ++i) {
-        const int row = i * 16 + (t >> 3);
-        v[i] = *reinterpret_cast<const uint4*>(tile + row * 128 + (((t & 7) ^ (row & 7)) << 4));
+// One step of ROWS tokens, by 128 threads, a chunk of 16 int8 and row each. The
+// int8 chunk c of row r lies at c ^ (r % 8), the two FP16 chunks that it becomes
+// (of 8 values, 2 (c % 4) and the next, in the tile of the step's first or
+// second 64 k) at theirs. A shared-memory phase of 8 lanes takes four chunks of
+// the two rows r and r ^ 5, which meet 8 different places in the load (r and
+// r ^ 5 differ in bit 2) and in both stores (they differ in bit 0).
+struct TokenPlace {
+    int row, chunk, sub;
+    __device__ explicit TokenPlace(int t) {
+        const int lane = t & 31, w = t >> 5;
+        row = (w >> 1) * 8 + ((lane >> 3) ^ (5 * ((lane >> 2) & 1)));
+        chunk = lane & 3;
+        sub = w & 1;
     }
+};
+
+template <int ROWS>
+__device__ __forceinline__ void load_tokens(const unsigned char* tile, const TokenPlace& p, uint4 (&v)[ROWS / 16]) {
+    const unsigned char* at = tile + p.row * 128 + (((4 * p.sub + p.chunk) ^ (p.row & 7)) << 4);
+#pragma unroll
+    for (int i = 0; i < ROWS / 16; ++i) v[i] = *reinterpret_cast<const uint4*>(at + i * 16 * 128);
 }
 
-// ... to two FP16 tiles of 64 k, ROWS * 128 bytes each. A chunk of 16 int8
-// becomes two chunks of 8 FP16, and the threads of the second tile write theirs
-// in the other order, so that a phase's 8 stores meet 8 different chunks.
 template <int ROWS>
-__device__ __forceinline__ void widen_tokens(const uint4 (&v)[ROWS / 16], unsigned char* op, int t) {
-    const int c = t & 7, sub = c >> 2, f = 2 * (c & 3), x = (t >> 3) & 7;  // row % 8: rows are 16 apart
-    unsigned char* o = op + sub * (ROWS * 128) + (t >> 3) * 128;
-    const int first = ((f + sub) ^ x) << 4, second = ((f + 1 - sub) ^ x) << 4;
+__device__ __forceinline__ void widen_tokens(const uint4 (&v)[ROWS / 16], unsigned char* op, const TokenPlace& p) {
+    unsigned char* o = op + p.sub * (ROWS * 128) + p.row * 128;
+    const int first = ((2 * p.chunk) ^ (p.row & 7)) << 4, second = first ^ 16;
 #pragma unroll
     for (int i = 0; i < ROWS / 16; ++i) {
         uint4 a, b;
@@ -98,8 +107,8 @@ __device__ __forceinline__ void widen_tokens(const uint4 (&v)[ROWS / 16], unsign
         widen4(v[i].y, a.z, a.w);
         widen4(v[i].z, b.x, b.y);
         widen4(v[i].w, b.z, b.w);
-        *reinterpret_cast<uint4*>(o + i * 2048 + first) = sub ? b : a;
-        *reinterpret_cast<uint4*>(o + i * 2048 + second) = sub ? a : b;
+        *reinterpret_cast<uint4*>(o + i * 16 * 128 + first) = a;
+        *reinterpret_cast<uint4*>(o + i * 16 * 128 + second) = b;
     }
 }
 
@@ -110,9 +119,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64
 
 template <int NT>
 struct TileConfig {  // NT tokens a CTA
-    static constexpr int kSlots = NT == 16 ? 5 : NT == 32 ? 4 : NT == 64 ? 3 : 4;  // int8 ring
-    static constexpr int kOps = NT <= 64 ? 2 : 3;                                // widened slots
+    static constexpr int kSlots = NT == 16 ? 5 : NT == 32 ? 4 : 3;                 // int8 ring
+    static constexpr int kOps = NT <= 64 ? 2 : 4;                                // widened slots
     static constexpr int kCtas = NT <= 64 ? 2 : 1;                               // CTAs an SM
+    static constexpr int kAGroups = 2, kBGroups = NT <= 64 ? 1 : 2;              // groups of 4 warps
+    static constexpr int kAWarps = 4 * kAGroups, kBWarps = 4 * kBGroups;
+    static constexpr int kThreads = 32 * (kAWarps + kBWarps + 2);
     static constexpr int kAcc = NT < 32 ? 32 : NT;                               // accumulator columns
     static constexpr int kCols = kAcc + kOps * kStepCols <= 256 ? 256 : 512;     // allocated
     static constexpr uint32_t kSlotBytes = kABytes + NT * kStepK;
@@ -121,13 +133,16 @@ struct TileConfig {  // NT tokens a CTA
 };
 
 // A tile of 128 channels by NT tokens, one CTA, or a cluster of `splits` CTAs
-// that share its k. Ten warps: 0-3 widen channels and read the result back,
-// 4-7 widen tokens, 8 loads, 9 multiplies. For few tokens the way of the
-// weights from HBM bounds it; two CTAs an SM then keep about 150 KB of weights
-// in flight on each. Split along k, the CTAs' integer partial sums meet in
-// shared memory: CTA r adds and stores its share of the columns.
+// that share its k. Warps: kAWarps widen channels and read the result back,
+// kBWarps widen tokens, one loads, one multiplies. Widening a step is a chain of
+// latencies (wait, load, convert, store, hand over: 1400 cycles for 128 channels
+// and 128 tokens, of which the matrix unit needs 512), so two groups of four
+// warps take the steps in turn. For few tokens the way of the weights from HBM
+// bounds it; two CTAs an SM then keep about 150 KB of them in flight on each.
+// Split along k, the CTAs' integer partial sums meet in shared memory: CTA r
+// adds and stores its share of the columns.
 template <int NT, bool F32>
-__global__ void __launch_bounds__(320, TileConfig<NT>::kCtas)
+__global__ void __launch_bounds__(TileConfig<NT>::kThreads, TileConfig<NT>::kCtas)
     matmul_int8_tile_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
                             const MatmulTcParams q) {
     using C = TileConfig<NT>;
@@ -137,6 +152,7 @@ __global__ void __launch_bounds__(320, TileConfig<NT>::kCtas)
     __shared__ uint32_t tmem_slot;
     __shared__ float a_scale[NT], w_scale[kTileN];
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    constexpr int kLoadWarp = C::kAWarps + C::kBWarps, kMulWarp = kLoadWarp + 1;
     unsigned char* ops = smem + C::kSlots * C::kSlotBytes;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int split = q.splits > 1 ? (int)cluster_rank() : 0;
@@ -159,7 +175,7 @@ __global__ void __launch_bounds__(320, TileConfig<NT>::kCtas)
         mbar_init(&acc_full, 1);
         mbar_fence_init();
     }
-    if (warp == 9) tmem_alloc<1>(&tmem_slot, C::kCols);
+    if (warp == kMulWarp) tmem_alloc<1>(&tmem_slot, C::kCols);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -168,9 +184,8 @@ __global__ void __launch_bounds__(320, TileConfig<NT>::kCtas)
     pdl_trigger();
     const uint32_t acc = tmem_slot, acols = acc + C::kAcc;
     bool ok = true;
-    float ws = 0.0f;
 
-    if (warp == 8) {
+    if (warp == kLoadWarp) {
         if (lane == 0) {
             tma_prefetch_map(&wmap);
             tma_prefetch_map(&amap);
@@ -203,7 +218,7 @@ __global__ void __launch_bounds__(320, TileConfig<NT>::kCtas)
                 for (int i = issued > C::kSlots ? issued - C::kSlots : 0; i < issued; ++i)
                     mbar_wait(&raw_full[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
         }
-    } else if (warp == 9) {
+    } else if (warp == kMulWarp) {
         if (lane == 0) {
             constexpr uint32_t idesc = UmmaF16<kTileN, NT>::kDesc;
             for (int i = 0; i < count; ++i) {
@@ -224,58 +239,66 @@ __global__ void __launch_bounds__(320, TileConfig<NT>::kCtas)
             if (!ok) mbar_wait(&acc_full, 0, q.wait_ns);
         }
     } else {
-        const uint32_t lanes = acols + ((uint32_t)(warp * 32) << 16);
-        // the scales wait in shared memory (tokens) and a register (channel)
+        const bool channels = warp < C::kAWarps;
+        // this warp's group takes the steps group, group + groups, ...
+        const int group = channels ? warp / 4 : (warp - C::kAWarps) / 4, groups = channels ? C::kAGroups : C::kBGroups;
+        const int t = tid & 127;  // within the group; for channels the lane of tensor memory
+        const uint32_t lanes = acols + ((uint32_t)(t & 96) << 16);
+        const TokenPlace place(t);
+        // the scales wait in shared memory for the result
         pdl_wait();
-        if (warp < 4) {
-            if (n0 + tid < q.p.N) ws = __ldg(q.p.w_scale + n0 + tid);
-            w_scale[tid] = ws;
-        } else if (tid - 128 < NT && m0 + tid - 128 < q.p.M) {
-            a_scale[tid - 128] = __ldg(q.p.a_scale + m0 + tid - 128);
+        if (group == 0) {
+            if (channels) w_scale[t] = n0 + t < q.p.N ? __ldg(q.p.w_scale + n0 + t) : 0.0f;
+            else if (t < NT) a_scale[t] = m0 + t < q.p.M ? __ldg(q.p.a_scale + m0 + t) : 0.0f;
         }
-        for (int i = 0; i < count; ++i) {
+        for (int i = group; i < count; i += groups) {
             const int s = i % C::kSlots, o = i % C::kOps;
             const unsigned char* slot = smem + s * C::kSlotBytes;
             uint4 v[8];  // tokens: NT / 16 of them
+            uint4(&vt)[NT / 16] = reinterpret_cast<uint4(&)[NT / 16]>(v);
             ok = warp_wait(&raw_full[s], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
             if (!ok) break;
-            if (warp < 4) load_channels(slot, tid, v);
-            else load_tokens<NT>(slot + kABytes, tid - 128, reinterpret_cast<uint4(&)[NT / 16]>(v));
+            if (channels) load_channels(slot, t, v);
+            else load_tokens<NT>(slot + kABytes, place, vt);
             __syncwarp();
             if (lane == 0) mbar_arrive(&raw_empty[s]);
             ok = i < C::kOps || warp_wait(&op_empty[o], (uint32_t)(i / C::kOps - 1) & 1, q.wait_ns);
             if (!ok) break;
-            if (warp < 4) {
+            if (channels) {
                 tmem_fence_after();
                 widen_channels(v, lanes + o * kStepCols);
                 tmem_wait_st();
                 tmem_fence_before();
             } else {
-                widen_tokens<NT>(reinterpret_cast<uint4(&)[NT / 16]>(v), ops + o * C::kOpBytes, tid - 128);
+                widen_tokens<NT>(vt, ops + o * C::kOpBytes, place);
                 fence_proxy_async_smem();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&op_full[o]);
         }
     }
+    // the scales; also: nobody reads the ring or the operands any more once the
+    // accumulators are complete
+    __syncthreads();
     __syncwarp();
 
     // accumulators: lane = channel n0 + tid, column = token m0 + c
     const long long left = q.p.M - m0;
     const int cols = left < NT ? (int)left : NT;
     int* part = reinterpret_cast<int*>(smem);  // [NT][128] of the ring, which is idle by then
-    if (warp < 4) {
+    if (warp < C::kAWarps) {
         ok = warp_wait(&acc_full, 0, q.wait_ns) && ok;
         if (ok) {
             tmem_fence_after();
-            const int n = n0 + tid;
-            for (int c0 = 0; c0 < cols; c0 += 16) {
+            const int t = tid & 127, n = n0 + t;
+            const float ws = w_scale[t];
+            for (int c0 = 16 * (warp / 4); c0 < cols; c0 += 16 * C::kAGroups) {
                 float v[16];
-                tmem_ld16(acc + ((uint32_t)(warp * 32) << 16) + c0, v);
+                tmem_ld16(acc + ((uint32_t)(t & 96) << 16) + c0, v);
                 tmem_wait_ld();
                 if (q.splits > 1) {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) part[(c0 + c) * kTileN + tid] = __float2int_rn(v[c]);
+                    for (int c = 0; c < 16; ++c) part[(c0 + c) * kTileN + t] = __float2int_rn(v[c]);
                 } else if (n < q.p.N) {
                     const size_t at = (size_t)(m0 + c0) * (size_t)q.p.N + (size_t)n;
 #pragma unroll
@@ -292,7 +315,7 @@ __global__ void __launch_bounds__(320, TileConfig<NT>::kCtas)
     __syncthreads();
     // the columns go back before the cluster meets: no CTA holds tensor memory
     // while it waits for another one, which may still wait for some
-    if (warp == 9) {
+    if (warp == kMulWarp) {
         tmem_fence_after();
         tmem_dealloc<1>(acc, C::kCols);
     }
