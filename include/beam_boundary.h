@@ -327,7 +327,11 @@ BEAM_API beam_status beam_qk_norm_ex(beam_stream_t stream, uint16_t* q, uint16_t
  *   K       a multiple of 16, 16 <= K <= BEAM_MATMUL_MAX_K
  *   M, N    0 launches nothing; M at most 2^31 - 1
  *   out     [M, N], BF16 for BEAM_OUT_BF16, FP32 for BEAM_OUT_FP32; aligned to
- *           its element, overlapping no other operand
+ *           its element
+ *   workspace  device memory for this call alone, 16-byte aligned, of at least
+ *           beam_matmul_int8_workspace(M, N, K) bytes (NULL where that is 0);
+ *           need not be cleared
+ * out and workspace overlap neither each other nor an input.
  * A scale that is infinite or NaN makes its row's or channel's products with
  * acc = 0 NaN (0 * inf), as the FP32 products above say.
  * flags: BEAM_OPT_PDL launches with programmatic stream serialisation: the
@@ -337,7 +341,11 @@ BEAM_API beam_status beam_qk_norm_ex(beam_stream_t stream, uint16_t* q, uint16_t
  */
 BEAM_API beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, const float* a_scale,
                                       const int8_t* w, const float* w_scale, int64_t M, int N,
-                                      int K, int out_type, void* out, uint32_t flags);
+                                      int K, int out_type, void* out, void* workspace,
+                                      int64_t workspace_bytes, uint32_t flags);
+
+/* Bytes of workspace of beam_matmul_int8 (0 for most shapes), -1 for a bad shape. */
+BEAM_API int64_t beam_matmul_int8_workspace(int64_t M, int N, int K);
 
 /*
  * Synchronises `stream`, then reads and clears the current device's status

@@ -76,6 +76,18 @@ def _on_current_device(**tensors):
                          f"call under `with torch.cuda.device({dev.index}):`")
 
 
+def _workspace(nbytes: int, device, stream):
+    """Device memory for one call, from the pool of the stream that uses it: freed at the
+    call's end, it goes to later work of that stream alone. None for no bytes."""
+    import torch
+    if not nbytes:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _opts(opts):
     if opts is None:
         return None
@@ -385,10 +397,13 @@ def matmul_int8(a, a_scale, w, w_scale, out_dtype=None, out=None, stream=None, p
     _check(out, "out", out_dtype, 2)
     _shape(out, "out", (M, N))
     _on_current_device(a=a, a_scale=a_scale, w=w, w_scale=w_scale, out=out)
-    st = _lib.load().beam_matmul_int8(
+    lib = _lib.load()
+    ws_bytes = max(0, lib.beam_matmul_int8_workspace(M, N, K))
+    ws = _workspace(ws_bytes, a.device, stream)
+    st = lib.beam_matmul_int8(
         _stream_ptr(stream), a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), M, N, K,
         _lib.BEAM_OUT_FP32 if out_dtype == torch.float32 else _lib.BEAM_OUT_BF16, out.data_ptr(),
-        _lib.BEAM_OPT_PDL if pdl else 0)
+        ws.data_ptr() if ws_bytes else None, ws_bytes, _lib.BEAM_OPT_PDL if pdl else 0)
     if st != 0:
         raise BeamError(st, "beam_matmul_int8")
     return out
@@ -466,9 +481,7 @@ def moe_balance_loss(logits, topk_idx, alpha: float, seq_offsets=None, loss=None
     _on_current_device(loss=loss, counts=counts, **ops)
     lib = _lib.load()
     ws_bytes = max(0, lib.beam_moe_balance_workspace(T, E, S))
-    # from the pool of the stream that uses it, so that no other stream takes it over too early
-    with torch.cuda.stream(stream):
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=logits.device)
+    ws = _workspace(ws_bytes, logits.device, stream)
     st = lib.beam_moe_balance_loss(_stream_ptr(stream), logits.data_ptr(), topk_idx.data_ptr(), off, T, E,
                                    topk_idx.shape[1], S, float(alpha), loss.data_ptr(),
                                    counts.data_ptr(), ws.data_ptr(), ws_bytes)

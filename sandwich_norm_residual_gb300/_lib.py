@@ -71,7 +71,8 @@ SIGNATURES = {
                              _i32]),
     "beam_qk_norm_ex": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _i32,
                                 _f32, _i32, _u32]),
-    "beam_matmul_int8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _u32]),
+    "beam_matmul_int8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _i64, _u32]),
+    "beam_matmul_int8_workspace": (_i64, [_i64, _i32, _i32]),
     "beam_moe_balance_loss": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i64, _f32, _vp, _vp, _vp,
                                      _i64]),
     "beam_moe_balance_workspace": (_i64, [_i64, _i32, _i64]),

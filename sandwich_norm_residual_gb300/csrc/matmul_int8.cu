@@ -16,6 +16,8 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
     return na && nb && a0 < b0 + nb && b0 < a0 + na;
 }
 
+constexpr int kMaxSms = 152;  // workers of a launch at most, and what workspaces are sized for
+
 bool misaligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1u)) != 0; }
 
 template <bool F32>
@@ -98,69 +100,139 @@ beam_status allow_smem(const void* fn, size_t bytes, std::atomic<unsigned long l
     return BEAM_OK;
 }
 
-template <int NT, bool F32>
-beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, cudaStream_t stream, bool pdl) {
-    using C = beam::TileConfig<NT>;
+// The split of a product into tiles of NT tokens by 128 CG channels
+template <int NT, int CG>
+void plan(const MatmulParams& p, int sms, beam::MatmulTcParams* q) {
+    q->p = p;
+    q->m_tiles = (int)((p.M + NT - 1) / NT);
+    q->steps = (p.K + beam::kStepK - 1) / beam::kStepK;
+    q->tiles = (int64_t)q->m_tiles * ((p.N + beam::kTileN * CG - 1) / (beam::kTileN * CG));
+    q->workers = sms / CG;
+    if (CG == 2) {
+        q->waves = (int)((q->tiles + q->workers - 1) / q->workers);
+        q->sharers = 0;
+        return;
+    }
+    // the tiles behind the last full wave are shared, with four steps a worker at least
+    q->waves = (int)(q->tiles / q->workers);
+    const int64_t shared = (q->tiles - (int64_t)q->waves * q->workers) * q->steps;
+    const int64_t most = (shared + 3) / 4;
+    q->sharers = (int)(most < q->workers ? most : q->workers);
+}
+
+template <int NT>
+int64_t part_bytes(const beam::MatmulTcParams& q) {
+    return (int64_t)q.sharers * 2 * NT * beam::kTileN * 4;
+}
+
+template <int NT, int CG, bool F32>
+beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* part, cudaStream_t stream, bool pdl) {
+    using C = beam::TileConfig<NT, CG>;
     static std::atomic<unsigned long long> allowed{0};
-    const void* fn = reinterpret_cast<const void*>(beam::matmul_int8_tile_kernel<NT, F32>);
-    const beam_status st = allow_smem(fn, C::kSmem, &allowed, dev.ordinal);
+    const void* fn = reinterpret_cast<const void*>(beam::matmul_int8_tile_kernel<NT, CG, F32>);
+    beam_status st = allow_smem(fn, C::kSmem, &allowed, dev.ordinal);
     if (st != BEAM_OK) return st;
     CUtensorMap wmap, amap;
-    if (!row_map(&wmap, p.w, p.N, p.K, beam::kTileN) || !row_map(&amap, p.a, p.M, p.K, NT)) return BEAM_ERR_CUDA;
+    if (!row_map(&wmap, p.w, p.N, p.K, beam::kTileN) || !row_map(&amap, p.a, p.M, p.K, C::kRows)) return BEAM_ERR_CUDA;
     beam::MatmulTcParams q{};
-    q.p = p;
-    q.n_tiles = (p.N + beam::kTileN - 1) / beam::kTileN;
-    q.m_tiles = (int)((p.M + NT - 1) / NT);
-    const int64_t tiles = (int64_t)q.n_tiles * q.m_tiles;
-    // k is split where there are too few tiles for the SMs: as many CTAs a tile
-    // as fit at once, each with two steps at least
-    const int steps = (p.K + beam::kStepK - 1) / beam::kStepK;
-    int64_t splits = (int64_t)dev.sms * C::kCtas / tiles;
-    if (splits > steps / 2) splits = steps / 2;
-    q.splits = splits < 1 ? 1 : splits > 8 ? 8 : (int)splits;
-    if (tiles * q.splits > 0x7FFFFFFF) return BEAM_ERR_SHAPE;
+    plan<NT, CG>(p, dev.sms < kMaxSms ? dev.sms : kMaxSms, &q);
+    q.part = static_cast<float*>(part);
     q.wait_ns = beam::kMatmulWaitNs;
     q.status = dev.status_word;
+    const int64_t workers = q.waves ? (q.tiles < q.workers ? q.tiles : q.workers) : q.sharers;
     void* args[] = {&wmap, &amap, &q};
-    return launch(fn, dim3((unsigned)(tiles * q.splits)), dim3(C::kThreads), args, C::kSmem, stream, pdl, q.splits);
+    st = launch(fn, dim3((unsigned)(workers * CG)), dim3(C::kThreads), args, C::kSmem, stream, pdl, CG);
+    const int64_t split = q.sharers ? q.tiles - (int64_t)q.waves * q.workers : 0;
+    if (st != BEAM_OK || split == 0 || split == q.sharers) return st;  // none, or each a worker's own
+    void* join_args[] = {&q};
+    return launch(reinterpret_cast<const void*>(beam::matmul_int8_join_kernel<NT, F32>), dim3((unsigned)split, NT / 8),
+                  dim3(beam::kTileN), join_args, 0, stream, true);
+}
+
+// Tokens a tile: as few as hold M; many tokens go to pairs of CTAs
+enum class Shape { kFew, k16, k32, k64, k128, kPair };
+
+Shape choose(int64_t M, int N) {
+    if (M <= 8) return Shape::kFew;
+    if (M <= 16) return Shape::k16;
+    if (M <= 32) return Shape::k32;
+    if (M <= 64) return Shape::k64;
+    const int64_t pairs = ((M + 255) / 256) * ((N + 255) / 256);
+    return M > 128 && pairs >= 76 ? Shape::kPair : Shape::k128;
 }
 
 template <bool F32>
-beam_status launch_tiles(const MatmulParams& p, const beam::Device& dev, cudaStream_t stream, bool pdl) {
-    if (p.M <= 16) return launch_tile<16, F32>(p, dev, stream, pdl);
-    if (p.M <= 32) return launch_tile<32, F32>(p, dev, stream, pdl);
-    if (p.M <= 64) return launch_tile<64, F32>(p, dev, stream, pdl);
-    return launch_tile<128, F32>(p, dev, stream, pdl);
+beam_status launch_tiles(Shape shape, const MatmulParams& p, const beam::Device& dev, void* part, cudaStream_t stream,
+                         bool pdl) {
+    switch (shape) {
+    case Shape::k16: return launch_tile<16, 1, F32>(p, dev, part, stream, pdl);
+    case Shape::k32: return launch_tile<32, 1, F32>(p, dev, part, stream, pdl);
+    case Shape::k64: return launch_tile<64, 1, F32>(p, dev, part, stream, pdl);
+    case Shape::k128: return launch_tile<128, 1, F32>(p, dev, part, stream, pdl);
+    default: return launch_tile<256, 2, F32>(p, dev, part, stream, pdl);
+    }
+}
+
+bool bad_shape(int64_t M, int N, int K) {
+    return M < 0 || M > 0x7FFFFFFF || N < 0 || K < 16 || (K & 15) || K > BEAM_MATMUL_MAX_K;
 }
 
 }  // namespace
 
-extern "C" beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, const float* a_scale,
-                                        const int8_t* w, const float* w_scale, int64_t M, int N, int K,
-                                        int out_type, void* out, uint32_t flags) {
-    if (M < 0 || M > 0x7FFFFFFF || N < 0 || K < 16 || (K & 15) || K > BEAM_MATMUL_MAX_K) return BEAM_ERR_SHAPE;
-    if ((out_type != BEAM_OUT_BF16 && out_type != BEAM_OUT_FP32) || (flags & ~BEAM_OPT_PDL)) return BEAM_ERR_ARG;
+extern "C" {
+
+int64_t beam_matmul_int8_workspace(int64_t M, int N, int K) {
+    if (bad_shape(M, N, K)) return -1;
+    if (M == 0 || N == 0) return 0;
+    const MatmulParams p{nullptr, nullptr, nullptr, nullptr, nullptr, M, N, K};
+    beam::MatmulTcParams q{};
+    switch (choose(M, N)) {
+    case Shape::k16: plan<16, 1>(p, kMaxSms, &q); return part_bytes<16>(q);
+    case Shape::k32: plan<32, 1>(p, kMaxSms, &q); return part_bytes<32>(q);
+    case Shape::k64: plan<64, 1>(p, kMaxSms, &q); return part_bytes<64>(q);
+    case Shape::k128: plan<128, 1>(p, kMaxSms, &q); return part_bytes<128>(q);
+    default: return 0;
+    }
+}
+
+beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, const float* a_scale, const int8_t* w,
+                             const float* w_scale, int64_t M, int N, int K, int out_type, void* out, void* workspace,
+                             int64_t workspace_bytes, uint32_t flags) {
+    if (bad_shape(M, N, K)) return BEAM_ERR_SHAPE;
+    const int64_t need = beam_matmul_int8_workspace(M, N, K);
+    if ((out_type != BEAM_OUT_BF16 && out_type != BEAM_OUT_FP32) || workspace_bytes < need || (flags & ~BEAM_OPT_PDL))
+        return BEAM_ERR_ARG;
     if (M == 0 || N == 0) return BEAM_OK;
-    if (!a || !a_scale || !w || !w_scale || !out) return BEAM_ERR_NULL;
+    if (!a || !a_scale || !w || !w_scale || !out || (need && !workspace)) return BEAM_ERR_NULL;
     const bool f32 = out_type == BEAM_OUT_FP32;
     const unsigned out_size = f32 ? 4u : 2u;
     if (misaligned(a, 16) || misaligned(w, 16) || misaligned(a_scale, 4) || misaligned(w_scale, 4) ||
-        misaligned(out, out_size))
+        misaligned(out, out_size) || (need && misaligned(workspace, 16)))
         return BEAM_ERR_ALIGN;
-    const size_t ob = (size_t)M * (size_t)N * out_size;
-    if (overlaps(out, ob, a, (size_t)M * (size_t)K) || overlaps(out, ob, w, (size_t)N * (size_t)K) ||
-        overlaps(out, ob, a_scale, (size_t)M * 4u) || overlaps(out, ob, w_scale, (size_t)N * 4u))
-        return BEAM_ERR_ALIAS;
+    const size_t ob = (size_t)M * (size_t)N * out_size, nb = (size_t)need;
+    const struct {
+        const void* p;
+        size_t n;
+    } in[] = {{a, (size_t)M * (size_t)K}, {w, (size_t)N * (size_t)K}, {a_scale, (size_t)M * 4u},
+              {w_scale, (size_t)N * 4u}};
+    for (const auto& i : in)
+        if (overlaps(out, ob, i.p, i.n) || overlaps(workspace, nb, i.p, i.n)) return BEAM_ERR_ALIAS;
+    if (overlaps(out, ob, workspace, nb)) return BEAM_ERR_ALIAS;
     beam::Device dev;
     const beam_status st = beam::device(&dev);
     if (st != BEAM_OK) return st;
     MatmulParams p{a, a_scale, w, w_scale, out, M, N, K};
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const bool pdl = (flags & BEAM_OPT_PDL) != 0;
-    if (M > 8) return f32 ? launch_tiles<true>(p, dev, cs, pdl) : launch_tiles<false>(p, dev, cs, pdl);
+    const Shape shape = choose(M, N);
+    if (shape != Shape::kFew)
+        return f32 ? launch_tiles<true>(shape, p, dev, workspace, cs, pdl)
+                   : launch_tiles<false>(shape, p, dev, workspace, cs, pdl);
     void* args[] = {&p};
     const int mb = M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : 8;
     const void* fn = f32 ? few_kernel<true>(mb) : few_kernel<false>(mb);
     constexpr int kR = 2, kWarps = 8;
     return launch(fn, dim3((unsigned)((N + kR * kWarps - 1) / (kR * kWarps))), dim3(256), args, 0, cs, pdl);
 }
+
+}  // extern "C"

@@ -33,10 +33,51 @@ constexpr uint64_t kMatmulWaitNs = 2000000000ull;   // every wait gives up after
 
 struct MatmulTcParams {
     MatmulParams p;
-    int m_tiles, n_tiles;
-    int splits;               // CTAs of a cluster, each with a part of k
+    int m_tiles;              // tiles of NT tokens
+    int steps;                // of k
+    long long tiles;
+    // `workers` CTAs (CG = 1) or pairs (CG = 2). Worker c takes the whole tiles
+    // c, c + workers, ... of the first waves * workers, and of the steps of the
+    // tiles behind those its share of an even split among the first `sharers`.
+    int waves, workers, sharers;
+    float* part;              // [workers][2][NT][128]: sums of tiles that a worker has a part of
     uint64_t wait_ns;
     unsigned int* status;
+};
+
+// What a worker does, in order: segments of a tile's steps [k0, k1)
+struct Segment {
+    long long tile;
+    int k0, k1;
+};
+
+class Schedule {
+    const MatmulTcParams& q;
+    const int worker;
+    int wave = 0;
+    long long at, end;  // steps of the split tiles, counted from the first of them
+
+public:
+    __device__ Schedule(const MatmulTcParams& q_, int worker_) : q(q_), worker(worker_) {
+        const long long total = (q.tiles - (long long)q.waves * q.workers) * q.steps;
+        const bool shares = worker < q.sharers && total > 0;
+        at = shares ? total * worker / q.sharers : 0;
+        end = shares ? total * (worker + 1) / q.sharers : 0;
+    }
+    __device__ bool next(Segment& s) {
+        if (wave < q.waves) {
+            s.tile = (long long)wave++ * q.workers + worker;
+            s.k0 = 0;
+            s.k1 = q.steps;
+            return s.tile < q.tiles;
+        }
+        if (at >= end) return false;
+        s.tile = (long long)q.waves * q.workers + at / q.steps;
+        s.k0 = (int)(at % q.steps);
+        s.k1 = (int)min((long long)q.steps, s.k0 + (end - at));
+        at += s.k1 - s.k0;
+        return true;
+    }
 };
 
 // four int8 -> four FP16, in the order 0, 2, 1, 3: what a sum over k does not
@@ -117,228 +158,279 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, ns));
 }
 
-template <int NT>
-struct TileConfig {  // NT tokens a CTA
-    static constexpr int kSlots = NT == 16 ? 5 : NT == 32 ? 4 : 3;                 // int8 ring
-    static constexpr int kOps = NT <= 64 ? 2 : 4;                                // widened slots
-    static constexpr int kCtas = NT <= 64 ? 2 : 1;                               // CTAs an SM
-    static constexpr int kAGroups = 2, kBGroups = NT <= 64 ? 1 : 2;              // groups of 4 warps
-    static constexpr int kAWarps = 4 * kAGroups, kBWarps = 4 * kBGroups;
-    static constexpr int kThreads = 32 * (kAWarps + kBWarps + 2);
-    static constexpr int kAcc = NT < 32 ? 32 : NT;                               // accumulator columns
-    static constexpr int kCols = kAcc + kOps * kStepCols <= 256 ? 256 : 512;     // allocated
-    static constexpr uint32_t kSlotBytes = kABytes + NT * kStepK;
-    static constexpr uint32_t kOpBytes = NT * kStepK * 2;
-    static constexpr uint32_t kSmem = kSlots * kSlotBytes + kOps * kOpBytes + 1024;  // and alignment
+// NT tokens by 128 CG channels: one CTA (CG = 1) or a pair of CTAs on one
+// tensor tile (CG = 2), each with 128 channels and half of the tokens' rows
+template <int NT, int CG>
+struct TileConfig {
+    static constexpr int kRows = NT / CG;                                          // tokens widened by a CTA
+    static constexpr int kSlots = NT == 16 ? 10 : NT == 32 ? 9 : NT == 64 ? 6 : 3; // int8 ring
+    static constexpr int kOps = 4;                                                 // widened slots
+    static constexpr int kAccs = NT <= 128 ? 2 : 1;                                // accumulators
+    static constexpr int kAccCols = NT < 32 ? 32 : NT;
+    static constexpr int kAWarps = 8, kBWarps = kRows <= 64 ? 4 : 8, kEpiWarps = 4;
+    static constexpr int kAGroups = kAWarps / 4, kBGroups = kBWarps / 4;
+    // warps in groups of four: the schedulers' register files are separate
+    static constexpr int kThreads = 32 * (kAWarps + kBWarps + kEpiWarps + 4);
+    static constexpr uint32_t kSlotBytes = kABytes + kRows * kStepK;
+    static constexpr uint32_t kOpBytes = kRows * kStepK * 2;
+    static constexpr uint32_t kScaleAt = kSlots * kSlotBytes + kOps * kOpBytes;    // FP32 [2][NT]
+    static constexpr uint32_t kBarAt = kScaleAt + 2 * NT * 4;
+    static constexpr uint32_t kSmem = kBarAt + (2 * kSlots + 2 * kOps + 2 * kAccs + 1) * 8;
+    static_assert(kAccs * kAccCols + kOps * kStepCols <= 512, "tensor memory has 512 columns");
+    static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
 
-// A tile of 128 channels by NT tokens, one CTA, or a cluster of `splits` CTAs
-// that share its k. Warps: kAWarps widen channels and read the result back,
-// kBWarps widen tokens, one loads, one multiplies. Widening a step is a chain of
-// latencies (wait, load, convert, store, hand over: 1400 cycles for 128 channels
-// and 128 tokens, of which the matrix unit needs 512), so two groups of four
-// warps take the steps in turn. For few tokens the way of the weights from HBM
-// bounds it; two CTAs an SM then keep about 150 KB of them in flight on each.
-// Split along k, the CTAs' integer partial sums meet in shared memory: CTA r
-// adds and stores its share of the columns.
-template <int NT, bool F32>
-__global__ void __launch_bounds__(TileConfig<NT>::kThreads, TileConfig<NT>::kCtas)
+// Warps: 8 widen channels, 4 or 8 widen tokens, 4 read the result back, one
+// loads, one multiplies. Widening a step is a chain of latencies (wait, load,
+// convert, store, hand over: measured 1400 cycles for 128 channels and 128
+// tokens, of which the matrix unit needs 512), so groups of four warps take the
+// steps in turn. Everything runs on from tile to tile without a pause; with two
+// accumulators the result of one tile is stored under the next one's products.
+//
+// For few tokens the way of the weights from HBM bounds it: the ring keeps 160
+// KB of them in flight on every SM, and all SMs get the same number of steps,
+// whatever the number of tiles (`sharers`): a tile that several workers have
+// steps of leaves FP32 sums in `part`, which matmul_int8_join_kernel adds.
+// For many tokens the matrix unit bounds it; pairs of CTAs then halve the tokens
+// that each CTA widens, and what the matrix unit reads from shared memory.
+template <int NT, int CG, bool F32>
+__global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
     matmul_int8_tile_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
-                            const MatmulTcParams q) {
-    using C = TileConfig<NT>;
-    extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t raw_full[C::kSlots], raw_empty[C::kSlots], op_full[C::kOps], op_empty[C::kOps],
-        acc_full;
-    __shared__ uint32_t tmem_slot;
-    __shared__ float a_scale[NT], w_scale[kTileN];
-    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    constexpr int kLoadWarp = C::kAWarps + C::kBWarps, kMulWarp = kLoadWarp + 1;
+                            const __grid_constant__ MatmulTcParams q) {
+    using C = TileConfig<NT, CG>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    constexpr int kEpiWarp = C::kAWarps + C::kBWarps, kLoadWarp = kEpiWarp + C::kEpiWarps, kMulWarp = kLoadWarp + 1;
     unsigned char* ops = smem + C::kSlots * C::kSlotBytes;
+    float* a_scale = reinterpret_cast<float*>(smem + C::kScaleAt);
+    uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::kBarAt);  // a slot's int8 tiles have landed
+    uint64_t* raw_empty = raw_full + C::kSlots;                         // ... have been read
+    uint64_t* op_full = raw_empty + C::kSlots;                          // a step is widened (in both CTAs)
+    uint64_t* op_empty = op_full + C::kOps;                             // ... is multiplied
+    uint64_t* acc_full = op_empty + C::kOps;                            // a segment's sums are complete
+    uint64_t* acc_empty = acc_full + C::kAccs;                          // ... are read (in both CTAs)
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + C::kAccs);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int split = q.splits > 1 ? (int)cluster_rank() : 0;
-    const int tile = blockIdx.x / q.splits;
-    const int n0 = (tile / q.m_tiles) * kTileN;
-    const long long m0 = (long long)(tile % q.m_tiles) * NT;
-    const int steps = (q.p.K + kStepK - 1) / kStepK;
-    const int first = (int)((long long)steps * split / q.splits);
-    const int count = (int)((long long)steps * (split + 1) / q.splits) - first;
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+    const int worker = blockIdx.x / CG;
+    auto channel0 = [&](const Segment& s) { return ((int)(s.tile / q.m_tiles) * CG + (int)rank) * kTileN; };
+    auto token0 = [&](const Segment& s) { return (long long)(s.tile % q.m_tiles) * NT; };
 
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
             mbar_init(&raw_full[i], 1);
-            mbar_init(&raw_empty[i], 8);
+            mbar_init(&raw_empty[i], 8);  // the warps of one group each for channels and tokens
         }
         for (int i = 0; i < C::kOps; ++i) {
-            mbar_init(&op_full[i], 8);
+            mbar_init(&op_full[i], 8 * CG);
             mbar_init(&op_empty[i], 1);
         }
-        mbar_init(&acc_full, 1);
+        for (int i = 0; i < C::kAccs; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], C::kEpiWarps * CG);
+        }
         mbar_fence_init();
     }
-    if (warp == kMulWarp) tmem_alloc<1>(&tmem_slot, C::kCols);
+    if (warp == kMulWarp) tmem_alloc<CG, 512>(tmem_slot);
     tmem_fence_before();
-    __syncthreads();
+    if constexpr (CG == 2) cluster_sync();  // the other CTA's barriers are ready too
+    else __syncthreads();
     tmem_fence_after();
     // only now: a CTA that the trigger lets in allocates tensor memory too, and
     // must not take the columns that a CTA of this grid still waits for
     pdl_trigger();
-    const uint32_t acc = tmem_slot, acols = acc + C::kAcc;
+    const uint32_t acc = *tmem_slot, acols = acc + C::kAccs * C::kAccCols;
     bool ok = true;
+    Schedule todo(q, worker);
+    Segment seg;
+    int it = 0, n_seg = 0;  // steps and segments so far
 
     if (warp == kLoadWarp) {
         if (lane == 0) {
             tma_prefetch_map(&wmap);
             tma_prefetch_map(&amap);
             const uint64_t pol_w = q.m_tiles == 1 ? l2_evict_first() : l2_evict_normal(), pol_a = l2_evict_normal();
-            auto load_w = [&](int i, int s) {
-                mbar_arrive_expect_tx(&raw_full[s], C::kSlotBytes);
-                tma_load_2d(smem + s * C::kSlotBytes, &wmap, (first + i) * kStepK, n0, &raw_full[s], pol_w);
+            auto load_w = [&](int slot, const Segment& s, int k) {
+                mbar_arrive_expect_tx(&raw_full[slot], C::kSlotBytes);
+                tma_load_2d(smem + slot * C::kSlotBytes, &wmap, k * kStepK, channel0(s), &raw_full[slot], pol_w);
             };
-            auto load_a = [&](int i, int s) {
-                tma_load_2d(smem + s * C::kSlotBytes + kABytes, &amap, (first + i) * kStepK, (int)m0, &raw_full[s], pol_a);
+            auto load_a = [&](int slot, const Segment& s, int k) {
+                tma_load_2d(smem + slot * C::kSlotBytes + kABytes, &amap, k * kStepK,
+                            (int)token0(s) + (int)rank * C::kRows, &raw_full[slot], pol_a);
             };
             // the weights do not depend on the kernel before: the first slots' are
             // asked for ahead of the wait for it
-            const int head = count < C::kSlots ? count : C::kSlots;
-            for (int i = 0; i < head; ++i) load_w(i, i);
+            Schedule head(q, worker);
+            for (int i = 0; i < C::kSlots && head.next(seg);)
+                for (int k = seg.k0; k < seg.k1 && i < C::kSlots; ++k, ++i) load_w(i, seg, k);
             pdl_wait();
-            for (int i = 0; i < head; ++i) load_a(i, i);
-            int issued = head;
-            for (int i = head; i < count; ++i) {
-                const int s = i % C::kSlots;
-                if (!mbar_wait(&raw_empty[s], (uint32_t)(i / C::kSlots - 1) & 1, q.wait_ns)) {
-                    ok = false;
-                    break;
+            while (ok && todo.next(seg))
+                for (int k = seg.k0; k < seg.k1; ++k, ++it) {
+                    const int slot = it % C::kSlots;
+                    if (it >= C::kSlots) {
+                        ok = mbar_wait(&raw_empty[slot], (uint32_t)(it / C::kSlots - 1) & 1, q.wait_ns);
+                        if (!ok) break;
+                        load_w(slot, seg, k);
+                    }
+                    load_a(slot, seg, k);
                 }
-                load_w(i, s);
-                load_a(i, s);
-                issued = i + 1;
-            }
             if (!ok)  // copies in flight must land before the shared memory goes
-                for (int i = issued > C::kSlots ? issued - C::kSlots : 0; i < issued; ++i)
+                for (int i = it - C::kSlots; i < it; ++i)
                     mbar_wait(&raw_full[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
         }
     } else if (warp == kMulWarp) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = UmmaF16<kTileN, NT>::kDesc;
-            for (int i = 0; i < count; ++i) {
-                const int o = i % C::kOps;
-                if (!mbar_wait(&op_full[o], (uint32_t)(i / C::kOps) & 1, q.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                tmem_fence_after();
-                const uint32_t b = smem_u32(ops + o * C::kOpBytes);
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = UmmaF16<kTileN * CG, NT>::kDesc;
+            for (; ok && todo.next(seg); ++n_seg) {
+                const int a = n_seg % C::kAccs;
+                if (n_seg >= C::kAccs) ok = mbar_wait<CG>(&acc_empty[a], (uint32_t)(n_seg / C::kAccs - 1) & 1, q.wait_ns);
+                for (int k = seg.k0; ok && k < seg.k1; ++k, ++it) {
+                    const int o = it % C::kOps;
+                    ok = mbar_wait<CG>(&op_full[o], (uint32_t)(it / C::kOps) & 1, q.wait_ns);
+                    if (!ok) break;
+                    tmem_fence_after();
+                    const uint32_t b = smem_u32(ops + o * C::kOpBytes);
 #pragma unroll
-                for (int k = 0; k < kStepK / 16; ++k)
-                    umma_f16<1>(acc, acols + o * kStepCols + k * 8,
-                                umma_smem_desc(b + (k / 4) * (NT * 128) + (k % 4) * 32), idesc, i > 0 || k > 0);
-                umma_commit<1>(&op_empty[o]);
+                    for (int j = 0; j < kStepK / 16; ++j)
+                        umma_f16<CG>(acc + a * C::kAccCols, acols + o * kStepCols + j * 8,
+                                     umma_smem_desc(b + (j / 4) * (C::kRows * 128) + (j % 4) * 32), idesc,
+                                     k > seg.k0 || j > 0);
+                    umma_commit<CG>(&op_empty[o]);
+                }
+                umma_commit<CG>(&acc_full[a]);
+                if (!ok) mbar_wait(&acc_full[a], (uint32_t)(n_seg / C::kAccs) & 1, q.wait_ns);
             }
-            umma_commit<1>(&acc_full);
-            if (!ok) mbar_wait(&acc_full, 0, q.wait_ns);
         }
-    } else {
+    } else if (warp < kEpiWarp) {
         const bool channels = warp < C::kAWarps;
         // this warp's group takes the steps group, group + groups, ...
         const int group = channels ? warp / 4 : (warp - C::kAWarps) / 4, groups = channels ? C::kAGroups : C::kBGroups;
         const int t = tid & 127;  // within the group; for channels the lane of tensor memory
         const uint32_t lanes = acols + ((uint32_t)(t & 96) << 16);
         const TokenPlace place(t);
-        // the scales wait in shared memory for the result
-        pdl_wait();
-        if (group == 0) {
-            if (channels) w_scale[t] = n0 + t < q.p.N ? __ldg(q.p.w_scale + n0 + t) : 0.0f;
-            else if (t < NT) a_scale[t] = m0 + t < q.p.M ? __ldg(q.p.a_scale + m0 + t) : 0.0f;
-        }
-        for (int i = group; i < count; i += groups) {
-            const int s = i % C::kSlots, o = i % C::kOps;
-            const unsigned char* slot = smem + s * C::kSlotBytes;
-            uint4 v[8];  // tokens: NT / 16 of them
-            uint4(&vt)[NT / 16] = reinterpret_cast<uint4(&)[NT / 16]>(v);
-            ok = warp_wait(&raw_full[s], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
-            if (!ok) break;
-            if (channels) load_channels(slot, t, v);
-            else load_tokens<NT>(slot + kABytes, place, vt);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&raw_empty[s]);
-            ok = i < C::kOps || warp_wait(&op_empty[o], (uint32_t)(i / C::kOps - 1) & 1, q.wait_ns);
-            if (!ok) break;
-            if (channels) {
-                tmem_fence_after();
-                widen_channels(v, lanes + o * kStepCols);
-                tmem_wait_st();
-                tmem_fence_before();
-            } else {
-                widen_tokens<NT>(vt, ops + o * C::kOpBytes, place);
-                fence_proxy_async_smem();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&op_full[o]);
-        }
-    }
-    // the scales; also: nobody reads the ring or the operands any more once the
-    // accumulators are complete
-    __syncthreads();
-    __syncwarp();
-
-    // accumulators: lane = channel n0 + tid, column = token m0 + c
-    const long long left = q.p.M - m0;
-    const int cols = left < NT ? (int)left : NT;
-    int* part = reinterpret_cast<int*>(smem);  // [NT][128] of the ring, which is idle by then
-    if (warp < C::kAWarps) {
-        ok = warp_wait(&acc_full, 0, q.wait_ns) && ok;
-        if (ok) {
-            tmem_fence_after();
-            const int t = tid & 127, n = n0 + t;
-            const float ws = w_scale[t];
-            for (int c0 = 16 * (warp / 4); c0 < cols; c0 += 16 * C::kAGroups) {
-                float v[16];
-                tmem_ld16(acc + ((uint32_t)(t & 96) << 16) + c0, v);
-                tmem_wait_ld();
-                if (q.splits > 1) {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) part[(c0 + c) * kTileN + t] = __float2int_rn(v[c]);
-                } else if (n < q.p.N) {
-                    const size_t at = (size_t)(m0 + c0) * (size_t)q.p.N + (size_t)n;
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        if (c0 + c < cols)
-                            store_out<F32>(q.p.out, at + (size_t)c * (size_t)q.p.N,
-                                           __fmul_rn(__fmul_rn(v[c], a_scale[c0 + c]), ws));
+        while (ok && todo.next(seg)) {
+            const int first = it, n = seg.k1 - seg.k0;
+            it += n;
+            for (int i = first + (group + groups - first % groups) % groups; i < first + n; i += groups) {
+                const int s = i % C::kSlots, o = i % C::kOps;
+                const unsigned char* slot = smem + s * C::kSlotBytes;
+                uint4 v[8];  // tokens: kRows / 16 of them
+                uint4(&vt)[C::kRows / 16] = reinterpret_cast<uint4(&)[C::kRows / 16]>(v);
+                ok = warp_wait(&raw_full[s], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
+                if (!ok) break;
+                if (channels) load_channels(slot, t, v);
+                else load_tokens<C::kRows>(slot + kABytes, place, vt);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&raw_empty[s]);
+                ok = i < C::kOps || warp_wait(&op_empty[o], (uint32_t)(i / C::kOps - 1) & 1, q.wait_ns);
+                if (!ok) break;
+                if (channels) {
+                    tmem_fence_after();
+                    widen_channels(v, lanes + o * kStepCols);
+                    tmem_wait_st();
+                    tmem_fence_before();
+                } else {
+                    widen_tokens<C::kRows>(vt, ops + o * C::kOpBytes, place);
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 2) mbar_arrive_cluster(cluster_addr(&op_full[o], 0));
+                    else mbar_arrive(&op_full[o]);
                 }
             }
-            tmem_fence_before();
+        }
+    } else if (warp < kLoadWarp) {
+        // results: lane = channel, column = token
+        const int t = tid & 127;
+        pdl_wait();
+        for (; ok && todo.next(seg); ++n_seg) {
+            const int a = n_seg % C::kAccs, n = channel0(seg) + t;
+            const long long m0 = token0(seg), left = q.p.M - m0;
+            const int cols = left < NT ? (int)left : NT;
+            const bool whole = seg.k1 - seg.k0 == q.steps;
+            float* scales = a_scale + (n_seg & 1) * NT;
+            const float ws = n < q.p.N ? __ldg(q.p.w_scale + n) : 0.0f;
+            for (int c = t; c < cols; c += 128) scales[c] = __ldg(q.p.a_scale + m0 + c);
+            // one answer for the four warps, which also meet here: the scales are there
+            ok = group_and(1, warp_wait(&acc_full[a], (uint32_t)(n_seg / C::kAccs) & 1, q.wait_ns));
+            if (!ok) break;
+            tmem_fence_after();
+            // the first of this worker's split tiles goes to its part 0, the last to part 1
+            const bool second = seg.k0 == 0;
+            float* part = q.part + ((size_t)worker * 2 + second) * (size_t)(NT * kTileN) + t;
+            const size_t at = (size_t)m0 * (size_t)q.p.N + (size_t)n;
+            const uint32_t from = acc + a * C::kAccCols + ((uint32_t)(t & 96) << 16);
+            constexpr int kBatch = NT < 32 ? 16 : 32;
+            for (int c0 = 0; c0 < cols; c0 += kBatch) {
+                float v[kBatch];
+                if constexpr (kBatch == 16) tmem_ld16(from + c0, v);
+                else tmem_ld32(from + c0, v);
+                tmem_wait_ld();
+                if (c0 + kBatch >= cols) {  // all read: the accumulator is free
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CG == 2) mbar_arrive_cluster(cluster_addr(&acc_empty[a], 0));
+                        else mbar_arrive(&acc_empty[a]);
+                    }
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int c = 0; c < kBatch; ++c)
+                        if (c0 + c < cols) part[(c0 + c) * kTileN] = v[c];
+                } else if (n < q.p.N) {
+#pragma unroll
+                    for (int c = 0; c < kBatch; ++c)
+                        if (c0 + c < cols)
+                            store_out<F32>(q.p.out, at + (size_t)(c0 + c) * (size_t)q.p.N,
+                                           __fmul_rn(__fmul_rn(v[c], scales[c0 + c]), ws));
+                }
+            }
         }
     }
     if (!ok) atomicOr(q.status, 1u);
-    __syncthreads();
-    // the columns go back before the cluster meets: no CTA holds tensor memory
-    // while it waits for another one, which may still wait for some
+    __syncwarp();
+    tmem_fence_before();
+    if constexpr (CG == 2) cluster_sync();  // nobody leaves while the other CTA works with its memory
+    else __syncthreads();
     if (warp == kMulWarp) {
         tmem_fence_after();
-        tmem_dealloc<1>(acc, C::kCols);
+        tmem_dealloc<CG, 512>(acc);
     }
-    if (q.splits > 1) {
-        __syncwarp();
-        cluster_sync();  // every CTA's partial sums are written
-        const int lo = cols * split / q.splits, hi = cols * (split + 1) / q.splits;
-        if (tid < 256) {
-            const int r = tid & 127, n = n0 + r;
-            for (int c = lo + (tid >> 7); c < hi; c += 2) {
-                int sum = 0;
-                for (int i = 0; i < q.splits; ++i)
-                    sum += ld_cluster_s32(cluster_addr(part + c * kTileN + r, (uint32_t)i));
-                if (n < q.p.N) {
-                    const long long m = m0 + c;
-                    store_out<F32>(q.p.out, (size_t)m * (size_t)q.p.N + (size_t)n,
-                                   __fmul_rn(__fmul_rn((float)sum, a_scale[c]), w_scale[r]));
-                }
-            }
-        }
-        __syncwarp();
-        cluster_sync();  // nobody leaves while others read its sums
+}
+
+// Adds the sums of the tiles that several workers have steps of: a block for
+// eight tokens of a tile, thread = channel. They are integers (FP32 ones), added
+// as such.
+template <int NT, bool F32>
+__global__ void __launch_bounds__(kTileN) matmul_int8_join_kernel(const __grid_constant__ MatmulTcParams q) {
+    pdl_trigger();
+    const long long split = blockIdx.x, tile = (long long)q.waves * q.workers + split;
+    const int n = (int)(tile / q.m_tiles) * kTileN + threadIdx.x;
+    const long long m0 = (tile % q.m_tiles) * NT + blockIdx.y * 8;
+    // worker c has the steps [total c / sharers, total (c + 1) / sharers)
+    const long long total = (q.tiles - (long long)q.waves * q.workers) * q.steps;
+    const long long lo = split * q.steps, hi = lo + q.steps;
+    int c0 = (int)(lo * q.sharers / total);
+    while (total * (c0 + 1) / q.sharers <= lo) ++c0;
+    pdl_wait();
+    if (total * c0 / q.sharers <= lo && total * (c0 + 1) / q.sharers >= hi) return;  // one worker's: stored already
+    if (n >= q.p.N) return;
+    int sum[8] = {};
+    for (int c = c0; c < q.sharers && total * c / q.sharers < hi; ++c) {
+        const bool second = total * c / q.sharers <= lo;  // its segment of this tile begins at the tile's first step
+        const float* part = q.part + ((size_t)c * 2 + second) * (size_t)(NT * kTileN) + (size_t)blockIdx.y * 8 * kTileN +
+                            threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (m0 + i < q.p.M) sum[i] += __float2int_rn(__ldcg(part + i * kTileN));
     }
+    const float ws = __ldg(q.p.w_scale + n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (m0 + i < q.p.M)
+            store_out<F32>(q.p.out, (size_t)(m0 + i) * (size_t)q.p.N + (size_t)n,
+                           __fmul_rn(__fmul_rn((float)sum[i], __ldg(q.p.a_scale + m0 + i)), ws));
 }
 
 }  // namespace beam

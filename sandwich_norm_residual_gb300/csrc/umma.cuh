@@ -12,24 +12,24 @@ namespace beam {
 
 // ---------------------------------------------------------------- tensor memory
 
-// Allocates `cols` columns (a power of two, at least 32) for this CTA (CG = 1)
+// Allocates COLS columns (a power of two, at least 32) for this CTA (CG = 1)
 // or for both CTAs of a pair (CG = 2: a warp of each must call). Waits while
 // the SM's other CTAs hold too many; a CTA allocates once and waits for nothing
 // else while it holds none, so that wait ends. The address lands in *slot.
-template <int CG>
-__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
+template <int CG, uint32_t COLS>
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot) {
     if constexpr (CG == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(slot)), "r"(cols) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(slot)), "n"(COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     } else {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(slot)), "r"(cols) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(slot)), "n"(COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
 }
-template <int CG>
-__device__ __forceinline__ void tmem_dealloc(uint32_t base, uint32_t cols) {
-    if constexpr (CG == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(base), "r"(cols));
-    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(base), "r"(cols));
+template <int CG, uint32_t COLS>
+__device__ __forceinline__ void tmem_dealloc(uint32_t base) {
+    if constexpr (CG == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(base), "n"(COLS));
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(base), "n"(COLS));
 }
 
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -114,15 +114,37 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
 
 // Waits for the phase with the given parity, at most about limit_ns. The timer
 // is read only every 256 tries, so that short waits do not wait for it too.
+// CG = 2: arrivals come from both CTAs of the pair.
+template <int CG = 1>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+    auto done = [&] {
+        if constexpr (CG == 1) return mbar_try_wait(bar, parity);
+        uint32_t d;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(d) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+        return d != 0;
+    };
     uint64_t t0 = 0;
-    for (uint32_t tries = 1; !mbar_try_wait(bar, parity); ++tries) {
+    for (uint32_t tries = 1; !done(); ++tries) {
         if (tries & 255u) continue;
         const uint64_t now = global_ns();
         if (!t0) t0 = now;
         else if (now - t0 > limit_ns) return false;
     }
     return true;
+}
+
+// the `and` of ok over the 128 threads that meet at barrier `id`
+__device__ __forceinline__ bool group_and(int id, bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"((uint32_t)ok), "r"(id) : "memory");
+    return r != 0;
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -137,11 +159,6 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
-}
-__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;

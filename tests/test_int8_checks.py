@@ -79,10 +79,10 @@ def test_binding_checks_the_int8_boundaries():
 
 
 def test_matmul_argument_errors(lib):
-    AA, AS, W, WS, O = (A + (i << 33) for i in range(5))
+    AA, AS, W, WS, O, P = (A + (i << 33) for i in range(6))
 
-    def mm(M=4, N=40, K=64, a=AA, sa=AS, w=W, sw=WS, ty=0, o=O, flags=0):
-        return lib.beam_matmul_int8(None, a, sa, w, sw, M, N, K, ty, o, flags)
+    def mm(M=4, N=40, K=64, a=AA, sa=AS, w=W, sw=WS, ty=0, o=O, ws=P, nb=1 << 30, flags=0):
+        return lib.beam_matmul_int8(None, a, sa, w, sw, M, N, K, ty, o, ws, nb, flags)
 
     assert mm(M=-1) == _lib.BEAM_ERR_SHAPE
     assert mm(M=1 << 31) == _lib.BEAM_ERR_SHAPE
@@ -104,6 +104,17 @@ def test_matmul_argument_errors(lib):
     assert mm(o=W - 2) == _lib.BEAM_ERR_ALIAS
     assert mm(o=AS + 4) == _lib.BEAM_ERR_ALIAS
     assert mm(o=WS) == _lib.BEAM_ERR_ALIAS
+    # workspaces, where the shape needs one
+    need = lib.beam_matmul_int8_workspace
+    assert need(4, 40, 64) == 0 and need(0, 40, 64) == 0 and need(4, 40, 24) == -1
+    big = dict(M=64, N=5120, K=20480)
+    assert need(64, 5120, 20480) > 0
+    assert mm(nb=need(64, 5120, 20480) - 1, **big) == _lib.BEAM_ERR_ARG
+    assert mm(ws=None, **big) == _lib.BEAM_ERR_NULL
+    assert mm(ws=P + 4, **big) == _lib.BEAM_ERR_ALIGN
+    assert mm(ws=W + 16, **big) == _lib.BEAM_ERR_ALIAS
+    assert mm(ws=O + 64, **big) == _lib.BEAM_ERR_ALIAS
+    assert mm(ws=None, nb=0) in (_lib.BEAM_ERR_CUDA, _lib.BEAM_ERR_DEVICE)
     for flags in (0, _lib.BEAM_OPT_PDL):
         assert mm(o=O + 2, flags=flags) in (_lib.BEAM_ERR_CUDA, _lib.BEAM_ERR_DEVICE)
 
