@@ -154,8 +154,9 @@ __device__ __forceinline__ void widen_tokens(const uint4 (&v)[ROWS / 16], unsign
 }
 
 // all lanes: whether every lane's wait ended
+template <int CG = 1>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t ns) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, ns));
+    return __all_sync(0xFFFFFFFFu, mbar_wait<CG>(bar, parity, ns));
 }
 
 // NT tokens by 128 CG channels: one CTA (CG = 1) or a pair of CTAs on one
@@ -278,26 +279,34 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                     mbar_wait(&raw_full[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
         }
     } else if (warp == kMulWarp) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             constexpr uint32_t idesc = UmmaF16<kTileN * CG, NT>::kDesc;
+            const uint64_t b0 = umma_smem_desc(smem_u32(ops));
             for (; ok && todo.next(seg); ++n_seg) {
                 const int a = n_seg % C::kAccs;
-                if (n_seg >= C::kAccs) ok = mbar_wait<CG>(&acc_empty[a], (uint32_t)(n_seg / C::kAccs - 1) & 1, q.wait_ns);
+                const uint32_t d = acc + a * C::kAccCols;
+                if (n_seg >= C::kAccs)
+                    ok = warp_wait<CG>(&acc_empty[a], (uint32_t)(n_seg / C::kAccs - 1) & 1, q.wait_ns);
                 for (int k = seg.k0; ok && k < seg.k1; ++k, ++it) {
                     const int o = it % C::kOps;
-                    ok = mbar_wait<CG>(&op_full[o], (uint32_t)(it / C::kOps) & 1, q.wait_ns);
+                    ok = warp_wait<CG>(&op_full[o], (uint32_t)(it / C::kOps) & 1, q.wait_ns);
                     if (!ok) break;
                     tmem_fence_after();
-                    const uint32_t b = smem_u32(ops + o * C::kOpBytes);
+                    // the descriptor counts addresses in units of 16 bytes
+                    const uint64_t b = b0 + (uint32_t)o * (C::kOpBytes / 16);
+                    const uint32_t from = acols + o * kStepCols;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < kStepK / 16; ++j)
-                        umma_f16<CG>(acc + a * C::kAccCols, acols + o * kStepCols + j * 8,
-                                     umma_smem_desc(b + (j / 4) * (C::kRows * 128) + (j % 4) * 32), idesc,
-                                     k > seg.k0 || j > 0);
-                    umma_commit<CG>(&op_empty[o]);
+                        for (int j = 0; j < kStepK / 16; ++j)
+                            umma_f16<CG>(d, from + j * 8, b + ((j / 4) * (C::kRows * 128) + (j % 4) * 32) / 16, idesc,
+                                         k > seg.k0 || j > 0);
+                        umma_commit<CG>(&op_empty[o]);
+                    }
+                    __syncwarp();
                 }
-                umma_commit<CG>(&acc_full[a]);
-                if (!ok) mbar_wait(&acc_full[a], (uint32_t)(n_seg / C::kAccs) & 1, q.wait_ns);
+                if (elect_one()) umma_commit<CG>(&acc_full[a]);
+                __syncwarp();
+                if (!ok) warp_wait(&acc_full[a], (uint32_t)(n_seg / C::kAccs) & 1, q.wait_ns);
             }
         }
     } else if (warp < kEpiWarp) {

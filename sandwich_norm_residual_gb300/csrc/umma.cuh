@@ -85,6 +85,16 @@ __device__ __forceinline__ uint64_t umma_smem_desc(uint32_t addr) {
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// true in one lane of the (whole) warp. Code that only it runs inside a branch
+// the whole warp takes keeps the operands below in uniform registers; a branch
+// on the lane number does not, and moving them there took longer than the
+// matrix instruction (100 cycles each).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
 // D += A B^T over 16 k, or D = where add is 0; one thread (of the pair's first CTA)
 template <int CG>
 __device__ __forceinline__ void umma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {

@@ -53,6 +53,8 @@ SHAPES = [
     (100, 2565, 400), (128, 128, 128), (129, 129, 112),
     # several tiles in both directions, ragged in each
     (257, 255, 640), (517, 2565, 2576), (300, 4096, 256), (1000, 777, 336), (2048, 2048, 5120),
+    # enough tiles for pairs of CTAs: one ragged wave, and several
+    (2100, 2600, 400), (4100, 5000, 144),
 ]
 
 
