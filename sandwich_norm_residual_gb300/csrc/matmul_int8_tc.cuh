@@ -114,44 +114,42 @@ __device__ __forceinline__ void widen_channels(const uint4 (&v)[8], uint32_t at)
     }
 }
 
-// One step of ROWS tokens, by 128 threads, a chunk of 16 int8 and row each. The
-// int8 chunk c of row r lies at c ^ (r % 8), the two FP16 chunks that it becomes
-// (of 8 values, 2 (c % 4) and the next, in the tile of the step's first or
-// second 64 k) at theirs. A shared-memory phase of 8 lanes takes four chunks of
-// the two rows r and r ^ 5, which meet 8 different places in the load (r and
-// r ^ 5 differ in bit 2) and in both stores (they differ in bit 0).
-struct TokenPlace {
-    int row, chunk, sub;
-    __device__ explicit TokenPlace(int t) {
-        const int lane = t & 31, w = t >> 5;
-        row = (w >> 1) * 8 + ((lane >> 3) ^ (5 * ((lane >> 2) & 1)));
-        chunk = lane & 3;
-        sub = w & 1;
+// One step of ROWS tokens, by WARPS warps: a lane takes ROWS / (4 WARPS) chunks of
+// 16 int8. The int8 chunk c of row r lies at c ^ (r % 8); the two FP16 chunks
+// that it becomes (of 8 values, 2 (c % 4) and the next, in the tile of the step's
+// first or second 64 k) at theirs. A shared-memory phase of 8 lanes takes four
+// chunks of the two rows r and r ^ 5, which meet 8 different places in the load
+// (r and r ^ 5 differ in bit 2) and in both stores (they differ in bit 0).
+template <int ROWS, int WARPS>
+struct Tokens {
+    static constexpr int kChunks = ROWS / 4 / WARPS;
+    const int warp, x, chunk;  // x: row % 8
+    __device__ explicit Tokens(int t) : warp(t >> 5), x(((t >> 3) & 3) ^ (5 * ((t >> 2) & 1))), chunk(t & 3) {}
+    // the warps share 2 ROWS / 8 pieces: 8 rows of one half of the step
+    __device__ int sub(int i) const { return (i * WARPS + warp) & 1; }
+    __device__ int row(int i) const { return ((i * WARPS + warp) >> 1) * 8 + x; }
+
+    __device__ void load(const unsigned char* tile, uint4 (&v)[kChunks]) const {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+            v[i] = *reinterpret_cast<const uint4*>(tile + row(i) * 128 + (((4 * sub(i) + chunk) ^ x) << 4));
+    }
+    // to two FP16 tiles of 64 k, ROWS * 128 bytes each
+    __device__ void widen(const uint4 (&v)[kChunks], unsigned char* op) const {
+        const int first = ((2 * chunk) ^ x) << 4, second = first ^ 16;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            uint4 a, b;
+            widen4(v[i].x, a.x, a.y);
+            widen4(v[i].y, a.z, a.w);
+            widen4(v[i].z, b.x, b.y);
+            widen4(v[i].w, b.z, b.w);
+            unsigned char* o = op + sub(i) * (ROWS * 128) + row(i) * 128;
+            *reinterpret_cast<uint4*>(o + first) = a;
+            *reinterpret_cast<uint4*>(o + second) = b;
+        }
     }
 };
-
-template <int ROWS>
-__device__ __forceinline__ void load_tokens(const unsigned char* tile, const TokenPlace& p, uint4 (&v)[ROWS / 16]) {
-    const unsigned char* at = tile + p.row * 128 + (((4 * p.sub + p.chunk) ^ (p.row & 7)) << 4);
-#pragma unroll
-    for (int i = 0; i < ROWS / 16; ++i) v[i] = *reinterpret_cast<const uint4*>(at + i * 16 * 128);
-}
-
-template <int ROWS>
-__device__ __forceinline__ void widen_tokens(const uint4 (&v)[ROWS / 16], unsigned char* op, const TokenPlace& p) {
-    unsigned char* o = op + p.sub * (ROWS * 128) + p.row * 128;
-    const int first = ((2 * p.chunk) ^ (p.row & 7)) << 4, second = first ^ 16;
-#pragma unroll
-    for (int i = 0; i < ROWS / 16; ++i) {
-        uint4 a, b;
-        widen4(v[i].x, a.x, a.y);
-        widen4(v[i].y, a.z, a.w);
-        widen4(v[i].z, b.x, b.y);
-        widen4(v[i].w, b.z, b.w);
-        *reinterpret_cast<uint4*>(o + i * 16 * 128 + first) = a;
-        *reinterpret_cast<uint4*>(o + i * 16 * 128 + second) = b;
-    }
-}
 
 // all lanes: whether every lane's wait ended
 template <int CG = 1>
@@ -164,19 +162,29 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64
 template <int NT, int CG>
 struct TileConfig {
     static constexpr int kRows = NT / CG;                                          // tokens widened by a CTA
-    static constexpr int kSlots = NT == 16 ? 10 : NT == 32 ? 9 : NT == 64 ? 6 : 3; // int8 ring
-    static constexpr int kOps = 4;                                                 // widened slots
+    static constexpr int kSlots = NT == 16 ? 10 : NT == 32 ? 8 : NT == 64 ? 6 : 4; // int8 ring
+    static constexpr int kOps = NT <= 64 ? 4 : 3;                                  // widened slots
     static constexpr int kAccs = NT <= 128 ? 2 : 1;                                // accumulators
     static constexpr int kAccCols = NT < 32 ? 32 : NT;
-    static constexpr int kAWarps = 8, kBWarps = kRows <= 64 ? 4 : 8, kEpiWarps = 4;
-    static constexpr int kAGroups = kAWarps / 4, kBGroups = kBWarps / 4;
-    // warps in groups of four: the schedulers' register files are separate
+    // warps in groups: a group widens the channels, another the tokens of a step
+    static constexpr int kAGroups = 2, kBGroupWarps = kRows <= 32 ? 1 : 4, kBGroups = kRows <= 32 ? 4 : 2;
+    static constexpr int kAWarps = 4 * kAGroups, kBWarps = kBGroupWarps * kBGroups, kEpiWarps = 4;
+    // whole fours of warps: the schedulers' register files are separate
     static constexpr int kThreads = 32 * (kAWarps + kBWarps + kEpiWarps + 4);
+    // A wait by parity passes at once on a barrier whose phase before has not even
+    // ended, so a group must know that it has. Before step j it has seen the
+    // product of step j - groups - kOps end, and all before: enough for the slot's
+    // step before (j - kSlots) and the operand's (j - 2 kOps) in these cases, as is
+    // a slot that the same group always takes.
+    static constexpr bool safe(int groups) {
+        return (kSlots % groups == 0 || kSlots >= groups + kOps) && (kOps % groups == 0 || kOps >= groups);
+    }
+    static_assert(safe(kAGroups) && safe(kBGroups), "a group could read a slot before it is filled");
     static constexpr uint32_t kSlotBytes = kABytes + kRows * kStepK;
     static constexpr uint32_t kOpBytes = kRows * kStepK * 2;
     static constexpr uint32_t kScaleAt = kSlots * kSlotBytes + kOps * kOpBytes;    // FP32 [2][NT]
     static constexpr uint32_t kBarAt = kScaleAt + 2 * NT * 4;
-    static constexpr uint32_t kSmem = kBarAt + (2 * kSlots + 2 * kOps + 2 * kAccs + 1) * 8;
+    static constexpr uint32_t kSmem = kBarAt + (2 * kSlots + (1 + CG) * kOps + 2 * kAccs + 1) * 8;
     static_assert(kAccs * kAccCols + kOps * kStepCols <= 512, "tensor memory has 512 columns");
     static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
@@ -205,11 +213,12 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
     float* a_scale = reinterpret_cast<float*>(smem + C::kScaleAt);
     uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::kBarAt);  // a slot's int8 tiles have landed
     uint64_t* raw_empty = raw_full + C::kSlots;                         // ... have been read
-    uint64_t* op_full = raw_empty + C::kSlots;                          // a step is widened (in both CTAs)
+    uint64_t* op_full = raw_empty + C::kSlots;                          // a step is widened (in this CTA)
     uint64_t* op_empty = op_full + C::kOps;                             // ... is multiplied
     uint64_t* acc_full = op_empty + C::kOps;                            // a segment's sums are complete
     uint64_t* acc_empty = acc_full + C::kAccs;                          // ... are read (in both CTAs)
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + C::kAccs);
+    uint64_t* pair_full = acc_empty + C::kAccs;                         // (CG = 2, rank 0) ... widened in the other CTA
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pair_full + (CG - 1) * C::kOps);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
     const int worker = blockIdx.x / CG;
@@ -219,11 +228,12 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
             mbar_init(&raw_full[i], 1);
-            mbar_init(&raw_empty[i], 8);  // the warps of one group each for channels and tokens
+            mbar_init(&raw_empty[i], 4 + C::kBGroupWarps);  // the warps of a group each for channels and tokens
         }
         for (int i = 0; i < C::kOps; ++i) {
-            mbar_init(&op_full[i], 8 * CG);
+            mbar_init(&op_full[i], 4 + C::kBGroupWarps);
             mbar_init(&op_empty[i], 1);
+            if (CG == 2) mbar_init(&pair_full[i], 1);
         }
         for (int i = 0; i < C::kAccs; ++i) {
             mbar_init(&acc_full[i], 1);
@@ -289,7 +299,8 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                     ok = warp_wait<CG>(&acc_empty[a], (uint32_t)(n_seg / C::kAccs - 1) & 1, q.wait_ns);
                 for (int k = seg.k0; ok && k < seg.k1; ++k, ++it) {
                     const int o = it % C::kOps;
-                    ok = warp_wait<CG>(&op_full[o], (uint32_t)(it / C::kOps) & 1, q.wait_ns);
+                    ok = warp_wait(&op_full[o], (uint32_t)(it / C::kOps) & 1, q.wait_ns) &&
+                         (CG == 1 || warp_wait<CG>(&pair_full[o], (uint32_t)(it / C::kOps) & 1, q.wait_ns));
                     if (!ok) break;
                     tmem_fence_after();
                     // the descriptor counts addresses in units of 16 bytes
@@ -308,26 +319,42 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                 __syncwarp();
                 if (!ok) warp_wait(&acc_full[a], (uint32_t)(n_seg / C::kAccs) & 1, q.wait_ns);
             }
+        } else {
+            // the second CTA's widened steps, told to the first. By one warp that
+            // wrote nothing itself: an arrival in another CTA that publishes a
+            // warp's own writes takes 1500 cycles, and every warp would pay it.
+            while (ok && todo.next(seg))
+                for (int k = seg.k0; k < seg.k1; ++k, ++it) {
+                    const int o = it % C::kOps;
+                    ok = warp_wait(&op_full[o], (uint32_t)(it / C::kOps) & 1, q.wait_ns);
+                    if (!ok) break;
+                    tmem_fence_after();
+                    tmem_fence_before();
+                    if (lane == 0) mbar_arrive_cluster(cluster_addr(&pair_full[o], 0));
+                    __syncwarp();
+                }
         }
     } else if (warp < kEpiWarp) {
         const bool channels = warp < C::kAWarps;
         // this warp's group takes the steps group, group + groups, ...
-        const int group = channels ? warp / 4 : (warp - C::kAWarps) / 4, groups = channels ? C::kAGroups : C::kBGroups;
-        const int t = tid & 127;  // within the group; for channels the lane of tensor memory
+        const int group = channels ? warp / 4 : (warp - C::kAWarps) / C::kBGroupWarps;
+        const int groups = channels ? C::kAGroups : C::kBGroups;
+        const int t = tid & 127;  // for channels the lane of tensor memory
         const uint32_t lanes = acols + ((uint32_t)(t & 96) << 16);
-        const TokenPlace place(t);
+        using Rows = Tokens<C::kRows, C::kBGroupWarps>;
+        const Rows rows(tid & (32 * C::kBGroupWarps - 1));
         while (ok && todo.next(seg)) {
             const int first = it, n = seg.k1 - seg.k0;
             it += n;
             for (int i = first + (group + groups - first % groups) % groups; i < first + n; i += groups) {
                 const int s = i % C::kSlots, o = i % C::kOps;
                 const unsigned char* slot = smem + s * C::kSlotBytes;
-                uint4 v[8];  // tokens: kRows / 16 of them
-                uint4(&vt)[C::kRows / 16] = reinterpret_cast<uint4(&)[C::kRows / 16]>(v);
+                uint4 v[8];  // tokens: kChunks of them
+                uint4(&vt)[Rows::kChunks] = reinterpret_cast<uint4(&)[Rows::kChunks]>(v);
                 ok = warp_wait(&raw_full[s], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
                 if (!ok) break;
                 if (channels) load_channels(slot, t, v);
-                else load_tokens<C::kRows>(slot + kABytes, place, vt);
+                else rows.load(slot + kABytes, vt);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&raw_empty[s]);
                 ok = i < C::kOps || warp_wait(&op_empty[o], (uint32_t)(i / C::kOps - 1) & 1, q.wait_ns);
@@ -338,14 +365,11 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                     tmem_wait_st();
                     tmem_fence_before();
                 } else {
-                    widen_tokens<C::kRows>(vt, ops + o * C::kOpBytes, place);
+                    rows.widen(vt, ops + o * C::kOpBytes);
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) {
-                    if constexpr (CG == 2) mbar_arrive_cluster(cluster_addr(&op_full[o], 0));
-                    else mbar_arrive(&op_full[o]);
-                }
+                if (lane == 0) mbar_arrive(&op_full[o]);
             }
         }
     } else if (warp < kLoadWarp) {
@@ -379,7 +403,7 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                     tmem_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        if constexpr (CG == 2) mbar_arrive_cluster(cluster_addr(&acc_empty[a], 0));
+                        if constexpr (CG == 2) mbar_arrive_cluster_relaxed(cluster_addr(&acc_empty[a], 0));
                         else mbar_arrive(&acc_empty[a]);
                     }
                 }
