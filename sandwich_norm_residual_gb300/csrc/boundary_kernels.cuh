@@ -19,6 +19,7 @@
 #pragma once
 
 #include "row_sum.cuh"
+#include "status.cuh"
 #include "tma.cuh"
 
 namespace beam {

@@ -88,6 +88,18 @@ bool row_map(CUtensorMap* map, const int8_t* base, int64_t rows_total, int K, in
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// the same for groups of 32 whole rows, taken in the order that the tile kernel's
+// wide stores want: place 8 b + 2 j + e of a group holds row 8 j + 2 b + e
+bool permuted_map(CUtensorMap* map, const int8_t* base, int64_t rows_total, int K) {
+    const EncodeTiled encode = encode_tiled();
+    const cuuint64_t k = (cuuint64_t)K;
+    const cuuint64_t dims[5] = {k, 2, 4, 4, (cuuint64_t)(rows_total / 32)}, strides[4] = {k, 8 * k, 2 * k, 32 * k};
+    const cuuint32_t box[5] = {beam::kStepK, 2, 4, 4, beam::kTileN / 32}, unit[5] = {1, 1, 1, 1, 1};
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<int8_t*>(base), dims, strides, box, unit,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // raises a kernel's shared-memory limit, once on each device
 beam_status allow_smem(const void* fn, size_t bytes, std::atomic<unsigned long long>* done, int device) {
     const unsigned long long bit = 1ull << (device & 63);
@@ -132,15 +144,18 @@ beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* pa
     const void* fn = reinterpret_cast<const void*>(beam::matmul_int8_tile_kernel<NT, CG, F32>);
     beam_status st = allow_smem(fn, C::kSmem, &allowed, dev.ordinal);
     if (st != BEAM_OK) return st;
-    CUtensorMap wmap, amap;
-    if (!row_map(&wmap, p.w, p.N, p.K, beam::kTileN) || !row_map(&amap, p.a, p.M, p.K, C::kRows)) return BEAM_ERR_CUDA;
     beam::MatmulTcParams q{};
     plan<NT, CG>(p, dev.sms < kMaxSms ? dev.sms : kMaxSms, &q);
+    q.wide = !F32 && p.N % 8 == 0 && p.N >= beam::kTileN && !misaligned(p.out, 16);
+    CUtensorMap wmap, pmap, amap;
+    if (!row_map(&wmap, p.w, p.N, p.K, beam::kTileN) || !row_map(&amap, p.a, p.M, p.K, C::kRows)) return BEAM_ERR_CUDA;
+    if (!q.wide) pmap = wmap;
+    else if (!permuted_map(&pmap, p.w, p.N, p.K)) return BEAM_ERR_CUDA;
     q.part = static_cast<float*>(part);
     q.wait_ns = beam::kMatmulWaitNs;
     q.status = dev.status_word;
     const int64_t workers = q.waves ? (q.tiles < q.workers ? q.tiles : q.workers) : q.sharers;
-    void* args[] = {&wmap, &amap, &q};
+    void* args[] = {&wmap, &pmap, &amap, &q};
     st = launch(fn, dim3((unsigned)(workers * CG)), dim3(C::kThreads), args, C::kSmem, stream, pdl, CG);
     const int64_t split = q.sharers ? q.tiles - (int64_t)q.waves * q.workers : 0;
     if (st != BEAM_OK || split == 0 || split == q.sharers) return st;  // none, or each a worker's own

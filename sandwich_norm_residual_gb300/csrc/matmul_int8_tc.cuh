@@ -21,6 +21,7 @@
 #pragma once
 
 #include "matmul_int8.cuh"
+#include "packed.cuh"
 #include "umma.cuh"
 
 namespace beam {
@@ -40,6 +41,9 @@ struct MatmulTcParams {
     // c, c + workers, ... of the first waves * workers, and of the steps of the
     // tiles behind those its share of an even split among the first `sharers`.
     int waves, workers, sharers;
+    // BF16 rows of out start on 16 bytes and end there: whole tiles of 128 channels
+    // are then loaded in the order of `pmap` and stored 16 bytes a thread
+    int wide;
     float* part;              // [workers][2][NT][128]: sums of tiles that a worker has a part of
     uint64_t wait_ns;
     unsigned int* status;
@@ -204,8 +208,8 @@ struct TileConfig {
 // that each CTA widens, and what the matrix unit reads from shared memory.
 template <int NT, int CG, bool F32>
 __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
-    matmul_int8_tile_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
-                            const __grid_constant__ MatmulTcParams q) {
+    matmul_int8_tile_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap pmap,
+                            const __grid_constant__ CUtensorMap amap, const __grid_constant__ MatmulTcParams q) {
     using C = TileConfig<NT, CG>;
     extern __shared__ __align__(1024) unsigned char smem[];
     constexpr int kEpiWarp = C::kAWarps + C::kBWarps, kLoadWarp = kEpiWarp + C::kEpiWarps, kMulWarp = kLoadWarp + 1;
@@ -224,6 +228,11 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
     const int worker = blockIdx.x / CG;
     auto channel0 = [&](const Segment& s) { return ((int)(s.tile / q.m_tiles) * CG + (int)rank) * kTileN; };
     auto token0 = [&](const Segment& s) { return (long long)(s.tile % q.m_tiles) * NT; };
+    // Channels in the order that lets a thread store 8 of them at once (see the
+    // result): lane 8 b + 2 j + e of each 32 holds channel 8 j + 2 b + e
+    auto permuted = [&](const Segment& s) {
+        return !F32 && q.wide && s.k1 - s.k0 == q.steps && channel0(s) + kTileN <= q.p.N;
+    };
 
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
@@ -257,12 +266,14 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
 
     if (warp == kLoadWarp) {
         if (lane == 0) {
-            tma_prefetch_map(&wmap);
+            tma_prefetch_map(!F32 && q.wide ? &pmap : &wmap);
             tma_prefetch_map(&amap);
             const uint64_t pol_w = q.m_tiles == 1 ? l2_evict_first() : l2_evict_normal(), pol_a = l2_evict_normal();
             auto load_w = [&](int slot, const Segment& s, int k) {
                 mbar_arrive_expect_tx(&raw_full[slot], C::kSlotBytes);
-                tma_load_2d(smem + slot * C::kSlotBytes, &wmap, k * kStepK, channel0(s), &raw_full[slot], pol_w);
+                unsigned char* dst = smem + slot * C::kSlotBytes;
+                if (permuted(s)) tma_load_5d(dst, &pmap, k * kStepK, channel0(s) / 32, &raw_full[slot], pol_w);
+                else tma_load_2d(dst, &wmap, k * kStepK, channel0(s), &raw_full[slot], pol_w);
             };
             auto load_a = [&](int slot, const Segment& s, int k) {
                 tma_load_2d(smem + slot * C::kSlotBytes + kABytes, &amap, k * kStepK,
@@ -373,40 +384,80 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
             }
         }
     } else if (warp < kLoadWarp) {
-        // results: lane = channel, column = token
+        // Results: lane = channel, column = token. Rows of out have the channels side
+        // by side, so a warp that stores column by column writes 64 bytes (BF16) an
+        // instruction, and eight instructions a value bounded the whole tile (9 us of
+        // it for 256 x 256). Whole tiles are therefore read as 8 x 8 fragments,
+        // scaled two values an instruction, rounded and transposed in registers;
+        // with the channels' order of the load, thread t then holds the 8 channels
+        // 8 (t % 4) ... of token t / 4 and stores them at once.
         const int t = tid & 127;
         pdl_wait();
         for (; ok && todo.next(seg); ++n_seg) {
-            const int a = n_seg % C::kAccs, n = channel0(seg) + t;
+            const int a = n_seg % C::kAccs, n0 = channel0(seg), n = n0 + t;
             const long long m0 = token0(seg), left = q.p.M - m0;
             const int cols = left < NT ? (int)left : NT;
-            const bool whole = seg.k1 - seg.k0 == q.steps;
+            const bool whole = seg.k1 - seg.k0 == q.steps, wide = permuted(seg);
             float* scales = a_scale + (n_seg & 1) * NT;
-            const float ws = n < q.p.N ? __ldg(q.p.w_scale + n) : 0.0f;
+            float ws[4] = {0.f, 0.f, 0.f, 0.f};
+            if (wide) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    ws[b] = __ldg(q.p.w_scale + n0 + (t & 96) + 8 * ((t >> 3) & 3) + 2 * b + ((t >> 2) & 1));
+            } else if (n < q.p.N) {
+                ws[0] = __ldg(q.p.w_scale + n);
+            }
             for (int c = t; c < cols; c += 128) scales[c] = __ldg(q.p.a_scale + m0 + c);
             // one answer for the four warps, which also meet here: the scales are there
             ok = group_and(1, warp_wait(&acc_full[a], (uint32_t)(n_seg / C::kAccs) & 1, q.wait_ns));
             if (!ok) break;
             tmem_fence_after();
+            auto free_acc = [&] {  // this warp has read the accumulator
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 2) mbar_arrive_cluster_relaxed(cluster_addr(&acc_empty[a], 0));
+                    else mbar_arrive(&acc_empty[a]);
+                }
+            };
+            const uint32_t from = acc + a * C::kAccCols + ((uint32_t)(t & 96) << 16);
+            if (wide) {
+                uint16_t* row = static_cast<uint16_t*>(q.p.out) + (size_t)(m0 + (lane >> 2)) * (size_t)q.p.N +
+                                (size_t)(n0 + (t & 96) + 8 * (lane & 3));
+                for (int c0 = 0; c0 < cols; c0 += 16) {
+                    float v[2][8];  // lanes 0-15 and 16-31 of the warp's 32
+                    tmem_ld_16x256b(from + c0, v[0]);
+                    tmem_ld_16x256b(from + (16u << 16) + c0, v[1]);
+                    tmem_wait_ld();
+                    if (c0 + 16 >= cols) free_acc();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 as = *reinterpret_cast<const float2*>(scales + c0 + 8 * i + 2 * (lane & 3));
+                        uint32_t o[4];
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const float* f = v[b >> 1] + 4 * i + 2 * (b & 1);
+                            o[b] = transpose_b16(
+                                f2_to_bf2(mul2_rn(mul2_rn(make_float2(f[0], f[1]), as), make_float2(ws[b], ws[b]))));
+                        }
+                        if (c0 + 8 * i + (lane >> 2) < cols)
+                            *reinterpret_cast<uint4*>(row) = make_uint4(o[0], o[1], o[2], o[3]);
+                        row += 8 * (size_t)q.p.N;
+                    }
+                }
+                continue;
+            }
             // the first of this worker's split tiles goes to its part 0, the last to part 1
             const bool second = seg.k0 == 0;
             float* part = q.part + ((size_t)worker * 2 + second) * (size_t)(NT * kTileN) + t;
             const size_t at = (size_t)m0 * (size_t)q.p.N + (size_t)n;
-            const uint32_t from = acc + a * C::kAccCols + ((uint32_t)(t & 96) << 16);
             constexpr int kBatch = NT < 32 ? 16 : 32;
             for (int c0 = 0; c0 < cols; c0 += kBatch) {
                 float v[kBatch];
                 if constexpr (kBatch == 16) tmem_ld16(from + c0, v);
                 else tmem_ld32(from + c0, v);
                 tmem_wait_ld();
-                if (c0 + kBatch >= cols) {  // all read: the accumulator is free
-                    tmem_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (CG == 2) mbar_arrive_cluster_relaxed(cluster_addr(&acc_empty[a], 0));
-                        else mbar_arrive(&acc_empty[a]);
-                    }
-                }
+                if (c0 + kBatch >= cols) free_acc();
                 if (!whole) {
 #pragma unroll
                     for (int c = 0; c < kBatch; ++c)
@@ -416,7 +467,7 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                     for (int c = 0; c < kBatch; ++c)
                         if (c0 + c < cols)
                             store_out<F32>(q.p.out, at + (size_t)(c0 + c) * (size_t)q.p.N,
-                                           __fmul_rn(__fmul_rn(v[c], scales[c0 + c]), ws));
+                                           __fmul_rn(__fmul_rn(v[c], scales[c0 + c]), ws[0]));
                 }
             }
         }

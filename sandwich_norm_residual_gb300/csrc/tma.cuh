@@ -47,8 +47,6 @@ __device__ __forceinline__ void prefetch_l2_keep(const void* p, uint32_t bytes) 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-__device__ unsigned int g_status_word;  // bit 0: a bounded wait gave up
-
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -100,7 +98,5 @@ __device__ __forceinline__ void bulk_load(void* dst_smem, const void* src, uint3
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
         :: "r"(smem_u32(dst_smem)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
 }
-
-__device__ __forceinline__ void report_timeout() { atomicOr(&g_status_word, 1u); }
 
 }  // namespace beam

@@ -69,6 +69,23 @@ __device__ __forceinline__ void tmem_ld16(uint32_t at, float (&r)[16]) {
         : "r"(at) : "memory");
 }
 
+// 16 lanes from `at` on by 8 X columns, as fragments: thread t gets, for each 8
+// columns, r[4 i + 0, 1] of lane t / 4 and r[4 i + 2, 3] of lane t / 4 + 8, at the
+// columns 2 (t % 4) and the next
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t at, float (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(at) : "memory");
+}
+
+// transposes the 8 x 8 matrix of 16-bit values that a warp holds, thread t two
+// of row t / 4
+__device__ __forceinline__ uint32_t transpose_b16(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 // ---------------------------------------------------------------- matrix instruction
 
 // kind::f16: FP16 operands, K-major both, FP32 accumulators; M rows of A (in
@@ -195,6 +212,13 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
         "[%0], [%1, {%2, %3}], [%4], %5;"
         :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy) : "memory");
+}
+// the same for a 5-D tensor, at x in the first and y in the last dimension
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %6, %6, %6, %3}], [%4], %5;"
+        :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy), "r"(0) : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");

@@ -54,7 +54,7 @@ SHAPES = [
     # several tiles in both directions, ragged in each
     (257, 255, 640), (517, 2565, 2576), (300, 4096, 256), (1000, 777, 336), (2048, 2048, 5120),
     # enough tiles for pairs of CTAs: one ragged wave, and several
-    (2100, 2600, 400), (4100, 5000, 144),
+    (2100, 2600, 400), (4100, 5000, 144), (2048, 2570, 256), (2500, 3333, 160),
 ]
 
 
