@@ -173,8 +173,12 @@ struct TileConfig {
     // warps in groups: a group widens the channels, another the tokens of a step
     static constexpr int kAGroups = 2, kBGroupWarps = kRows <= 32 ? 1 : 4, kBGroups = kRows <= 32 ? 4 : 2;
     static constexpr int kAWarps = 4 * kAGroups, kBWarps = kBGroupWarps * kBGroups, kEpiWarps = 4;
+    // A loading warp needs 0.3 us a copy (wait, announce, issue), where a step's
+    // weights take 0.37 us from HBM: two take the steps in turn, and for few tokens
+    // two more copy the tokens (one for both: 0.58 us a step)
+    static constexpr int kLoadWarps = NT <= 32 ? 4 : 2;
     // whole fours of warps: the schedulers' register files are separate
-    static constexpr int kThreads = 32 * (kAWarps + kBWarps + kEpiWarps + 4);
+    static constexpr int kThreads = 32 * ((kAWarps + kBWarps + kEpiWarps + kLoadWarps + 1 + 3) / 4 * 4);
     // A wait by parity passes at once on a barrier whose phase before has not even
     // ended, so a group must know that it has. Before step j it has seen the
     // product of step j - groups - kOps end, and all before: enough for the slot's
@@ -184,6 +188,7 @@ struct TileConfig {
         return (kSlots % groups == 0 || kSlots >= groups + kOps) && (kOps % groups == 0 || kOps >= groups);
     }
     static_assert(safe(kAGroups) && safe(kBGroups), "a group could read a slot before it is filled");
+    static_assert(kSlots % 2 == 0, "a slot is always filled by the same loading warps");
     static constexpr uint32_t kSlotBytes = kABytes + kRows * kStepK;
     static constexpr uint32_t kOpBytes = kRows * kStepK * 2;
     static constexpr uint32_t kScaleAt = kSlots * kSlotBytes + kOps * kOpBytes;    // FP32 [2][NT]
@@ -212,7 +217,7 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                             const __grid_constant__ CUtensorMap amap, const __grid_constant__ MatmulTcParams q) {
     using C = TileConfig<NT, CG>;
     extern __shared__ __align__(1024) unsigned char smem[];
-    constexpr int kEpiWarp = C::kAWarps + C::kBWarps, kLoadWarp = kEpiWarp + C::kEpiWarps, kMulWarp = kLoadWarp + 1;
+    constexpr int kEpiWarp = C::kAWarps + C::kBWarps, kLoadWarp = kEpiWarp + C::kEpiWarps, kMulWarp = kLoadWarp + C::kLoadWarps;
     unsigned char* ops = smem + C::kSlots * C::kSlotBytes;
     float* a_scale = reinterpret_cast<float*>(smem + C::kScaleAt);
     uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::kBarAt);  // a slot's int8 tiles have landed
@@ -236,7 +241,7 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
-            mbar_init(&raw_full[i], 1);
+            mbar_init(&raw_full[i], C::kLoadWarps / 2);
             mbar_init(&raw_empty[i], 4 + C::kBGroupWarps);  // the warps of a group each for channels and tokens
         }
         for (int i = 0; i < C::kOps; ++i) {
@@ -264,13 +269,16 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
     Segment seg;
     int it = 0, n_seg = 0;  // steps and segments so far
 
-    if (warp == kLoadWarp) {
+    if (warp >= kLoadWarp && warp < kMulWarp) {
         if (lane == 0) {
-            tma_prefetch_map(!F32 && q.wide ? &pmap : &wmap);
-            tma_prefetch_map(&amap);
+            // this warp's part: every second step, channels, tokens or both
+            const int mine = (warp - kLoadWarp) & 1;
+            const bool both = C::kLoadWarps == 2, w_side = both || warp - kLoadWarp < 2, a_side = both || !w_side;
+            const uint32_t bytes = (w_side ? kABytes : 0u) + (a_side ? C::kRows * kStepK : 0u);
+            if (w_side) tma_prefetch_map(!F32 && q.wide ? &pmap : &wmap);
+            if (a_side) tma_prefetch_map(&amap);
             const uint64_t pol_w = q.m_tiles == 1 ? l2_evict_first() : l2_evict_normal(), pol_a = l2_evict_normal();
             auto load_w = [&](int slot, const Segment& s, int k) {
-                mbar_arrive_expect_tx(&raw_full[slot], C::kSlotBytes);
                 unsigned char* dst = smem + slot * C::kSlotBytes;
                 if (permuted(s)) tma_load_5d(dst, &pmap, k * kStepK, channel0(s) / 32, &raw_full[slot], pol_w);
                 else tma_load_2d(dst, &wmap, k * kStepK, channel0(s), &raw_full[slot], pol_w);
@@ -281,23 +289,32 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
             };
             // the weights do not depend on the kernel before: the first slots' are
             // asked for ahead of the wait for it
-            Schedule head(q, worker);
-            for (int i = 0; i < C::kSlots && head.next(seg);)
-                for (int k = seg.k0; k < seg.k1 && i < C::kSlots; ++k, ++i) load_w(i, seg, k);
+            if (w_side) {
+                Schedule head(q, worker);
+                for (int i = 0; i < C::kSlots && head.next(seg);)
+                    for (int k = seg.k0; k < seg.k1 && i < C::kSlots; ++k, ++i)
+                        if ((i & 1) == mine) {
+                            mbar_arrive_expect_tx(&raw_full[i], bytes);
+                            load_w(i, seg, k);
+                        }
+            }
             pdl_wait();
             while (ok && todo.next(seg))
                 for (int k = seg.k0; k < seg.k1; ++k, ++it) {
+                    if ((it & 1) != mine) continue;
                     const int slot = it % C::kSlots;
                     if (it >= C::kSlots) {
                         ok = mbar_wait(&raw_empty[slot], (uint32_t)(it / C::kSlots - 1) & 1, q.wait_ns);
                         if (!ok) break;
-                        load_w(slot, seg, k);
                     }
-                    load_a(slot, seg, k);
+                    if (it >= C::kSlots || !w_side) mbar_arrive_expect_tx(&raw_full[slot], bytes);
+                    if (it >= C::kSlots && w_side) load_w(slot, seg, k);
+                    if (a_side) load_a(slot, seg, k);
                 }
             if (!ok)  // copies in flight must land before the shared memory goes
                 for (int i = it - C::kSlots; i < it; ++i)
-                    mbar_wait(&raw_full[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
+                    if ((i & 1) == mine)
+                        mbar_wait(&raw_full[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
         }
     } else if (warp == kMulWarp) {
         if (rank == 0) {
