@@ -116,20 +116,20 @@ beam_status allow_smem(const void* fn, size_t bytes, std::atomic<unsigned long l
 template <int NT, int CG>
 void plan(const MatmulParams& p, int sms, beam::MatmulTcParams* q) {
     q->p = p;
-    q->m_tiles = (int)((p.M + NT - 1) / NT);
-    q->steps = (p.K + beam::kStepK - 1) / beam::kStepK;
-    q->tiles = (int64_t)q->m_tiles * ((p.N + beam::kTileN * CG - 1) / (beam::kTileN * CG));
-    q->workers = sms / CG;
+    q->m_tiles = (uint32_t)((p.M + NT - 1) / NT);
+    q->steps = (uint32_t)((p.K + beam::kStepK - 1) / beam::kStepK);
+    q->tiles = q->m_tiles * (uint32_t)((p.N + beam::kTileN * CG - 1) / (beam::kTileN * CG));
+    q->workers = (uint32_t)(sms / CG);
     if (CG == 2) {
-        q->waves = (int)((q->tiles + q->workers - 1) / q->workers);
-        q->sharers = 0;
+        q->waves = (q->tiles + q->workers - 1) / q->workers;
+        q->sharers = q->split = 0;
         return;
     }
     // the tiles behind the last full wave are shared, with four steps a worker at least
-    q->waves = (int)(q->tiles / q->workers);
-    const int64_t shared = (q->tiles - (int64_t)q->waves * q->workers) * q->steps;
-    const int64_t most = (shared + 3) / 4;
-    q->sharers = (int)(most < q->workers ? most : q->workers);
+    q->waves = q->tiles / q->workers;
+    q->split = (q->tiles - q->waves * q->workers) * q->steps;
+    const uint32_t most = (q->split + 3) / 4;
+    q->sharers = most < q->workers ? most : q->workers;
 }
 
 template <int NT>
@@ -154,13 +154,13 @@ beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* pa
     q.part = static_cast<float*>(part);
     q.wait_ns = beam::kMatmulWaitNs;
     q.status = dev.status_word;
-    const int64_t workers = q.waves ? (q.tiles < q.workers ? q.tiles : q.workers) : q.sharers;
+    const uint32_t workers = q.waves ? (q.tiles < q.workers ? q.tiles : q.workers) : q.sharers;
     void* args[] = {&wmap, &pmap, &amap, &q};
-    st = launch(fn, dim3((unsigned)(workers * CG)), dim3(C::kThreads), args, C::kSmem, stream, pdl, CG);
-    const int64_t split = q.sharers ? q.tiles - (int64_t)q.waves * q.workers : 0;
-    if (st != BEAM_OK || split == 0 || split == q.sharers) return st;  // none, or each a worker's own
+    st = launch(fn, dim3(workers * CG), dim3(C::kThreads), args, C::kSmem, stream, pdl, CG);
+    const uint32_t shared = q.split / q.steps;
+    if (st != BEAM_OK || shared == 0 || shared == q.sharers) return st;  // none, or each a worker's own
     void* join_args[] = {&q};
-    return launch(reinterpret_cast<const void*>(beam::matmul_int8_join_kernel<NT, F32>), dim3((unsigned)split, NT / 8),
+    return launch(reinterpret_cast<const void*>(beam::matmul_int8_join_kernel<NT, F32>), dim3(shared, NT / 8),
                   dim3(beam::kTileN), join_args, 0, stream, true);
 }
 
@@ -189,7 +189,9 @@ beam_status launch_tiles(Shape shape, const MatmulParams& p, const beam::Device&
 }
 
 bool bad_shape(int64_t M, int N, int K) {
-    return M < 0 || M > 0x7FFFFFFF || N < 0 || K < 16 || (K & 15) || K > BEAM_MATMUL_MAX_K;
+    // the last: tiles are counted in 32 bits (out would have 2^46 elements)
+    return M < 0 || M > 0x7FFFFFFF || N < 0 || K < 16 || (K & 15) || K > BEAM_MATMUL_MAX_K ||
+           ((M + 127) / 128) * ((N + 127ll) / 128) > 0x7FFFFFFF;
 }
 
 }  // namespace

@@ -34,13 +34,14 @@ constexpr uint64_t kMatmulWaitNs = 2000000000ull;   // every wait gives up after
 
 struct MatmulTcParams {
     MatmulParams p;
-    int m_tiles;              // tiles of NT tokens
-    int steps;                // of k
-    long long tiles;
+    uint32_t m_tiles;         // tiles of NT tokens
+    uint32_t steps;           // of k
+    uint32_t tiles;
     // `workers` CTAs (CG = 1) or pairs (CG = 2). Worker c takes the whole tiles
-    // c, c + workers, ... of the first waves * workers, and of the steps of the
-    // tiles behind those its share of an even split among the first `sharers`.
-    int waves, workers, sharers;
+    // c, c + workers, ... of the first waves * workers, and of the `split` steps of
+    // the tiles behind those its share of an even split among the first `sharers`
+    // (split * sharers < 2^32: fewer than 152 tiles of at most 512 steps).
+    uint32_t waves, workers, sharers, split;
     // BF16 rows of out start on 16 bytes and end there: whole tiles of 128 channels
     // are then loaded in the order of `pmap` and stored 16 bytes a thread
     int wide;
@@ -49,36 +50,48 @@ struct MatmulTcParams {
     unsigned int* status;
 };
 
-// What a worker does, in order: segments of a tile's steps [k0, k1)
+// What a worker does, in order: steps [k0, k1) of the tile at channel n0 (of the
+// CTA's own 128) and token m0
 struct Segment {
-    long long tile;
-    int k0, k1;
+    int n0, m0;
+    uint32_t k0, k1;
+    bool whole;
 };
 
+template <int NT, int CG>
 class Schedule {
     const MatmulTcParams& q;
-    const int worker;
-    int wave = 0;
-    long long at, end;  // steps of the split tiles, counted from the first of them
+    const uint32_t worker, rank;
+    uint32_t wave = 0, at = 0, end = 0;  // at, end: of the split steps
+
+    __device__ void place(Segment& s, uint32_t tile) const {
+        s.n0 = (int)((tile / q.m_tiles * CG + rank) * kTileN);
+        s.m0 = (int)(tile % q.m_tiles * NT);
+    }
 
 public:
-    __device__ Schedule(const MatmulTcParams& q_, int worker_) : q(q_), worker(worker_) {
-        const long long total = (q.tiles - (long long)q.waves * q.workers) * q.steps;
-        const bool shares = worker < q.sharers && total > 0;
-        at = shares ? total * worker / q.sharers : 0;
-        end = shares ? total * (worker + 1) / q.sharers : 0;
+    __device__ Schedule(const MatmulTcParams& q_, uint32_t worker_, uint32_t rank_) : q(q_), worker(worker_), rank(rank_) {
+        if (worker < q.sharers) {
+            at = q.split * worker / q.sharers;
+            end = q.split * (worker + 1) / q.sharers;
+        }
     }
     __device__ bool next(Segment& s) {
         if (wave < q.waves) {
-            s.tile = (long long)wave++ * q.workers + worker;
+            const uint32_t tile = wave++ * q.workers + worker;
+            if (tile >= q.tiles) return false;
+            place(s, tile);
             s.k0 = 0;
             s.k1 = q.steps;
-            return s.tile < q.tiles;
+            s.whole = true;
+            return true;
         }
         if (at >= end) return false;
-        s.tile = (long long)q.waves * q.workers + at / q.steps;
-        s.k0 = (int)(at % q.steps);
-        s.k1 = (int)min((long long)q.steps, s.k0 + (end - at));
+        const uint32_t t = at / q.steps;
+        place(s, q.waves * q.workers + t);
+        s.k0 = at - t * q.steps;
+        s.k1 = min(q.steps, s.k0 + (end - at));
+        s.whole = s.k1 - s.k0 == q.steps;
         at += s.k1 - s.k0;
         return true;
     }
@@ -230,13 +243,11 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pair_full + (CG - 1) * C::kOps);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
-    const int worker = blockIdx.x / CG;
-    auto channel0 = [&](const Segment& s) { return ((int)(s.tile / q.m_tiles) * CG + (int)rank) * kTileN; };
-    auto token0 = [&](const Segment& s) { return (long long)(s.tile % q.m_tiles) * NT; };
+    const uint32_t worker = blockIdx.x / CG;
     // Channels in the order that lets a thread store 8 of them at once (see the
     // result): lane 8 b + 2 j + e of each 32 holds channel 8 j + 2 b + e
     auto permuted = [&](const Segment& s) {
-        return !F32 && q.wide && s.k1 - s.k0 == q.steps && channel0(s) + kTileN <= q.p.N;
+        return !F32 && q.wide && s.whole && s.n0 + kTileN <= q.p.N;
     };
 
     if (tid == 0) {
@@ -265,7 +276,7 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
     pdl_trigger();
     const uint32_t acc = *tmem_slot, acols = acc + C::kAccs * C::kAccCols;
     bool ok = true;
-    Schedule todo(q, worker);
+    Schedule<NT, CG> todo(q, worker, rank);
     Segment seg;
     int it = 0, n_seg = 0;  // steps and segments so far
 
@@ -280,27 +291,27 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
             const uint64_t pol_w = q.m_tiles == 1 ? l2_evict_first() : l2_evict_normal(), pol_a = l2_evict_normal();
             auto load_w = [&](int slot, const Segment& s, int k) {
                 unsigned char* dst = smem + slot * C::kSlotBytes;
-                if (permuted(s)) tma_load_5d(dst, &pmap, k * kStepK, channel0(s) / 32, &raw_full[slot], pol_w);
-                else tma_load_2d(dst, &wmap, k * kStepK, channel0(s), &raw_full[slot], pol_w);
+                if (permuted(s)) tma_load_5d(dst, &pmap, k * kStepK, s.n0 / 32, &raw_full[slot], pol_w);
+                else tma_load_2d(dst, &wmap, k * kStepK, s.n0, &raw_full[slot], pol_w);
             };
             auto load_a = [&](int slot, const Segment& s, int k) {
                 tma_load_2d(smem + slot * C::kSlotBytes + kABytes, &amap, k * kStepK,
-                            (int)token0(s) + (int)rank * C::kRows, &raw_full[slot], pol_a);
+                            s.m0 + (int)rank * C::kRows, &raw_full[slot], pol_a);
             };
             // the weights do not depend on the kernel before: the first slots' are
             // asked for ahead of the wait for it
             if (w_side) {
-                Schedule head(q, worker);
+                Schedule<NT, CG> head(q, worker, rank);
                 for (int i = 0; i < C::kSlots && head.next(seg);)
-                    for (int k = seg.k0; k < seg.k1 && i < C::kSlots; ++k, ++i)
+                    for (uint32_t k = seg.k0; k < seg.k1 && i < C::kSlots; ++k, ++i)
                         if ((i & 1) == mine) {
                             mbar_arrive_expect_tx(&raw_full[i], bytes);
-                            load_w(i, seg, k);
+                            load_w(i, seg, (int)k);
                         }
             }
             pdl_wait();
             while (ok && todo.next(seg))
-                for (int k = seg.k0; k < seg.k1; ++k, ++it) {
+                for (uint32_t k = seg.k0; k < seg.k1; ++k, ++it) {
                     if ((it & 1) != mine) continue;
                     const int slot = it % C::kSlots;
                     if (it >= C::kSlots) {
@@ -308,8 +319,8 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                         if (!ok) break;
                     }
                     if (it >= C::kSlots || !w_side) mbar_arrive_expect_tx(&raw_full[slot], bytes);
-                    if (it >= C::kSlots && w_side) load_w(slot, seg, k);
-                    if (a_side) load_a(slot, seg, k);
+                    if (it >= C::kSlots && w_side) load_w(slot, seg, (int)k);
+                    if (a_side) load_a(slot, seg, (int)k);
                 }
             if (!ok)  // copies in flight must land before the shared memory goes
                 for (int i = it - C::kSlots; i < it; ++i)
@@ -325,7 +336,7 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                 const uint32_t d = acc + a * C::kAccCols;
                 if (n_seg >= C::kAccs)
                     ok = warp_wait<CG>(&acc_empty[a], (uint32_t)(n_seg / C::kAccs - 1) & 1, q.wait_ns);
-                for (int k = seg.k0; ok && k < seg.k1; ++k, ++it) {
+                for (uint32_t k = seg.k0; ok && k < seg.k1; ++k, ++it) {
                     const int o = it % C::kOps;
                     ok = warp_wait(&op_full[o], (uint32_t)(it / C::kOps) & 1, q.wait_ns) &&
                          (CG == 1 || warp_wait<CG>(&pair_full[o], (uint32_t)(it / C::kOps) & 1, q.wait_ns));
@@ -352,7 +363,7 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
             // wrote nothing itself: an arrival in another CTA that publishes a
             // warp's own writes takes 1500 cycles, and every warp would pay it.
             while (ok && todo.next(seg))
-                for (int k = seg.k0; k < seg.k1; ++k, ++it) {
+                for (uint32_t k = seg.k0; k < seg.k1; ++k, ++it) {
                     const int o = it % C::kOps;
                     ok = warp_wait(&op_full[o], (uint32_t)(it / C::kOps) & 1, q.wait_ns);
                     if (!ok) break;
@@ -372,7 +383,7 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
         using Rows = Tokens<C::kRows, C::kBGroupWarps>;
         const Rows rows(tid & (32 * C::kBGroupWarps - 1));
         while (ok && todo.next(seg)) {
-            const int first = it, n = seg.k1 - seg.k0;
+            const int first = it, n = (int)(seg.k1 - seg.k0);
             it += n;
             for (int i = first + (group + groups - first % groups) % groups; i < first + n; i += groups) {
                 const int s = i % C::kSlots, o = i % C::kOps;
@@ -411,10 +422,9 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
         const int t = tid & 127;
         pdl_wait();
         for (; ok && todo.next(seg); ++n_seg) {
-            const int a = n_seg % C::kAccs, n0 = channel0(seg), n = n0 + t;
-            const long long m0 = token0(seg), left = q.p.M - m0;
-            const int cols = left < NT ? (int)left : NT;
-            const bool whole = seg.k1 - seg.k0 == q.steps, wide = permuted(seg);
+            const int a = n_seg % C::kAccs, n0 = seg.n0, n = n0 + t, m0 = seg.m0;
+            const int cols = (int)min(q.p.M - m0, (long long)NT);
+            const bool wide = permuted(seg);
             float* scales = a_scale + (n_seg & 1) * NT;
             float ws[4] = {0.f, 0.f, 0.f, 0.f};
             if (wide) {
@@ -475,7 +485,7 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                 else tmem_ld32(from + c0, v);
                 tmem_wait_ld();
                 if (c0 + kBatch >= cols) free_acc();
-                if (!whole) {
+                if (!seg.whole) {
 #pragma unroll
                     for (int c = 0; c < kBatch; ++c)
                         if (c0 + c < cols) part[(c0 + c) * kTileN] = v[c];
@@ -506,20 +516,20 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
 template <int NT, bool F32>
 __global__ void __launch_bounds__(kTileN) matmul_int8_join_kernel(const __grid_constant__ MatmulTcParams q) {
     pdl_trigger();
-    const long long split = blockIdx.x, tile = (long long)q.waves * q.workers + split;
-    const int n = (int)(tile / q.m_tiles) * kTileN + threadIdx.x;
-    const long long m0 = (tile % q.m_tiles) * NT + blockIdx.y * 8;
-    // worker c has the steps [total c / sharers, total (c + 1) / sharers)
-    const long long total = (q.tiles - (long long)q.waves * q.workers) * q.steps;
-    const long long lo = split * q.steps, hi = lo + q.steps;
-    int c0 = (int)(lo * q.sharers / total);
-    while (total * (c0 + 1) / q.sharers <= lo) ++c0;
+    const uint32_t tile = q.waves * q.workers + blockIdx.x;
+    const int n = (int)(tile / q.m_tiles * kTileN + threadIdx.x);
+    const long long m0 = (long long)(tile % q.m_tiles) * NT + blockIdx.y * 8;
+    // worker c has the steps [split c / sharers, split (c + 1) / sharers)
+    const uint32_t lo = blockIdx.x * q.steps, hi = lo + q.steps;
+    uint32_t c = lo * q.sharers / q.split;
+    while (q.split * (c + 1) / q.sharers <= lo) ++c;
+    uint32_t begin = q.split * c / q.sharers;
     pdl_wait();
-    if (total * c0 / q.sharers <= lo && total * (c0 + 1) / q.sharers >= hi) return;  // one worker's: stored already
+    if (begin <= lo && q.split * (c + 1) / q.sharers >= hi) return;  // one worker's: stored already
     if (n >= q.p.N) return;
     int sum[8] = {};
-    for (int c = c0; c < q.sharers && total * c / q.sharers < hi; ++c) {
-        const bool second = total * c / q.sharers <= lo;  // its segment of this tile begins at the tile's first step
+    for (; begin < hi; begin = q.split * ++c / q.sharers) {
+        const bool second = begin <= lo;  // its segment of this tile begins at the tile's first step
         const float* part = q.part + ((size_t)c * 2 + second) * (size_t)(NT * kTileN) + (size_t)blockIdx.y * 8 * kTileN +
                             threadIdx.x;
 #pragma unroll
