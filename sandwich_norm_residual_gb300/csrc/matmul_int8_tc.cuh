@@ -206,7 +206,7 @@ struct TileConfig {
     static constexpr uint32_t kOpBytes = kRows * kStepK * 2;
     static constexpr uint32_t kScaleAt = kSlots * kSlotBytes + kOps * kOpBytes;    // FP32 [2][NT]
     static constexpr uint32_t kBarAt = kScaleAt + 2 * NT * 4;
-    static constexpr uint32_t kSmem = kBarAt + (2 * kSlots + (1 + CG) * kOps + 2 * kAccs + 1) * 8;
+    static constexpr uint32_t kSmem = kBarAt + (2 * kSlots + 2 * kOps + 2 * kAccs + 1) * 8;
     static_assert(kAccs * kAccCols + kOps * kStepCols <= 512, "tensor memory has 512 columns");
     static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
@@ -235,12 +235,11 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
     float* a_scale = reinterpret_cast<float*>(smem + C::kScaleAt);
     uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::kBarAt);  // a slot's int8 tiles have landed
     uint64_t* raw_empty = raw_full + C::kSlots;                         // ... have been read
-    uint64_t* op_full = raw_empty + C::kSlots;                          // a step is widened (in this CTA)
+    uint64_t* op_full = raw_empty + C::kSlots;                          // a step is widened (in both CTAs)
     uint64_t* op_empty = op_full + C::kOps;                             // ... is multiplied
     uint64_t* acc_full = op_empty + C::kOps;                            // a segment's sums are complete
     uint64_t* acc_empty = acc_full + C::kAccs;                          // ... are read (in both CTAs)
-    uint64_t* pair_full = acc_empty + C::kAccs;                         // (CG = 2, rank 0) ... widened in the other CTA
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pair_full + (CG - 1) * C::kOps);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + C::kAccs);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
     const uint32_t worker = blockIdx.x / CG;
@@ -256,9 +255,8 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
             mbar_init(&raw_empty[i], 4 + C::kBGroupWarps);  // the warps of a group each for channels and tokens
         }
         for (int i = 0; i < C::kOps; ++i) {
-            mbar_init(&op_full[i], 4 + C::kBGroupWarps);
+            mbar_init(&op_full[i], (4 + C::kBGroupWarps) * CG);
             mbar_init(&op_empty[i], 1);
-            if (CG == 2) mbar_init(&pair_full[i], 1);
         }
         for (int i = 0; i < C::kAccs; ++i) {
             mbar_init(&acc_full[i], 1);
@@ -338,8 +336,7 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                     ok = warp_wait<CG>(&acc_empty[a], (uint32_t)(n_seg / C::kAccs - 1) & 1, q.wait_ns);
                 for (uint32_t k = seg.k0; ok && k < seg.k1; ++k, ++it) {
                     const int o = it % C::kOps;
-                    ok = warp_wait(&op_full[o], (uint32_t)(it / C::kOps) & 1, q.wait_ns) &&
-                         (CG == 1 || warp_wait<CG>(&pair_full[o], (uint32_t)(it / C::kOps) & 1, q.wait_ns));
+                    ok = warp_wait<CG>(&op_full[o], (uint32_t)(it / C::kOps) & 1, q.wait_ns);
                     if (!ok) break;
                     tmem_fence_after();
                     // the descriptor counts addresses in units of 16 bytes
@@ -358,20 +355,6 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                 __syncwarp();
                 if (!ok) warp_wait(&acc_full[a], (uint32_t)(n_seg / C::kAccs) & 1, q.wait_ns);
             }
-        } else {
-            // the second CTA's widened steps, told to the first. By one warp that
-            // wrote nothing itself: an arrival in another CTA that publishes a
-            // warp's own writes takes 1500 cycles, and every warp would pay it.
-            while (ok && todo.next(seg))
-                for (uint32_t k = seg.k0; k < seg.k1; ++k, ++it) {
-                    const int o = it % C::kOps;
-                    ok = warp_wait(&op_full[o], (uint32_t)(it / C::kOps) & 1, q.wait_ns);
-                    if (!ok) break;
-                    tmem_fence_after();
-                    tmem_fence_before();
-                    if (lane == 0) mbar_arrive_cluster(cluster_addr(&pair_full[o], 0));
-                    __syncwarp();
-                }
         }
     } else if (warp < kEpiWarp) {
         const bool channels = warp < C::kAWarps;
@@ -408,7 +391,10 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&op_full[o]);
+                if (lane == 0) {
+                    if constexpr (CG == 2) mbar_arrive_cluster(cluster_addr(&op_full[o], 0));
+                    else mbar_arrive(&op_full[o]);
+                }
             }
         }
     } else if (warp < kLoadWarp) {
