@@ -11,6 +11,7 @@ fallback: without the built library, calls raise ``ImportError``.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import _lib
 from ._lib import LaunchOpts  # noqa: F401
@@ -74,6 +75,42 @@ def _on_current_device(**tensors):
     if dev.index != cur:
         raise ValueError(f"operands are on {dev} but the current device is cuda:{cur}: "
                          f"call under `with torch.cuda.device({dev.index}):`")
+
+
+_torch = None
+
+
+def _dims(t, n: int):
+    """The shape of an n-d tensor, or n times -1 (which no operand has) for anything else."""
+    shape = getattr(t, "shape", ())
+    return shape if len(shape) == n else (-1,) * n
+
+
+def _ready(*operands) -> bool:
+    """Whether every (tensor, dtype, shape) is as said, contiguous and on the current CUDA
+    device. The calls whose kernels take microseconds ask this first, in one cheap pass, and
+    look for what is wrong only when it says no."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    Tensor, dev = _torch.Tensor, None
+    for t, dtype, shape in operands:
+        if not (isinstance(t, Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+            return False
+        d = t.get_device()
+        if dev is None:
+            dev = d
+        if d != dev or d < 0:
+            return False
+    return dev == _torch.cuda.current_device()
+
+
+def _raw_stream(stream, t) -> int | None:
+    """The stream's handle, without a stream object for the current one."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(t.get_device()) or None
+    return stream.cuda_stream or None
 
 
 def _workspace(nbytes: int, device, stream):
@@ -326,19 +363,25 @@ def boundary_fused_int8(h, x, post_w, pre_w, n: int, eps: float = 1e-6, y_int8=N
     """Dense boundary with y as int8 and one FP32 scale per token; updates h in place,
     returns (y_int8 [T, D] int8, y_scale [T] float32), the operands of ``matmul_int8``."""
     import torch
-    for t, name in ((h, "h"), (x, "x")):
-        _check(t, name, torch.bfloat16, 2)
-    _check(post_w, "post_w", torch.bfloat16, 1)
-    _check(pre_w, "pre_w", torch.bfloat16, 1)
-    T, D = h.shape
-    if x.shape != h.shape or post_w.shape[0] != D or pre_w.shape[0] != D:
-        raise ValueError("shape mismatch: h, x [T, D]; post_w, pre_w [D]")
-    q, scale = _int8_out(h, y_int8, y_scale)
-    _on_current_device(h=h, x=x, post_w=post_w, pre_w=pre_w, y_int8=q, y_scale=scale)
-    st = _lib.load().beam_boundary_fused_int8(_stream_ptr(stream), h.data_ptr(), x.data_ptr(),
-                                              post_w.data_ptr(), pre_w.data_ptr(), int(n),
-                                              float(eps), T, D, q.data_ptr(), scale.data_ptr(),
-                                              _opts(opts))
+    bf16 = torch.bfloat16
+    T, D = rows = _dims(h, 2)
+    ready = _ready((h, bf16, rows), (x, bf16, rows), (post_w, bf16, (D,)), (pre_w, bf16, (D,)))
+    if not ready:
+        for t, name in ((h, "h"), (x, "x")):
+            _check(t, name, bf16, 2)
+        _check(post_w, "post_w", bf16, 1)
+        _check(pre_w, "pre_w", bf16, 1)
+        if x.shape != h.shape or post_w.shape[0] != D or pre_w.shape[0] != D:
+            raise ValueError("shape mismatch: h, x [T, D]; post_w, pre_w [D]")
+    if not ready or y_int8 is not None or y_scale is not None:
+        q, scale = _int8_out(h, y_int8, y_scale)
+        _on_current_device(h=h, x=x, post_w=post_w, pre_w=pre_w, y_int8=q, y_scale=scale)
+    else:
+        q = torch.empty(rows, dtype=torch.int8, device=h.device)
+        scale = torch.empty(T, dtype=torch.float32, device=h.device)
+    st = _lib.load().beam_boundary_fused_int8(_raw_stream(stream, h), h.data_ptr(), x.data_ptr(),
+                                              post_w.data_ptr(), pre_w.data_ptr(), n, eps, T, D,
+                                              q.data_ptr(), scale.data_ptr(), _opts(opts))
     if st != 0:
         raise BeamError(st, "beam_boundary_fused_int8")
     return q, scale
@@ -350,25 +393,38 @@ def moe_combine_boundary_int8(h, expert_out, topk_w, post_w, pre_w, n: int, eps:
     """MoE boundary with y as int8 and one FP32 scale per token; updates h in place, returns
     (y_int8, y_scale). ``route_scale`` multiplies the combined sum (1: topk_w carries it)."""
     import torch
-    _check(h, "h", torch.bfloat16, 2)
-    _check(expert_out, "expert_out", torch.bfloat16, 3)
-    _check(topk_w, "topk_w", torch.float32, 2)
-    _check(post_w, "post_w", torch.bfloat16, 1)
-    _check(pre_w, "pre_w", torch.bfloat16, 1)
-    T, D = h.shape
-    if (expert_out.shape != (T, _lib.BEAM_MOE_TOPK, D) or topk_w.shape != (T, _lib.BEAM_MOE_TOPK)
-            or post_w.shape[0] != D or pre_w.shape[0] != D):
-        raise ValueError("shape mismatch: h [T, D]; expert_out [T, 8, D]; topk_w [T, 8]")
-    q, scale = _int8_out(h, y_int8, y_scale)
-    _on_current_device(h=h, expert_out=expert_out, topk_w=topk_w, post_w=post_w, pre_w=pre_w,
-                       y_int8=q, y_scale=scale)
+    bf16, K = torch.bfloat16, _lib.BEAM_MOE_TOPK
+    T, D = rows = _dims(h, 2)
+    ready = _ready((h, bf16, rows), (expert_out, bf16, (T, K, D)), (topk_w, torch.float32, (T, K)),
+                   (post_w, bf16, (D,)), (pre_w, bf16, (D,)))
+    if not ready:
+        _check(h, "h", bf16, 2)
+        _check(expert_out, "expert_out", bf16, 3)
+        _check(topk_w, "topk_w", torch.float32, 2)
+        _check(post_w, "post_w", bf16, 1)
+        _check(pre_w, "pre_w", bf16, 1)
+        if (expert_out.shape != (T, K, D) or topk_w.shape != (T, K) or post_w.shape[0] != D
+                or pre_w.shape[0] != D):
+            raise ValueError("shape mismatch: h [T, D]; expert_out [T, 8, D]; topk_w [T, 8]")
+    if not ready or y_int8 is not None or y_scale is not None:
+        q, scale = _int8_out(h, y_int8, y_scale)
+        _on_current_device(h=h, expert_out=expert_out, topk_w=topk_w, post_w=post_w, pre_w=pre_w,
+                           y_int8=q, y_scale=scale)
+    else:
+        q = torch.empty(rows, dtype=torch.int8, device=h.device)
+        scale = torch.empty(T, dtype=torch.float32, device=h.device)
     st = _lib.load().beam_moe_combine_boundary_int8(
-        _stream_ptr(stream), h.data_ptr(), expert_out.data_ptr(), topk_w.data_ptr(),
-        float(route_scale), post_w.data_ptr(), pre_w.data_ptr(), int(n), float(eps), T, D,
+        _raw_stream(stream, h), h.data_ptr(), expert_out.data_ptr(), topk_w.data_ptr(),
+        route_scale, post_w.data_ptr(), pre_w.data_ptr(), n, eps, T, D,
         q.data_ptr(), scale.data_ptr(), _opts(opts))
     if st != 0:
         raise BeamError(st, "beam_moe_combine_boundary_int8")
     return q, scale
+
+
+@functools.lru_cache(maxsize=4096)
+def _matmul_workspace(M: int, N: int, K: int) -> int:
+    return max(0, _lib.load().beam_matmul_int8_workspace(M, N, K))
 
 
 def matmul_int8(a, a_scale, w, w_scale, out_dtype=None, out=None, stream=None, pdl: bool = False):
@@ -381,28 +437,32 @@ def matmul_int8(a, a_scale, w, w_scale, out_dtype=None, out=None, stream=None, p
     stream must not write w.
     """
     import torch
-    _check(a, "a", torch.int8, 2)
-    _check(a_scale, "a_scale", torch.float32, 1)
-    _check(w, "w", torch.int8, 2)
-    _check(w_scale, "w_scale", torch.float32, 1)
-    (M, K), N = a.shape, w.shape[0]
-    if w.shape[1] != K or a_scale.shape[0] != M or w_scale.shape[0] != N:
-        raise ValueError("shape mismatch: a [M, K]; a_scale [M]; w [N, K]; w_scale [N]")
+    (M, K), (N, _) = _dims(a, 2), _dims(w, 2)
+    ready = _ready((a, torch.int8, (M, K)), (a_scale, torch.float32, (M,)), (w, torch.int8, (N, K)),
+                   (w_scale, torch.float32, (N,)))
+    if not ready:
+        _check(a, "a", torch.int8, 2)
+        _check(a_scale, "a_scale", torch.float32, 1)
+        _check(w, "w", torch.int8, 2)
+        _check(w_scale, "w_scale", torch.float32, 1)
+        if w.shape[1] != K or a_scale.shape[0] != M or w_scale.shape[0] != N:
+            raise ValueError("shape mismatch: a [M, K]; a_scale [M]; w [N, K]; w_scale [N]")
     if out_dtype is None:
         out_dtype = torch.bfloat16 if out is None else out.dtype
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError(f"out_dtype must be bfloat16 or float32 (got {out_dtype})")
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty((M, N), dtype=out_dtype, device=a.device)
-    _check(out, "out", out_dtype, 2)
-    _shape(out, "out", (M, N))
-    _on_current_device(a=a, a_scale=a_scale, w=w, w_scale=w_scale, out=out)
-    lib = _lib.load()
-    ws_bytes = max(0, lib.beam_matmul_int8_workspace(M, N, K))
+    if given or not ready:
+        _check(out, "out", out_dtype, 2)
+        _shape(out, "out", (M, N))
+        _on_current_device(a=a, a_scale=a_scale, w=w, w_scale=w_scale, out=out)
+    ws_bytes = _matmul_workspace(M, N, K)
     ws = _workspace(ws_bytes, a.device, stream)
-    st = lib.beam_matmul_int8(
-        _stream_ptr(stream), a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), M, N, K,
-        _lib.BEAM_OUT_FP32 if out_dtype == torch.float32 else _lib.BEAM_OUT_BF16, out.data_ptr(),
+    st = _lib.load().beam_matmul_int8(
+        _raw_stream(stream, a), a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), M, N, K,
+        _lib.BEAM_OUT_FP32 if out_dtype is torch.float32 else _lib.BEAM_OUT_BF16, out.data_ptr(),
         ws.data_ptr() if ws_bytes else None, ws_bytes, _lib.BEAM_OPT_PDL if pdl else 0)
     if st != 0:
         raise BeamError(st, "beam_matmul_int8")
@@ -440,18 +500,24 @@ def moe_route(logits, bias, n_group: int = 8, topk_group: int = 4, topk: int = 8
     return idx, w
 
 
-def _sequences(seq_offsets, **operands):
-    """(pointer, S) of the sequence offsets, which join the operands of the device check."""
+def _sequences(seq_offsets) -> int:
+    """S, of [S + 1] sequence offsets (1 for None)."""
     import torch
-    S, ptr = 1, None
-    if seq_offsets is not None:
-        _check(seq_offsets, "seq_offsets", torch.int32, 1)
-        S = seq_offsets.shape[0] - 1
-        if S < 1:
-            raise ValueError("seq_offsets must have at least two entries")
-        operands["seq_offsets"] = seq_offsets
-        ptr = seq_offsets.data_ptr()
-    return ptr, S, operands
+    if seq_offsets is None:
+        return 1
+    _check(seq_offsets, "seq_offsets", torch.int32, 1)
+    if seq_offsets.shape[0] < 2:
+        raise ValueError("seq_offsets must have at least two entries")
+    return seq_offsets.shape[0] - 1
+
+
+def _given(**operands) -> dict:
+    return {name: t for name, t in operands.items() if t is not None}
+
+
+@functools.lru_cache(maxsize=4096)
+def _balance_workspace(T: int, E: int, S: int) -> int:
+    return max(0, _lib.load().beam_moe_balance_workspace(T, E, S))
 
 
 def moe_balance_loss(logits, topk_idx, alpha: float, seq_offsets=None, loss=None, counts=None,
@@ -464,27 +530,33 @@ def moe_balance_loss(logits, topk_idx, alpha: float, seq_offsets=None, loss=None
     Returns (loss float32 [S], counts int32 [S, E]).
     """
     import torch
-    _check(logits, "logits", torch.float32, 2)
-    _check(topk_idx, "topk_idx", torch.int32, 2)
-    T, E = logits.shape
-    if topk_idx.shape[0] != T:
-        raise ValueError("shape mismatch: logits [T, E]; topk_idx [T, topk]")
-    off, S, ops = _sequences(seq_offsets, logits=logits, topk_idx=topk_idx)
+    S = _sequences(seq_offsets)
+    (T, E), (_, K) = _dims(logits, 2), _dims(topk_idx, 2)
+    ready = _ready((logits, torch.float32, (T, E)), (topk_idx, torch.int32, (T, K)),
+                   *(() if seq_offsets is None else ((seq_offsets, torch.int32, (S + 1,)),)))
+    if not ready:
+        _check(logits, "logits", torch.float32, 2)
+        _check(topk_idx, "topk_idx", torch.int32, 2)
+        if topk_idx.shape[0] != T:
+            raise ValueError("shape mismatch: logits [T, E]; topk_idx [T, topk]")
+    given = loss is not None or counts is not None
     if loss is None:
         loss = torch.empty(S, dtype=torch.float32, device=logits.device)
     if counts is None:
         counts = torch.empty((S, E), dtype=torch.int32, device=logits.device)
-    _check(loss, "loss", torch.float32, 1)
-    _check(counts, "counts", torch.int32, 2)
-    _shape(loss, "loss", (S,))
-    _shape(counts, "counts", (S, E))
-    _on_current_device(loss=loss, counts=counts, **ops)
-    lib = _lib.load()
-    ws_bytes = max(0, lib.beam_moe_balance_workspace(T, E, S))
+    if given or not ready:
+        _check(loss, "loss", torch.float32, 1)
+        _check(counts, "counts", torch.int32, 2)
+        _shape(loss, "loss", (S,))
+        _shape(counts, "counts", (S, E))
+        _on_current_device(**_given(logits=logits, topk_idx=topk_idx, seq_offsets=seq_offsets, loss=loss,
+                                    counts=counts))
+    ws_bytes = _balance_workspace(T, E, S)
     ws = _workspace(ws_bytes, logits.device, stream)
-    st = lib.beam_moe_balance_loss(_stream_ptr(stream), logits.data_ptr(), topk_idx.data_ptr(), off, T, E,
-                                   topk_idx.shape[1], S, float(alpha), loss.data_ptr(),
-                                   counts.data_ptr(), ws.data_ptr(), ws_bytes)
+    st = _lib.load().beam_moe_balance_loss(
+        _raw_stream(stream, logits), logits.data_ptr(), topk_idx.data_ptr(),
+        None if seq_offsets is None else seq_offsets.data_ptr(), T, E, K, S, alpha, loss.data_ptr(),
+        counts.data_ptr(), ws.data_ptr() if ws_bytes else None, ws_bytes)
     if st != 0:
         raise BeamError(st, "beam_moe_balance_loss")
     return loss, counts
@@ -498,21 +570,27 @@ def moe_balance_loss_backward(dloss, logits, counts, topk: int, alpha: float, se
     arguments as there. Returns dlogits float32 [T, E] (0 for padding).
     """
     import torch
-    _check(dloss, "dloss", torch.float32, 1)
-    _check(logits, "logits", torch.float32, 2)
-    _check(counts, "counts", torch.int32, 2)
-    T, E = logits.shape
-    off, S, ops = _sequences(seq_offsets, dloss=dloss, logits=logits, counts=counts)
-    _shape(dloss, "dloss", (S,))
-    _shape(counts, "counts", (S, E))
-    if dlogits is None:
+    S = _sequences(seq_offsets)
+    T, E = rows = _dims(logits, 2)
+    ready = _ready((dloss, torch.float32, (S,)), (logits, torch.float32, rows), (counts, torch.int32, (S, E)),
+                   *(() if seq_offsets is None else ((seq_offsets, torch.int32, (S + 1,)),)))
+    if not ready:
+        _check(dloss, "dloss", torch.float32, 1)
+        _check(logits, "logits", torch.float32, 2)
+        _check(counts, "counts", torch.int32, 2)
+        _shape(dloss, "dloss", (S,))
+        _shape(counts, "counts", (S, E))
+    given = dlogits is not None
+    if not given:
         dlogits = torch.empty_like(logits)
-    _check(dlogits, "dlogits", torch.float32, 2)
-    _shape(dlogits, "dlogits", (T, E))
-    _on_current_device(dlogits=dlogits, **ops)
-    st = _lib.load().beam_moe_balance_loss_backward(_stream_ptr(stream), dloss.data_ptr(), logits.data_ptr(),
-                                                    counts.data_ptr(), off, T, E, int(topk), S,
-                                                    float(alpha), dlogits.data_ptr())
+    if given or not ready:
+        _check(dlogits, "dlogits", torch.float32, 2)
+        _shape(dlogits, "dlogits", (T, E))
+        _on_current_device(**_given(dloss=dloss, logits=logits, counts=counts, seq_offsets=seq_offsets,
+                                    dlogits=dlogits))
+    st = _lib.load().beam_moe_balance_loss_backward(
+        _raw_stream(stream, logits), dloss.data_ptr(), logits.data_ptr(), counts.data_ptr(),
+        None if seq_offsets is None else seq_offsets.data_ptr(), T, E, topk, S, alpha, dlogits.data_ptr())
     if st != 0:
         raise BeamError(st, "beam_moe_balance_loss_backward")
     return dlogits

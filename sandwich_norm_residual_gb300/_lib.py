@@ -91,6 +91,8 @@ _lib = None
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load the library (built by ``sandwich_norm_residual_gb300.build``); no fallback."""
     global _lib
+    if path is None and _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
