@@ -14,7 +14,7 @@
 // at index b + s. Along the staircase of (block, sequence) pairs that overlap,
 // b + s grows, so no two pairs share a record, nothing needs to be zeroed, there
 // are no floating-point atomics and the result is the same in every run. A
-// second kernel adds a sequence's records in order, in 64 bits.
+// second kernel adds a sequence's records in order.
 #pragma once
 
 #include <cstdint>
@@ -81,11 +81,23 @@ __device__ __forceinline__ void for_sequences(const BalanceParams& p, long long 
     if (t < t1) gap(t, t1);
 }
 
-// s = sigmoid(z) and e = exp(-z), each within a few units of 2^-24 of its value
+// s = sigmoid(z) and e = exp(-z) on the special-function unit: 4 instructions
+// where expf and a division take 20, which would keep the forward pass busy for
+// as long as its memory traffic. The product in the exponent is rounded once, so
+// e and s are within |z| + 4 units of 2^-24 of their values; below 2^-126 they are 0.
 __device__ __forceinline__ float sigmoid_e(float z, float* e_out) {
-    const float e = expf(-z);
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(z, -0x1.715476p+0f)));  // log2(e)
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(__fadd_rn(1.0f, e)));
     *e_out = e;
-    return __fdividef(1.0f, 1.0f + e);
+    return s;
+}
+
+// (s, c) += t with the rounding error of s kept in c (Knuth's TwoSum)
+__device__ __forceinline__ void sum_into(float& s, float& c, float t) {
+    const float n = __fadd_rn(s, t), b = __fsub_rn(n, s);
+    c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(n, b)), __fsub_rn(t, b)));
+    s = n;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -174,9 +186,11 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_records_kernel(const 
 }
 
 // One block a sequence: its records added in order (groups of threads take
-// every G-th record, then the groups in order), the counts and the loss.
+// every G-th record, then the groups in order), the counts and the loss. Sums are
+// FP32 pairs: FP64 additions, 64 times slower than FP32 ones on this GPU, took 45
+// us for a sequence in 304 blocks.
 __global__ void __launch_bounds__(kBalanceFinalThreads) balance_loss_kernel(const BalanceParams p) {
-    __shared__ double sq[kBalanceFinalSums];  // [groups][E]
+    __shared__ float2 sq[kBalanceFinalSums];  // [groups][E]
     __shared__ double part[kBalanceFinalThreads / 32];
     const int tid = threadIdx.x, s = blockIdx.x, quads = p.E / 4;
     pdl_wait();
@@ -187,26 +201,33 @@ __global__ void __launch_bounds__(kBalanceFinalThreads) balance_loss_kernel(cons
     const int first = n ? (int)(lo / p.chunk) : 0, last = n ? (int)((hi - 1) / p.chunk) : -1;
     const int groups = kBalanceFinalThreads / quads;
     const int g = tid / quads, quad = tid % quads;
-    double q[4] = {0, 0, 0, 0};
-    long long c[4] = {0, 0, 0, 0};
+    float q[4] = {0, 0, 0, 0}, qc[4] = {0, 0, 0, 0};
+    int c[4] = {0, 0, 0, 0};
     if (g < groups) {
 #pragma unroll 4
         for (int r = first + g; r <= last; r += groups) {
             const size_t at = ((size_t)r + (size_t)s) * (size_t)p.E + 4 * quad;
             const float4 f = __ldcg(reinterpret_cast<const float4*>(p.rec_q + at));
             const int4 k = __ldcg(reinterpret_cast<const int4*>(p.rec_c + at));
-            q[0] += f.x, q[1] += f.y, q[2] += f.z, q[3] += f.w;
+            sum_into(q[0], qc[0], f.x);
+            sum_into(q[1], qc[1], f.y);
+            sum_into(q[2], qc[2], f.z);
+            sum_into(q[3], qc[3], f.w);
             c[0] += k.x, c[1] += k.y, c[2] += k.z, c[3] += k.w;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sq[g * p.E + 4 * quad + i] = q[i];
+        for (int i = 0; i < 4; ++i) sq[g * p.E + 4 * quad + i] = make_float2(q[i], qc[i]);
     }
     __syncthreads();
-    double mine = 0;
+    float sum = 0.f, comp = 0.f;
     if (tid < p.E)
-        for (int k = 0; k < groups; ++k) mine += sq[k * p.E + tid];
+        for (int k = 0; k < groups; ++k) {
+            const float2 v = sq[k * p.E + tid];
+            sum_into(sum, comp, v.x);
+            comp += v.y;
+        }
     __syncthreads();
-    long long* scn = reinterpret_cast<long long*>(sq);
+    int* scn = reinterpret_cast<int*>(sq);
     if (g < groups) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) scn[g * p.E + 4 * quad + i] = c[i];
@@ -214,19 +235,19 @@ __global__ void __launch_bounds__(kBalanceFinalThreads) balance_loss_kernel(cons
     __syncthreads();
     double term = 0;
     if (tid < p.E) {
-        long long count = 0;
+        int count = 0;
         for (int k = 0; k < groups; ++k) count += scn[k * p.E + tid];
-        p.counts[(size_t)s * (size_t)p.E + tid] = (int32_t)count;
-        term = (double)count * mine;
+        p.counts[(size_t)s * (size_t)p.E + tid] = count;
+        term = (double)count * ((double)sum + (double)comp);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) term += __shfl_xor_sync(0xFFFFFFFFu, term, o);
     if ((tid & 31) == 0) part[tid >> 5] = term;
     __syncthreads();
     if (tid == 0) {
-        double sum = 0;
-        for (int w = 0; w < kBalanceFinalThreads / 32; ++w) sum += part[w];
-        p.loss[s] = n ? (float)(p.factor / ((double)n * (double)n) * sum) : 0.0f;
+        double total = 0;
+        for (int w = 0; w < (p.E + 31) / 32; ++w) total += part[w];
+        p.loss[s] = n ? (float)(p.factor / ((double)n * (double)n) * total) : 0.0f;
     }
 }
 

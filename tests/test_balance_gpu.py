@@ -1,11 +1,11 @@
 """The router's balance loss, its counts and its gradient against the formula in 64 bits.
 
-Tolerances, u = 2^-24: the kernel's sigmoid is a call of expf (2 ulp), one add and one division
-(2 ulp): 8 u relative with both ends' half steps. p adds a sum of up to 512 sigmoids held as 16 a
-lane and 5 shuffle levels (21 u), a division (1 u) and 9 u of its own sigmoid: 40 u. A sequence's Q
-adds at most `chunk` FP32 additions a block: 64 u up to 1024 tokens a warp. 1e-5 = 168 u covers
-every loss here; gradients also carry the cancellation in counts_e - sum_i counts_i p_i, so their
-bound is relative to counts_e + sum_i counts_i p_i."""
+Tolerances, u = 2^-24: in the kernel's sigmoid the exponent is rounded once (|z| u, at most 88 u
+before e leaves FP32), exp2, the addition and the reciprocal add 2 + 1 + 1 u; p adds a sum of up to
+512 sigmoids held as 16 a lane and 5 shuffle levels (21 u), whose own errors are those of its largest
+terms, and a division (1 u). A sequence's Q adds 16 tokens a warp and 16 warps in FP32 (32 u). 150 u in
+all, and REL = 1e-5 is 168 u. Gradients also carry the cancellation in counts_e - sum_i counts_i p_i, so
+their bound is relative to counts_e + sum_i counts_i p_i."""
 from __future__ import annotations
 
 import numpy as np
