@@ -20,14 +20,17 @@ constexpr int kMaxSms = 152;  // workers of a launch at most, and what workspace
 
 bool misaligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1u)) != 0; }
 
+// Kernel for up to 8 tokens, and its channels a warp. At N = 6144, K = 5120 the
+// shapes below take 6.5, 7.4, 9.0 and 11.2 us for 1, 2, 4 and 8 tokens; two
+// channels a warp take 9.7 and 24 us for 4 and 8, four take 7.2 us for 1, and a
+// second set of weights in flight (fewer warps an SM) 8.4 us for 1.
 template <bool F32>
-const void* few_kernel(int mb) {
-    switch (mb) {
-    case 1: return reinterpret_cast<const void*>(beam::matmul_int8_few_kernel<1, 2, 4, F32>);
-    case 2: return reinterpret_cast<const void*>(beam::matmul_int8_few_kernel<2, 2, 4, F32>);
-    case 4: return reinterpret_cast<const void*>(beam::matmul_int8_few_kernel<4, 2, 4, F32>);
-    default: return reinterpret_cast<const void*>(beam::matmul_int8_few_kernel<8, 2, 4, F32>);
-    }
+const void* few_kernel(int64_t M, int* channels) {
+    *channels = M <= 2 ? 2 : 4;
+    if (M <= 1) return reinterpret_cast<const void*>(beam::matmul_int8_few_kernel<1, 2, 4, F32>);
+    if (M <= 2) return reinterpret_cast<const void*>(beam::matmul_int8_few_kernel<2, 2, 4, F32>);
+    if (M <= 4) return reinterpret_cast<const void*>(beam::matmul_int8_few_kernel<4, 4, 3, F32>);
+    return reinterpret_cast<const void*>(beam::matmul_int8_few_kernel<8, 4, 2, F32>);
 }
 
 beam_status launch(const void* fn, dim3 grid, dim3 block, void** args, size_t smem, cudaStream_t stream, bool pdl,
@@ -112,40 +115,54 @@ beam_status allow_smem(const void* fn, size_t bytes, std::atomic<unsigned long l
     return BEAM_OK;
 }
 
+// What a join takes in steps of k: the sums written, the second kernel
+template <int CG>
+constexpr uint32_t kJoinSteps = CG == 1 ? 8 : 26;
+
 // The split of a product into tiles of NT tokens by 128 CG channels
 template <int NT, int CG>
-void plan(const MatmulParams& p, int sms, beam::MatmulTcParams* q) {
-    q->p = p;
-    q->m_tiles = (uint32_t)((p.M + NT - 1) / NT);
-    q->steps = (uint32_t)((p.K + beam::kStepK - 1) / beam::kStepK);
-    q->tiles = q->m_tiles * (uint32_t)((p.N + beam::kTileN * CG - 1) / (beam::kTileN * CG));
-    q->workers = (uint32_t)(sms / CG);
-    if (CG == 2) {
-        q->waves = (q->tiles + q->workers - 1) / q->workers;
-        q->sharers = q->split = 0;
-        return;
+beam::MatmulTcParams plan(const MatmulParams& p, int sms) {
+    beam::MatmulTcParams q{};
+    q.p = p;
+    q.m_tiles = (uint32_t)((p.M + NT - 1) / NT);
+    q.steps = (uint32_t)((p.K + beam::kStepK - 1) / beam::kStepK);
+    q.tiles = q.m_tiles * (uint32_t)((p.N + beam::kTileN * CG - 1) / (beam::kTileN * CG));
+    q.workers = (uint32_t)(sms / CG);
+    // The tiles behind the last full wave are shared, with four steps a worker at
+    // least, where that shortens the wave by more than the join takes (kJoinSteps).
+    // Single CTAs: M = 517, N = 2565, K = 2576, 105 tiles of 21 steps: 19.6 us
+    // unshared, 20.9 us shared; M = 64, N = 5120, K = 20480, 40 of 160: 75 and 29 us.
+    // Pairs: M = 1024, N = 5120, K = 5120, 80 tiles of 40 steps: 53 and 41 us; M = 512,
+    // 40 tiles: 31 and 39 us.
+    q.waves = q.tiles / q.workers;
+    q.split = (q.tiles - q.waves * q.workers) * q.steps;
+    const uint32_t most = (q.split + 3) / 4;
+    q.sharers = most < q.workers ? most : q.workers;
+    if (q.split && q.steps <= (q.split + q.sharers - 1) / q.sharers + kJoinSteps<CG>) {
+        q.waves += 1;
+        q.split = q.sharers = 0;
     }
-    // the tiles behind the last full wave are shared, with four steps a worker at least
-    q->waves = q->tiles / q->workers;
-    q->split = (q->tiles - q->waves * q->workers) * q->steps;
-    const uint32_t most = (q->split + 3) / 4;
-    q->sharers = most < q->workers ? most : q->workers;
+    return q;
 }
 
-template <int NT>
+template <int NT, int CG>
 int64_t part_bytes(const beam::MatmulTcParams& q) {
-    return (int64_t)q.sharers * 2 * NT * beam::kTileN * 4;
+    return (int64_t)q.sharers * CG * 2 * NT * beam::kTileN * 4;
 }
 
 template <int NT, int CG, bool F32>
-beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* part, cudaStream_t stream, bool pdl) {
+beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* part, int64_t workspace_bytes,
+                        cudaStream_t stream, bool pdl) {
     using C = beam::TileConfig<NT, CG>;
     static std::atomic<unsigned long long> allowed{0};
     const void* fn = reinterpret_cast<const void*>(beam::matmul_int8_tile_kernel<NT, CG, F32>);
     beam_status st = allow_smem(fn, C::kSmem, &allowed, dev.ordinal);
     if (st != BEAM_OK) return st;
-    beam::MatmulTcParams q{};
-    plan<NT, CG>(p, dev.sms < kMaxSms ? dev.sms : kMaxSms, &q);
+    beam::MatmulTcParams q = plan<NT, CG>(p, dev.sms < kMaxSms ? dev.sms : kMaxSms);
+    if (part_bytes<NT, CG>(q) > workspace_bytes) {  // planned for 152 SMs; with fewer, more may be shared
+        q.waves += 1;
+        q.split = q.sharers = 0;
+    }
     q.wide = !F32 && p.N % 8 == 0 && p.N >= beam::kTileN && !misaligned(p.out, 16);
     CUtensorMap wmap, pmap, amap;
     if (!row_map(&wmap, p.w, p.N, p.K, beam::kTileN) || !row_map(&amap, p.a, p.M, p.K, C::kRows)) return BEAM_ERR_CUDA;
@@ -157,34 +174,44 @@ beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* pa
     const uint32_t workers = q.waves ? (q.tiles < q.workers ? q.tiles : q.workers) : q.sharers;
     void* args[] = {&wmap, &pmap, &amap, &q};
     st = launch(fn, dim3(workers * CG), dim3(C::kThreads), args, C::kSmem, stream, pdl, CG);
-    const uint32_t shared = q.split / q.steps;
-    if (st != BEAM_OK || shared == 0 || shared == q.sharers) return st;  // none, or each a worker's own
+    const uint32_t shared = q.split / q.steps;  // tiles
+    if (st != BEAM_OK || shared == 0) return st;
     void* join_args[] = {&q};
-    return launch(reinterpret_cast<const void*>(beam::matmul_int8_join_kernel<NT, F32>), dim3(shared, NT / 8),
-                  dim3(beam::kTileN), join_args, 0, stream, true);
+    // started early where it follows the shared steps alone: behind whole waves its
+    // blocks, waiting on the SMs that are done, cost 2 us
+    return launch(reinterpret_cast<const void*>(beam::matmul_int8_join_kernel<NT, CG, F32>),
+                  dim3(shared, NT / beam::kJoinCols, CG), dim3(beam::kTileN), join_args, 0, stream, q.waves == 0);
 }
 
-// Tokens a tile: as few as hold M; many tokens go to pairs of CTAs
+// Tokens a tile: as few as hold M; beyond 128, single CTAs or pairs, whichever
+// finishes first by the measured time of a step (0.56 and 0.62 us), of a join and
+// of a result that nothing hides (0.7 and 1.5 us)
 enum class Shape { kFew, k16, k32, k64, k128, kPair };
 
-Shape choose(int64_t M, int N) {
-    if (M <= 8) return Shape::kFew;
-    if (M <= 16) return Shape::k16;
-    if (M <= 32) return Shape::k32;
-    if (M <= 64) return Shape::k64;
-    const int64_t pairs = ((M + 255) / 256) * ((N + 255) / 256);
-    return M > 128 && pairs >= 76 ? Shape::kPair : Shape::k128;
+Shape choose(const MatmulParams& p) {
+    if (p.M <= 8) return Shape::kFew;
+    if (p.M <= 16) return Shape::k16;
+    if (p.M <= 32) return Shape::k32;
+    if (p.M <= 64) return Shape::k64;
+    if (p.M <= 128) return Shape::k128;
+    auto ns = [](const beam::MatmulTcParams& q, uint32_t join, double step, double result) {
+        const uint32_t shared = q.split ? (q.split + q.sharers - 1) / q.sharers + join : 0;
+        return q.waves * (q.steps * step + result) + shared * step;
+    };
+    return ns(plan<128, 1>(p, kMaxSms), kJoinSteps<1>, 560, 700) < ns(plan<256, 2>(p, kMaxSms), kJoinSteps<2>, 620, 1500)
+               ? Shape::k128
+               : Shape::kPair;
 }
 
 template <bool F32>
-beam_status launch_tiles(Shape shape, const MatmulParams& p, const beam::Device& dev, void* part, cudaStream_t stream,
-                         bool pdl) {
+beam_status launch_tiles(Shape shape, const MatmulParams& p, const beam::Device& dev, void* part, int64_t bytes,
+                         cudaStream_t stream, bool pdl) {
     switch (shape) {
-    case Shape::k16: return launch_tile<16, 1, F32>(p, dev, part, stream, pdl);
-    case Shape::k32: return launch_tile<32, 1, F32>(p, dev, part, stream, pdl);
-    case Shape::k64: return launch_tile<64, 1, F32>(p, dev, part, stream, pdl);
-    case Shape::k128: return launch_tile<128, 1, F32>(p, dev, part, stream, pdl);
-    default: return launch_tile<256, 2, F32>(p, dev, part, stream, pdl);
+    case Shape::k16: return launch_tile<16, 1, F32>(p, dev, part, bytes, stream, pdl);
+    case Shape::k32: return launch_tile<32, 1, F32>(p, dev, part, bytes, stream, pdl);
+    case Shape::k64: return launch_tile<64, 1, F32>(p, dev, part, bytes, stream, pdl);
+    case Shape::k128: return launch_tile<128, 1, F32>(p, dev, part, bytes, stream, pdl);
+    default: return launch_tile<256, 2, F32>(p, dev, part, bytes, stream, pdl);
     }
 }
 
@@ -202,13 +229,13 @@ int64_t beam_matmul_int8_workspace(int64_t M, int N, int K) {
     if (bad_shape(M, N, K)) return -1;
     if (M == 0 || N == 0) return 0;
     const MatmulParams p{nullptr, nullptr, nullptr, nullptr, nullptr, M, N, K};
-    beam::MatmulTcParams q{};
-    switch (choose(M, N)) {
-    case Shape::k16: plan<16, 1>(p, kMaxSms, &q); return part_bytes<16>(q);
-    case Shape::k32: plan<32, 1>(p, kMaxSms, &q); return part_bytes<32>(q);
-    case Shape::k64: plan<64, 1>(p, kMaxSms, &q); return part_bytes<64>(q);
-    case Shape::k128: plan<128, 1>(p, kMaxSms, &q); return part_bytes<128>(q);
-    default: return 0;
+    switch (choose(p)) {
+    case Shape::kFew: return 0;
+    case Shape::k16: return part_bytes<16, 1>(plan<16, 1>(p, kMaxSms));
+    case Shape::k32: return part_bytes<32, 1>(plan<32, 1>(p, kMaxSms));
+    case Shape::k64: return part_bytes<64, 1>(plan<64, 1>(p, kMaxSms));
+    case Shape::k128: return part_bytes<128, 1>(plan<128, 1>(p, kMaxSms));
+    default: return part_bytes<256, 2>(plan<256, 2>(p, kMaxSms));
     }
 }
 
@@ -241,15 +268,15 @@ beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, const float*
     MatmulParams p{a, a_scale, w, w_scale, out, M, N, K};
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const bool pdl = (flags & BEAM_OPT_PDL) != 0;
-    const Shape shape = choose(M, N);
+    const Shape shape = choose(p);
     if (shape != Shape::kFew)
-        return f32 ? launch_tiles<true>(shape, p, dev, workspace, cs, pdl)
-                   : launch_tiles<false>(shape, p, dev, workspace, cs, pdl);
+        return f32 ? launch_tiles<true>(shape, p, dev, workspace, workspace_bytes, cs, pdl)
+                   : launch_tiles<false>(shape, p, dev, workspace, workspace_bytes, cs, pdl);
     void* args[] = {&p};
-    const int mb = M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : 8;
-    const void* fn = f32 ? few_kernel<true>(mb) : few_kernel<false>(mb);
-    constexpr int kR = 2, kWarps = 8;
-    return launch(fn, dim3((unsigned)((N + kR * kWarps - 1) / (kR * kWarps))), dim3(256), args, 0, cs, pdl);
+    int channels = 0;
+    const void* fn = f32 ? few_kernel<true>(M, &channels) : few_kernel<false>(M, &channels);
+    const int per_block = channels * beam::kFewWarps;
+    return launch(fn, dim3((unsigned)((N + per_block - 1) / per_block)), dim3(32 * beam::kFewWarps), args, 0, cs, pdl);
 }
 
 }  // extern "C"

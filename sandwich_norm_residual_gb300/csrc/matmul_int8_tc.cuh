@@ -45,7 +45,7 @@ struct MatmulTcParams {
     // BF16 rows of out start on 16 bytes and end there: whole tiles of 128 channels
     // are then loaded in the order of `pmap` and stored 16 bytes a thread
     int wide;
-    float* part;              // [workers][2][NT][128]: sums of tiles that a worker has a part of
+    float* part;              // [workers][CG][2][NT][128]: sums of tiles that a worker has a part of
     uint64_t wait_ns;
     unsigned int* status;
 };
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
             }
             // the first of this worker's split tiles goes to its part 0, the last to part 1
             const bool second = seg.k0 == 0;
-            float* part = q.part + ((size_t)worker * 2 + second) * (size_t)(NT * kTileN) + t;
+            float* part = q.part + ((size_t)blockIdx.x * 2 + second) * (size_t)(NT * kTileN) + t;
             const size_t at = (size_t)m0 * (size_t)q.p.N + (size_t)n;
             constexpr int kBatch = NT < 32 ? 16 : 32;
             for (int c0 = 0; c0 < cols; c0 += kBatch) {
@@ -497,37 +497,55 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
 }
 
 // Adds the sums of the tiles that several workers have steps of: a block for
-// eight tokens of a tile, thread = channel. They are integers (FP32 ones), added
-// as such.
-template <int NT, bool F32>
+// kJoinCols tokens of a tile, thread = channel. They are integers (FP32 ones),
+// added as such. What it takes (3 us) is its launch and one way to L2 and back,
+// so few values a thread and eight workers' at once.
+constexpr int kJoinCols = 2, kJoinWorkers = 8;
+
+template <int NT, int CG, bool F32>
 __global__ void __launch_bounds__(kTileN) matmul_int8_join_kernel(const __grid_constant__ MatmulTcParams q) {
     pdl_trigger();
     const uint32_t tile = q.waves * q.workers + blockIdx.x;
-    const int n = (int)(tile / q.m_tiles * kTileN + threadIdx.x);
-    const long long m0 = (long long)(tile % q.m_tiles) * NT + blockIdx.y * 8;
+    const uint32_t rank = blockIdx.z;  // the CTA's 128 channels of the tile
+    const int n = (int)((tile / q.m_tiles * CG + rank) * kTileN + threadIdx.x), c0 = blockIdx.y * kJoinCols;
+    const long long m0 = (long long)(tile % q.m_tiles) * NT + c0;
     // worker c has the steps [split c / sharers, split (c + 1) / sharers)
     const uint32_t lo = blockIdx.x * q.steps, hi = lo + q.steps;
     uint32_t c = lo * q.sharers / q.split;
     while (q.split * (c + 1) / q.sharers <= lo) ++c;
     uint32_t begin = q.split * c / q.sharers;
+    const bool whole = begin <= lo && q.split * (c + 1) / q.sharers >= hi;  // one worker's: stored already
     pdl_wait();
-    if (begin <= lo && q.split * (c + 1) / q.sharers >= hi) return;  // one worker's: stored already
-    if (n >= q.p.N) return;
-    int sum[8] = {};
-    for (; begin < hi; begin = q.split * ++c / q.sharers) {
-        const bool second = begin <= lo;  // its segment of this tile begins at the tile's first step
-        const float* part = q.part + ((size_t)c * 2 + second) * (size_t)(NT * kTileN) + (size_t)blockIdx.y * 8 * kTileN +
-                            threadIdx.x;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (m0 + i < q.p.M) sum[i] += __float2int_rn(__ldcg(part + i * kTileN));
-    }
+    if (whole || n >= q.p.N || m0 >= q.p.M) return;
     const float ws = __ldg(q.p.w_scale + n);
+    float as[kJoinCols];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < kJoinCols; ++i) as[i] = m0 + i < q.p.M ? __ldg(q.p.a_scale + m0 + i) : 0.0f;
+    int sum[kJoinCols] = {};
+    while (begin < hi) {
+        float v[kJoinWorkers][kJoinCols] = {};
+#pragma unroll
+        for (int j = 0; j < kJoinWorkers; ++j) {
+            if (begin < hi) {
+                const bool second = begin <= lo;  // its segment of this tile begins at the tile's first step
+                const float* part = q.part + (((size_t)c * CG + rank) * 2 + second) * (size_t)(NT * kTileN) +
+                                    c0 * kTileN + threadIdx.x;
+#pragma unroll
+                for (int i = 0; i < kJoinCols; ++i)
+                    if (m0 + i < q.p.M) v[j][i] = __ldcg(part + i * kTileN);
+                begin = q.split * ++c / q.sharers;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kJoinWorkers; ++j)
+#pragma unroll
+            for (int i = 0; i < kJoinCols; ++i) sum[i] += __float2int_rn(v[j][i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kJoinCols; ++i)
         if (m0 + i < q.p.M)
             store_out<F32>(q.p.out, (size_t)(m0 + i) * (size_t)q.p.N + (size_t)n,
-                           __fmul_rn(__fmul_rn((float)sum[i], __ldg(q.p.a_scale + m0 + i)), ws));
+                           __fmul_rn(__fmul_rn((float)sum[i], as[i]), ws));
 }
 
 }  // namespace beam

@@ -55,6 +55,8 @@ SHAPES = [
     (257, 255, 640), (517, 2565, 2576), (300, 4096, 256), (1000, 777, 336), (2048, 2048, 5120),
     # enough tiles for pairs of CTAs: one ragged wave, and several
     (2100, 2600, 400), (4100, 5000, 144), (2048, 2570, 256), (2500, 3333, 160),
+    # whole waves and shared tiles: single CTAs, pairs
+    (16, 20480, 1040), (700, 5120, 2560), (1030, 5110, 2064), (150, 300, 20480),
 ]
 
 
