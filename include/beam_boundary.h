@@ -229,8 +229,8 @@ BEAM_API beam_status beam_router_sigmoid_fast(beam_stream_t stream, const float*
  *   topk_idx    [T, topk] int32 in [0, E), topk in [1, BEAM_ROUTE_MAX_TOPK]
  *   seq_offsets [S + 1] int32, non-decreasing, within [0, T]: sequence i holds the
  *               tokens seq_offsets[i] .. seq_offsets[i + 1] - 1; or NULL for one
- *               sequence of T tokens (S = 1). Tokens of no sequence (padding) are
- *               not read. An empty sequence has loss 0 and counts 0.
+ *               sequence of T tokens (S = 1). Tokens of no sequence (padding) count
+ *               for nothing, whatever their rows hold. An empty sequence has loss 0 and counts 0.
  *   loss [S] FP32; counts [S, E] int32, 16-byte aligned; every element written
  *   workspace   device memory for this call alone, 16-byte aligned, of at least
  *               beam_moe_balance_workspace(T, E, S) bytes; need not be cleared

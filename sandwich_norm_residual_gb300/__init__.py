@@ -526,7 +526,7 @@ def moe_balance_loss(logits, topk_idx, alpha: float, seq_offsets=None, loss=None
 
     logits: [T, E] float32; topk_idx: [T, topk] int32, as ``moe_route`` gives them;
     seq_offsets: [S + 1] int32 first tokens of the sequences and the end of the last (None: one
-    sequence); tokens outside are padding and not read.
+    sequence); tokens outside are padding and count for nothing.
     Returns (loss float32 [S], counts int32 [S, E]).
     """
     import torch

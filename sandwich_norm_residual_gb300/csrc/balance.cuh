@@ -55,13 +55,20 @@ __device__ __forceinline__ long long seq_end(const BalanceParams& p, int s) {
     return p.off ? (long long)__ldg(p.off + s + 1) : p.T;
 }
 
-// the first sequence that ends behind token t (S: none does)
+// The first sequence that ends behind token t (S: none does); the whole warp. 32
+// places are looked at in one way to memory, where halving the range takes one for
+// each bit of S.
 __device__ __forceinline__ int find_seq(const BalanceParams& p, long long t) {
-    int lo = 0, hi = p.S;
-    while (lo < hi) {
-        const int mid = lo + (hi - lo) / 2;
-        if (seq_end(p, mid) > t) hi = mid;
-        else lo = mid + 1;
+    int lo = 0, n = p.S;  // the answer lies in [lo, lo + n]
+    const int lane = threadIdx.x & 31;
+    while (n > 0) {
+        const int step = (n + 31) / 32, at = lo + min((lane + 1) * step, n) - 1;
+        const unsigned behind = __ballot_sync(0xFFFFFFFFu, seq_end(p, at) > t);
+        // the sequences before the first place that lies behind t do not
+        const int k = behind ? __ffs(behind) - 1 : 32;
+        const int skipped = min(k * step, n);
+        lo += skipped;
+        n = behind ? min(step, n - skipped) - 1 : 0;
     }
     return lo;
 }
@@ -133,6 +140,16 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_records_kernel(const 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
     const long long t0 = (long long)blockIdx.x * p.chunk, t1 = min(t0 + p.chunk, p.T);
+    // this warp's tokens, across the sequences; the next one's row is on its way
+    // before anything else is known
+    long long t = t0 + warp;
+    float4 nx[V];
+    if (t < t1) load_row<V>(p, t, lane, nx);
+    auto skip = [&](long long hi) {
+        if (t >= hi) return;
+        t += (hi - t + kBalanceWarps - 1) / kBalanceWarps * kBalanceWarps;
+        if (t < t1) load_row<V>(p, t, lane, nx);
+    };
     for_sequences(p, t0, t1, [&](int s, long long lo, long long hi) {
         for (int e = tid; e < V * 128; e += kBalanceThreads) sc[e] = 0;
         __syncthreads();
@@ -145,13 +162,11 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_records_kernel(const 
         float4 q[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) q[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-        float4 nx[V];
-        if (lo + warp < hi) load_row<V>(p, lo + warp, lane, nx);
-        for (long long t = lo + warp; t < hi; t += kBalanceWarps) {
+        for (; t < hi; t += kBalanceWarps) {
             float4 z[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) z[v] = nx[v];
-            if (t + kBalanceWarps < hi) load_row<V>(p, t + kBalanceWarps, lane, nx);
+            if (t + kBalanceWarps < t1) load_row<V>(p, t + kBalanceWarps, lane, nx);
             float sum = 0.f, unused;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -182,7 +197,7 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_records_kernel(const 
             p.rec_c[rec + e] = sc[e];
         }
         __syncthreads();
-    }, [](long long, long long) {});
+    }, [&](long long, long long hi) { skip(hi); });
 }
 
 // One block a sequence: its records added in order (groups of threads take
@@ -255,9 +270,14 @@ template <int V>
 __global__ void __launch_bounds__(kBalanceThreads) balance_grad_kernel(const BalanceParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long t0 = (long long)blockIdx.x * p.chunk, t1 = min(t0 + p.chunk, p.T);
-    for_sequences(p, t0, t1, [&](int s, long long lo, long long hi) {
-        const double n = (double)(min(seq_end(p, s), p.T) - max(seq_begin(p, s), 0ll));
-        const float g = (float)((double)__ldg(p.dloss + s) * p.factor / (n * n));
+    const float factor = (float)p.factor;
+    long long t = t0 + warp;  // this warp's tokens, across the sequences
+    float4 nx[V];
+    if (t < t1) load_row<V>(p, t, lane, nx);
+    for_sequences(p, t0, t1, [&](int s, long long, long long hi) {
+        // in FP32, a few roundings: FP64 here took 4 us of every block
+        const float n = (float)(min(seq_end(p, s), p.T) - max(seq_begin(p, s), 0ll));
+        const float g = __fdiv_rn(__fdiv_rn(__fmul_rn(__ldg(p.dloss + s), factor), n), n);
         float4 c[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -266,13 +286,11 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_grad_kernel(const Bal
                                    : make_int4(0, 0, 0, 0);
             c[v] = make_float4((float)k.x, (float)k.y, (float)k.z, (float)k.w);
         }
-        float4 nx[V];
-        if (lo + warp < hi) load_row<V>(p, lo + warp, lane, nx);
-        for (long long t = lo + warp; t < hi; t += kBalanceWarps) {
+        for (; t < hi; t += kBalanceWarps) {
             float4 z[V], d[V];  // d: s (1 - s)
 #pragma unroll
             for (int v = 0; v < V; ++v) z[v] = nx[v];
-            if (t + kBalanceWarps < hi) load_row<V>(p, t + kBalanceWarps, lane, nx);
+            if (t + kBalanceWarps < t1) load_row<V>(p, t + kBalanceWarps, lane, nx);
             float sum = 0.f, mix = 0.f;
             // 1 - s is e s, which keeps its digits where s is near 1; where z < 0
             // (e may be infinite there) 1 - s itself loses none
@@ -301,12 +319,15 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_grad_kernel(const Bal
                                        d[v].z * f * (c[v].z - mean), d[v].w * f * (c[v].w - mean)));
             }
         }
-    }, [&](long long lo, long long hi) {
+    }, [&](long long, long long hi) {
         // tokens of no sequence: no gradient
-        for (long long t = lo + warp; t < hi; t += kBalanceWarps)
+        for (; t < hi; t += kBalanceWarps) {
             for (int e = 4 * lane; e < p.E; e += 128)
                 __stcs(reinterpret_cast<float4*>(p.dlogits + (size_t)t * (size_t)p.E + e),
                        make_float4(0.f, 0.f, 0.f, 0.f));
+            if (t + kBalanceWarps < hi) continue;
+            if (t + kBalanceWarps < t1) load_row<V>(p, t + kBalanceWarps, lane, nx);
+        }
     });
 }
 

@@ -180,7 +180,7 @@ beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* pa
     // started early where it follows the shared steps alone: behind whole waves its
     // blocks, waiting on the SMs that are done, cost 2 us
     return launch(reinterpret_cast<const void*>(beam::matmul_int8_join_kernel<NT, CG, F32>),
-                  dim3(shared, NT / beam::kJoinCols, CG), dim3(beam::kTileN), join_args, 0, stream, q.waves == 0);
+                  dim3(shared, NT / beam::Join<NT>::kCols, CG), dim3(beam::kTileN), join_args, 0, stream, q.waves == 0);
 }
 
 // Tokens a tile: as few as hold M; beyond 128, single CTAs or pairs, whichever

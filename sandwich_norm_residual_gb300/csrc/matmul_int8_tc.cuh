@@ -497,15 +497,20 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
 }
 
 // Adds the sums of the tiles that several workers have steps of: a block for
-// kJoinCols tokens of a tile, thread = channel. They are integers (FP32 ones),
-// added as such. What it takes (3 us) is its launch and one way to L2 and back,
-// so few values a thread and eight workers' at once.
-constexpr int kJoinCols = 2, kJoinWorkers = 8;
+// kCols tokens of a tile, thread = channel. They are integers (FP32 ones), added
+// as such. What it takes (3 us) is its launch and one way to L2 and back, so few
+// values a thread (but not so few that blocks are counted in thousands: 2 tokens a
+// block cost 3 us more than 8 at NT = 128) and several workers' at once.
+template <int NT>
+struct Join {
+    static constexpr int kCols = NT <= 32 ? 2 : NT == 64 ? 4 : 8, kWorkers = NT <= 64 ? 8 : 4;
+};
 
 template <int NT, int CG, bool F32>
 __global__ void __launch_bounds__(kTileN) matmul_int8_join_kernel(const __grid_constant__ MatmulTcParams q) {
     pdl_trigger();
     const uint32_t tile = q.waves * q.workers + blockIdx.x;
+    constexpr int kJoinCols = Join<NT>::kCols, kJoinWorkers = Join<NT>::kWorkers;
     const uint32_t rank = blockIdx.z;  // the CTA's 128 channels of the tile
     const int n = (int)((tile / q.m_tiles * CG + rank) * kTileN + threadIdx.x), c0 = blockIdx.y * kJoinCols;
     const long long m0 = (long long)(tile % q.m_tiles) * NT + c0;
