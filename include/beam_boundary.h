@@ -337,8 +337,11 @@ BEAM_API beam_status beam_qk_norm_ex(beam_stream_t stream, uint16_t* q, uint16_t
  * acc = 0 NaN (0 * inf), as the FP32 products above say.
  * flags: BEAM_OPT_PDL launches with programmatic stream serialisation: the
  * kernel reads w before the previous kernel on the stream has completed (that
- * kernel must not write w), and everything else after. Any other flag gives
- * BEAM_ERR_ARG.
+ * kernel must not write w), and everything else after. BEAM_OPT_TEST_WAIT_TIMEOUT
+ * is a test hook for the bounded waits of the kernels for more than 8 tokens: the
+ * copies of every tile's second 128 k are never issued, the waits for them give up
+ * after 1 ms, out holds anything and beam_sync_status returns BEAM_ERR_TIMEOUT.
+ * Any other flag, and the hook with 8 tokens or fewer, gives BEAM_ERR_ARG.
  */
 BEAM_API beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, const float* a_scale,
                                       const int8_t* w, const float* w_scale, int64_t M, int N,

@@ -152,7 +152,8 @@ int64_t part_bytes(const beam::MatmulTcParams& q) {
 
 template <int NT, int CG, bool F32>
 beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* part, int64_t workspace_bytes,
-                        cudaStream_t stream, bool pdl) {
+                        cudaStream_t stream, uint32_t flags) {
+    const bool pdl = (flags & BEAM_OPT_PDL) != 0, drop = (flags & BEAM_OPT_TEST_WAIT_TIMEOUT) != 0;
     using C = beam::TileConfig<NT, CG>;
     static std::atomic<unsigned long long> allowed{0};
     const void* fn = reinterpret_cast<const void*>(beam::matmul_int8_tile_kernel<NT, CG, F32>);
@@ -169,7 +170,8 @@ beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* pa
     if (!q.wide) pmap = wmap;
     else if (!permuted_map(&pmap, p.w, p.N, p.K)) return BEAM_ERR_CUDA;
     q.part = static_cast<float*>(part);
-    q.wait_ns = beam::kMatmulWaitNs;
+    q.wait_ns = drop ? beam::kMatmulTestWaitNs : beam::kMatmulWaitNs;
+    q.drop = drop;
     q.status = dev.status_word;
     const uint32_t workers = q.waves ? (q.tiles < q.workers ? q.tiles : q.workers) : q.sharers;
     void* args[] = {&wmap, &pmap, &amap, &q};
@@ -205,13 +207,13 @@ Shape choose(const MatmulParams& p) {
 
 template <bool F32>
 beam_status launch_tiles(Shape shape, const MatmulParams& p, const beam::Device& dev, void* part, int64_t bytes,
-                         cudaStream_t stream, bool pdl) {
+                         cudaStream_t stream, uint32_t flags) {
     switch (shape) {
-    case Shape::k16: return launch_tile<16, 1, F32>(p, dev, part, bytes, stream, pdl);
-    case Shape::k32: return launch_tile<32, 1, F32>(p, dev, part, bytes, stream, pdl);
-    case Shape::k64: return launch_tile<64, 1, F32>(p, dev, part, bytes, stream, pdl);
-    case Shape::k128: return launch_tile<128, 1, F32>(p, dev, part, bytes, stream, pdl);
-    default: return launch_tile<256, 2, F32>(p, dev, part, bytes, stream, pdl);
+    case Shape::k16: return launch_tile<16, 1, F32>(p, dev, part, bytes, stream, flags);
+    case Shape::k32: return launch_tile<32, 1, F32>(p, dev, part, bytes, stream, flags);
+    case Shape::k64: return launch_tile<64, 1, F32>(p, dev, part, bytes, stream, flags);
+    case Shape::k128: return launch_tile<128, 1, F32>(p, dev, part, bytes, stream, flags);
+    default: return launch_tile<256, 2, F32>(p, dev, part, bytes, stream, flags);
     }
 }
 
@@ -244,7 +246,9 @@ beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, const float*
                              int64_t workspace_bytes, uint32_t flags) {
     if (bad_shape(M, N, K)) return BEAM_ERR_SHAPE;
     const int64_t need = beam_matmul_int8_workspace(M, N, K);
-    if ((out_type != BEAM_OUT_BF16 && out_type != BEAM_OUT_FP32) || workspace_bytes < need || (flags & ~BEAM_OPT_PDL))
+    if ((out_type != BEAM_OUT_BF16 && out_type != BEAM_OUT_FP32) || workspace_bytes < need ||
+        (flags & ~(BEAM_OPT_PDL | BEAM_OPT_TEST_WAIT_TIMEOUT)) ||
+        ((flags & BEAM_OPT_TEST_WAIT_TIMEOUT) && choose({nullptr, nullptr, nullptr, nullptr, nullptr, M, N, K}) == Shape::kFew))
         return BEAM_ERR_ARG;
     if (M == 0 || N == 0) return BEAM_OK;
     if (!a || !a_scale || !w || !w_scale || !out || (need && !workspace)) return BEAM_ERR_NULL;
@@ -267,16 +271,16 @@ beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, const float*
     if (st != BEAM_OK) return st;
     MatmulParams p{a, a_scale, w, w_scale, out, M, N, K};
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    const bool pdl = (flags & BEAM_OPT_PDL) != 0;
     const Shape shape = choose(p);
     if (shape != Shape::kFew)
-        return f32 ? launch_tiles<true>(shape, p, dev, workspace, workspace_bytes, cs, pdl)
-                   : launch_tiles<false>(shape, p, dev, workspace, workspace_bytes, cs, pdl);
+        return f32 ? launch_tiles<true>(shape, p, dev, workspace, workspace_bytes, cs, flags)
+                   : launch_tiles<false>(shape, p, dev, workspace, workspace_bytes, cs, flags);
     void* args[] = {&p};
     int channels = 0;
     const void* fn = f32 ? few_kernel<true>(M, &channels) : few_kernel<false>(M, &channels);
     const int per_block = channels * beam::kFewWarps;
-    return launch(fn, dim3((unsigned)((N + per_block - 1) / per_block)), dim3(32 * beam::kFewWarps), args, 0, cs, pdl);
+    return launch(fn, dim3((unsigned)((N + per_block - 1) / per_block)), dim3(32 * beam::kFewWarps), args, 0, cs,
+                  (flags & BEAM_OPT_PDL) != 0);
 }
 
 }  // extern "C"

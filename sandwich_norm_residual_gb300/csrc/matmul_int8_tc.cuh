@@ -31,6 +31,7 @@ constexpr int kTileN = 128;                         // channels of a CTA: the la
 constexpr int kStepCols = kStepK / 2;               // columns of A for a step (two FP16 a column)
 constexpr uint32_t kABytes = kTileN * kStepK;       // int8 channels of a step
 constexpr uint64_t kMatmulWaitNs = 2000000000ull;   // every wait gives up after 2 s
+constexpr uint64_t kMatmulTestWaitNs = 1000000ull;  // the test hook's: 1 ms
 
 struct MatmulTcParams {
     MatmulParams p;
@@ -47,6 +48,7 @@ struct MatmulTcParams {
     int wide;
     float* part;              // [workers][CG][2][NT][128]: sums of tiles that a worker has a part of
     uint64_t wait_ns;
+    int drop;                 // test hook: the second step's copies are never issued
     unsigned int* status;
 };
 
@@ -288,11 +290,13 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
             if (a_side) tma_prefetch_map(&amap);
             const uint64_t pol_w = q.m_tiles == 1 ? l2_evict_first() : l2_evict_normal(), pol_a = l2_evict_normal();
             auto load_w = [&](int slot, const Segment& s, int k) {
+                if (q.drop && k == 1) return;
                 unsigned char* dst = smem + slot * C::kSlotBytes;
                 if (permuted(s)) tma_load_5d(dst, &pmap, k * kStepK, s.n0 / 32, &raw_full[slot], pol_w);
                 else tma_load_2d(dst, &wmap, k * kStepK, s.n0, &raw_full[slot], pol_w);
             };
             auto load_a = [&](int slot, const Segment& s, int k) {
+                if (q.drop && k == 1) return;
                 tma_load_2d(smem + slot * C::kSlotBytes + kABytes, &amap, k * kStepK,
                             s.m0 + (int)rank * C::kRows, &raw_full[slot], pol_a);
             };

@@ -251,3 +251,25 @@ def test_routing_then_balance():
     assert np.array_equal(counts.cpu().numpy(), ref[1]) and int(counts.sum()) == 8 * T
     assert abs(loss.item() - ref[0][0]) <= REL * ref[0][0]
     assert np.all(np.abs(dz.cpu().numpy() - ref[2]) <= REL * ref[3] + 2.0 ** -140)
+
+
+@pytest.mark.slow
+def test_more_logits_than_32_bits_count():
+    T, E, K = 8_500_000, 256, 2  # 2.2e9 logits
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    z = torch.randn((T, E), device="cuda", generator=g)
+    idx = torch.randint(0, E, (T, K), device="cuda", generator=g, dtype=torch.int32)
+    cut = T - 1000
+    off = torch.tensor([0, cut, T], dtype=torch.int32, device="cuda")
+    loss, counts = snr.moe_balance_loss(z, idx, 1.0, seq_offsets=off)
+    d = torch.ones(2, device="cuda")
+    dz = snr.moe_balance_loss_backward(d, z, counts, K, 1.0, seq_offsets=off)
+    snr.sync_status()
+    tail = want(z[cut:].cpu().numpy(), idx[cut:].cpu().numpy(), [0, T - cut], 1.0, np.ones(1))
+    assert np.array_equal(counts[1].cpu().numpy(), tail[1][0])
+    assert abs(loss[1].item() - tail[0][0]) <= REL * tail[0][0]
+    assert np.all(np.abs(dz[cut:].cpu().numpy() - tail[2]) <= REL * tail[3] + 2.0 ** -140)
+    assert torch.equal(counts[0], torch.bincount(idx[:cut].reshape(-1), minlength=E).int())
+    # 1.0 * sum f P with counts and probabilities near uniform
+    assert abs(loss[0].item() - 1.0) < 1e-3

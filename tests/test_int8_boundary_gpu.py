@@ -180,3 +180,16 @@ def test_no_tokens_and_a_side_stream():
     side.wait_stream(torch.cuda.current_stream())
     torch.cuda.synchronize()
     same(run(inp, 2, 1e-6, stream=side), want(inp, 2, 1e-6))
+
+
+@pytest.mark.slow
+def test_rows_past_32_bits():
+    T, D = 420_000, 5120  # 2.15e9 elements
+    w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    h = torch.randn((T, D), dtype=torch.bfloat16, device="cuda")
+    x = torch.randn((T, D), dtype=torch.bfloat16, device="cuda")
+    tail = slice(T - 100, T)
+    inp = dict(h=h[tail].cpu(), x=x[tail].cpu(), post_w=w.cpu(), pre_w=w.cpu())
+    q, s = snr.boundary_fused_int8(h, x, w, w, 9)
+    snr.sync_status()
+    same((bits(h[tail]), q[tail].cpu().numpy(), s[tail].cpu().numpy()), want(inp, 9, 1e-6))

@@ -91,6 +91,7 @@ def test_matmul_argument_errors(lib):
         assert mm(K=K) == _lib.BEAM_ERR_SHAPE
     assert mm(ty=2) == _lib.BEAM_ERR_ARG
     assert mm(flags=_lib.BEAM_OPT_FORCE_EXACT_SUM) == _lib.BEAM_ERR_ARG
+    assert mm(flags=_lib.BEAM_OPT_TEST_WAIT_TIMEOUT) == _lib.BEAM_ERR_ARG  # nothing waits for 8 tokens or fewer
     assert mm(M=0, a=None) == _lib.BEAM_OK
     assert mm(N=0, w=None) == _lib.BEAM_OK
     for name in ("a", "sa", "w", "sw", "o"):

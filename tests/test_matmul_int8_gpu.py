@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import sandwich_norm_residual_gb300 as snr
-from sandwich_norm_residual_gb300 import build
+from sandwich_norm_residual_gb300 import _lib, build
 
 pytestmark = pytest.mark.gpu
 
@@ -57,6 +57,8 @@ SHAPES = [
     (2100, 2600, 400), (4100, 5000, 144), (2048, 2570, 256), (2500, 3333, 160),
     # whole waves and shared tiles: single CTAs, pairs
     (16, 20480, 1040), (700, 5120, 2560), (1030, 5110, 2064), (150, 300, 20480),
+    # fewer channels than a tile of them
+    (20, 1, 32), (300, 3, 16), (150, 127, 144),
 ]
 
 
@@ -186,3 +188,89 @@ def test_boundary_then_product_in_a_graph(T):
     full = y.double().cpu() @ (w.double() * sw.double()[:, None]).cpu().t()
     lim = (0.5 + 2.0 ** -16) * s.double().cpu()[:, None] * (w.double().abs().sum(1) * sw.double()).cpu()[None, :]
     assert ((out.double().cpu() - full).abs() <= lim + 2.0 ** -8 * (full.abs() + lim)).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 200, 1024), (100, 5120, 2560), (2048, 2560, 640)])
+def test_waits_run_out_and_the_next_call_is_whole(M, N, K):
+    a, sa, w, sw = inputs(M, N, K, 4)
+    d = [torch.from_numpy(v).cuda() for v in (a, sa, w, sw)]
+    out = torch.zeros((M, N), device="cuda")
+    nb = _lib.load().beam_matmul_int8_workspace(M, N, K)
+    ws = torch.empty(max(nb, 16), dtype=torch.uint8, device="cuda")
+    st = _lib.load().beam_matmul_int8(torch.cuda.current_stream().cuda_stream or None, *(t.data_ptr() for t in d), M,
+                                      N, K, _lib.BEAM_OUT_FP32, out.data_ptr(), ws.data_ptr(), nb,
+                                      _lib.BEAM_OPT_TEST_WAIT_TIMEOUT)
+    assert st == _lib.BEAM_OK
+    with pytest.raises(snr.BeamError) as e:
+        snr.sync_status()
+    assert e.value.status == _lib.BEAM_ERR_TIMEOUT
+    check((a, sa, w, sw))
+
+
+def test_two_streams_at_once():
+    """Products of every kernel in flight on two streams, each with its own workspace."""
+    shapes = [(1, 700, 2048), (30, 1500, 4096), (64, 2000, 2048), (200, 1000, 2048), (2048, 2560, 512)]
+    jobs = []
+    for i, s in enumerate(shapes):
+        ops = inputs(*s, i)
+        jobs.append(([torch.from_numpy(v).cuda() for v in ops], torch.from_numpy(want(*ops))))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for r in range(10):
+        for k, st in enumerate(streams):
+            for j in range(len(jobs)):
+                d, ref = jobs[(j + k * 2 + r) % len(jobs)]
+                with torch.cuda.stream(st):
+                    outs.append((snr.matmul_int8(*d, out_dtype=torch.float32), ref))
+    torch.cuda.synchronize()
+    snr.sync_status()
+    for got, ref in outs:
+        assert torch.equal(got.cpu(), ref)
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("M,N,K", [(66000, 33000, 16), (70000, 130, 65536), (20, 70000, 65536)])
+def test_operands_and_results_past_32_bits(M, N, K):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    a = torch.randint(-5, 6, (M, K), dtype=torch.int8, device="cuda", generator=g)
+    w = torch.randint(-5, 6, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    sa, sw = torch.rand(M, device="cuda") + 0.5, torch.rand(N, device="cuda") + 0.5
+    out = snr.matmul_int8(a, sa, w, sw)
+    snr.sync_status()
+    for m in (slice(0, 64), slice(M // 2, M // 2 + 64), slice(M - 64, M)):
+        for n in (slice(0, 64), slice(N - 64, N)):
+            ref = (a[m].double() @ w[n].double().t()).float() * sa[m][:, None] * sw[n][None, :]
+            assert torch.equal(out[m, n], ref.to(torch.bfloat16))
+
+
+def test_a_timeline_of_boundary_product_norm_and_routing():
+    """An int8 decoder layer's front half: boundary, query and key projections, per-head norm; then the
+    router's FP32 logits from the same int8 rows, routing, the balance of its choices, and the int8
+    combine of the experts' outputs."""
+    T, D = 48, 1024
+    rng = np.random.default_rng(0)
+    bf = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(torch.bfloat16).cuda()  # noqa: E731
+    i8 = lambda *s: torch.from_numpy(rng.integers(-127, 128, s, dtype=np.int8)).cuda()  # noqa: E731
+    h, x, pw, qw = bf(T, D), bf(T, D), bf(D), bf(D)
+    y, s = snr.boundary_fused_int8(h, x, pw, qw, 5)
+    wq, wk, wr = i8(8 * 128, D), i8(2 * 128, D), i8(256, D)
+    sq, sk, sr = (torch.full((w.shape[0],), 1e-3, device="cuda") for w in (wq, wk, wr))
+    q = snr.matmul_int8(y, s, wq, sq).view(T, 8, 128)
+    k = snr.matmul_int8(y, s, wk, sk).view(T, 2, 128)
+    logits = snr.matmul_int8(y, s, wr, sr, out_dtype=torch.float32)
+    q0 = q.clone()
+    one = torch.ones(128, dtype=torch.bfloat16, device="cuda")
+    snr.qk_norm(q, k, one, one, torch.arange(T, dtype=torch.int32, device="cuda"), mode="ssmax")
+    idx, wts = snr.moe_route(logits, torch.zeros(256, device="cuda"))
+    loss, counts = snr.moe_balance_loss(logits, idx, 0.01)
+    e = bf(T, 8, D)
+    y2, s2 = snr.moe_combine_boundary_int8(h, e, wts, pw, qw, 6)
+    snr.sync_status()
+    yn, sn = y.cpu().numpy(), s.cpu().numpy()
+    for got, w, sw in ((q0.view(T, -1), wq, sq), (logits, wr, sr)):
+        ref = torch.from_numpy(want(yn, sn, w.cpu().numpy(), sw.cpu().numpy()))
+        assert torch.equal(got.cpu(), ref.to(got.dtype))
+    assert int(counts.sum()) == 8 * T and torch.isfinite(loss).all()
+    assert int(y2.abs().amax()) == 127 and torch.isfinite(s2).all()
