@@ -38,20 +38,25 @@ WORKLOAD = (f"layer boundary pair, T={T_TOKENS} tokens per GPU, D={D}: dense bou
 # DRAM traffic per launch from one ncu capture (dram__bytes_read.sum +
 # dram__bytes_write.sum), valid only for the kernel source it was taken on.
 NCU_TRAFFIC = {
-    "moe": {"bytes_per_launch": 1_511_092_480 + 300_573_440, "source_sha": "b6b335c48b9cdff0"},
-    "dense": {"bytes_per_launch": 335_653_376 + 264_058_624, "source_sha": "b6b335c48b9cdff0"},
+    "moe": {"bytes_per_launch": 1_511_711_232 + 301_067_520, "source_sha": "ee686e2405c42fca"},
+    "dense": {"bytes_per_launch": 335_664_384 + 265_312_512, "source_sha": "ee686e2405c42fca"},
 }
 
 # Routing is bound by instruction issue, not HBM: its warp-instructions per
 # launch at T = 16384 (ncu smsp__inst_executed.sum) give its issue roofline,
 # valid while the kernel source matches.
-ROUTE_ISSUE = {"warp_instructions_per_launch": 11_224_712, "source_sha": "b6b335c48b9cdff0"}
+ROUTE_ISSUE = {"warp_instructions_per_launch": 11_225_399, "source_sha": "ee686e2405c42fca"}
+
+
+# the sources of the kernels that those captures are of
+CAPTURED_SOURCES = ("beam_boundary.cu", "boundary_kernels.cuh", "packed.cuh", "route.cuh",
+                    "router_sigmoid.cuh", "row_sum.cuh", "status.cuh", "tma.cuh")
 
 
 def kernel_source_sha() -> str:
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "sandwich_norm_residual_gb300", "csrc")
-    for f in sorted(os.listdir(csrc)):
+    for f in CAPTURED_SOURCES:
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]
@@ -383,6 +388,16 @@ def nvfp4_bytes(T: int, moe: bool) -> int:
 QK_HEADS, QK_KV_HEADS, QK_DIM, QK_SEQ = 48, 8, 128, 2048
 
 
+def int8_bytes(T: int, moe: bool) -> int:
+    """h and the branch (x, or 8 expert rows and weights) read, h', the codes and a scale written."""
+    branch = T * (16 * D + 32) if moe else T * 2 * D
+    return T * 2 * D + branch + T * 2 * D + T * D + 4 * T + 4 * D
+
+
+def matmul_int8_bytes(M: int, N: int, K: int, out_size: int = 2) -> int:
+    return (M + N) * (K + 4) + M * N * out_size
+
+
 def qk_bytes(T: int, rope: bool) -> int:
     # q and k read and written in place, one position per token, the two weight
     # vectors; RoPE also reads the cos|sin table once (2048 positions x 128 FP32)
@@ -492,6 +507,48 @@ def next_rows(snr, device, dev, peak: float, sm_mhz: float | None = None) -> dic
         mo["h"], mo["expert_out"], mo["topk_w"], mo["post_w"], mo["pre_w"], MOE_N, EPS, gs,
         y_fp4=yq, y_scale=ys, stream=stream), stream)
     out["moe_boundary_nvfp4"] = dict(entry(us, nvfp4_bytes(T, True)), launches=nl)
+    del yq, ys
+
+    # the boundaries with y as int8, and the query projection (48 heads of 128) that
+    # reads the dense one's rows: of the whole prefill, of 64 tokens and of one
+    yi = torch.empty((T, D), dtype=torch.int8, device=device)
+    yis = torch.empty(T, dtype=torch.float32, device=device)
+    us, nl = _time_launches(lambda i: snr.moe_combine_boundary_int8(
+        mo["h"], mo["expert_out"], mo["topk_w"], mo["post_w"], mo["pre_w"], MOE_N, EPS, y_int8=yi,
+        y_scale=yis, stream=stream), stream)
+    out["moe_boundary_int8"] = dict(entry(us, int8_bytes(T, True)), launches=nl)
+    us, nl = _time_launches(lambda i: snr.boundary_fused_int8(
+        dn["h"], dn["x"], dn["post_w"], dn["pre_w"], DENSE_N, EPS, y_int8=yi, y_scale=yis,
+        stream=stream), stream)
+    out["dense_boundary_int8"] = dict(entry(us, int8_bytes(T, False)), launches=nl)
+    N = QK_HEADS * QK_DIM
+    gen = torch.Generator(device=device)
+    gen.manual_seed(3)
+    nbuf = 8  # 252 MB of weights in turn: L2 holds half
+    wi = torch.randint(-127, 128, (nbuf, N, D), dtype=torch.int8, device=device, generator=gen)
+    ws = torch.full((N,), 1e-3, dtype=torch.float32, device=device)
+    for M in (T, 64, 1):
+        o = torch.empty((M, N), dtype=torch.bfloat16, device=device)
+        us, nl = _time_launches(lambda i, M=M, o=o: snr.matmul_int8(
+            yi[:M], yis[:M], wi[i % nbuf], ws, out=o, stream=stream), stream)
+        row = dict(entry(us, matmul_int8_bytes(M, N, D)), launches=nl)
+        row["TFLOPs"] = round(2 * M * N * D / (us * 1e-6) / 1e12, 1)
+        out[f"matmul_int8_M{M}"] = row
+    del wi, yi, o
+
+    # the router's balance loss over 8 sequences, and its gradient; four buffers of logits in turn
+    nbuf = 4
+    z = torch.from_numpy((synth.normal(3, 8, nbuf * T * 256) * 2.0).reshape(nbuf, T, 256)).to(device)
+    off = torch.arange(0, T + 1, T // 8, dtype=torch.int32, device=device)
+    loss = torch.empty(8, dtype=torch.float32, device=device)
+    counts = torch.empty((8, 256), dtype=torch.int32, device=device)
+    dz = torch.empty((T, 256), dtype=torch.float32, device=device)
+    us, nl = _time_launches(lambda i: snr.moe_balance_loss(
+        z[i % nbuf], idx, 1e-3, seq_offsets=off, loss=loss, counts=counts, stream=stream), stream)
+    out["balance_loss"] = dict(entry(us, T * (4 * 256 + 4 * 8)), launches=nl)
+    us, nl = _time_launches(lambda i: snr.moe_balance_loss_backward(
+        loss, z[i % nbuf], counts, 8, 1e-3, seq_offsets=off, dlogits=dz, stream=stream), stream)
+    out["balance_loss_backward"] = dict(entry(us, T * 8 * 256), launches=nl)
     snr.sync_status(stream)
     return out
 

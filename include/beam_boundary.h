@@ -325,7 +325,8 @@ BEAM_API beam_status beam_qk_norm_ex(beam_stream_t stream, uint16_t* q, uint16_t
  *   a       [M, K] int8 tokens (all 256 codes); 16-byte aligned
  *   a_scale [M] FP32; w_scale [N] FP32; 4-byte aligned
  *   w       [N, K] int8 channels (one row per output channel); 16-byte aligned
- *   K       a multiple of 16, 16 <= K <= BEAM_MATMUL_MAX_K
+ *   K       a multiple of 16 (so must be the D of an int8 boundary that feeds it),
+ *           16 <= K <= BEAM_MATMUL_MAX_K
  *   M, N    0 launches nothing; M at most 2^31 - 1, ceil(M/128) ceil(N/128) too
  *   out     [M, N], BF16 for BEAM_OUT_BF16, FP32 for BEAM_OUT_FP32; aligned to
  *           its element

@@ -380,7 +380,7 @@ def boundary_fused_int8(h, x, post_w, pre_w, n: int, eps: float = 1e-6, y_int8=N
         q = torch.empty(rows, dtype=torch.int8, device=h.device)
         scale = torch.empty(T, dtype=torch.float32, device=h.device)
     st = _lib.load().beam_boundary_fused_int8(_raw_stream(stream, h), h.data_ptr(), x.data_ptr(),
-                                              post_w.data_ptr(), pre_w.data_ptr(), n, eps, T, D,
+                                              post_w.data_ptr(), pre_w.data_ptr(), int(n), float(eps), T, D,
                                               q.data_ptr(), scale.data_ptr(), _opts(opts))
     if st != 0:
         raise BeamError(st, "beam_boundary_fused_int8")
@@ -415,7 +415,7 @@ def moe_combine_boundary_int8(h, expert_out, topk_w, post_w, pre_w, n: int, eps:
         scale = torch.empty(T, dtype=torch.float32, device=h.device)
     st = _lib.load().beam_moe_combine_boundary_int8(
         _raw_stream(stream, h), h.data_ptr(), expert_out.data_ptr(), topk_w.data_ptr(),
-        route_scale, post_w.data_ptr(), pre_w.data_ptr(), n, eps, T, D,
+        float(route_scale), post_w.data_ptr(), pre_w.data_ptr(), int(n), float(eps), T, D,
         q.data_ptr(), scale.data_ptr(), _opts(opts))
     if st != 0:
         raise BeamError(st, "beam_moe_combine_boundary_int8")
@@ -555,7 +555,7 @@ def moe_balance_loss(logits, topk_idx, alpha: float, seq_offsets=None, loss=None
     ws = _workspace(ws_bytes, logits.device, stream)
     st = _lib.load().beam_moe_balance_loss(
         _raw_stream(stream, logits), logits.data_ptr(), topk_idx.data_ptr(),
-        None if seq_offsets is None else seq_offsets.data_ptr(), T, E, K, S, alpha, loss.data_ptr(),
+        None if seq_offsets is None else seq_offsets.data_ptr(), T, E, K, S, float(alpha), loss.data_ptr(),
         counts.data_ptr(), ws.data_ptr() if ws_bytes else None, ws_bytes)
     if st != 0:
         raise BeamError(st, "beam_moe_balance_loss")
@@ -590,7 +590,7 @@ def moe_balance_loss_backward(dloss, logits, counts, topk: int, alpha: float, se
                                     dlogits=dlogits))
     st = _lib.load().beam_moe_balance_loss_backward(
         _raw_stream(stream, logits), dloss.data_ptr(), logits.data_ptr(), counts.data_ptr(),
-        None if seq_offsets is None else seq_offsets.data_ptr(), T, E, topk, S, alpha, dlogits.data_ptr())
+        None if seq_offsets is None else seq_offsets.data_ptr(), T, E, int(topk), S, float(alpha), dlogits.data_ptr())
     if st != 0:
         raise BeamError(st, "beam_moe_balance_loss_backward")
     return dlogits

@@ -279,6 +279,10 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
     Schedule<NT, CG> todo(q, worker, rank);
     Segment seg;
     int it = 0, n_seg = 0;  // steps and segments so far
+    // Before any bounded wait, for the kernel before this one: it may run for longer
+    // than the bound, and nothing arrives until it is done. The loading warps wait
+    // for it behind their first copies.
+    if (warp < kLoadWarp || warp >= kMulWarp) pdl_wait();
 
     if (warp >= kLoadWarp && warp < kMulWarp) {
         if (lane == 0) {
@@ -410,7 +414,6 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
         // with the channels' order of the load, thread t then holds the 8 channels
         // 8 (t % 4) ... of token t / 4 and stores them at once.
         const int t = tid & 127;
-        pdl_wait();
         for (; ok && todo.next(seg); ++n_seg) {
             const int a = n_seg % C::kAccs, n0 = seg.n0, n = n0 + t, m0 = seg.m0;
             const int cols = (int)min(q.p.M - m0, (long long)NT);
