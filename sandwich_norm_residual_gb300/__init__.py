@@ -344,17 +344,25 @@ def moe_combine_boundary_nvfp4(h, expert_out, topk_w, post_w, pre_w, n: int, eps
     return q, sf
 
 
+def _int8_given(q, scale, rows) -> tuple:
+    """The caller's outputs, as operands of ``_ready``."""
+    import torch
+    return ((() if q is None else ((q, torch.int8, rows),))
+            + (() if scale is None else ((scale, torch.float32, rows[:1]),)))
+
+
 def _int8_out(h, q, scale):
     import torch
-    T, D = h.shape
     if q is None:
-        q = torch.empty((T, D), dtype=torch.int8, device=h.device)
+        q = torch.empty(h.shape, dtype=torch.int8, device=h.device)
+    else:
+        _check(q, "y_int8", torch.int8, 2)
+        _shape(q, "y_int8", h.shape)
     if scale is None:
-        scale = torch.empty(T, dtype=torch.float32, device=h.device)
-    _check(q, "y_int8", torch.int8, 2)
-    _check(scale, "y_scale", torch.float32, 1)
-    _shape(q, "y_int8", (T, D))
-    _shape(scale, "y_scale", (T,))
+        scale = torch.empty(h.shape[0], dtype=torch.float32, device=h.device)
+    else:
+        _check(scale, "y_scale", torch.float32, 1)
+        _shape(scale, "y_scale", h.shape[:1])
     return q, scale
 
 
@@ -365,7 +373,8 @@ def boundary_fused_int8(h, x, post_w, pre_w, n: int, eps: float = 1e-6, y_int8=N
     import torch
     bf16 = torch.bfloat16
     T, D = rows = _dims(h, 2)
-    ready = _ready((h, bf16, rows), (x, bf16, rows), (post_w, bf16, (D,)), (pre_w, bf16, (D,)))
+    ready = _ready((h, bf16, rows), (x, bf16, rows), (post_w, bf16, (D,)), (pre_w, bf16, (D,)),
+                   *_int8_given(y_int8, y_scale, rows))
     if not ready:
         for t, name in ((h, "h"), (x, "x")):
             _check(t, name, bf16, 2)
@@ -373,12 +382,9 @@ def boundary_fused_int8(h, x, post_w, pre_w, n: int, eps: float = 1e-6, y_int8=N
         _check(pre_w, "pre_w", bf16, 1)
         if x.shape != h.shape or post_w.shape[0] != D or pre_w.shape[0] != D:
             raise ValueError("shape mismatch: h, x [T, D]; post_w, pre_w [D]")
-    if not ready or y_int8 is not None or y_scale is not None:
-        q, scale = _int8_out(h, y_int8, y_scale)
+    q, scale = _int8_out(h, y_int8, y_scale)
+    if not ready:
         _on_current_device(h=h, x=x, post_w=post_w, pre_w=pre_w, y_int8=q, y_scale=scale)
-    else:
-        q = torch.empty(rows, dtype=torch.int8, device=h.device)
-        scale = torch.empty(T, dtype=torch.float32, device=h.device)
     st = _lib.load().beam_boundary_fused_int8(_raw_stream(stream, h), h.data_ptr(), x.data_ptr(),
                                               post_w.data_ptr(), pre_w.data_ptr(), int(n), float(eps), T, D,
                                               q.data_ptr(), scale.data_ptr(), _opts(opts))
@@ -396,7 +402,7 @@ def moe_combine_boundary_int8(h, expert_out, topk_w, post_w, pre_w, n: int, eps:
     bf16, K = torch.bfloat16, _lib.BEAM_MOE_TOPK
     T, D = rows = _dims(h, 2)
     ready = _ready((h, bf16, rows), (expert_out, bf16, (T, K, D)), (topk_w, torch.float32, (T, K)),
-                   (post_w, bf16, (D,)), (pre_w, bf16, (D,)))
+                   (post_w, bf16, (D,)), (pre_w, bf16, (D,)), *_int8_given(y_int8, y_scale, rows))
     if not ready:
         _check(h, "h", bf16, 2)
         _check(expert_out, "expert_out", bf16, 3)
@@ -406,13 +412,10 @@ def moe_combine_boundary_int8(h, expert_out, topk_w, post_w, pre_w, n: int, eps:
         if (expert_out.shape != (T, K, D) or topk_w.shape != (T, K) or post_w.shape[0] != D
                 or pre_w.shape[0] != D):
             raise ValueError("shape mismatch: h [T, D]; expert_out [T, 8, D]; topk_w [T, 8]")
-    if not ready or y_int8 is not None or y_scale is not None:
-        q, scale = _int8_out(h, y_int8, y_scale)
+    q, scale = _int8_out(h, y_int8, y_scale)
+    if not ready:
         _on_current_device(h=h, expert_out=expert_out, topk_w=topk_w, post_w=post_w, pre_w=pre_w,
                            y_int8=q, y_scale=scale)
-    else:
-        q = torch.empty(rows, dtype=torch.int8, device=h.device)
-        scale = torch.empty(T, dtype=torch.float32, device=h.device)
     st = _lib.load().beam_moe_combine_boundary_int8(
         _raw_stream(stream, h), h.data_ptr(), expert_out.data_ptr(), topk_w.data_ptr(),
         float(route_scale), post_w.data_ptr(), pre_w.data_ptr(), int(n), float(eps), T, D,
@@ -438,8 +441,10 @@ def matmul_int8(a, a_scale, w, w_scale, out_dtype=None, out=None, stream=None, p
     """
     import torch
     (M, K), (N, _) = _dims(a, 2), _dims(w, 2)
+    if out_dtype is None:
+        out_dtype = getattr(out, "dtype", torch.bfloat16)
     ready = _ready((a, torch.int8, (M, K)), (a_scale, torch.float32, (M,)), (w, torch.int8, (N, K)),
-                   (w_scale, torch.float32, (N,)))
+                   (w_scale, torch.float32, (N,)), *(() if out is None else ((out, out_dtype, (M, N)),)))
     if not ready:
         _check(a, "a", torch.int8, 2)
         _check(a_scale, "a_scale", torch.float32, 1)
@@ -447,14 +452,11 @@ def matmul_int8(a, a_scale, w, w_scale, out_dtype=None, out=None, stream=None, p
         _check(w_scale, "w_scale", torch.float32, 1)
         if w.shape[1] != K or a_scale.shape[0] != M or w_scale.shape[0] != N:
             raise ValueError("shape mismatch: a [M, K]; a_scale [M]; w [N, K]; w_scale [N]")
-    if out_dtype is None:
-        out_dtype = torch.bfloat16 if out is None else out.dtype
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError(f"out_dtype must be bfloat16 or float32 (got {out_dtype})")
-    given = out is not None
-    if not given:
+    if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=a.device)
-    if given or not ready:
+    if not ready:
         _check(out, "out", out_dtype, 2)
         _shape(out, "out", (M, N))
         _on_current_device(a=a, a_scale=a_scale, w=w, w_scale=w_scale, out=out)
@@ -533,18 +535,19 @@ def moe_balance_loss(logits, topk_idx, alpha: float, seq_offsets=None, loss=None
     S = _sequences(seq_offsets)
     (T, E), (_, K) = _dims(logits, 2), _dims(topk_idx, 2)
     ready = _ready((logits, torch.float32, (T, E)), (topk_idx, torch.int32, (T, K)),
-                   *(() if seq_offsets is None else ((seq_offsets, torch.int32, (S + 1,)),)))
+                   *(() if seq_offsets is None else ((seq_offsets, torch.int32, (S + 1,)),)),
+                   *(() if loss is None else ((loss, torch.float32, (S,)),)),
+                   *(() if counts is None else ((counts, torch.int32, (S, E)),)))
     if not ready:
         _check(logits, "logits", torch.float32, 2)
         _check(topk_idx, "topk_idx", torch.int32, 2)
         if topk_idx.shape[0] != T:
             raise ValueError("shape mismatch: logits [T, E]; topk_idx [T, topk]")
-    given = loss is not None or counts is not None
     if loss is None:
         loss = torch.empty(S, dtype=torch.float32, device=logits.device)
     if counts is None:
         counts = torch.empty((S, E), dtype=torch.int32, device=logits.device)
-    if given or not ready:
+    if not ready:
         _check(loss, "loss", torch.float32, 1)
         _check(counts, "counts", torch.int32, 2)
         _shape(loss, "loss", (S,))
@@ -573,17 +576,17 @@ def moe_balance_loss_backward(dloss, logits, counts, topk: int, alpha: float, se
     S = _sequences(seq_offsets)
     T, E = rows = _dims(logits, 2)
     ready = _ready((dloss, torch.float32, (S,)), (logits, torch.float32, rows), (counts, torch.int32, (S, E)),
-                   *(() if seq_offsets is None else ((seq_offsets, torch.int32, (S + 1,)),)))
+                   *(() if seq_offsets is None else ((seq_offsets, torch.int32, (S + 1,)),)),
+                   *(() if dlogits is None else ((dlogits, torch.float32, rows),)))
     if not ready:
         _check(dloss, "dloss", torch.float32, 1)
         _check(logits, "logits", torch.float32, 2)
         _check(counts, "counts", torch.int32, 2)
         _shape(dloss, "dloss", (S,))
         _shape(counts, "counts", (S, E))
-    given = dlogits is not None
-    if not given:
+    if dlogits is None:
         dlogits = torch.empty_like(logits)
-    if given or not ready:
+    if not ready:
         _check(dlogits, "dlogits", torch.float32, 2)
         _shape(dlogits, "dlogits", (T, E))
         _on_current_device(**_given(dloss=dloss, logits=logits, counts=counts, seq_offsets=seq_offsets,

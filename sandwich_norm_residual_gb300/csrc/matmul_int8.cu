@@ -186,7 +186,7 @@ beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* pa
 }
 
 // Tokens a tile: as few as hold M; beyond 128, single CTAs or pairs, whichever
-// finishes first by the measured time of a step (0.46 and 0.62 us), of a join and
+// finishes first by the measured time of a step (0.52 and 0.60 us), of a join and
 // of a result that nothing hides (0.7 and 1.5 us)
 enum class Shape { kFew, k16, k32, k64, k128, kPair };
 
@@ -200,7 +200,7 @@ Shape choose(const MatmulParams& p) {
         const uint32_t shared = q.split ? (q.split + q.sharers - 1) / q.sharers + join : 0;
         return q.waves * (q.steps * step + result) + shared * step;
     };
-    return ns(plan<128, 1>(p, kMaxSms), kJoinSteps<1>, 460, 700) < ns(plan<256, 2>(p, kMaxSms), kJoinSteps<2>, 620, 1500)
+    return ns(plan<128, 1>(p, kMaxSms), kJoinSteps<1>, 520, 700) < ns(plan<256, 2>(p, kMaxSms), kJoinSteps<2>, 600, 1500)
                ? Shape::k128
                : Shape::kPair;
 }
