@@ -20,6 +20,8 @@
 // exact.
 #pragma once
 
+#include <type_traits>
+
 #include "matmul_int8.cuh"
 #include "packed.cuh"
 #include "umma.cuh"
@@ -473,7 +475,8 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
             // the first of this worker's split tiles goes to its part 0, the last to part 1
             const bool second = seg.k0 == 0;
             float* part = q.part + ((size_t)blockIdx.x * 2 + second) * (size_t)(NT * kTileN) + t;
-            const size_t at = (size_t)m0 * (size_t)q.p.N + (size_t)n;
+            using Out = std::conditional_t<F32, float, uint16_t>;
+            Out* out = static_cast<Out*>(q.p.out) + (size_t)m0 * (size_t)q.p.N + (size_t)n;
             constexpr int kBatch = NT < 32 ? 16 : 32;
             for (int c0 = 0; c0 < cols; c0 += kBatch) {
                 float v[kBatch];
@@ -481,16 +484,26 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                 else tmem_ld32(from + c0, v);
                 tmem_wait_ld();
                 if (c0 + kBatch >= cols) free_acc();
+                const bool full = c0 + kBatch <= cols;
                 if (!seg.whole) {
+                    if (full) {
 #pragma unroll
-                    for (int c = 0; c < kBatch; ++c)
-                        if (c0 + c < cols) part[(c0 + c) * kTileN] = v[c];
+                        for (int c = 0; c < kBatch; ++c) part[(c0 + c) * kTileN] = v[c];
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kBatch; ++c)
+                            if (c0 + c < cols) part[(c0 + c) * kTileN] = v[c];
+                    }
                 } else if (n < q.p.N) {
 #pragma unroll
-                    for (int c = 0; c < kBatch; ++c)
-                        if (c0 + c < cols)
-                            store_out<F32>(q.p.out, at + (size_t)(c0 + c) * (size_t)q.p.N,
-                                           __fmul_rn(__fmul_rn(v[c], scales[c0 + c]), ws[0]));
+                    for (int c = 0; c < kBatch; c += 2) {
+                        const float2 as = *reinterpret_cast<const float2*>(scales + c0 + c);
+                        const float2 o = mul2_rn(mul2_rn(make_float2(v[c], v[c + 1]), as), make_float2(ws[0], ws[0]));
+                        if (full || c0 + c < cols) store_out<F32>(out, 0, o.x);
+                        out += q.p.N;
+                        if (full || c0 + c + 1 < cols) store_out<F32>(out, 0, o.y);
+                        out += q.p.N;
+                    }
                 }
             }
         }
