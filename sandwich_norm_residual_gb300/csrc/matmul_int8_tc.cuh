@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
         // with the channels' order of the load, thread t then holds the 8 channels
         // 8 (t % 4) ... of token t / 4 and stores them at once.
         const int t = tid & 127;
-        for (; ok && todo.next(seg); ++n_seg) {
+        for (; ok && todo.next(seg); ++n_seg, it += (int)(seg.k1 - seg.k0)) {
             const int a = n_seg % C::kAccs, n0 = seg.n0, n = n0 + t, m0 = seg.m0;
             const int cols = (int)min(q.p.M - m0, (long long)NT);
             const bool wide = permuted(seg);
@@ -507,6 +507,11 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                 }
             }
         }
+        // the last steps' arrivals, which nobody else waits for, have come (in a pair,
+        // from the other CTA) before the shared memory goes
+        if (ok && it > 0)
+            for (int i = max(it - C::kOps, 0); i < it; ++i)
+                ok = warp_wait(&op_empty[i % C::kOps], (uint32_t)(i / C::kOps) & 1, q.wait_ns) && ok;
     }
     if (!ok) atomicOr(q.status, 1u);
     __syncwarp();

@@ -131,11 +131,11 @@ def test_nothing_to_do():
     assert snr.matmul_int8(w, torch.ones(5, device="cuda"), z, torch.zeros(0, device="cuda")).shape == (5, 0)
 
 
-@pytest.mark.parametrize("M", [1, 48, 700])
-def test_graph_replay_on_a_side_stream_and_pdl(M):
-    a, sa, w, sw = inputs(M, 500, 1040, 3)
+@pytest.mark.parametrize("M,N", [(1, 500), (48, 500), (700, 500), (2048, 5120)])
+def test_graph_replay_on_a_side_stream_and_pdl(M, N):
+    a, sa, w, sw = inputs(M, N, 1040, 3)
     d = [torch.from_numpy(v).cuda() for v in (a, sa, w, sw)]
-    outs = [torch.empty((M, 500), device="cuda") for _ in range(3)]
+    outs = [torch.empty((M, N), device="cuda") for _ in range(3)]
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
