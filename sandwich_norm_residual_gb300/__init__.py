@@ -103,7 +103,7 @@ def _ready(*operands) -> bool:
             dev = d
         if d != dev or d < 0:
             return False
-    return dev == _torch.cuda.current_device()
+    return dev == _torch._C._cuda_getDevice()  # initialised: the operands are CUDA tensors
 
 
 def _raw_stream(stream, t) -> int | None:
@@ -346,21 +346,23 @@ def moe_combine_boundary_nvfp4(h, expert_out, topk_w, post_w, pre_w, n: int, eps
 
 def _int8_given(q, scale, rows) -> tuple:
     """The caller's outputs, as operands of ``_ready``."""
+    if q is None and scale is None:
+        return ()
     import torch
     return ((() if q is None else ((q, torch.int8, rows),))
             + (() if scale is None else ((scale, torch.float32, rows[:1]),)))
 
 
-def _int8_out(h, q, scale):
+def _int8_out(h, q, scale, checked: bool):
     import torch
     if q is None:
         q = torch.empty(h.shape, dtype=torch.int8, device=h.device)
-    else:
+    elif not checked:
         _check(q, "y_int8", torch.int8, 2)
         _shape(q, "y_int8", h.shape)
     if scale is None:
         scale = torch.empty(h.shape[0], dtype=torch.float32, device=h.device)
-    else:
+    elif not checked:
         _check(scale, "y_scale", torch.float32, 1)
         _shape(scale, "y_scale", h.shape[:1])
     return q, scale
@@ -382,7 +384,7 @@ def boundary_fused_int8(h, x, post_w, pre_w, n: int, eps: float = 1e-6, y_int8=N
         _check(pre_w, "pre_w", bf16, 1)
         if x.shape != h.shape or post_w.shape[0] != D or pre_w.shape[0] != D:
             raise ValueError("shape mismatch: h, x [T, D]; post_w, pre_w [D]")
-    q, scale = _int8_out(h, y_int8, y_scale)
+    q, scale = _int8_out(h, y_int8, y_scale, ready)
     if not ready:
         _on_current_device(h=h, x=x, post_w=post_w, pre_w=pre_w, y_int8=q, y_scale=scale)
     st = _lib.load().beam_boundary_fused_int8(_raw_stream(stream, h), h.data_ptr(), x.data_ptr(),
@@ -412,7 +414,7 @@ def moe_combine_boundary_int8(h, expert_out, topk_w, post_w, pre_w, n: int, eps:
         if (expert_out.shape != (T, K, D) or topk_w.shape != (T, K) or post_w.shape[0] != D
                 or pre_w.shape[0] != D):
             raise ValueError("shape mismatch: h [T, D]; expert_out [T, 8, D]; topk_w [T, 8]")
-    q, scale = _int8_out(h, y_int8, y_scale)
+    q, scale = _int8_out(h, y_int8, y_scale, ready)
     if not ready:
         _on_current_device(h=h, expert_out=expert_out, topk_w=topk_w, post_w=post_w, pre_w=pre_w,
                            y_int8=q, y_scale=scale)
