@@ -233,7 +233,8 @@ BEAM_API beam_status beam_router_sigmoid_fast(beam_stream_t stream, const float*
  *               for nothing, whatever their rows hold. An empty sequence has loss 0 and counts 0.
  *   loss [S] FP32; counts [S, E] int32, 16-byte aligned; every element written
  *   workspace   device memory for this call alone, 16-byte aligned, of at least
- *               beam_moe_balance_workspace(T, E, S) bytes; need not be cleared
+ *               beam_moe_balance_workspace(T, E, S) bytes (NULL where that is 0); need
+ *               not be cleared
  * 4-byte aligned where nothing else is said. Outputs and workspace overlap
  * neither each other nor an input. T at most 2^31 - 1.
  * A token whose sigmoids are all 0 has p = 0. A NaN logit makes its sequence's
@@ -247,7 +248,7 @@ BEAM_API beam_status beam_moe_balance_loss(beam_stream_t stream, const float* lo
                                            float* loss, int32_t* counts, void* workspace,
                                            int64_t workspace_bytes);
 
-/* Bytes of workspace of beam_moe_balance_loss, -1 for a bad shape. */
+/* Bytes of workspace of beam_moe_balance_loss (0 up to 512 tokens), -1 for a bad shape. */
 BEAM_API int64_t beam_moe_balance_workspace(int64_t T, int E, int64_t S);
 
 /*

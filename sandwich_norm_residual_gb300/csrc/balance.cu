@@ -20,14 +20,15 @@ bool misaligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t
 
 bool bad_shape(int64_t T, int E, int K, int64_t S, const void* off) {
     return T < 0 || T > 0x7FFFFFFF || E < 4 || (E & 3) || E > BEAM_BALANCE_MAX_EXPERTS || K < 1 ||
-           K > BEAM_ROUTE_MAX_TOPK || S < 1 || S > 0x7FFFFFFF - beam::kBalanceBlocks || (!off && S != 1);
+           K > BEAM_ROUTE_MAX_TOPK || S < 1 || S > 0x7FFFFFFF || (!off && S != 1);
 }
 
-// Tokens a block: at least one for each warp, and few enough blocks that two
-// are resident on every SM
+// Tokens a block: at least one for each warp, few enough blocks that two are
+// resident on every SM, and at most 64 for each warp, which adds them in FP32
 void split(int64_t T, BalanceParams* p) {
     int64_t chunk = (T + beam::kBalanceBlocks - 1) / beam::kBalanceBlocks;
     if (chunk < beam::kBalanceWarps) chunk = beam::kBalanceWarps;
+    if (chunk > 64 * beam::kBalanceWarps) chunk = 64 * beam::kBalanceWarps;
     p->chunk = (int)chunk;
     p->blocks = (int)((T + chunk - 1) / chunk);
 }
@@ -40,6 +41,14 @@ const void* records_kernel(int E) {
     case 1: return reinterpret_cast<const void*>(beam::balance_records_kernel<1>);
     case 2: return reinterpret_cast<const void*>(beam::balance_records_kernel<2>);
     default: return reinterpret_cast<const void*>(beam::balance_records_kernel<4>);
+    }
+}
+
+const void* small_kernel(int E) {
+    switch (vectors(E)) {
+    case 1: return reinterpret_cast<const void*>(beam::balance_small_kernel<1>);
+    case 2: return reinterpret_cast<const void*>(beam::balance_small_kernel<2>);
+    default: return reinterpret_cast<const void*>(beam::balance_small_kernel<4>);
     }
 }
 
@@ -75,6 +84,7 @@ extern "C" {
 
 int64_t beam_moe_balance_workspace(int64_t T, int E, int64_t S) {
     if (bad_shape(T, E, 1, S, &T)) return -1;
+    if (T <= beam::kBalanceSmall) return 0;
     BalanceParams p{};
     split(T, &p);
     return ((int64_t)p.blocks + S) * E * 8;
@@ -86,9 +96,9 @@ beam_status beam_moe_balance_loss(beam_stream_t stream, const float* logits, con
     if (bad_shape(T, E, topk, S, seq_offsets)) return BEAM_ERR_SHAPE;
     const int64_t need = beam_moe_balance_workspace(T, E, S);
     if (!std::isfinite(alpha) || workspace_bytes < need) return BEAM_ERR_ARG;
-    if ((T && (!logits || !topk_idx)) || !loss || !counts || !workspace) return BEAM_ERR_NULL;
+    if ((T && (!logits || !topk_idx)) || !loss || !counts || (need && !workspace)) return BEAM_ERR_NULL;
     if (misaligned(logits, 16) || misaligned(topk_idx, 4) || misaligned(seq_offsets, 4) || misaligned(loss, 4) ||
-        misaligned(counts, 16) || misaligned(workspace, 16))
+        misaligned(counts, 16) || (need && misaligned(workspace, 16)))
         return BEAM_ERR_ALIGN;
     const struct {
         const void* p;
@@ -113,20 +123,18 @@ beam_status beam_moe_balance_loss(beam_stream_t stream, const float* logits, con
     p.E = E;
     p.K = topk;
     p.S = (int)S;
-    split(T, &p);
-    p.rec_q = static_cast<float*>(workspace);
-    p.rec_c = reinterpret_cast<int32_t*>(p.rec_q + ((size_t)p.blocks + (size_t)S) * (size_t)E);
     p.factor = (double)alpha * E / topk;
     p.loss = loss;
     p.counts = counts;
     p.status = dev.status_word;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (p.blocks) {
-        st = launch(records_kernel(E), p.blocks, beam::kBalanceThreads, &p, cs, false);
-        if (st != BEAM_OK) return st;
-    }
-    return launch(reinterpret_cast<const void*>(beam::balance_loss_kernel), p.S, beam::kBalanceFinalThreads, &p, cs,
-                  p.blocks != 0);
+    if (T <= beam::kBalanceSmall) return launch(small_kernel(E), p.S, beam::kBalanceThreads, &p, cs, false);
+    split(T, &p);
+    p.rec_q = static_cast<float*>(workspace);
+    p.rec_c = reinterpret_cast<int32_t*>(p.rec_q + ((size_t)p.blocks + (size_t)S) * (size_t)E);
+    st = launch(records_kernel(E), p.blocks, beam::kBalanceThreads, &p, cs, false);
+    if (st != BEAM_OK) return st;
+    return launch(reinterpret_cast<const void*>(beam::balance_loss_kernel), p.S, beam::kBalanceFinalThreads, &p, cs, true);
 }
 
 beam_status beam_moe_balance_loss_backward(beam_stream_t stream, const float* dloss, const float* logits,

@@ -20,7 +20,7 @@ def lib():
 def test_forward_argument_errors(lib):
     Z, I, O, L, C, W = (A + (i << 33) for i in range(6))
 
-    def fw(T=100, E=256, K=8, S=3, alpha=1.0, z=Z, i=I, o=O, ls=L, c=C, w=W, nb=None):
+    def fw(T=1000, E=256, K=8, S=3, alpha=1.0, z=Z, i=I, o=O, ls=L, c=C, w=W, nb=None):
         nb = lib.beam_moe_balance_workspace(T, E, S) if nb is None else nb
         return lib.beam_moe_balance_loss(None, z, i, o, T, E, K, S, alpha, ls, c, w, nb)
 
@@ -28,7 +28,7 @@ def test_forward_argument_errors(lib):
                dict(S=1 << 31), dict(o=None)):
         assert fw(**kw) == _lib.BEAM_ERR_SHAPE, kw
     assert fw(alpha=float("nan")) == _lib.BEAM_ERR_ARG
-    need = lib.beam_moe_balance_workspace(100, 256, 3)
+    need = lib.beam_moe_balance_workspace(1000, 256, 3)
     assert need > 0 and fw(nb=need - 1) == _lib.BEAM_ERR_ARG
     for name in ("z", "i", "ls", "c", "w"):
         assert fw(**{name: None}) == _lib.BEAM_ERR_NULL
@@ -39,14 +39,17 @@ def test_forward_argument_errors(lib):
     assert fw() in REACHED
     assert fw(o=None, S=1) in REACHED
     assert fw(T=0, z=None, i=None) in REACHED  # the sequences' zeros are still written
+    assert fw(T=512, w=None, nb=0) in REACHED
 
 
 def test_workspace_sizes(lib):
     ws = lib.beam_moe_balance_workspace
     assert ws(100, 255, 1) == -1 and ws(100, 256, 0) == -1 and ws(-1, 256, 1) == -1
-    assert ws(0, 256, 2) == 2 * 256 * 8
-    # one record for each of at most 304 blocks and for each sequence
-    assert ws(1 << 30, 256, 5) <= (304 + 5) * 256 * 8
+    assert ws(0, 256, 2) == 0 and ws(512, 256, 600) == 0  # one kernel, no records
+    assert ws(513, 256, 2) > 0
+    # one record for each block and for each sequence: 304 blocks, and no more than 1024 tokens in one
+    assert ws(100_000, 256, 5) <= (304 + 5) * 256 * 8
+    assert ws(1 << 30, 256, 5) == ((1 << 20) + 5) * 256 * 8
 
 
 def test_backward_argument_errors(lib):
