@@ -150,6 +150,20 @@ int choose_vpt(int nvec, bool moe) {
     return 0;
 }
 
+// The dense rows with y as int8: 4 to 6 vectors where they waste under 1/16 of
+// the slots, else 5 even where a quarter is wasted. Fewer vectors mean more
+// threads a row, and the row's three reductions then cost more than idle slots:
+// T = 8000, D = 4104: 2 vectors 96 us, 5 vectors 79 us; T = 4000, D = 8200: 3
+// vectors 108 us, 5 vectors 79 us.
+int choose_vpt_int8(int nvec) {
+    for (int v : {5, 4, 6}) {
+        const int nt = threads_for(nvec, v);
+        if (nt && (nt * v - nvec) * 16 <= nvec) return v;
+    }
+    const int nt = threads_for(nvec, 5);
+    return nt && (nt * 5 - nvec) * 4 <= nvec ? 5 : choose_vpt(nvec, false);
+}
+
 // Bound on |c - c_exact| / (u^2 T) for the compensated sum, u = 2^-24, T the
 // exact sum. Terms are >= 0. A lane adds m terms with TwoSum and a rounded
 // compensation: error <= 0.505 m (m+1) u^2 T, |c| <= 1.01 m u T. Every merge
@@ -285,7 +299,10 @@ beam_status launch(bool moe, beam_stream_t stream, uint16_t* h, const uint16_t* 
     if (st != BEAM_OK) return st;
 
     const int nvec = D / 8;
-    const int vpt = (opts && opts->vec_per_thread) ? opts->vec_per_thread : choose_vpt(nvec, moe);
+    const int out = quant ? quant->kind : beam::kOutBf16;
+    const int vpt = (opts && opts->vec_per_thread)        ? opts->vec_per_thread
+                    : (out == beam::kOutInt8 && !moe) ? choose_vpt_int8(nvec)
+                                                      : choose_vpt(nvec, moe);
     const int nt = threads_for(nvec, vpt);
     if (!nt) return BEAM_ERR_SHAPE;
 
@@ -294,7 +311,6 @@ beam_status launch(bool moe, beam_stream_t stream, uint16_t* h, const uint16_t* 
     const bool full = has_full(vpt) && nt * vpt == nvec;
     const int wbytes = full ? 4 * D : 0;
     const int slot_bytes = 4 * D;
-    const int out = quant ? quant->kind : beam::kOutBf16;
     int kind = moe ? kMoeRegs : kDenseRing;
     int stages = 0;
     KernelFn fn = nullptr;
