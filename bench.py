@@ -38,14 +38,14 @@ WORKLOAD = (f"layer boundary pair, T={T_TOKENS} tokens per GPU, D={D}: dense bou
 # DRAM traffic per launch from one ncu capture (dram__bytes_read.sum +
 # dram__bytes_write.sum), valid only for the kernel source it was taken on.
 NCU_TRAFFIC = {
-    "moe": {"bytes_per_launch": 1_511_711_232 + 301_067_520, "source_sha": "ee686e2405c42fca"},
-    "dense": {"bytes_per_launch": 335_664_384 + 265_312_512, "source_sha": "ee686e2405c42fca"},
+    "moe": {"bytes_per_launch": 1_511_286_784 + 300_368_128, "source_sha": "0bac5777e84e45f3"},
+    "dense": {"bytes_per_launch": 335_712_256 + 265_319_936, "source_sha": "0bac5777e84e45f3"},
 }
 
 # Routing is bound by instruction issue, not HBM: its warp-instructions per
 # launch at T = 16384 (ncu smsp__inst_executed.sum) give its issue roofline,
 # valid while the kernel source matches.
-ROUTE_ISSUE = {"warp_instructions_per_launch": 11_225_399, "source_sha": "ee686e2405c42fca"}
+ROUTE_ISSUE = {"warp_instructions_per_launch": 11_201_646, "source_sha": "0bac5777e84e45f3"}
 
 
 # the sources of the kernels that those captures are of
