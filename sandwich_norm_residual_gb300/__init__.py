@@ -7,9 +7,15 @@ fallback: without the built library, calls raise ``ImportError``.
 
     y = boundary_fused(h, x, post_w, pre_w, n, eps)          # h updated in place
     y = moe_combine_boundary(h, expert_out, topk_w, post_w, pre_w, n, eps)
+
+Every call takes ``stream`` (default: the current stream). Operands that other streams write
+must be ready on it. Outputs that the caller does not give come from the memory pool of that
+stream, as any tensor made under ``torch.cuda.stream(stream)``: before another stream reads
+one, make it wait for ``stream``, and let it ``record_stream`` what is freed before it is done.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 
@@ -113,16 +119,25 @@ def _raw_stream(stream, t) -> int | None:
     return stream.cuda_stream or None
 
 
-def _workspace(nbytes: int, device, stream):
-    """Device memory for one call, from the pool of the stream that uses it: freed at the
-    call's end, it goes to later work of that stream alone. None for no bytes."""
+_HERE = contextlib.nullcontext()
+
+
+def _pool(stream):
+    """A context in which tensors come from the memory pool of the stream that the call runs on.
+    Another stream's pool may hand out memory that work queued there still reads or writes, and
+    takes it back for such work when it is freed. Entering a stream takes 10 us, so only where
+    it is not the current one."""
     import torch
-    if not nbytes:
-        return None
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(stream.device_index):
+        return _HERE
+    return torch.cuda.stream(stream)
+
+
+def _workspace(nbytes: int, device):
+    """Device memory for one call (within ``_pool``): freed at the call's end, it goes to later
+    work of the call's stream alone. None for no bytes."""
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
 def _opts(opts):
@@ -147,7 +162,8 @@ def boundary_fused(h, x, post_w, pre_w, n: int, eps: float = 1e-6, y=None, strea
     if x.shape != h.shape or post_w.shape[0] != D or pre_w.shape[0] != D:
         raise ValueError("shape mismatch: h, x [T, D]; post_w, pre_w [D]")
     if y is None:
-        y = torch.empty_like(h)
+        with _pool(stream):
+            y = torch.empty_like(h)
     _check(y, "y", torch.bfloat16, 2)
     _shape(y, "y", (T, D))
     _on_current_device(h=h, x=x, post_w=post_w, pre_w=pre_w, y=y)
@@ -182,7 +198,8 @@ def moe_combine_boundary(h, expert_out, topk_w, post_w, pre_w, n: int, eps: floa
     if post_w.shape[0] != D or pre_w.shape[0] != D:
         raise ValueError("shape mismatch: post_w, pre_w [D]")
     if y is None:
-        y = torch.empty_like(h)
+        with _pool(stream):
+            y = torch.empty_like(h)
     _check(y, "y", torch.bfloat16, 2)
     _shape(y, "y", (T, D))
     _on_current_device(h=h, expert_out=expert_out, topk_w=topk_w, post_w=post_w, pre_w=pre_w, y=y)
@@ -220,10 +237,11 @@ def _check_any(t, name: str, dtype, ndim: int):
         raise ValueError(f"{name} must be a contiguous {ndim}-d tensor")
 
 
-def _like_host(h):
+def _like_host(h, stream):
     import torch
     if h.device.type == "cuda":
-        return torch.empty_like(h)
+        with _pool(stream):
+            return torch.empty_like(h)
     return torch.empty(h.shape, dtype=h.dtype, pin_memory=True)
 
 
@@ -242,7 +260,7 @@ def boundary_fused_host(h, x, post_w, pre_w, n: int, eps: float = 1e-6, y=None, 
     if x.shape != h.shape or post_w.shape[0] != D or pre_w.shape[0] != D:
         raise ValueError("shape mismatch: h, x [T, D]; post_w, pre_w [D]")
     if y is None:
-        y = _like_host(h)
+        y = _like_host(h, stream)
     _check_any(y, "y", torch.bfloat16, 2)
     _shape(y, "y", (T, D))
     st = _lib.load().beam_boundary_fused_host(_stream_ptr(stream), h.data_ptr(), x.data_ptr(),
@@ -268,7 +286,7 @@ def moe_combine_boundary_host(h, expert_out, topk_w, post_w, pre_w, n: int, eps:
             or pre_w.shape[0] != D):
         raise ValueError(f"shape mismatch: h [T, D]; expert_out [T, {K}, D]; topk_w [T, {K}]")
     if y is None:
-        y = _like_host(h)
+        y = _like_host(h, stream)
     _check_any(y, "y", torch.bfloat16, 2)
     _shape(y, "y", (T, D))
     st = _lib.load().beam_moe_combine_boundary_host(
@@ -279,15 +297,16 @@ def moe_combine_boundary_host(h, expert_out, topk_w, post_w, pre_w, n: int, eps:
     return y
 
 
-def _nvfp4_out(h, q, sf):
+def _nvfp4_out(h, q, sf, stream):
     import torch
     T, D = h.shape
     if D % 16:
         raise ValueError("NVFP4 output needs D to be a multiple of 16")
-    if q is None:
-        q = torch.empty((T, D // 2), dtype=torch.uint8, device=h.device)
-    if sf is None:
-        sf = torch.empty((T, D // 16), dtype=torch.uint8, device=h.device)
+    with _pool(stream):
+        if q is None:
+            q = torch.empty((T, D // 2), dtype=torch.uint8, device=h.device)
+        if sf is None:
+            sf = torch.empty((T, D // 16), dtype=torch.uint8, device=h.device)
     _check(q, "y_fp4", torch.uint8, 2)
     _check(sf, "y_scale", torch.uint8, 2)
     if tuple(q.shape) != (T, D // 2) or tuple(sf.shape) != (T, D // 16):
@@ -307,7 +326,7 @@ def boundary_fused_nvfp4(h, x, post_w, pre_w, n: int, eps: float, y_global_scale
     T, D = h.shape
     if x.shape != h.shape or post_w.shape[0] != D or pre_w.shape[0] != D:
         raise ValueError("shape mismatch: h, x [T, D]; post_w, pre_w [D]")
-    q, sf = _nvfp4_out(h, y_fp4, y_scale)
+    q, sf = _nvfp4_out(h, y_fp4, y_scale, stream)
     _on_current_device(h=h, x=x, post_w=post_w, pre_w=pre_w, y_fp4=q, y_scale=sf)
     st = _lib.load().beam_boundary_fused_nvfp4(_stream_ptr(stream), h.data_ptr(), x.data_ptr(),
                                                post_w.data_ptr(), pre_w.data_ptr(), int(n),
@@ -332,7 +351,7 @@ def moe_combine_boundary_nvfp4(h, expert_out, topk_w, post_w, pre_w, n: int, eps
     if (expert_out.shape != (T, _lib.BEAM_MOE_TOPK, D) or topk_w.shape != (T, _lib.BEAM_MOE_TOPK)
             or post_w.shape[0] != D or pre_w.shape[0] != D):
         raise ValueError("shape mismatch: h [T, D]; expert_out [T, 8, D]; topk_w [T, 8]")
-    q, sf = _nvfp4_out(h, y_fp4, y_scale)
+    q, sf = _nvfp4_out(h, y_fp4, y_scale, stream)
     _on_current_device(h=h, expert_out=expert_out, topk_w=topk_w, post_w=post_w, pre_w=pre_w,
                        y_fp4=q, y_scale=sf)
     st = _lib.load().beam_moe_combine_boundary_nvfp4(
@@ -353,16 +372,18 @@ def _int8_given(q, scale, rows) -> tuple:
             + (() if scale is None else ((scale, torch.float32, rows[:1]),)))
 
 
-def _int8_out(h, q, scale, checked: bool):
+def _int8_out(h, q, scale, stream, checked: bool):
     import torch
-    if q is None:
-        q = torch.empty(h.shape, dtype=torch.int8, device=h.device)
-    elif not checked:
+    new_q, new_scale = q is None, scale is None
+    with _pool(stream):
+        if new_q:
+            q = torch.empty(h.shape, dtype=torch.int8, device=h.device)
+        if new_scale:
+            scale = torch.empty(h.shape[0], dtype=torch.float32, device=h.device)
+    if not new_q and not checked:
         _check(q, "y_int8", torch.int8, 2)
         _shape(q, "y_int8", h.shape)
-    if scale is None:
-        scale = torch.empty(h.shape[0], dtype=torch.float32, device=h.device)
-    elif not checked:
+    if not new_scale and not checked:
         _check(scale, "y_scale", torch.float32, 1)
         _shape(scale, "y_scale", h.shape[:1])
     return q, scale
@@ -384,7 +405,7 @@ def boundary_fused_int8(h, x, post_w, pre_w, n: int, eps: float = 1e-6, y_int8=N
         _check(pre_w, "pre_w", bf16, 1)
         if x.shape != h.shape or post_w.shape[0] != D or pre_w.shape[0] != D:
             raise ValueError("shape mismatch: h, x [T, D]; post_w, pre_w [D]")
-    q, scale = _int8_out(h, y_int8, y_scale, ready)
+    q, scale = _int8_out(h, y_int8, y_scale, stream, ready)
     if not ready:
         _on_current_device(h=h, x=x, post_w=post_w, pre_w=pre_w, y_int8=q, y_scale=scale)
     st = _lib.load().beam_boundary_fused_int8(_raw_stream(stream, h), h.data_ptr(), x.data_ptr(),
@@ -414,7 +435,7 @@ def moe_combine_boundary_int8(h, expert_out, topk_w, post_w, pre_w, n: int, eps:
         if (expert_out.shape != (T, K, D) or topk_w.shape != (T, K) or post_w.shape[0] != D
                 or pre_w.shape[0] != D):
             raise ValueError("shape mismatch: h [T, D]; expert_out [T, 8, D]; topk_w [T, 8]")
-    q, scale = _int8_out(h, y_int8, y_scale, ready)
+    q, scale = _int8_out(h, y_int8, y_scale, stream, ready)
     if not ready:
         _on_current_device(h=h, expert_out=expert_out, topk_w=topk_w, post_w=post_w, pre_w=pre_w,
                            y_int8=q, y_scale=scale)
@@ -456,14 +477,15 @@ def matmul_int8(a, a_scale, w, w_scale, out_dtype=None, out=None, stream=None, p
             raise ValueError("shape mismatch: a [M, K]; a_scale [M]; w [N, K]; w_scale [N]")
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError(f"out_dtype must be bfloat16 or float32 (got {out_dtype})")
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    ws_bytes = _matmul_workspace(M, N, K)
+    with _pool(stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        ws = _workspace(ws_bytes, a.device)
     if not ready:
         _check(out, "out", out_dtype, 2)
         _shape(out, "out", (M, N))
         _on_current_device(a=a, a_scale=a_scale, w=w, w_scale=w_scale, out=out)
-    ws_bytes = _matmul_workspace(M, N, K)
-    ws = _workspace(ws_bytes, a.device, stream)
     st = _lib.load().beam_matmul_int8(
         _raw_stream(stream, a), a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), M, N, K,
         _lib.BEAM_OUT_FP32 if out_dtype is torch.float32 else _lib.BEAM_OUT_BF16, out.data_ptr(),
@@ -487,10 +509,11 @@ def moe_route(logits, bias, n_group: int = 8, topk_group: int = 4, topk: int = 8
     T, E = logits.shape
     if bias.shape[0] != E:
         raise ValueError("bias must have one entry per expert")
-    if idx is None:
-        idx = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
-    if w is None:
-        w = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
+    with _pool(stream):
+        if idx is None:
+            idx = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
+        if w is None:
+            w = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
     _check(idx, "idx", torch.int32, 2)
     _check(w, "w", torch.float32, 2)
     _shape(idx, "idx", (T, topk))
@@ -545,10 +568,13 @@ def moe_balance_loss(logits, topk_idx, alpha: float, seq_offsets=None, loss=None
         _check(topk_idx, "topk_idx", torch.int32, 2)
         if topk_idx.shape[0] != T:
             raise ValueError("shape mismatch: logits [T, E]; topk_idx [T, topk]")
-    if loss is None:
-        loss = torch.empty(S, dtype=torch.float32, device=logits.device)
-    if counts is None:
-        counts = torch.empty((S, E), dtype=torch.int32, device=logits.device)
+    ws_bytes = _balance_workspace(T, E, S)
+    with _pool(stream):
+        if loss is None:
+            loss = torch.empty(S, dtype=torch.float32, device=logits.device)
+        if counts is None:
+            counts = torch.empty((S, E), dtype=torch.int32, device=logits.device)
+        ws = _workspace(ws_bytes, logits.device)
     if not ready:
         _check(loss, "loss", torch.float32, 1)
         _check(counts, "counts", torch.int32, 2)
@@ -556,8 +582,6 @@ def moe_balance_loss(logits, topk_idx, alpha: float, seq_offsets=None, loss=None
         _shape(counts, "counts", (S, E))
         _on_current_device(**_given(logits=logits, topk_idx=topk_idx, seq_offsets=seq_offsets, loss=loss,
                                     counts=counts))
-    ws_bytes = _balance_workspace(T, E, S)
-    ws = _workspace(ws_bytes, logits.device, stream)
     st = _lib.load().beam_moe_balance_loss(
         _raw_stream(stream, logits), logits.data_ptr(), topk_idx.data_ptr(),
         None if seq_offsets is None else seq_offsets.data_ptr(), T, E, K, S, float(alpha), loss.data_ptr(),
@@ -587,7 +611,8 @@ def moe_balance_loss_backward(dloss, logits, counts, topk: int, alpha: float, se
         _shape(dloss, "dloss", (S,))
         _shape(counts, "counts", (S, E))
     if dlogits is None:
-        dlogits = torch.empty_like(logits)
+        with _pool(stream):
+            dlogits = torch.empty_like(logits)
     if not ready:
         _check(dlogits, "dlogits", torch.float32, 2)
         _shape(dlogits, "dlogits", (T, E))
@@ -609,7 +634,8 @@ def router_sigmoid(z, out=None, stream=None, fast: bool = False):
     if not isinstance(z, torch.Tensor) or z.dtype != torch.float32 or not z.is_contiguous():
         raise TypeError("z must be a contiguous float32 tensor")
     if out is None:
-        out = torch.empty_like(z)
+        with _pool(stream):
+            out = torch.empty_like(z)
     if not isinstance(out, torch.Tensor) or out.dtype != torch.float32 or not out.is_contiguous():
         raise TypeError("out must be a contiguous float32 tensor")
     _shape(out, "out", tuple(z.shape))
