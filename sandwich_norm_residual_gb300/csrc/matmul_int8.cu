@@ -10,13 +10,12 @@
 namespace {
 
 using beam::MatmulParams;
+using beam::Shape;
 
 bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
     return na && nb && a0 < b0 + nb && b0 < a0 + na;
 }
-
-constexpr int kMaxSms = 152;  // workers of a launch at most, and what workspaces are sized for
 
 bool misaligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1u)) != 0; }
 
@@ -115,41 +114,6 @@ beam_status allow_smem(const void* fn, size_t bytes, std::atomic<unsigned long l
     return BEAM_OK;
 }
 
-// What a join takes in steps of k: the sums written, the second kernel
-template <int CG>
-constexpr uint32_t kJoinSteps = CG == 1 ? 8 : 26;
-
-// The split of a product into tiles of NT tokens by 128 CG channels
-template <int NT, int CG>
-beam::MatmulTcParams plan(const MatmulParams& p, int sms) {
-    beam::MatmulTcParams q{};
-    q.p = p;
-    q.m_tiles = (uint32_t)((p.M + NT - 1) / NT);
-    q.steps = (uint32_t)((p.K + beam::kStepK - 1) / beam::kStepK);
-    q.tiles = q.m_tiles * (uint32_t)((p.N + beam::kTileN * CG - 1) / (beam::kTileN * CG));
-    q.workers = (uint32_t)(sms / CG);
-    // The tiles behind the last full wave are shared, with four steps a worker at
-    // least, where that shortens the wave by more than the join takes (kJoinSteps).
-    // Single CTAs: M = 517, N = 2565, K = 2576, 105 tiles of 21 steps: 19.6 us
-    // unshared, 20.9 us shared; M = 64, N = 5120, K = 20480, 40 of 160: 75 and 29 us.
-    // Pairs: M = 1024, N = 5120, K = 5120, 80 tiles of 40 steps: 53 and 41 us; M = 512,
-    // 40 tiles: 31 and 39 us.
-    q.waves = q.tiles / q.workers;
-    q.split = (q.tiles - q.waves * q.workers) * q.steps;
-    const uint32_t most = (q.split + 3) / 4;
-    q.sharers = most < q.workers ? most : q.workers;
-    if (q.split && q.steps <= (q.split + q.sharers - 1) / q.sharers + kJoinSteps<CG>) {
-        q.waves += 1;
-        q.split = q.sharers = 0;
-    }
-    return q;
-}
-
-template <int NT, int CG>
-int64_t part_bytes(const beam::MatmulTcParams& q) {
-    return (int64_t)q.sharers * CG * 2 * NT * beam::kTileN * 4;
-}
-
 template <int NT, int CG, bool F32>
 beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* part, int64_t workspace_bytes,
                         cudaStream_t stream, uint32_t flags) {
@@ -159,11 +123,14 @@ beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* pa
     const void* fn = reinterpret_cast<const void*>(beam::matmul_int8_tile_kernel<NT, CG, F32>);
     beam_status st = allow_smem(fn, C::kSmem, &allowed, dev.ordinal);
     if (st != BEAM_OK) return st;
-    beam::MatmulTcParams q = plan<NT, CG>(p, dev.sms < kMaxSms ? dev.sms : kMaxSms);
-    if (part_bytes<NT, CG>(q) > workspace_bytes) {  // planned for 152 SMs; with fewer, more may be shared
+    beam::MatmulTcParams q{};
+    static_cast<beam::TilePlan&>(q) =
+        beam::plan<NT, CG>(p.M, p.N, p.K, dev.sms < beam::kMaxSms ? dev.sms : beam::kMaxSms);
+    if (beam::part_bytes<NT, CG>(q) > workspace_bytes) {  // planned for 152 SMs; with fewer, more may be shared
         q.waves += 1;
         q.split = q.sharers = 0;
     }
+    q.p = p;
     q.wide = !F32 && p.N % 8 == 0 && p.N >= beam::kTileN && !misaligned(p.out, 16);
     CUtensorMap wmap, pmap, amap;
     if (!row_map(&wmap, p.w, p.N, p.K, beam::kTileN) || !row_map(&amap, p.a, p.M, p.K, C::kRows)) return BEAM_ERR_CUDA;
@@ -183,26 +150,6 @@ beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* pa
     // blocks, waiting on the SMs that are done, cost 2 us
     return launch(reinterpret_cast<const void*>(beam::matmul_int8_join_kernel<NT, CG, F32>),
                   dim3(shared, NT / beam::Join<NT>::kCols, CG), dim3(beam::kTileN), join_args, 0, stream, q.waves == 0);
-}
-
-// Tokens a tile: as few as hold M; beyond 128, single CTAs or pairs, whichever
-// finishes first by the measured time of a step (0.52 and 0.60 us), of a join and
-// of a result that nothing hides (0.7 and 1.5 us)
-enum class Shape { kFew, k16, k32, k64, k128, kPair };
-
-Shape choose(const MatmulParams& p) {
-    if (p.M <= 8) return Shape::kFew;
-    if (p.M <= 16) return Shape::k16;
-    if (p.M <= 32) return Shape::k32;
-    if (p.M <= 64) return Shape::k64;
-    if (p.M <= 128) return Shape::k128;
-    auto ns = [](const beam::MatmulTcParams& q, uint32_t join, double step, double result) {
-        const uint32_t shared = q.split ? (q.split + q.sharers - 1) / q.sharers + join : 0;
-        return q.waves * (q.steps * step + result) + shared * step;
-    };
-    return ns(plan<128, 1>(p, kMaxSms), kJoinSteps<1>, 520, 700) < ns(plan<256, 2>(p, kMaxSms), kJoinSteps<2>, 600, 1500)
-               ? Shape::k128
-               : Shape::kPair;
 }
 
 template <bool F32>
@@ -230,15 +177,7 @@ extern "C" {
 int64_t beam_matmul_int8_workspace(int64_t M, int N, int K) {
     if (bad_shape(M, N, K)) return -1;
     if (M == 0 || N == 0) return 0;
-    const MatmulParams p{nullptr, nullptr, nullptr, nullptr, nullptr, M, N, K};
-    switch (choose(p)) {
-    case Shape::kFew: return 0;
-    case Shape::k16: return part_bytes<16, 1>(plan<16, 1>(p, kMaxSms));
-    case Shape::k32: return part_bytes<32, 1>(plan<32, 1>(p, kMaxSms));
-    case Shape::k64: return part_bytes<64, 1>(plan<64, 1>(p, kMaxSms));
-    case Shape::k128: return part_bytes<128, 1>(plan<128, 1>(p, kMaxSms));
-    default: return part_bytes<256, 2>(plan<256, 2>(p, kMaxSms));
-    }
+    return beam::workspace_bytes(M, N, K);
 }
 
 beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, const float* a_scale, const int8_t* w,
@@ -248,7 +187,7 @@ beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, const float*
     const int64_t need = beam_matmul_int8_workspace(M, N, K);
     if ((out_type != BEAM_OUT_BF16 && out_type != BEAM_OUT_FP32) || workspace_bytes < need ||
         (flags & ~(BEAM_OPT_PDL | BEAM_OPT_TEST_WAIT_TIMEOUT)) ||
-        ((flags & BEAM_OPT_TEST_WAIT_TIMEOUT) && choose({nullptr, nullptr, nullptr, nullptr, nullptr, M, N, K}) == Shape::kFew))
+        ((flags & BEAM_OPT_TEST_WAIT_TIMEOUT) && beam::choose(M, N, K) == Shape::kFew))
         return BEAM_ERR_ARG;
     if (M == 0 || N == 0) return BEAM_OK;
     if (!a || !a_scale || !w || !w_scale || !out || (need && !workspace)) return BEAM_ERR_NULL;
@@ -271,7 +210,7 @@ beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, const float*
     if (st != BEAM_OK) return st;
     MatmulParams p{a, a_scale, w, w_scale, out, M, N, K};
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    const Shape shape = choose(p);
+    const Shape shape = beam::choose(M, N, K);
     if (shape != Shape::kFew)
         return f32 ? launch_tiles<true>(shape, p, dev, workspace, workspace_bytes, cs, flags)
                    : launch_tiles<false>(shape, p, dev, workspace, workspace_bytes, cs, flags);
@@ -279,7 +218,7 @@ beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, const float*
     int channels = 0;
     const void* fn = f32 ? few_kernel<true>(M, &channels) : few_kernel<false>(M, &channels);
     const int per_block = channels * beam::kFewWarps;
-    return launch(fn, dim3((unsigned)((N + per_block - 1) / per_block)), dim3(32 * beam::kFewWarps), args, 0, cs,
+    return launch(fn, dim3((unsigned)(((int64_t)N + per_block - 1) / per_block)), dim3(32 * beam::kFewWarps), args, 0, cs,
                   (flags & BEAM_OPT_PDL) != 0);
 }
 

@@ -23,28 +23,19 @@
 #include <type_traits>
 
 #include "matmul_int8.cuh"
+#include "matmul_int8_plan.h"
 #include "packed.cuh"
 #include "umma.cuh"
 
 namespace beam {
 
-constexpr int kStepK = 128;                         // k of one ring slot and of one operand slot
-constexpr int kTileN = 128;                         // channels of a CTA: the lanes of tensor memory
 constexpr int kStepCols = kStepK / 2;               // columns of A for a step (two FP16 a column)
 constexpr uint32_t kABytes = kTileN * kStepK;       // int8 channels of a step
 constexpr uint64_t kMatmulWaitNs = 2000000000ull;   // every wait gives up after 2 s
 constexpr uint64_t kMatmulTestWaitNs = 1000000ull;  // the test hook's: 1 ms
 
-struct MatmulTcParams {
+struct MatmulTcParams : TilePlan {
     MatmulParams p;
-    uint32_t m_tiles;         // tiles of NT tokens
-    uint32_t steps;           // of k
-    uint32_t tiles;
-    // `workers` CTAs (CG = 1) or pairs (CG = 2). Worker c takes the whole tiles
-    // c, c + workers, ... of the first waves * workers, and of the `split` steps of
-    // the tiles behind those its share of an even split among the first `sharers`
-    // (split * sharers < 2^32: fewer than 152 tiles of at most 512 steps).
-    uint32_t waves, workers, sharers, split;
     // BF16 rows of out start on 16 bytes and end there: whole tiles of 128 channels
     // are then loaded in the order of `pmap` and stored 16 bytes a thread
     int wide;
@@ -253,7 +244,7 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
     // Channels in the order that lets a thread store 8 of them at once (see the
     // result): lane 8 b + 2 j + e of each 32 holds channel 8 j + 2 b + e
     auto permuted = [&](const Segment& s) {
-        return !F32 && q.wide && s.whole && s.n0 + kTileN <= q.p.N;
+        return !F32 && q.wide && s.whole && whole_channels(q.p.N, s.n0);
     };
 
     if (tid == 0) {
