@@ -115,8 +115,8 @@ beam_status allow_smem(const void* fn, size_t bytes, std::atomic<unsigned long l
 }
 
 template <int NT, int CG, bool F32>
-beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* part, int64_t workspace_bytes,
-                        cudaStream_t stream, uint32_t flags) {
+beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* part, cudaStream_t stream,
+                        uint32_t flags) {
     const bool pdl = (flags & BEAM_OPT_PDL) != 0, drop = (flags & BEAM_OPT_TEST_WAIT_TIMEOUT) != 0;
     using C = beam::TileConfig<NT, CG>;
     static std::atomic<unsigned long long> allowed{0};
@@ -124,12 +124,7 @@ beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* pa
     beam_status st = allow_smem(fn, C::kSmem, &allowed, dev.ordinal);
     if (st != BEAM_OK) return st;
     beam::MatmulTcParams q{};
-    static_cast<beam::TilePlan&>(q) =
-        beam::plan<NT, CG>(p.M, p.N, p.K, dev.sms < beam::kMaxSms ? dev.sms : beam::kMaxSms);
-    if (beam::part_bytes<NT, CG>(q) > workspace_bytes) {  // planned for 152 SMs; with fewer, more may be shared
-        q.waves += 1;
-        q.split = q.sharers = 0;
-    }
+    static_cast<beam::TilePlan&>(q) = beam::launch_plan<NT, CG>(p.M, p.N, p.K, dev.sms);
     q.p = p;
     q.wide = !F32 && p.N % 8 == 0 && p.N >= beam::kTileN && !misaligned(p.out, 16);
     CUtensorMap wmap, pmap, amap;
@@ -153,14 +148,14 @@ beam_status launch_tile(const MatmulParams& p, const beam::Device& dev, void* pa
 }
 
 template <bool F32>
-beam_status launch_tiles(Shape shape, const MatmulParams& p, const beam::Device& dev, void* part, int64_t bytes,
+beam_status launch_tiles(Shape shape, const MatmulParams& p, const beam::Device& dev, void* part,
                          cudaStream_t stream, uint32_t flags) {
     switch (shape) {
-    case Shape::k16: return launch_tile<16, 1, F32>(p, dev, part, bytes, stream, flags);
-    case Shape::k32: return launch_tile<32, 1, F32>(p, dev, part, bytes, stream, flags);
-    case Shape::k64: return launch_tile<64, 1, F32>(p, dev, part, bytes, stream, flags);
-    case Shape::k128: return launch_tile<128, 1, F32>(p, dev, part, bytes, stream, flags);
-    default: return launch_tile<256, 2, F32>(p, dev, part, bytes, stream, flags);
+    case Shape::k16: return launch_tile<16, 1, F32>(p, dev, part, stream, flags);
+    case Shape::k32: return launch_tile<32, 1, F32>(p, dev, part, stream, flags);
+    case Shape::k64: return launch_tile<64, 1, F32>(p, dev, part, stream, flags);
+    case Shape::k128: return launch_tile<128, 1, F32>(p, dev, part, stream, flags);
+    default: return launch_tile<256, 2, F32>(p, dev, part, stream, flags);
     }
 }
 
@@ -212,8 +207,8 @@ beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, const float*
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const Shape shape = beam::choose(M, N, K);
     if (shape != Shape::kFew)
-        return f32 ? launch_tiles<true>(shape, p, dev, workspace, workspace_bytes, cs, flags)
-                   : launch_tiles<false>(shape, p, dev, workspace, workspace_bytes, cs, flags);
+        return f32 ? launch_tiles<true>(shape, p, dev, workspace, cs, flags)
+                   : launch_tiles<false>(shape, p, dev, workspace, cs, flags);
     void* args[] = {&p};
     int channels = 0;
     const void* fn = f32 ? few_kernel<true>(M, &channels) : few_kernel<false>(M, &channels);

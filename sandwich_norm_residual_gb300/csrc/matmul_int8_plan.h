@@ -65,6 +65,18 @@ int64_t part_bytes(const TilePlan& q) {
     return (int64_t)q.sharers * CG * 2 * NT * kTileN * 4;
 }
 
+// The plan of a launch on `sms` SMs. Workspaces are sized and checked for kMaxSms:
+// with fewer, tiles that need more than that are not shared.
+template <int NT, int CG>
+TilePlan launch_plan(int64_t M, int64_t N, int K, int sms) {
+    TilePlan q = plan<NT, CG>(M, N, K, sms < kMaxSms ? sms : kMaxSms);
+    if (part_bytes<NT, CG>(q) > part_bytes<NT, CG>(plan<NT, CG>(M, N, K, kMaxSms))) {
+        q.waves += 1;
+        q.split = q.sharers = 0;
+    }
+    return q;
+}
+
 // Tokens a tile: as few as hold M; beyond 128, single CTAs or pairs, whichever
 // finishes first by the measured time of a step (0.52 and 0.60 us), of a join and
 // of a result that nothing hides (0.7 and 1.5 us)

@@ -36,4 +36,13 @@ void plan_fields(int shape, int64_t M, int64_t N, int K, int sms, int64_t* out) 
     });
 }
 
+// the same for the plan of a launch on a device of `sms` SMs
+void launch_fields(int shape, int64_t M, int64_t N, int K, int sms, int64_t* out) {
+    with_shape(shape, [&]<int NT, int CG>() {
+        const TilePlan q = launch_plan<NT, CG>(M, N, K, sms);
+        const int64_t v[8] = {q.m_tiles, q.steps, q.tiles, q.waves, q.workers, q.sharers, q.split, part_bytes<NT, CG>(q)};
+        std::copy(v, v + 8, out);
+    });
+}
+
 }

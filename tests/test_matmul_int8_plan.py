@@ -69,3 +69,24 @@ def test_every_step_of_every_tile_is_taken_once(lib):
                 cuts = [q["split"] * c // q["sharers"] for c in range(q["sharers"] + 1)]
                 assert all(a < b for a, b in zip(cuts, cuts[1:])) and cuts[-1] == q["split"]
                 assert q["bytes"] == q["sharers"] * cg * 2 * nt * 128 * 4
+
+
+def test_a_launch_on_fewer_sms_needs_no_more_than_the_workspace_that_was_asked_for(lib):
+    """152 tiles are one wave of 152 SMs and need none; 148 SMs would share the last four."""
+    shapes = [(100, 152 * 128, 5120), (64, 5120, 20480), (300, 20480, 5120), (1030, 5110, 2064), (9, 70, 16),
+              (2048, 76 * 256, 20480)]
+    seen = 0
+    for M, N, K in shapes:
+        shape, need = lib.plan_choose(M, N, K), lib.plan_workspace(M, N, K)
+        for sms in range(2, 200):
+            raw = fields(lib, "plan_fields", shape, M, N, K, sms)
+            q = fields(lib, "launch_fields", shape, M, N, K, sms)
+            assert q["bytes"] <= need
+            seen += raw["bytes"] > need and sms < 152
+            if q["split"] == 0:  # whole tiles then cover everything
+                assert q["waves"] * q["workers"] >= q["tiles"]
+            else:
+                assert q["split"] == (q["tiles"] - q["waves"] * q["workers"]) * q["steps"]
+            assert q["workers"] <= 152
+    assert fields(lib, "plan_fields", lib.plan_choose(100, 152 * 128, 5120), 100, 152 * 128, 5120, 148)["bytes"] > 0
+    assert lib.plan_workspace(100, 152 * 128, 5120) == 0 and seen
