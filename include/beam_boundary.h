@@ -208,8 +208,9 @@ BEAM_API beam_status beam_router_sigmoid(beam_stream_t stream, const float* z, f
  */
 BEAM_API beam_status beam_router_sigmoid_fast(beam_stream_t stream, const float* z, float* s, int64_t count);
 
-/* Most experts of beam_moe_balance_loss. */
+/* Most experts and most sequences of beam_moe_balance_loss. */
 #define BEAM_BALANCE_MAX_EXPERTS 512
+#define BEAM_BALANCE_MAX_SEQUENCES 0x7FFFFFC0
 
 /*
  * Balance loss of the router in front of the MoE combine, with the per-expert
@@ -236,7 +237,8 @@ BEAM_API beam_status beam_router_sigmoid_fast(beam_stream_t stream, const float*
  *               beam_moe_balance_workspace(T, E, S) bytes (NULL where that is 0); need
  *               not be cleared
  * 4-byte aligned where nothing else is said. Outputs and workspace overlap
- * neither each other nor an input. T at most 2^31 - 1.
+ * neither each other nor an input. T at most 2^31 - 1, S at most
+ * BEAM_BALANCE_MAX_SEQUENCES.
  * A token whose sigmoids are all 0 has p = 0. A NaN logit makes its sequence's
  * loss NaN. An expert id outside [0, E) is not counted; offsets that decrease or
  * leave [0, T] make losses and counts unspecified (no address outside the

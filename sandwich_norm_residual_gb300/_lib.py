@@ -25,6 +25,7 @@ BEAM_QK_HEAD_DIM = 128
 BEAM_QK_ROPE = 0
 BEAM_QK_SSMAX = 1
 BEAM_BALANCE_MAX_EXPERTS = 512
+BEAM_BALANCE_MAX_SEQUENCES = 0x7FFFFFC0
 BEAM_OUT_BF16 = 0
 BEAM_OUT_FP32 = 1
 BEAM_MATMUL_MAX_K = 65536

@@ -20,7 +20,7 @@ bool misaligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t
 
 bool bad_shape(int64_t T, int E, int K, int64_t S, const void* off) {
     return T < 0 || T > 0x7FFFFFFF || E < 4 || (E & 3) || E > BEAM_BALANCE_MAX_EXPERTS || K < 1 ||
-           K > BEAM_ROUTE_MAX_TOPK || S < 1 || S > 0x7FFFFFFF || (!off && S != 1);
+           K > BEAM_ROUTE_MAX_TOPK || S < 1 || S > BEAM_BALANCE_MAX_SEQUENCES || (!off && S != 1);
 }
 
 // Tokens a block: at least one for each warp, few enough blocks that two are

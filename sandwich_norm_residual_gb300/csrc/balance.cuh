@@ -60,7 +60,7 @@ __device__ __forceinline__ long long seq_end(const BalanceParams& p, int s) {
 // places are looked at in one way to memory, where halving the range takes one for
 // each bit of S.
 __device__ __forceinline__ int find_seq(const BalanceParams& p, long long t) {
-    int lo = 0, n = p.S;  // the answer lies in [lo, lo + n]
+    int lo = 0, n = p.S;  // the answer lies in [lo, lo + n]; 32 steps stay below 2^31 (n <= 2^31 - 64)
     const int lane = threadIdx.x & 31;
     while (n > 0) {
         const int step = (n + 31) / 32, at = lo + min((lane + 1) * step, n) - 1;
