@@ -340,11 +340,14 @@ BEAM_API beam_status beam_qk_norm_ex(beam_stream_t stream, uint16_t* q, uint16_t
  * A scale that is infinite or NaN makes its row's or channel's products with
  * acc = 0 NaN (0 * inf), as the FP32 products above say.
  * flags: BEAM_OPT_PDL launches with programmatic stream serialisation: the
- * kernel reads w before the previous kernel on the stream has completed (that
- * kernel must not write w), and everything else after. BEAM_OPT_TEST_WAIT_TIMEOUT
- * is a test hook for the bounded waits of the kernels for more than 8 tokens: the
- * copies of every tile's second 128 k are never issued, the waits for them give up
- * after 1 ms, out holds anything and beam_sync_status returns BEAM_ERR_TIMEOUT.
+ * kernel reads w while kernels before it on the stream still run, and everything
+ * else once they have completed. Use it only when the kernels just before this
+ * call on the stream do not write w, as said at that flag: not the previous one,
+ * nor one that a chain of launches with the flag leaves running.
+ * BEAM_OPT_TEST_WAIT_TIMEOUT is a test hook for the bounded waits of the kernels for
+ * more than 8 tokens: the copies of every tile's second 128 k are never issued, the
+ * waits for them give up after 1 ms, out holds anything and beam_sync_status returns
+ * BEAM_ERR_TIMEOUT.
  * Any other flag, and the hook with 8 tokens or fewer, gives BEAM_ERR_ARG.
  */
 BEAM_API beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, const float* a_scale,
@@ -359,8 +362,9 @@ BEAM_API int64_t beam_matmul_int8_workspace(int64_t M, int N, int K);
  * Synchronises `stream`, then reads and clears the current device's status
  * word. Returns BEAM_OK; BEAM_ERR_TIMEOUT if a kernel's bounded wait gave up
  * since the last read; BEAM_ERR_ARG if beam_qk_norm met a position out of
- * range, or beam_moe_balance_loss an expert or offset out of range; or BEAM_ERR_CUDA if the synchronisation failed. The word is shared
- * by all streams and threads using the device.
+ * range, or beam_moe_balance_loss an expert or offset out of range; or
+ * BEAM_ERR_CUDA if the synchronisation failed. The word is shared by all streams
+ * and threads using the device.
  */
 BEAM_API beam_status beam_sync_status(beam_stream_t stream);
 
@@ -405,8 +409,10 @@ typedef struct {
  * post_w and pre_w and asks L2 to prefetch its first rows (a hint that reads
  * no data into the kernel), then waits for that kernel to finish before it
  * reads h, x, expert_out or topk_w, and lets the next kernel start its own
- * prologue early. Use it only when the kernels just before this call on the
- * stream do not write post_w or pre_w. */
+ * prologue early, even before its own wait is over: after a chain of such
+ * launches the kernel in front of the chain may still run. Use it only when the
+ * kernels just before this call on the stream, back to and including the last one
+ * launched without the flag, do not write post_w or pre_w. */
 #define BEAM_OPT_PDL 0x4u
 
 BEAM_API beam_status beam_boundary_fused_ex(beam_stream_t stream, uint16_t* h, const uint16_t* x,
