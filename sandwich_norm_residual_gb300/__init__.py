@@ -140,6 +140,14 @@ def _workspace(nbytes: int, device):
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
+def _c_int(v) -> int:
+    """A number that the C ABI takes as int (ctypes would cut it to its low 32 bits)."""
+    v = int(v)
+    if not -0x80000000 <= v <= 0x7FFFFFFF:
+        raise ValueError(f"{v} is more than a 32-bit argument holds")
+    return v
+
+
 def _opts(opts):
     if opts is None:
         return None
@@ -169,7 +177,7 @@ def boundary_fused(h, x, post_w, pre_w, n: int, eps: float = 1e-6, y=None, strea
     _on_current_device(h=h, x=x, post_w=post_w, pre_w=pre_w, y=y)
     lib = _lib.load()
     args = (_stream_ptr(stream), h.data_ptr(), x.data_ptr(), post_w.data_ptr(), pre_w.data_ptr(),
-            int(n), float(eps), T, D, y.data_ptr())
+            _c_int(n), float(eps), T, _c_int(D), y.data_ptr())
     st = lib.beam_boundary_fused(*args) if opts is None else lib.beam_boundary_fused_ex(
         *args, _opts(opts))
     if st != 0:
@@ -209,13 +217,13 @@ def moe_combine_boundary(h, expert_out, topk_w, post_w, pre_w, n: int, eps: floa
             raise ValueError("route_scale and opts cannot be combined")
         st = lib.beam_moe_combine_boundary_scaled(
             _stream_ptr(stream), h.data_ptr(), expert_out.data_ptr(), topk_w.data_ptr(),
-            float(route_scale), post_w.data_ptr(), pre_w.data_ptr(), int(n), float(eps), T, D,
+            float(route_scale), post_w.data_ptr(), pre_w.data_ptr(), _c_int(n), float(eps), T, _c_int(D),
             y.data_ptr())
         if st != 0:
             raise BeamError(st, "beam_moe_combine_boundary_scaled")
         return y
     args = (_stream_ptr(stream), h.data_ptr(), expert_out.data_ptr(), topk_w.data_ptr(),
-            post_w.data_ptr(), pre_w.data_ptr(), int(n), float(eps), T, D, y.data_ptr())
+            post_w.data_ptr(), pre_w.data_ptr(), _c_int(n), float(eps), T, _c_int(D), y.data_ptr())
     st = lib.beam_moe_combine_boundary(*args) if opts is None else \
         lib.beam_moe_combine_boundary_ex(*args, _opts(opts))
     if st != 0:
@@ -264,8 +272,8 @@ def boundary_fused_host(h, x, post_w, pre_w, n: int, eps: float = 1e-6, y=None, 
     _check_any(y, "y", torch.bfloat16, 2)
     _shape(y, "y", (T, D))
     st = _lib.load().beam_boundary_fused_host(_stream_ptr(stream), h.data_ptr(), x.data_ptr(),
-                                              post_w.data_ptr(), pre_w.data_ptr(), int(n),
-                                              float(eps), T, D, y.data_ptr())
+                                              post_w.data_ptr(), pre_w.data_ptr(), _c_int(n),
+                                              float(eps), T, _c_int(D), y.data_ptr())
     if st != 0:
         raise BeamError(st, "beam_boundary_fused_host")
     return y
@@ -291,7 +299,7 @@ def moe_combine_boundary_host(h, expert_out, topk_w, post_w, pre_w, n: int, eps:
     _shape(y, "y", (T, D))
     st = _lib.load().beam_moe_combine_boundary_host(
         _stream_ptr(stream), h.data_ptr(), expert_out.data_ptr(), topk_w.data_ptr(),
-        post_w.data_ptr(), pre_w.data_ptr(), int(n), float(eps), T, D, y.data_ptr())
+        post_w.data_ptr(), pre_w.data_ptr(), _c_int(n), float(eps), T, _c_int(D), y.data_ptr())
     if st != 0:
         raise BeamError(st, "beam_moe_combine_boundary_host")
     return y
@@ -329,8 +337,8 @@ def boundary_fused_nvfp4(h, x, post_w, pre_w, n: int, eps: float, y_global_scale
     q, sf = _nvfp4_out(h, y_fp4, y_scale, stream)
     _on_current_device(h=h, x=x, post_w=post_w, pre_w=pre_w, y_fp4=q, y_scale=sf)
     st = _lib.load().beam_boundary_fused_nvfp4(_stream_ptr(stream), h.data_ptr(), x.data_ptr(),
-                                               post_w.data_ptr(), pre_w.data_ptr(), int(n),
-                                               float(eps), T, D, float(y_global_scale),
+                                               post_w.data_ptr(), pre_w.data_ptr(), _c_int(n),
+                                               float(eps), T, _c_int(D), float(y_global_scale),
                                                q.data_ptr(), sf.data_ptr(), _opts(opts))
     if st != 0:
         raise BeamError(st, "beam_boundary_fused_nvfp4")
@@ -356,7 +364,7 @@ def moe_combine_boundary_nvfp4(h, expert_out, topk_w, post_w, pre_w, n: int, eps
                        y_fp4=q, y_scale=sf)
     st = _lib.load().beam_moe_combine_boundary_nvfp4(
         _stream_ptr(stream), h.data_ptr(), expert_out.data_ptr(), topk_w.data_ptr(),
-        post_w.data_ptr(), pre_w.data_ptr(), int(n), float(eps), T, D, float(y_global_scale),
+        post_w.data_ptr(), pre_w.data_ptr(), _c_int(n), float(eps), T, _c_int(D), float(y_global_scale),
         q.data_ptr(), sf.data_ptr(), _opts(opts))
     if st != 0:
         raise BeamError(st, "beam_moe_combine_boundary_nvfp4")
@@ -409,7 +417,7 @@ def boundary_fused_int8(h, x, post_w, pre_w, n: int, eps: float = 1e-6, y_int8=N
     if not ready:
         _on_current_device(h=h, x=x, post_w=post_w, pre_w=pre_w, y_int8=q, y_scale=scale)
     st = _lib.load().beam_boundary_fused_int8(_raw_stream(stream, h), h.data_ptr(), x.data_ptr(),
-                                              post_w.data_ptr(), pre_w.data_ptr(), int(n), float(eps), T, D,
+                                              post_w.data_ptr(), pre_w.data_ptr(), _c_int(n), float(eps), T, _c_int(D),
                                               q.data_ptr(), scale.data_ptr(), _opts(opts))
     if st != 0:
         raise BeamError(st, "beam_boundary_fused_int8")
@@ -441,7 +449,7 @@ def moe_combine_boundary_int8(h, expert_out, topk_w, post_w, pre_w, n: int, eps:
                            y_int8=q, y_scale=scale)
     st = _lib.load().beam_moe_combine_boundary_int8(
         _raw_stream(stream, h), h.data_ptr(), expert_out.data_ptr(), topk_w.data_ptr(),
-        float(route_scale), post_w.data_ptr(), pre_w.data_ptr(), int(n), float(eps), T, D,
+        float(route_scale), post_w.data_ptr(), pre_w.data_ptr(), _c_int(n), float(eps), T, _c_int(D),
         q.data_ptr(), scale.data_ptr(), _opts(opts))
     if st != 0:
         raise BeamError(st, "beam_moe_combine_boundary_int8")
@@ -478,6 +486,7 @@ def matmul_int8(a, a_scale, w, w_scale, out_dtype=None, out=None, stream=None, p
             raise ValueError("shape mismatch: a [M, K]; a_scale [M]; w [N, K]; w_scale [N]")
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError(f"out_dtype must be bfloat16 or float32 (got {out_dtype})")
+    N, K = _c_int(N), _c_int(K)
     ws_bytes = _matmul_workspace(M, N, K)
     with _pool(stream):
         if out is None:
@@ -520,8 +529,8 @@ def moe_route(logits, bias, n_group: int = 8, topk_group: int = 4, topk: int = 8
     _shape(idx, "idx", (T, topk))
     _shape(w, "w", (T, topk))
     _on_current_device(logits=logits, bias=bias, idx=idx, w=w)
-    st = _lib.load().beam_moe_route_ex(_stream_ptr(stream), logits.data_ptr(), bias.data_ptr(), T, E,
-                                       int(n_group), int(topk_group), int(topk), float(route_scale),
+    st = _lib.load().beam_moe_route_ex(_stream_ptr(stream), logits.data_ptr(), bias.data_ptr(), T, _c_int(E),
+                                       _c_int(n_group), _c_int(topk_group), _c_int(topk), float(route_scale),
                                        idx.data_ptr(), w.data_ptr(), _lib.BEAM_OPT_PDL if pdl else 0)
     if st != 0:
         raise BeamError(st, "beam_moe_route_ex")
@@ -569,6 +578,7 @@ def moe_balance_loss(logits, topk_idx, alpha: float, seq_offsets=None, loss=None
         _check(topk_idx, "topk_idx", torch.int32, 2)
         if topk_idx.shape[0] != T:
             raise ValueError("shape mismatch: logits [T, E]; topk_idx [T, topk]")
+    E, K = _c_int(E), _c_int(K)
     ws_bytes = _balance_workspace(T, E, S)
     with _pool(stream):
         if loss is None:
@@ -621,7 +631,8 @@ def moe_balance_loss_backward(dloss, logits, counts, topk: int, alpha: float, se
                                     dlogits=dlogits))
     st = _lib.load().beam_moe_balance_loss_backward(
         _raw_stream(stream, logits), dloss.data_ptr(), logits.data_ptr(), counts.data_ptr(),
-        None if seq_offsets is None else seq_offsets.data_ptr(), T, E, int(topk), S, float(alpha), dlogits.data_ptr())
+        None if seq_offsets is None else seq_offsets.data_ptr(), T, _c_int(E), _c_int(topk), S, float(alpha),
+        dlogits.data_ptr())
     if st != 0:
         raise BeamError(st, "beam_moe_balance_loss_backward")
     return dlogits
@@ -679,7 +690,7 @@ def qk_norm(q, k, q_w, k_w, pos, eps: float = 1e-6, mode: str = "rope", rope_tab
     _on_current_device(**ops)
     st = _lib.load().beam_qk_norm_ex(_stream_ptr(stream), q.data_ptr(), k.data_ptr(), q_w.data_ptr(),
                                      k_w.data_ptr(), pos.data_ptr(), tab or None, max_pos, T,
-                                     q.shape[1], k.shape[1], q.shape[2], float(eps), m,
+                                     _c_int(q.shape[1]), _c_int(k.shape[1]), _c_int(q.shape[2]), float(eps), m,
                                      (_lib.BEAM_OPT_FORCE_EXACT_SUM if force_exact else 0)
                                      | (_lib.BEAM_OPT_PDL if pdl else 0))
     if st != 0:
