@@ -369,14 +369,17 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_grad_kernel(const Bal
                 one(z[v].w, d[v].w, c[v].w);
             }
             const float inv = inverse_or_zero(warp_sum(sum));
-            const float mean = warp_sum(mix) * inv, f = g * inv;
+            const float mean = warp_sum(mix) * inv;
+            // d inv is at most 1; g inv would leave FP32 where every sigmoid is near
+            // 2^-126 and g carries a loss scale
+            auto out = [&](float di, float ci) { return (di * inv) * (g * (ci - mean)); };
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int e = 128 * v + 4 * lane;
                 if (e < p.E)
                     __stcs(reinterpret_cast<float4*>(p.dlogits + (size_t)t * (size_t)p.E + e),
-                           make_float4(d[v].x * f * (c[v].x - mean), d[v].y * f * (c[v].y - mean),
-                                       d[v].z * f * (c[v].z - mean), d[v].w * f * (c[v].w - mean)));
+                           make_float4(out(d[v].x, c[v].x), out(d[v].y, c[v].y), out(d[v].z, c[v].z),
+                                       out(d[v].w, c[v].w)));
             }
         }
     }, [&](long long, long long hi) {
