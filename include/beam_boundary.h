@@ -221,10 +221,12 @@ BEAM_API beam_status beam_router_sigmoid_fast(beam_stream_t stream, const float*
  *   counts_e = how often expert e stands in the tokens' topk_idx
  *   loss     = alpha * sum_e f_e P_e,  f_e = E / (topk n) counts_e,
  *              P_e = (1/n) sum_t p_te
- * FP32 sigmoids (within |logit| + 4 units of 2^-24, not the correctly rounded ones of
- * beam_router_sigmoid) and rows, compensated sums over tokens, 64-bit ones over experts, one
- * rounding of the loss; sigmoids below 2^-126 count as 0. Every run gives the same
- * bits.
+ * FP32 sigmoids (within 8 units of 2^-24, relative, whatever the logit; not the
+ * correctly rounded ones of beam_router_sigmoid; below 2^-126 they count as 0) and
+ * rows. A sequence's Q_e = n P_e is added in FP32 over the at most 64 tokens of a warp
+ * and the 16 warps of a block, with compensation (two FP32 numbers a sum) over blocks;
+ * the sum over experts and the factor are 64-bit, the loss is rounded once. Every run
+ * gives the same bits.
  *   logits      [T, E] FP32, E a multiple of 4, at most BEAM_BALANCE_MAX_EXPERTS;
  *               16-byte aligned
  *   topk_idx    [T, topk] int32 in [0, E), topk in [1, BEAM_ROUTE_MAX_TOPK]

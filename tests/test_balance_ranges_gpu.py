@@ -1,5 +1,5 @@
-"""The balance loss at the ends of its ranges: gradients where one factor leaves FP32 although the
-product does not."""
+"""The balance loss at the ends of its ranges: the sigmoid's stated bound over all logits, gradients
+where one factor leaves FP32 although the product does not."""
 from __future__ import annotations
 
 import numpy as np
@@ -22,6 +22,27 @@ def built():
 def sigmoid(z):
     with np.errstate(over="ignore"):
         return 1 / (1 + np.exp(-z.astype(np.float64)))
+
+
+@pytest.mark.parametrize("T", [512, 40000])  # one kernel; records and a second kernel
+def test_the_sigmoid_is_within_its_bound_at_every_logit(T):
+    """A sequence for every token, of four experts whose other logits are infinite (sigmoid 1) and
+    whose one choice is the first expert: the loss is alpha 4 p_0 = p_0 = s / (3 + s).
+
+    In units of 2^-24: the sigmoid's stated 8, of which the sum in the denominator takes s / (3 + s)
+    back; the sum itself 2 roundings, the division 1, the product 1, the loss 1: 13 at most."""
+    z = np.full((T, 4), np.inf, np.float32)
+    z[:, 0] = np.linspace(-87, 88, T).astype(np.float32)
+    z[:2, 0] = np.float32(-44.371693), np.float32(-44.526)
+    idx = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    off = torch.arange(T + 1, dtype=torch.int32, device="cuda")
+    loss, counts = snr.moe_balance_loss(torch.from_numpy(z).cuda(), idx, 0.25, seq_offsets=off)
+    snr.sync_status()
+    s = sigmoid(z[:, 0])
+    want = s / (3 + s)
+    err = np.abs(loss.cpu().numpy() - want) / want / U
+    assert err.max() <= 13, (z[err.argmax(), 0], err.max())
+    assert bool((counts[:, 0] == 1).all()) and int(counts.sum()) == T
 
 
 @pytest.mark.parametrize("T", [1, 700])
