@@ -324,10 +324,11 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                     if (it >= C::kSlots && w_side) load_w(slot, seg, (int)k);
                     if (a_side) load_a(slot, seg, (int)k);
                 }
-            if (!ok)  // copies in flight must land before the shared memory goes
-                for (int i = it - C::kSlots; i < it; ++i)
-                    if ((i & 1) == mine)
-                        mbar_wait(&raw_full[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
+            // Copies in flight must land before the shared memory goes: also where every
+            // step was issued, as the warps that read them may have given up before
+            for (int i = max(it - C::kSlots, 0); i < it; ++i)
+                if ((i & 1) == mine)
+                    mbar_wait(&raw_full[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
         }
     } else if (warp == kMulWarp) {
         if (rank == 0) {
