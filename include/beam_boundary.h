@@ -324,9 +324,11 @@ BEAM_API beam_status beam_qk_norm_ex(beam_stream_t stream, uint16_t* q, uint16_t
  *   out[m, n] = RN( RN32( RN32( (float)acc * a_scale[m] ) * w_scale[n] ) ),
  *   acc = sum_k a[m, k] * w[n, k]
  * The last rounding is to BF16, or nothing when out is FP32.
- * acc is the integer sum, exact as long as no partial sum of its terms leaves
- * +-2^24 (so always for K <= 1024); where one does, acc carries FP32 rounding
- * of its partial sums.
+ * acc is the integer sum. For up to 8 tokens it is exact (32-bit integers). For
+ * more it is exact as long as no partial sum of its terms, in whatever order,
+ * leaves +-2^24: always for K <= 1024, and where sum_k |a w| <= 2^24. Beyond, the
+ * matrix unit adds in FP32, off by at most K 2^-23 sum_k |a w| in all; a result
+ * of such sums can change with M and N, so when a batch grows from 8 tokens to 9.
  *   a       [M, K] int8 tokens (all 256 codes); 16-byte aligned
  *   a_scale [M] FP32; w_scale [N] FP32; 4-byte aligned
  *   w       [N, K] int8 channels (one row per output channel); 16-byte aligned

@@ -467,6 +467,8 @@ def matmul_int8(a, a_scale, w, w_scale, out_dtype=None, out=None, stream=None, p
     a: [M, K] int8 and a_scale: [M] float32, as an int8 boundary writes them; w: [N, K] int8
     and w_scale: [N] float32. K must be a multiple of 16.
     Returns [M, N] in out_dtype: bfloat16 (the default) or float32.
+    Integer sums are exact for up to 8 tokens, and for more while no partial sum leaves +-2^24
+    (always for K <= 1024); beyond, they carry FP32 roundings and can change with M and N.
     pdl: launch with programmatic dependent launch (BEAM_OPT_PDL), which reads w while kernels
     before it on the stream still run: neither the previous one may write w, nor one in front of
     a chain of calls with pdl (write w; a call with pdl; this call with pdl: w may be read too early).

@@ -3,8 +3,12 @@
 // GB300's tcgen05 has no integer kind, and its legacy integer path is slow. But
 // every int8 is an FP16 number, a product of two is an integer of at most 2^14,
 // and FP32 accumulators hold integers below 2^24 exactly: so the FP16 kind at
-// its full rate gives the integer product. What has to be added is the widening
-// on the way from shared memory to the operands:
+// its full rate gives the integer product, as long as partial sums stay below that
+// (codes of an rms of 32 reach 2^18 at K = 65536). An accumulator runs on over all
+// steps that a CTA has of a tile: emptied into 32-bit integers every 1024 k, sums
+// would be exact for any codes, but the pairs' accumulator takes half of tensor
+// memory and would stand still meanwhile. What has to be added is the widening on
+// the way from shared memory to the operands:
 //   - 128 channels are the rows of A. A lives in tensor memory, which the
 //     widening warps write directly (thread = channel row = lane), so widened
 //     channels never pass through shared memory;
@@ -517,8 +521,8 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
 }
 
 // Adds the sums of the tiles that several workers have steps of: a block for
-// kCols tokens of a tile, thread = channel. They are integers (FP32 ones), added
-// as such. What it takes (3 us) is its launch and one way to L2 and back, so few
+// kCols tokens of a tile, thread = channel. They are FP32 numbers that are integers,
+// also past 2^24, and at most 2^30: added as 32-bit integers, without rounding. What it takes (3 us) is its launch and one way to L2 and back, so few
 // values a thread (but not so few that blocks are counted in thousands: 2 tokens a
 // block cost 3 us more than 8 at NT = 128) and several workers' at once.
 template <int NT>
