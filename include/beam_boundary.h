@@ -252,7 +252,7 @@ BEAM_API beam_status beam_moe_balance_loss(beam_stream_t stream, const float* lo
                                            float* loss, int32_t* counts, void* workspace,
                                            int64_t workspace_bytes);
 
-/* Bytes of workspace of beam_moe_balance_loss (0 up to 512 tokens), -1 for a bad shape. */
+/* Bytes of workspace of beam_moe_balance_loss (0 for few tokens), -1 for a bad shape. */
 BEAM_API int64_t beam_moe_balance_workspace(int64_t T, int E, int64_t S);
 
 /*

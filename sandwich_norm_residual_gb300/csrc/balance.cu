@@ -23,6 +23,11 @@ bool bad_shape(int64_t T, int E, int K, int64_t S, const void* off) {
            K > BEAM_ROUTE_MAX_TOPK || S < 1 || S > BEAM_BALANCE_MAX_SEQUENCES || (!off && S != 1);
 }
 
+// Whether one kernel does it all
+bool one_kernel(int64_t T, int E, int64_t S) {
+    return T <= beam::kBalanceSmall && T * E <= S * beam::kBalanceSmallLogits;
+}
+
 // Tokens a block: at least one for each warp, few enough blocks that two are
 // resident on every SM, and at most 64 for each warp, which adds them in FP32
 void split(int64_t T, BalanceParams* p) {
@@ -84,7 +89,7 @@ extern "C" {
 
 int64_t beam_moe_balance_workspace(int64_t T, int E, int64_t S) {
     if (bad_shape(T, E, 1, S, &T)) return -1;
-    if (T <= beam::kBalanceSmall) return 0;
+    if (one_kernel(T, E, S)) return 0;
     BalanceParams p{};
     split(T, &p);
     return ((int64_t)p.blocks + S) * E * 8;
@@ -128,7 +133,7 @@ beam_status beam_moe_balance_loss(beam_stream_t stream, const float* logits, con
     p.counts = counts;
     p.status = dev.status_word;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (T <= beam::kBalanceSmall) return launch(small_kernel(E), p.S, beam::kBalanceThreads, &p, cs, false);
+    if (one_kernel(T, E, S)) return launch(small_kernel(E), p.S, beam::kBalanceThreads, &p, cs, false);
     split(T, &p);
     p.rec_q = static_cast<float*>(workspace);
     p.rec_c = reinterpret_cast<int32_t*>(p.rec_q + ((size_t)p.blocks + (size_t)S) * (size_t)E);

@@ -28,7 +28,8 @@ namespace beam {
 constexpr int kBalanceThreads = 512;
 constexpr int kBalanceWarps = kBalanceThreads / 32;
 constexpr int kBalanceBlocks = 304;  // two blocks on each of 152 SMs
-constexpr int kBalanceSmall = 512;   // tokens up to which one kernel does it all
+constexpr int kBalanceSmall = 512;   // tokens up to which one kernel may do it all (balance_small_kernel)
+constexpr int kBalanceSmallLogits = 384 * 256;  // ... and logits for each sequence
 constexpr int kBalanceFinalThreads = 1024;
 constexpr int kBalanceFinalSums = 4 * kBalanceFinalThreads;  // 4 experts a thread
 
@@ -291,9 +292,14 @@ __global__ void __launch_bounds__(kBalanceFinalThreads) balance_loss_kernel(cons
     }
 }
 
-// Few tokens: a block a sequence, without records and without a second kernel
-// (T = 128: 6.7 us instead of 8.2, and one launch and one workspace less for the
-// host: a pass both ways 25 us instead of 30)
+// Few tokens: a block a sequence, without records and without a second kernel: one
+// launch and one workspace less, which are 5 us of the host (a pass both ways through
+// the binding 33 us instead of 38). On the GPU its one block for a sequence grows with
+// the rows that each warp takes in turn, where records keep near 8 us. One sequence,
+// one kernel against two, us: E = 256: T = 128 7.0, 7.9; 192 8.5, 8.0; 384 13.0, 8.5;
+// 512 16.1, 8.4. E = 64: 256 8.6, 8.0; 512 13.6, 7.9. E = 512: 128 8.9, 9.0; 192 11.2,
+// 9.3; 512 24.6, 10.0. Four sequences, T = 512: E = 256 6.9, 8.1; E = 512 9.4, 9.2. The
+// limits are near where the GPU loses what the host gains.
 template <int V>
 __global__ void __launch_bounds__(kBalanceThreads) balance_small_kernel(const BalanceParams p) {
     __shared__ float sq[kBalanceWarps][V * 128];
