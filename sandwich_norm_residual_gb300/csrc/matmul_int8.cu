@@ -22,7 +22,10 @@ bool misaligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t
 // Kernel for up to 8 tokens, and its channels a warp. At N = 6144, K = 5120 the
 // shapes below take 6.5, 7.4, 9.0 and 11.2 us for 1, 2, 4 and 8 tokens; two
 // channels a warp take 9.7 and 24 us for 4 and 8, four take 7.2 us for 1, and a
-// second set of weights in flight (fewer warps an SM) 8.4 us for 1.
+// second set of weights in flight (fewer warps an SM) 8.4 us for 1. The tensor cores'
+// tile of 16 tokens takes 14 us there at any of these M. At N = 5120, K = 20480 it
+// takes 25 us, these shapes 17, 21, 23 and 36 us for 1, 2, 4 and 8 tokens: from 5
+// tokens on a long k would be faster there, but sums are exact here.
 template <bool F32>
 const void* few_kernel(int64_t M, int* channels) {
     *channels = M <= 2 ? 2 : 4;

@@ -43,10 +43,11 @@ __device__ __forceinline__ uint4 ld_weights(const int8_t* p) {
 
 // Up to MB tokens by R channels a warp, on the integer dot product: the lanes take
 // 16 bytes each of 512 consecutive k, U such steps of the R weight rows in flight
-// at once. Bound by the weights' way from HBM: every weight byte is read once, and
-// one dp4a per token handles four of them, so up to 8 tokens keep the integer pipe
-// below the memory's pace. Sums are exact in 32 bits. M = 1, N = 6144, K = 5120:
-// 6.5 us, of which 2.2 are the launch; the weights alone take 4.7 us at the copy rate.
+// at once. Every weight byte is read once, and sums are exact in 32 bits. One token is
+// bound by the weights' way from HBM: M = 1, N = 6144, K = 5120: 6.5 us, of which 2.2
+// are the launch; the weights alone take 4.7 us at the copy rate. More tokens are not:
+// each costs every warp its rows again (through L1) and one dp4a for four weights, and
+// their sums leave registers for fewer weights in flight (M = 8: 11.2 us).
 constexpr int kFewWarps = 8;
 
 template <int MB, int R, int U, bool F32>

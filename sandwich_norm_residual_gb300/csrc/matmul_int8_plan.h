@@ -78,8 +78,13 @@ TilePlan launch_plan(int64_t M, int64_t N, int K, int sms) {
 }
 
 // Tokens a tile: as few as hold M; beyond 128, single CTAs or pairs, whichever
-// finishes first by the measured time of a step (0.52 and 0.60 us), of a join and
-// of a result that nothing hides (0.7 and 1.5 us)
+// finishes first by what a step (0.52 and 0.60 us), a join and a result that nothing
+// hides (0.7 and 1.5 us) take. Both were timed for M = 129 to 1500 in 12 sizes at
+// (N, K) = (5120, 5120), (6144, 5120), (20480, 5120), (5120, 20480), (2565, 2576) and
+// (2048, 2048): these weights take the faster at all 72. In a long run of steps single
+// CTAs take 0.45 us a step and pairs 0.58; with 0.45 as the weight six of the sizes
+// take the slower shape, by up to a quarter (M = 200, N = 20480, K = 5120: 49.5 us in
+// single CTAs, 39.8 in pairs; M = 512, N = K = 5120: 30.0 and 29.0).
 enum class Shape { kFew, k16, k32, k64, k128, kPair };
 
 inline Shape choose(int64_t M, int64_t N, int K) {
