@@ -91,6 +91,17 @@ __device__ __forceinline__ void for_sequences(const BalanceParams& p, long long 
     if (t < t1) gap(t, t1);
 }
 
+// a b + c, rounded once
+__device__ __forceinline__ float2 fma2_rn(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
 // s = sigmoid(z) and e = exp(-z) of two logits on the special-function unit, where
 // expf and a division would keep the forward pass busy for as long as its memory
 // traffic. e = 2^t 2^r: t is -z log2(e) rounded, r what the rounding of the product

@@ -40,15 +40,4 @@ BEAM_F32X2_OP(add2_rn, "add.rn.f32x2")
 BEAM_F32X2_OP(sub2_rn, "sub.rn.f32x2")
 #undef BEAM_F32X2_OP
 
-// a b + c, rounded once
-__device__ __forceinline__ float2 fma2_rn(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
-        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-
 }  // namespace beam
