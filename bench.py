@@ -440,12 +440,28 @@ def _time_launches(fn, stream, reps: int | None = None, warmup: int = 3) -> tupl
     return _time_loop(fn, stream, reps), reps
 
 
+def _time_graph(fn, n: int, stream) -> tuple[float, int]:
+    """The same of calls that take the GPU less time than the host: fn(0) to fn(n - 1) in a CUDA
+    graph, replayed. Returns (us per call, calls)."""
+    import torch
+    with torch.cuda.stream(stream):
+        fn(0)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        for i in range(n):
+            fn(i)
+    us, replays = _time_launches(lambda i: g.replay(), stream)
+    return us / n, replays * n
+
+
 def next_rows(snr, device, dev, peak: float, sm_mhz: float | None = None) -> dict:
     """The scope table's next rows at T = 16384, each timed on its own and
     reported beside the step (none is part of it): group-limited top-8 routing,
-    per-head Q/K norm with RoPE or SSMax (8 sequences of 2048 positions), and
-    the two boundaries with y written as NVFP4. Routing also reports its issue
-    roofline: 4 warp-instructions per SM per clock at `sm_mhz`."""
+    per-head Q/K norm with RoPE or SSMax (8 sequences of 2048 positions),
+    the two boundaries with y written as NVFP4 and as int8, the int8 product and the
+    balance loss with its gradient (these in CUDA graphs). Routing also reports its
+    issue roofline: 4 warp-instructions per SM per clock at `sm_mhz`."""
     import torch
     import synth
     stream = torch.cuda.Stream(device)
@@ -529,25 +545,26 @@ def next_rows(snr, device, dev, peak: float, sm_mhz: float | None = None) -> dic
     ws = torch.full((N,), 1e-3, dtype=torch.float32, device=device)
     for M in (T, 64, 1):
         o = torch.empty((M, N), dtype=torch.bfloat16, device=device)
-        us, nl = _time_launches(lambda i, M=M, o=o: snr.matmul_int8(
-            yi[:M], yis[:M], wi[i % nbuf], ws, out=o, stream=stream), stream)
+        us, nl = _time_graph(lambda i, a=yi[:M], s=yis[:M], o=o: snr.matmul_int8(
+            a, s, wi[i % nbuf], ws, out=o, stream=stream), nbuf, stream)
         row = dict(entry(us, matmul_int8_bytes(M, N, D)), launches=nl)
         row["TFLOPs"] = round(2 * M * N * D / (us * 1e-6) / 1e12, 1)
         out[f"matmul_int8_M{M}"] = row
     del wi, yi, o
 
-    # the router's balance loss over 8 sequences, and its gradient; four buffers of logits in turn
-    nbuf = 4
+    # the router's balance loss over 8 sequences, and its gradient; 16 buffers of logits in
+    # turn (268 MB, twice what L2 holds)
+    nbuf = 16
     z = torch.from_numpy((synth.normal(3, 8, nbuf * T * 256) * 2.0).reshape(nbuf, T, 256)).to(device)
     off = torch.arange(0, T + 1, T // 8, dtype=torch.int32, device=device)
     loss = torch.empty(8, dtype=torch.float32, device=device)
     counts = torch.empty((8, 256), dtype=torch.int32, device=device)
     dz = torch.empty((T, 256), dtype=torch.float32, device=device)
-    us, nl = _time_launches(lambda i: snr.moe_balance_loss(
-        z[i % nbuf], idx, 1e-3, seq_offsets=off, loss=loss, counts=counts, stream=stream), stream)
+    us, nl = _time_graph(lambda i: snr.moe_balance_loss(
+        z[i], idx, 1e-3, seq_offsets=off, loss=loss, counts=counts, stream=stream), nbuf, stream)
     out["balance_loss"] = dict(entry(us, T * (4 * 256 + 4 * 8)), launches=nl)
-    us, nl = _time_launches(lambda i: snr.moe_balance_loss_backward(
-        loss, z[i % nbuf], counts, 8, 1e-3, seq_offsets=off, dlogits=dz, stream=stream), stream)
+    us, nl = _time_graph(lambda i: snr.moe_balance_loss_backward(
+        loss, z[i], counts, 8, 1e-3, seq_offsets=off, dlogits=dz, stream=stream), nbuf, stream)
     out["balance_loss_backward"] = dict(entry(us, T * 8 * 256), launches=nl)
     snr.sync_status(stream)
     return out
