@@ -362,8 +362,11 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
                 }
                 if (elect_one()) umma_commit<CG>(&acc_full[a]);
                 __syncwarp();
-                if (!ok) warp_wait(&acc_full[a], (uint32_t)(n_seg / C::kAccs) & 1, q.wait_ns);
             }
+            // its instructions have ended before tensor memory and shared memory go, also
+            // where the warps that read the result have given up
+            if (n_seg > 0)
+                warp_wait(&acc_full[(n_seg - 1) % C::kAccs], (uint32_t)((n_seg - 1) / C::kAccs) & 1, q.wait_ns);
         }
     } else if (warp < kEpiWarp) {
         const bool channels = warp < C::kAWarps;
