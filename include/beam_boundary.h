@@ -263,6 +263,9 @@ BEAM_API int64_t beam_moe_balance_workspace(int64_t T, int E, int64_t S);
  *   seq_offsets, alpha and topk the same as there
  *   dlogits [T, E] FP32, 16-byte aligned, overlapping no input; every element is
  *   written, 0 for a token of no sequence and for one whose sigmoids are all 0
+ * FP32 arithmetic: within 128 units of 2^-24 of the two terms' sizes, that is with
+ * counts_e + sum_i counts_i p_ti in the last bracket (what lies below 2^-126 may
+ * come out as 0).
  */
 BEAM_API beam_status beam_moe_balance_loss_backward(beam_stream_t stream, const float* dloss,
                                                     const float* logits, const int32_t* counts,

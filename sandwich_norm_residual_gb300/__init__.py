@@ -400,7 +400,8 @@ def _int8_out(h, q, scale, stream, checked: bool):
 def boundary_fused_int8(h, x, post_w, pre_w, n: int, eps: float = 1e-6, y_int8=None, y_scale=None,
                         stream=None, opts=None):
     """Dense boundary with y as int8 and one FP32 scale per token; updates h in place,
-    returns (y_int8 [T, D] int8, y_scale [T] float32), the operands of ``matmul_int8``."""
+    returns (y_int8 [T, D] int8, y_scale [T] float32), the operands of ``matmul_int8`` (which
+    needs D to be a multiple of 16)."""
     import torch
     bf16 = torch.bfloat16
     T, D = rows = _dims(h, 2)
@@ -566,7 +567,8 @@ def moe_balance_loss(logits, topk_idx, alpha: float, seq_offsets=None, loss=None
     logits: [T, E] float32; topk_idx: [T, topk] int32, as ``moe_route`` gives them;
     seq_offsets: [S + 1] int32 first tokens of the sequences and the end of the last (None: one
     sequence); tokens outside are padding and count for nothing.
-    Returns (loss float32 [S], counts int32 [S, E]).
+    Returns (loss float32 [S], counts int32 [S, E]). Autograd does not see the call: the gradient
+    for the logits comes from ``moe_balance_loss_backward``.
     """
     import torch
     S = _sequences(seq_offsets)
