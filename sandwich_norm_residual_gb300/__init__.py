@@ -9,7 +9,7 @@ fallback: without the built library, calls raise ``ImportError``.
     y = moe_combine_boundary(h, expert_out, topk_w, post_w, pre_w, n, eps)
 
 Every call takes ``stream`` (default: the current stream). Operands that other streams write
-must be ready on it. Outputs that the caller does not give come from the memory pool of that
+must be ready on it, and are kept (or recorded on it) until it is done with them. Outputs that the caller does not give come from the memory pool of that
 stream, as any tensor made under ``torch.cuda.stream(stream)``: before another stream reads
 one, make it wait for ``stream``, and let it ``record_stream`` what is freed before it is done.
 """
@@ -128,7 +128,11 @@ def _pool(stream):
     takes it back for such work when it is freed. Entering a stream takes 10 us, so only where
     it is not the current one."""
     import torch
-    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(stream.device_index):
+    if stream is None:
+        return _HERE
+    if not hasattr(stream, "device_index"):  # anything that carries a handle is a stream here
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    if stream.cuda_stream == torch._C._cuda_getCurrentRawStream(stream.device_index):
         return _HERE
     return torch.cuda.stream(stream)
 

@@ -101,3 +101,15 @@ def test_the_current_stream_is_not_entered_again(made, name):
     current, got, entered = made
     call(stream=MAIN)
     assert got == [MAIN] * n and entered == []
+
+
+def test_a_bare_handle_is_a_stream(made, monkeypatch):
+    """What the calls ask of a stream is its handle alone."""
+    class Handle:
+        cuda_stream = 2
+
+    current, got, entered = made
+    monkeypatch.setattr(torch.cuda, "ExternalStream", FakeStream)
+    for name in ("boundary_fused", "moe_route", "matmul_int8"):
+        CALLS[name][1](stream=Handle())
+    assert [s.cuda_stream for s in entered] == [2, 2, 2] and all(s.cuda_stream == 2 for s in got)
