@@ -9,9 +9,10 @@ fallback: without the built library, calls raise ``ImportError``.
     y = moe_combine_boundary(h, expert_out, topk_w, post_w, pre_w, n, eps)
 
 Every call takes ``stream`` (default: the current stream). Operands that other streams write
-must be ready on it, and are kept (or recorded on it) until it is done with them. Outputs that the caller does not give come from the memory pool of that
-stream, as any tensor made under ``torch.cuda.stream(stream)``: before another stream reads
-one, make it wait for ``stream``, and let it ``record_stream`` what is freed before it is done.
+must be ready on it, and are kept (or recorded on it) until it is done with them. Outputs that
+the caller does not give come from the memory pool of that stream, as any tensor made under
+``torch.cuda.stream(stream)``: before another stream reads one, make it wait for ``stream``, and
+let it ``record_stream`` what is freed before it is done.
 """
 from __future__ import annotations
 

@@ -525,9 +525,10 @@ __global__ void __launch_bounds__(TileConfig<NT, CG>::kThreads, 1)
 
 // Adds the sums of the tiles that several workers have steps of: a block for
 // kCols tokens of a tile, thread = channel. They are FP32 numbers that are integers,
-// also past 2^24, and at most 2^30: added as 32-bit integers, without rounding. What it takes (3 us) is its launch and one way to L2 and back, so few
-// values a thread (but not so few that blocks are counted in thousands: 2 tokens a
-// block cost 3 us more than 8 at NT = 128) and several workers' at once.
+// also past 2^24, and at most 2^30: added as 32-bit integers, without rounding. What
+// it takes (3 us) is its launch and one way to L2 and back, so few values a thread
+// (but not so few that blocks are counted in thousands: 2 tokens a block cost 3 us
+// more than 8 at NT = 128) and several workers' at once.
 template <int NT>
 struct Join {
     static constexpr int kCols = NT <= 32 ? 2 : NT == 64 ? 4 : 8, kWorkers = NT <= 64 ? 8 : 4;
