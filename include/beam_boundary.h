@@ -273,6 +273,9 @@ BEAM_API beam_status beam_moe_balance_loss_backward(beam_stream_t stream, const 
                                                     int topk, int64_t S, float alpha,
                                                     float* dlogits);
 
+/* Most experts of the calls below. */
+#define BEAM_MOE_MAX_EXPERTS 512
+
 /* Head dimension and modes of beam_qk_norm. */
 #define BEAM_QK_HEAD_DIM 128
 #define BEAM_QK_ROPE 0
@@ -364,6 +367,57 @@ BEAM_API beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, con
 
 /* Bytes of workspace of beam_matmul_int8 (0 for most shapes), -1 for a bad shape. */
 BEAM_API int64_t beam_matmul_int8_workspace(int64_t M, int N, int K);
+
+/* Values, or rows by columns of channels, that share a scale; most rows and most channels
+ * of the FP8 products. */
+#define BEAM_FP8_BLOCK 128
+#define BEAM_MATMUL_FP8_MAX_ROWS 0x7FFFF000
+
+/*
+ * Product of E4M3 numbers (OCP E4M3FN) with FP32 scales: one for each 128 values of a
+ * token, as the FP8 boundaries and beam_swiglu_fp8 write them, one for each 128 by 128
+ * block of channels. An addition of this library; the pages name dynamic FP8 (SGLang page,
+ * the quantisation formats it serves) and print no format.
+ *   out[m, n] = RN( sum_b s_b P_b ),  b = 0 .. ceil(K / 128) - 1 in order,
+ *   s_b = RN32( a_scale[m, b] * w_scale[n / 128, b] ),
+ *   P_b = sum of a[m, k] * w[n, k] over k = 128 b .. min(128 b + 128, K) - 1,
+ * each step of the sum one FP32 multiply-add, the last rounding to BF16 or, when out is
+ * FP32, nothing. The matrix unit adds the exact products of P_b in FP32, off by at most
+ * 2^-22 sum |a w|. Small products share a sum over b among up to eight CTAs and add their FP32
+ * parts: results do not depend on the run, but can change with M, N and K where they do
+ * so, in the order of an FP32 sum.
+ *   a       [M, K] E4M3 codes; w [N, K] (one row per output channel); 16-byte aligned
+ *   a_scale [M, ceil(K / 128)] FP32; w_scale [ceil(N / 128), ceil(K / 128)] FP32; 4-byte aligned
+ *   K       a multiple of 16, 16 <= K <= BEAM_MATMUL_MAX_K
+ *   M, N    0 launches nothing; at most BEAM_MATMUL_FP8_MAX_ROWS, N K < 2^40, and tiles of 64
+ *           rows by 128 channels at most 2^31 - 1
+ *   out     [M, N], BF16 for BEAM_OUT_BF16, FP32 for BEAM_OUT_FP32; aligned to its element;
+ *           overlaps no input
+ * A code that is NaN makes its row's or channel's results NaN, a scale that is NaN or
+ * infinite those that it scales (0 * inf).
+ * flags: 0, or BEAM_OPT_TEST_WAIT_TIMEOUT, a test hook for the bounded waits: the copies of every
+ * tile's second 128 k are never issued, the waits for them give up after 1 ms, out holds
+ * anything and beam_sync_status returns BEAM_ERR_TIMEOUT.
+ */
+BEAM_API beam_status beam_matmul_fp8(beam_stream_t stream, const uint8_t* a, const float* a_scale,
+                                     const uint8_t* w, const float* w_scale, int64_t M, int N, int K,
+                                     int out_type, void* out, uint32_t flags);
+
+/*
+ * The same for the rows of E experts, each with its own channels: row m of expert e, that is
+ * offsets[e] <= m < offsets[e + 1], is multiplied by w[e].
+ *   a [R, K], a_scale [R, ceil(K / 128)], out [R, N]: rows sorted by expert (beam_moe_gather)
+ *   offsets [E + 1] int32, non-decreasing, within [0, R], as beam_moe_sort writes them; read on
+ *           the device. Rows of no expert (before the first, behind the last) are not read
+ *           for a result, whatever they hold, and out keeps there what it held.
+ *   w [E, N, K] E4M3; w_scale [E, ceil(N / 128), ceil(K / 128)]; E in [1, BEAM_MOE_MAX_EXPERTS]
+ * Offsets that decrease or leave [0, R] make out unspecified (no address outside the operands
+ * is touched); beam_sync_status then returns BEAM_ERR_ARG.
+ */
+BEAM_API beam_status beam_matmul_fp8_experts(beam_stream_t stream, const uint8_t* a, const float* a_scale,
+                                             const int32_t* offsets, const uint8_t* w,
+                                             const float* w_scale, int64_t R, int E, int N, int K,
+                                             int out_type, void* out, uint32_t flags);
 
 /*
  * Synchronises `stream`, then reads and clears the current device's status

@@ -26,7 +26,7 @@ from ._lib import LaunchOpts  # noqa: F401
 __all__ = ["boundary_fused", "moe_combine_boundary", "boundary_fused_host",
            "moe_combine_boundary_host", "boundary_fused_nvfp4",
            "moe_combine_boundary_nvfp4", "boundary_fused_int8", "moe_combine_boundary_int8",
-           "matmul_int8", "moe_route", "moe_balance_loss", "moe_balance_loss_backward",
+           "matmul_int8", "matmul_fp8", "matmul_fp8_experts", "moe_route", "moe_balance_loss", "moe_balance_loss_backward",
            "router_sigmoid", "qk_norm", "sync_status",
            "exact_sum_count",
            "version", "BeamError", "LaunchOpts", "library"]
@@ -511,6 +511,81 @@ def matmul_int8(a, a_scale, w, w_scale, out_dtype=None, out=None, stream=None, p
     if st != 0:
         raise BeamError(st, "beam_matmul_int8")
     return out
+
+
+def _blocks(n: int) -> int:
+    return -(-n // _lib.BEAM_FP8_BLOCK)
+
+
+def _fp8_product(a, a_scale, offsets, w, w_scale, out_dtype, out, stream, name: str):
+    import torch
+    fp8, grouped = torch.float8_e4m3fn, offsets is not None
+    M, K = _dims(a, 2)
+    E, N = _dims(w, 3)[:2] if grouped else (1, _dims(w, 2)[0])
+    experts = (E,) if grouped else ()
+    if out_dtype is None:
+        out_dtype = getattr(out, "dtype", torch.bfloat16)
+    scales = (M, _blocks(K)), (*experts, _blocks(N), _blocks(K))
+    ready = _ready((a, fp8, (M, K)), (a_scale, torch.float32, scales[0]), (w, fp8, (*experts, N, K)),
+                   (w_scale, torch.float32, scales[1]),
+                   *(((offsets, torch.int32, (E + 1,)),) if grouped else ()),
+                   *(() if out is None else ((out, out_dtype, (M, N)),)))
+    if not ready:
+        _check(a, "a", fp8, 2)
+        _check(a_scale, "a_scale", torch.float32, 2)
+        _check(w, "w", fp8, 3 if grouped else 2)
+        _check(w_scale, "w_scale", torch.float32, 3 if grouped else 2)
+        if w.shape[-1] != K:
+            raise ValueError(f"shape mismatch: a has rows of {K}, w of {w.shape[-1]}")
+        _shape(a_scale, "a_scale", scales[0])
+        _shape(w_scale, "w_scale", scales[1])
+        if grouped:
+            _check(offsets, "offsets", torch.int32, 1)
+            _shape(offsets, "offsets", (E + 1,))
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise TypeError(f"out_dtype must be bfloat16 or float32 (got {out_dtype})")
+    N, K, E = _c_int(N), _c_int(K), _c_int(E)
+    if out is None:
+        with _pool(stream):
+            out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    if not ready:
+        _check(out, "out", out_dtype, 2)
+        _shape(out, "out", (M, N))
+        _on_current_device(**_given(a=a, a_scale=a_scale, offsets=offsets, w=w, w_scale=w_scale, out=out))
+    kind = _lib.BEAM_OUT_FP32 if out_dtype is torch.float32 else _lib.BEAM_OUT_BF16
+    lib, s = _lib.load(), _raw_stream(stream, a)
+    if grouped:
+        st = lib.beam_matmul_fp8_experts(s, a.data_ptr(), a_scale.data_ptr(), offsets.data_ptr(), w.data_ptr(),
+                                         w_scale.data_ptr(), M, E, N, K, kind, out.data_ptr(), 0)
+    else:
+        st = lib.beam_matmul_fp8(s, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), M, N, K,
+                                 kind, out.data_ptr(), 0)
+    if st != 0:
+        raise BeamError(st, name)
+    return out
+
+
+def matmul_fp8(a, a_scale, w, w_scale, out_dtype=None, out=None, stream=None):
+    """Product of E4M3 tokens and channels with a scale for each block of 128.
+
+    a: [M, K] float8_e4m3fn and a_scale: [M, ceil(K/128)] float32, as an FP8 boundary writes them;
+    w: [N, K] float8_e4m3fn and w_scale: [ceil(N/128), ceil(K/128)] float32. K must be a multiple of 16.
+    Returns [M, N] in out_dtype: bfloat16 (the default) or float32.
+    """
+    return _fp8_product(a, a_scale, None, w, w_scale, out_dtype, out, stream, "beam_matmul_fp8")
+
+
+def matmul_fp8_experts(a, a_scale, offsets, w, w_scale, out_dtype=None, out=None, stream=None):
+    """``matmul_fp8`` of each expert's rows with its own channels.
+
+    a: [R, K] and a_scale, the rows sorted by expert (``moe_gather``); offsets: [E + 1] int32 as
+    ``moe_sort`` gives them: expert e has the rows offsets[e] .. offsets[e + 1] - 1;
+    w: [E, N, K]; w_scale: [E, ceil(N/128), ceil(K/128)]. Returns [R, N]; rows of no expert are left
+    as they were (in an ``out`` that the call makes, with whatever its memory held).
+    """
+    if offsets is None:
+        raise TypeError("offsets must be a torch.Tensor")
+    return _fp8_product(a, a_scale, offsets, w, w_scale, out_dtype, out, stream, "beam_matmul_fp8_experts")
 
 
 def moe_route(logits, bias, n_group: int = 8, topk_group: int = 4, topk: int = 8,

@@ -29,6 +29,9 @@ BEAM_BALANCE_MAX_SEQUENCES = 0x7FFFFFC0
 BEAM_OUT_BF16 = 0
 BEAM_OUT_FP32 = 1
 BEAM_MATMUL_MAX_K = 65536
+BEAM_MATMUL_FP8_MAX_ROWS = 0x7FFFF000
+BEAM_MOE_MAX_EXPERTS = 512
+BEAM_FP8_BLOCK = 128
 BEAM_OPT_FORCE_EXACT_SUM = 0x1
 BEAM_OPT_TEST_WAIT_TIMEOUT = 0x2
 BEAM_OPT_PDL = 0x4
@@ -74,6 +77,9 @@ SIGNATURES = {
                                 _f32, _i32, _u32]),
     "beam_matmul_int8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _i64, _u32]),
     "beam_matmul_int8_workspace": (_i64, [_i64, _i32, _i32]),
+    "beam_matmul_fp8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _u32]),
+    "beam_matmul_fp8_experts": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp,
+                                       _u32]),
     "beam_moe_balance_loss": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i64, _f32, _vp, _vp, _vp,
                                      _i64]),
     "beam_moe_balance_workspace": (_i64, [_i64, _i32, _i64]),

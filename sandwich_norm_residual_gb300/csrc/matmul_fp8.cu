@@ -1,0 +1,187 @@
+// Host side of the 8-bit floating-point product: argument checks (before any CUDA
+// call), the choice of the kernel and the launch.
+#include "matmul_fp8.cuh"
+
+#include <atomic>
+
+#include "beam_boundary.h"
+#include "device.h"
+#include "host.h"
+
+namespace {
+
+using beam::Fp8Params;
+using beam::Fp8Room;
+using beam::misaligned;
+using beam::overlaps;
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static std::atomic<void*> cached{nullptr};
+    void* fn = cached.load(std::memory_order_acquire);
+    if (!fn) {
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        cached.store(fn, std::memory_order_release);
+    }
+    return reinterpret_cast<EncodeTiled>(fn);
+}
+
+// matrices of 8-bit rows of K, one behind the other, in tiles of `rows` rows of one matrix by
+// one step of k, 128-byte swizzle; dims = 2: one matrix
+bool tile_map(CUtensorMap* map, const void* base, int dims, int64_t matrices, int64_t rows_each, int K, int rows) {
+    const EncodeTiled encode = encode_tiled();
+    const cuuint64_t size[3] = {(cuuint64_t)K, (cuuint64_t)rows_each, (cuuint64_t)matrices};
+    const cuuint64_t strides[2] = {(cuuint64_t)K, (cuuint64_t)K * (cuuint64_t)rows_each};
+    const cuuint32_t box[3] = {beam::kFp8Step, (cuuint32_t)rows, 1}, unit[3] = {1, 1, 1};
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)dims, const_cast<void*>(base), size, strides, box, unit,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int CG>
+const void* kernel(bool f32) {
+    return f32 ? reinterpret_cast<const void*>(beam::matmul_fp8_kernel<CG, true>)
+               : reinterpret_cast<const void*>(beam::matmul_fp8_kernel<CG, false>);
+}
+
+template <int CG>
+cudaLaunchConfig_t config(int workers, int split, cudaStream_t stream, cudaLaunchAttribute* attr) {
+    using C = beam::Fp8Tile<CG>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(workers * split * CG));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = stream;
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = (unsigned)(split * CG);
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split * CG > 1 ? 1 : 0;
+    return cfg;
+}
+
+// Raises the kernels' shared-memory limits and asks how many clusters fit, once on each device
+beam_status room(const beam::Device& dev, Fp8Room* out) {
+    static std::atomic<uint64_t> known[64];  // 0: not yet
+    std::atomic<uint64_t>& slot = known[dev.ordinal & 63];
+    uint64_t v = slot.load(std::memory_order_acquire);
+    if (!v) {
+        for (int f32 = 0; f32 < 2; ++f32)
+            if (cudaFuncSetAttribute(kernel<1>(f32), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)beam::Fp8Tile<1>::kSmem) != cudaSuccess ||
+                cudaFuncSetAttribute(kernel<2>(f32), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)beam::Fp8Tile<2>::kSmem) != cudaSuccess) {
+                cudaGetLastError();
+                return BEAM_ERR_CUDA;
+            }
+        cudaLaunchAttribute attr;
+        for (int i = 0; i < 5; ++i) {
+            int n = dev.sms;
+            const cudaLaunchConfig_t cfg = i == 4 ? config<2>(1, 1, nullptr, &attr) : config<1>(1, 1 << i, nullptr, &attr);
+            if (i > 0 && cudaOccupancyMaxActiveClusters(&n, i == 4 ? kernel<2>(false) : kernel<1>(false), &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                return BEAM_ERR_CUDA;
+            }
+            v |= (uint64_t)(n < 1 ? 0 : n > 4095 ? 4095 : n) << (12 * i);
+        }
+        slot.store(v, std::memory_order_release);
+    }
+    for (int i = 0; i < 4; ++i) out->clusters[i] = (int)(v >> (12 * i)) & 4095;
+    out->pairs = (int)(v >> 48) & 4095;
+    return out->pairs < 1 ? BEAM_ERR_CUDA : BEAM_OK;
+}
+
+template <int CG>
+beam_status launch(const Fp8Params& q, const beam::Fp8Plan& plan, const CUtensorMap& wmap, const CUtensorMap& amap64,
+                   const CUtensorMap& amap16, bool f32, cudaStream_t stream) {
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = config<CG>(plan.workers, plan.split, stream, &attr);
+    void* args[] = {const_cast<CUtensorMap*>(&wmap), const_cast<CUtensorMap*>(&amap64), const_cast<CUtensorMap*>(&amap16),
+                    const_cast<Fp8Params*>(&q)};
+    if (cudaLaunchKernelExC(&cfg, kernel<CG>(f32), args) != cudaSuccess) {
+        cudaGetLastError();
+        return BEAM_ERR_CUDA;
+    }
+    return BEAM_OK;
+}
+
+beam_status product(beam_stream_t stream, const uint8_t* a, const float* a_scale, const int32_t* offsets, bool grouped,
+                    const uint8_t* w, const float* w_scale, int64_t R, int E, int N, int K, int out_type, void* out,
+                    uint32_t flags) {
+    if (R < 0 || R > BEAM_MATMUL_FP8_MAX_ROWS || N < 0 || N > BEAM_MATMUL_FP8_MAX_ROWS || K < 16 || (K & 15) ||
+        K > BEAM_MATMUL_MAX_K || E < 1 || E > BEAM_MOE_MAX_EXPERTS || (int64_t)N * K >= (int64_t(1) << 40) ||
+        beam::fp8_most_tiles(R, E, ((int64_t)N + beam::kFp8Chan - 1) / beam::kFp8Chan, beam::kFp8Few) > 0x7FFFFFFF)
+        return BEAM_ERR_SHAPE;
+    if ((out_type != BEAM_OUT_BF16 && out_type != BEAM_OUT_FP32) || (flags & ~BEAM_OPT_TEST_WAIT_TIMEOUT)) return BEAM_ERR_ARG;
+    if (R == 0 || N == 0) return BEAM_OK;
+    if (!a || !a_scale || !w || !w_scale || !out || (grouped && !offsets)) return BEAM_ERR_NULL;
+    const bool f32 = out_type == BEAM_OUT_FP32;
+    const unsigned out_size = f32 ? 4u : 2u;
+    if (misaligned(a, 16) || misaligned(w, 16) || misaligned(a_scale, 4) || misaligned(w_scale, 4) ||
+        misaligned(offsets, 4) || misaligned(out, out_size))
+        return BEAM_ERR_ALIGN;
+    const size_t steps = ((size_t)K + 127) / 128, ob = (size_t)R * (size_t)N * out_size;
+    const struct {
+        const void* p;
+        size_t n;
+    } in[] = {{a, (size_t)R * (size_t)K}, {w, (size_t)E * (size_t)N * (size_t)K}, {a_scale, (size_t)R * steps * 4u},
+              {w_scale, (size_t)E * (((size_t)N + 127) / 128) * steps * 4u}, {offsets, grouped ? ((size_t)E + 1) * 4u : 0}};
+    for (const auto& i : in)
+        if (overlaps(out, ob, i.p, i.n)) return BEAM_ERR_ALIAS;
+    beam::Device dev;
+    beam_status st = beam::device(&dev);
+    if (st != BEAM_OK) return st;
+    Fp8Room fits;
+    st = room(dev, &fits);
+    if (st != BEAM_OK) return st;
+    const beam::Fp8Plan plan = beam::fp8_plan(R, E, N, K, fits);
+    const bool drop = (flags & BEAM_OPT_TEST_WAIT_TIMEOUT) != 0;
+    Fp8Params q{};
+    q.a_scale = a_scale;
+    q.w_scale = w_scale;
+    q.out = out;
+    q.offsets = offsets;
+    q.R = R;
+    q.E = E;
+    q.N = N;
+    q.steps = (uint32_t)steps;
+    q.n_tiles = (uint32_t)(((int64_t)N + beam::kFp8Chan * (plan.pair ? 2 : 1) - 1) / (beam::kFp8Chan * (plan.pair ? 2 : 1)));
+    q.most = plan.pair ? beam::kFp8Many : beam::kFp8Few;
+    q.split = plan.split;
+    q.wide = !f32 && N % 8 == 0 && !misaligned(out, 16);
+    q.wait_ns = drop ? beam::kFp8TestWaitNs : beam::kFp8WaitNs;
+    q.drop = drop;
+    q.status = dev.status_word;
+    CUtensorMap wmap, amap64, amap16;
+    if (!tile_map(&wmap, w, 3, E, N, K, beam::kFp8Chan) || !tile_map(&amap64, a, 2, 1, R, K, 64) ||
+        !tile_map(&amap16, a, 2, 1, R, K, 16))
+        return BEAM_ERR_CUDA;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    return plan.pair ? launch<2>(q, plan, wmap, amap64, amap16, f32, cs) : launch<1>(q, plan, wmap, amap64, amap16, f32, cs);
+}
+
+}  // namespace
+
+extern "C" {
+
+beam_status beam_matmul_fp8(beam_stream_t stream, const uint8_t* a, const float* a_scale, const uint8_t* w,
+                            const float* w_scale, int64_t M, int N, int K, int out_type, void* out, uint32_t flags) {
+    return product(stream, a, a_scale, nullptr, false, w, w_scale, M, 1, N, K, out_type, out, flags);
+}
+
+beam_status beam_matmul_fp8_experts(beam_stream_t stream, const uint8_t* a, const float* a_scale, const int32_t* offsets,
+                                    const uint8_t* w, const float* w_scale, int64_t R, int E, int N, int K, int out_type,
+                                    void* out, uint32_t flags) {
+    return product(stream, a, a_scale, offsets, true, w, w_scale, R, E, N, K, out_type, out, flags);
+}
+
+}  // extern "C"

@@ -78,6 +78,23 @@ __device__ __forceinline__ void tmem_ld_16x256b(uint32_t at, float (&r)[8]) {
                  : "r"(at) : "memory");
 }
 
+// the same for 32 columns, without waiting: the values are there behind tmem_wait_ld
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t at, float (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(at) : "memory");
+}
+// the wait, which the uses of r cannot be moved ahead of
+__device__ __forceinline__ void tmem_wait_ld(float (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                   "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
+                 :: "memory");
+}
+
 // transposes the 8 x 8 matrix of 16-bit values that a warp holds, thread t two
 // of row t / 4
 __device__ __forceinline__ uint32_t transpose_b16(uint32_t v) {
@@ -125,6 +142,25 @@ __device__ __forceinline__ void umma_f16(uint32_t d, uint32_t a, uint64_t b, uin
                      :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
 }
 
+// kind::f8f6f4 on E4M3 operands, K-major both, FP32 accumulators: M rows of A by n (a
+// multiple of 16) rows of B, both in shared memory (CG = 2: half of either in each CTA)
+template <uint32_t M>
+__device__ __forceinline__ uint32_t umma_e4m3_desc(uint32_t n) {
+    return (1u << 4) | ((n >> 3) << 17) | ((M >> 4) << 24);
+}
+// D += A B^T over 32 k, or D = where add is 0; one thread (of the pair's first CTA)
+template <int CG>
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    if constexpr (CG == 1)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+}
+
 // one arrival on `bar` (CG = 2: on that barrier of both CTAs) when every matrix
 // instruction that this thread issued so far has finished
 template <int CG>
@@ -135,6 +171,11 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
     else
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
                      :: "r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+}
+// the same in a cluster of several pairs: `ctas` has a bit for each CTA of this pair
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint32_t ctas) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 :: "r"(smem_u32(bar)), "h"((uint16_t)ctas) : "memory");
 }
 
 // ---------------------------------------------------------------- barriers, clusters, TMA
@@ -196,12 +237,21 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
 }
+// the same, publishing what the warp wrote to that CTA's shared memory before
+__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-// every thread of every CTA of the cluster
+// sixteen bytes of shared memory of a CTA of the cluster
+__device__ __forceinline__ void st_cluster(uint32_t addr, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
+                 :: "r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+// every thread of every CTA of the cluster; writes before it are seen behind it
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
@@ -224,6 +274,35 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, i
         "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
         "[%0], [%1, {%2, %6, %6, %6, %3}], [%4], %5;"
         :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy), "r"(0) : "memory");
+}
+// a 3-D tile of the last dimension's slice z. PAIR: its bytes are counted on the barrier at the
+// cluster address `bar`, which may be the other CTA's of the pair; else `bar` is this CTA's.
+template <bool PAIR>
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar, uint64_t policy) {
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3, %4}], [%5], %6;"
+            :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3, %4}], [%5], %6;"
+            :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy) : "memory");
+}
+// a 2-D tile, counted as above
+template <bool PAIR>
+__device__ __forceinline__ void tma_load_2d_on(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t policy) {
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3}], [%4], %5;"
+            :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3}], [%4], %5;"
+            :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
