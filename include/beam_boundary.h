@@ -273,9 +273,6 @@ BEAM_API beam_status beam_moe_balance_loss_backward(beam_stream_t stream, const 
                                                     int topk, int64_t S, float alpha,
                                                     float* dlogits);
 
-/* Most experts of the calls below. */
-#define BEAM_MOE_MAX_EXPERTS 512
-
 /* Head dimension and modes of beam_qk_norm. */
 #define BEAM_QK_HEAD_DIM 128
 #define BEAM_QK_ROPE 0
@@ -367,6 +364,109 @@ BEAM_API beam_status beam_matmul_int8(beam_stream_t stream, const int8_t* a, con
 
 /* Bytes of workspace of beam_matmul_int8 (0 for most shapes), -1 for a bad shape. */
 BEAM_API int64_t beam_matmul_int8_workspace(int64_t M, int N, int K);
+
+/* Most experts, and most choices (tokens times topk) and sorted rows, of the calls between
+ * routing and combine. */
+#define BEAM_MOE_MAX_EXPERTS 512
+#define BEAM_MOE_MAX_PAIRS 0x7FFFF000
+
+/*
+ * Tokens sorted by expert, between beam_moe_route and the experts' products (the pages sort
+ * inside their fused MoE kernels and print no interface; an addition of this library). The
+ * pairs (t, k), in the order of topk_idx, sorted by expert without changing the order within
+ * one:
+ *   offsets[e]  pairs of the experts before e, e = 0 .. E: expert e has the rows
+ *               offsets[e] .. offsets[e + 1] - 1 of what beam_moe_gather writes
+ *   slots[t, k] the row of pair (t, k), -1 for none
+ *   topk_idx [T, topk] int32: an expert in [0, E), or -1 for none (padding, a choice that
+ *            is left out); the same expert may stand in a token's choices twice
+ *   topk in [1, BEAM_ROUTE_MAX_TOPK], E in [1, BEAM_MOE_MAX_EXPERTS], T topk at most BEAM_MOE_MAX_PAIRS
+ *   offsets [E + 1], slots [T, topk] int32: every element is written, for T = 0 too
+ *   workspace  device memory for this call alone, 16-byte aligned, of at least
+ *            beam_moe_sort_workspace(T, topk, E) bytes (NULL where that is 0); need not be cleared
+ * 4-byte aligned where nothing else is said. Outputs and workspace overlap neither each other
+ * nor topk_idx. Any other number in topk_idx counts as -1; beam_sync_status then
+ * returns BEAM_ERR_ARG. Every run gives the same result.
+ */
+BEAM_API beam_status beam_moe_sort(beam_stream_t stream, const int32_t* topk_idx, int64_t T, int topk,
+                                   int E, int32_t* offsets, int32_t* slots, void* workspace,
+                                   int64_t workspace_bytes);
+
+/* Bytes of workspace of beam_moe_sort (0 for few choices), -1 for a bad shape. */
+BEAM_API int64_t beam_moe_sort_workspace(int64_t T, int topk, int E);
+
+/*
+ * Each token's row, and its row of scales, copied to the rows of its choices:
+ *   out[slots[t, k]] = x[t],  out_scale[slots[t, k]] = scale[t]
+ *   x     [T] rows of row_bytes bytes of any type, a multiple of 4, at most 4 BEAM_MAX_D
+ *   scale [T] rows of scale_bytes bytes, a multiple of 4 (the scales of an FP8 or int8 boundary);
+ *         scale_bytes = 0: none, and scale and out_scale are not looked at
+ *   slots [T, topk] int32 as beam_moe_sort writes them, topk in [1, BEAM_ROUTE_MAX_TOPK]
+ *   out, out_scale [R] rows; R at most BEAM_MOE_MAX_PAIRS (T topk holds whatever the choices are).
+ *         A row that no choice has keeps what it held.
+ * Pointers 4-byte aligned; where rows and addresses are multiples of 16 bytes they move as such.
+ * Outputs overlap neither each other nor an input. A slot outside [0, R) counts as -1, and where
+ * it is not -1 beam_sync_status returns BEAM_ERR_ARG; two choices with the same slot leave in that row
+ * words of either (beam_moe_sort gives every choice its own).
+ */
+BEAM_API beam_status beam_moe_gather(beam_stream_t stream, const void* x, int64_t row_bytes,
+                                     const void* scale, int64_t scale_bytes, const int32_t* slots,
+                                     int64_t T, int topk, int64_t R, void* out, void* out_scale);
+
+/*
+ * Gradient of beam_moe_gather for x: dx[t] = RN( sum_k drows[slots[t, k]] ), FP32 sums, k ascending;
+ * a choice of -1 adds nothing, a token of none gets 0.
+ *   drows [R, D], dx [T, D], both BF16 (type = BEAM_OUT_BF16) or FP32 (BEAM_OUT_FP32);
+ *         16-byte aligned; D a multiple of 8, 8 <= D <= BEAM_MAX_D
+ * Other arguments and errors as beam_moe_gather.
+ */
+BEAM_API beam_status beam_moe_gather_backward(beam_stream_t stream, const void* drows,
+                                              const int32_t* slots, int64_t T, int topk, int64_t R,
+                                              int D, int type, void* dx);
+
+/*
+ * The experts' outputs back to their tokens, with the routing weights applied:
+ *   out[t] = RN( acc ),  acc = fma chain over k ascending of topk_w[t, k] * rows[slots[t, k]]
+ * in FP32 from 0, as in beam_moe_combine_boundary: out as that call's x, bit for bit.
+ * A choice of -1 adds nothing, whatever its weight; a token of none gets 0.
+ *   rows [R, D], out [T, D], both BF16 or FP32 by `type`; topk_w [T, topk] FP32, 4-byte aligned
+ * Other arguments and errors as beam_moe_gather_backward.
+ */
+BEAM_API beam_status beam_moe_combine(beam_stream_t stream, const void* rows, const int32_t* slots,
+                                      const float* topk_w, int64_t T, int topk, int64_t R, int D,
+                                      int type, void* out);
+
+/*
+ * Gradients of beam_moe_combine for the gradient dx [T, D] of its out:
+ *   drows[slots[t, k]] = RN( topk_w[t, k] * dx[t] )     [R, D]
+ *   dw[t, k]           = sum_j dx[t, j] * rows[slots[t, k], j]   [T, topk] FP32, 0 for a choice of -1
+ * The sum is FP32, in an order that depends on D and `type` only. A row of drows that no choice has
+ * keeps what it held. dx, rows and drows BF16 or FP32 by `type`; drows and dw overlap
+ * neither each other nor an input; other arguments and errors as beam_moe_combine.
+ */
+BEAM_API beam_status beam_moe_combine_backward(beam_stream_t stream, const void* dx, const void* rows,
+                                               const int32_t* slots, const float* topk_w, int64_t T,
+                                               int topk, int64_t R, int D, int type, void* drows,
+                                               float* dw);
+
+/*
+ * The experts' activation between their two products, written as the second's operand. The
+ * pages' experts and dense layers are SwiGLU ones (vLLM page, "MoE and residual stream"). FP32:
+ *   y = (g * (1 / (1 + e^-g))) * u,  g = gate_up[r, j], u = gate_up[r, F + j],
+ * then codes and scales as beam_boundary_fused_fp8 makes them, from the FP32 y (no rounding to
+ * BF16 between).
+ * e^x and the reciprocal are the hardware's: y is within (6 + 2 |g|) units of 2^-24, relative; where
+ * e^-g overflows (g < -88.7) it is 0.
+ *   gate_up   [R, 2 F] BF16, 16-byte aligned; F a multiple of 16, 16 <= F <= BEAM_MATMUL_MAX_K
+ *   live_rows device int32, or NULL: rows from *live_rows on are neither read nor written (the last of
+ *             beam_moe_sort's offsets). Outside [0, R] it counts as 0 or R and beam_sync_status
+ *             returns BEAM_ERR_ARG.
+ *   y_fp8     [R, F] E4M3 codes, 8-byte aligned; y_scale [R, ceil(F / 128)] FP32, 4-byte aligned;
+ *             they overlap neither each other nor an input. R at most BEAM_MOE_MAX_PAIRS
+ */
+BEAM_API beam_status beam_swiglu_fp8(beam_stream_t stream, const uint16_t* gate_up,
+                                     const int32_t* live_rows, int64_t R, int F, uint8_t* y_fp8,
+                                     float* y_scale);
 
 /* Values, or rows by columns of channels, that share a scale; most rows and most channels
  * of the FP8 products. */
@@ -550,6 +650,33 @@ BEAM_API beam_status beam_moe_combine_boundary_int8(beam_stream_t stream, uint16
                                            float route_scale, const uint16_t* post_w,
                                            const uint16_t* pre_w, int n, float eps, int64_t T,
                                            int D, int8_t* y_int8, float* y_scale,
+                                           const beam_launch_opts* opts);
+
+/*
+ * The dense and MoE boundaries with y leaving as E4M3 (OCP E4M3FN) with one FP32 scale for each
+ * 128 values of a row, the activations of beam_matmul_fp8. The pages name dynamic FP8 and
+ * print no format; this one is an addition of this library. y is computed as in the BF16 calls (rounded
+ * to BF16), then, for each block b of 128 consecutive values of a row (the last may be shorter):
+ *   amax = max |y|,  y_scale[t, b] = RN32(amax / 448)
+ *   q_j  = E4M3(RN32(y_j * RN32(448 / amax))),  nearest even, saturating, signs kept
+ * (for amax < 2^-100, y and amax are first multiplied by 2^64, which is exact).
+ *   y_fp8   [T, D] E4M3 codes; y_scale [T, ceil(D / 128)] FP32; both 16-byte aligned
+ *   D a multiple of 8, as in the BF16 calls; no BF16 y is written.
+ *   route_scale as in beam_moe_combine_boundary_scaled (1 when topk_w carries it)
+ * Other arguments and errors as beam_boundary_fused_int8 / beam_moe_combine_boundary_int8.
+ * A block of zeros gets codes 0 and scale 0. A block that holds an infinity or a NaN gets
+ * codes 0 and the scale inf or NaN, so that a product with that row is NaN.
+ */
+BEAM_API beam_status beam_boundary_fused_fp8(beam_stream_t stream, uint16_t* h, const uint16_t* x,
+                                     const uint16_t* post_w, const uint16_t* pre_w, int n,
+                                     float eps, int64_t T, int D, uint8_t* y_fp8, float* y_scale,
+                                     const beam_launch_opts* opts);
+
+BEAM_API beam_status beam_moe_combine_boundary_fp8(beam_stream_t stream, uint16_t* h,
+                                           const uint16_t* expert_out, const float* topk_w,
+                                           float route_scale, const uint16_t* post_w,
+                                           const uint16_t* pre_w, int n, float eps, int64_t T,
+                                           int D, uint8_t* y_fp8, float* y_scale,
                                            const beam_launch_opts* opts);
 
 /*

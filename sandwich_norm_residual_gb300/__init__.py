@@ -26,7 +26,9 @@ from ._lib import LaunchOpts  # noqa: F401
 __all__ = ["boundary_fused", "moe_combine_boundary", "boundary_fused_host",
            "moe_combine_boundary_host", "boundary_fused_nvfp4",
            "moe_combine_boundary_nvfp4", "boundary_fused_int8", "moe_combine_boundary_int8",
-           "matmul_int8", "matmul_fp8", "matmul_fp8_experts", "moe_route", "moe_balance_loss", "moe_balance_loss_backward",
+           "boundary_fused_fp8", "moe_combine_boundary_fp8",
+           "matmul_int8", "matmul_fp8", "matmul_fp8_experts", "swiglu_fp8",
+           "moe_sort", "moe_gather", "moe_gather_backward", "moe_combine", "moe_combine_backward", "moe_route", "moe_balance_loss", "moe_balance_loss_backward",
            "router_sigmoid", "qk_norm", "sync_status",
            "exact_sum_count",
            "version", "BeamError", "LaunchOpts", "library"]
@@ -462,6 +464,99 @@ def moe_combine_boundary_int8(h, expert_out, topk_w, post_w, pre_w, n: int, eps:
     return q, scale
 
 
+def _blocks(n: int) -> int:
+    """How many scales n values have."""
+    return -(-n // _lib.BEAM_FP8_BLOCK)
+
+
+def _fp8_given(q, scale, rows) -> tuple:
+    """The caller's FP8 outputs, as operands of ``_ready``."""
+    if q is None and scale is None:
+        return ()
+    import torch
+    return ((() if q is None else ((q, torch.float8_e4m3fn, rows),))
+            + (() if scale is None else ((scale, torch.float32, (rows[0], _blocks(rows[1]))),)))
+
+
+def _fp8_out(rows, device, q, scale, stream, checked: bool):
+    import torch
+    new_q, new_scale = q is None, scale is None
+    scales = (rows[0], _blocks(rows[1]))
+    with _pool(stream):
+        if new_q:
+            q = torch.empty(rows, dtype=torch.float8_e4m3fn, device=device)
+        if new_scale:
+            scale = torch.empty(scales, dtype=torch.float32, device=device)
+    if not new_q and not checked:
+        _check(q, "y_fp8", torch.float8_e4m3fn, 2)
+        _shape(q, "y_fp8", rows)
+    if not new_scale and not checked:
+        _check(scale, "y_scale", torch.float32, 2)
+        _shape(scale, "y_scale", scales)
+    return q, scale
+
+
+def boundary_fused_fp8(h, x, post_w, pre_w, n: int, eps: float = 1e-6, y_fp8=None, y_scale=None,
+                       stream=None, opts=None):
+    """Dense boundary with y as E4M3 and one FP32 scale for each 128 values of a row; updates h in
+    place, returns (y_fp8 [T, D] float8_e4m3fn, y_scale [T, ceil(D/128)] float32), the operands of
+    ``matmul_fp8`` (which needs D to be a multiple of 16)."""
+    import torch
+    bf16 = torch.bfloat16
+    T, D = rows = _dims(h, 2)
+    ready = _ready((h, bf16, rows), (x, bf16, rows), (post_w, bf16, (D,)), (pre_w, bf16, (D,)),
+                   *_fp8_given(y_fp8, y_scale, rows))
+    if not ready:
+        for t, name in ((h, "h"), (x, "x")):
+            _check(t, name, bf16, 2)
+        _check(post_w, "post_w", bf16, 1)
+        _check(pre_w, "pre_w", bf16, 1)
+        if x.shape != h.shape or post_w.shape[0] != D or pre_w.shape[0] != D:
+            raise ValueError("shape mismatch: h, x [T, D]; post_w, pre_w [D]")
+    q, scale = _fp8_out(rows, h.device, y_fp8, y_scale, stream, ready)
+    if not ready:
+        _on_current_device(h=h, x=x, post_w=post_w, pre_w=pre_w, y_fp8=q, y_scale=scale)
+    st = _lib.load().beam_boundary_fused_fp8(_raw_stream(stream, h), h.data_ptr(), x.data_ptr(),
+                                             post_w.data_ptr(), pre_w.data_ptr(), _c_int(n), float(eps), T, _c_int(D),
+                                             q.data_ptr(), scale.data_ptr(), _opts(opts))
+    if st != 0:
+        raise BeamError(st, "beam_boundary_fused_fp8")
+    return q, scale
+
+
+def moe_combine_boundary_fp8(h, expert_out, topk_w, post_w, pre_w, n: int, eps: float = 1e-6,
+                             y_fp8=None, y_scale=None, stream=None, opts=None,
+                             route_scale: float = 1.0):
+    """MoE boundary with y as E4M3 and one FP32 scale for each 128 values of a row; updates h in
+    place, returns (y_fp8, y_scale). ``route_scale`` multiplies the combined sum (1: topk_w
+    carries it)."""
+    import torch
+    bf16, K = torch.bfloat16, _lib.BEAM_MOE_TOPK
+    T, D = rows = _dims(h, 2)
+    ready = _ready((h, bf16, rows), (expert_out, bf16, (T, K, D)), (topk_w, torch.float32, (T, K)),
+                   (post_w, bf16, (D,)), (pre_w, bf16, (D,)), *_fp8_given(y_fp8, y_scale, rows))
+    if not ready:
+        _check(h, "h", bf16, 2)
+        _check(expert_out, "expert_out", bf16, 3)
+        _check(topk_w, "topk_w", torch.float32, 2)
+        _check(post_w, "post_w", bf16, 1)
+        _check(pre_w, "pre_w", bf16, 1)
+        if (expert_out.shape != (T, K, D) or topk_w.shape != (T, K) or post_w.shape[0] != D
+                or pre_w.shape[0] != D):
+            raise ValueError("shape mismatch: h [T, D]; expert_out [T, 8, D]; topk_w [T, 8]")
+    q, scale = _fp8_out(rows, h.device, y_fp8, y_scale, stream, ready)
+    if not ready:
+        _on_current_device(h=h, expert_out=expert_out, topk_w=topk_w, post_w=post_w, pre_w=pre_w,
+                           y_fp8=q, y_scale=scale)
+    st = _lib.load().beam_moe_combine_boundary_fp8(
+        _raw_stream(stream, h), h.data_ptr(), expert_out.data_ptr(), topk_w.data_ptr(),
+        float(route_scale), post_w.data_ptr(), pre_w.data_ptr(), _c_int(n), float(eps), T, _c_int(D),
+        q.data_ptr(), scale.data_ptr(), _opts(opts))
+    if st != 0:
+        raise BeamError(st, "beam_moe_combine_boundary_fp8")
+    return q, scale
+
+
 @functools.lru_cache(maxsize=4096)
 def _matmul_workspace(M: int, N: int, K: int) -> int:
     return max(0, _lib.load().beam_matmul_int8_workspace(M, N, K))
@@ -511,10 +606,6 @@ def matmul_int8(a, a_scale, w, w_scale, out_dtype=None, out=None, stream=None, p
     if st != 0:
         raise BeamError(st, "beam_matmul_int8")
     return out
-
-
-def _blocks(n: int) -> int:
-    return -(-n // _lib.BEAM_FP8_BLOCK)
 
 
 def _fp8_product(a, a_scale, offsets, w, w_scale, out_dtype, out, stream, name: str):
@@ -586,6 +677,238 @@ def matmul_fp8_experts(a, a_scale, offsets, w, w_scale, out_dtype=None, out=None
     if offsets is None:
         raise TypeError("offsets must be a torch.Tensor")
     return _fp8_product(a, a_scale, offsets, w, w_scale, out_dtype, out, stream, "beam_matmul_fp8_experts")
+
+
+def swiglu_fp8(gate_up, offsets=None, y_fp8=None, y_scale=None, stream=None):
+    """``silu(gate) * up`` of rows [gate | up], as E4M3 with one FP32 scale for each 128 values.
+
+    gate_up: [R, 2 F] bfloat16, F a multiple of 16; offsets: int32 as ``moe_sort`` gives them: rows from
+    the last one on are neither read nor written (None: all rows count).
+    Returns (y_fp8 [R, F] float8_e4m3fn, y_scale [R, ceil(F/128)] float32), operands of the FP8 products.
+    """
+    import torch
+    R, F2 = _dims(gate_up, 2)
+    rows, E = (R, F2 // 2), _dims(offsets, 1)[0] if offsets is not None else 0
+    ready = _ready((gate_up, torch.bfloat16, (R, F2)),
+                   *(() if offsets is None else ((offsets, torch.int32, (E,)),)), *_fp8_given(y_fp8, y_scale, rows))
+    if not ready:
+        _check(gate_up, "gate_up", torch.bfloat16, 2)
+        if offsets is not None:
+            _check(offsets, "offsets", torch.int32, 1)
+    if F2 % 2:
+        raise ValueError("gate_up must have an even number of columns")
+    if offsets is not None and E < 1:
+        raise ValueError("offsets must have at least one entry")
+    q, scale = _fp8_out(rows, gate_up.device, y_fp8, y_scale, stream, ready)
+    if not ready:
+        _on_current_device(**_given(gate_up=gate_up, offsets=offsets, y_fp8=q, y_scale=scale))
+    st = _lib.load().beam_swiglu_fp8(_raw_stream(stream, gate_up), gate_up.data_ptr(),
+                                     None if offsets is None else offsets.data_ptr() + 4 * (E - 1), R,
+                                     _c_int(rows[1]), q.data_ptr(), scale.data_ptr())
+    if st != 0:
+        raise BeamError(st, "beam_swiglu_fp8")
+    return q, scale
+
+
+@functools.lru_cache(maxsize=4096)
+def _sort_workspace(T: int, K: int, E: int) -> int:
+    return max(0, _lib.load().beam_moe_sort_workspace(T, K, E))
+
+
+def moe_sort(topk_idx, n_experts: int, offsets=None, slots=None, stream=None):
+    """Choices sorted by expert, in their order within one.
+
+    topk_idx: [T, topk] int32 as ``moe_route`` gives them, -1 for no expert.
+    Returns (offsets int32 [n_experts + 1], slots int32 [T, topk]): expert e has the sorted rows
+    offsets[e] .. offsets[e + 1] - 1; slots[t, k] is the row of choice k of token t, -1 for none.
+    """
+    import torch
+    T, K = _dims(topk_idx, 2)
+    E = _c_int(n_experts)
+    ready = _ready((topk_idx, torch.int32, (T, K)),
+                   *(() if offsets is None else ((offsets, torch.int32, (E + 1,)),)),
+                   *(() if slots is None else ((slots, torch.int32, (T, K)),)))
+    if not ready:
+        _check(topk_idx, "topk_idx", torch.int32, 2)
+    if E < 1:
+        raise ValueError(f"n_experts must be at least 1 (got {E})")
+    K = _c_int(K)
+    ws_bytes = _sort_workspace(T, K, E)
+    with _pool(stream):
+        if offsets is None:
+            offsets = torch.empty(E + 1, dtype=torch.int32, device=topk_idx.device)
+        if slots is None:
+            slots = torch.empty((T, K), dtype=torch.int32, device=topk_idx.device)
+        ws = _workspace(ws_bytes, topk_idx.device)
+    if not ready:
+        _check(offsets, "offsets", torch.int32, 1)
+        _check(slots, "slots", torch.int32, 2)
+        _shape(offsets, "offsets", (E + 1,))
+        _shape(slots, "slots", (T, K))
+        _on_current_device(topk_idx=topk_idx, offsets=offsets, slots=slots)
+    st = _lib.load().beam_moe_sort(_raw_stream(stream, topk_idx), topk_idx.data_ptr(), T, K, E, offsets.data_ptr(),
+                                   slots.data_ptr(), ws.data_ptr() if ws_bytes else None, ws_bytes)
+    if st != 0:
+        raise BeamError(st, "beam_moe_sort")
+    return offsets, slots
+
+
+def moe_gather(x, slots, scale=None, out=None, out_scale=None, stream=None):
+    """Each token's row, and its scale or row of scales, copied to the rows of its choices.
+
+    x: [T, D] of any type whose rows are a multiple of 4 bytes; slots: [T, topk] int32 as ``moe_sort``
+    gives them; scale: [T] or [T, S] float32, as a boundary writes them with y in 8 bits.
+    Returns out [R, D], or (out, out_scale [R] or [R, S]) with scales; R is T * topk where the call makes them.
+    Rows that no choice has are left as they were (in what the call makes: as its memory was).
+    The gradient for x comes from ``moe_gather_backward``.
+    """
+    import torch
+    T, D = _dims(x, 2)
+    K = _dims(slots, 2)[1]
+    S = tuple(getattr(scale, "shape", (T,)))[1:]
+    if out is not None:
+        R = _dims(out, 2)[0]
+    else:
+        R = _dims(out_scale, 1 + len(S))[0] if out_scale is not None else T * K
+    dtype = getattr(x, "dtype", None)
+    ready = _ready((x, dtype, (T, D)), (slots, torch.int32, (T, K)),
+                   *(() if scale is None else ((scale, torch.float32, (T, *S)),)),
+                   *(() if out is None else ((out, dtype, (R, D)),)),
+                   *(() if out_scale is None else ((out_scale, torch.float32, (R, *S)),)))
+    if not ready:
+        _check(x, "x", dtype, 2)
+        _check(slots, "slots", torch.int32, 2)
+        if slots.shape[0] != T:
+            raise ValueError("shape mismatch: x [T, D]; slots [T, topk]")
+        if scale is not None:
+            if getattr(scale, "dim", lambda: 0)() not in (1, 2):
+                raise ValueError("scale must be a 1-d or 2-d tensor")
+            _check(scale, "scale", torch.float32, 1 + len(S))
+            _shape(scale, "scale", (T, *S))
+    if scale is None and out_scale is not None:
+        raise ValueError("out_scale without scale")
+    with _pool(stream):
+        if out is None:
+            out = torch.empty((R, D), dtype=dtype, device=x.device)
+        if scale is not None and out_scale is None:
+            out_scale = torch.empty((R, *S), dtype=torch.float32, device=x.device)
+    if not ready:
+        _check(out, "out", dtype, 2)
+        _shape(out, "out", (R, D))
+        if scale is not None:
+            _check(out_scale, "out_scale", torch.float32, 1 + len(S))
+            _shape(out_scale, "out_scale", (R, *S))
+        _on_current_device(**_given(x=x, slots=slots, scale=scale, out=out, out_scale=out_scale))
+    scale_bytes = 0 if scale is None else 4 * (S[0] if S else 1)
+    st = _lib.load().beam_moe_gather(
+        _raw_stream(stream, x), x.data_ptr(), D * x.element_size(), None if scale is None else scale.data_ptr(),
+        scale_bytes, slots.data_ptr(), T, _c_int(K), R, out.data_ptr(), None if scale is None else out_scale.data_ptr())
+    if st != 0:
+        raise BeamError(st, "beam_moe_gather")
+    return out if scale is None else (out, out_scale)
+
+
+def _row_type(t, name: str) -> int:
+    import torch
+    dtype = getattr(t, "dtype", None)
+    if dtype is torch.bfloat16:
+        return _lib.BEAM_OUT_BF16
+    if dtype is torch.float32:
+        return _lib.BEAM_OUT_FP32
+    raise TypeError(f"{name} must be a bfloat16 or float32 tensor (got {dtype})")
+
+
+def _sum_rows(rows, slots, topk_w, out, stream, names, call: str):
+    """``moe_combine`` and, without weights, the gradient of ``moe_gather``."""
+    import torch
+    kind, (R, D), (T, K) = _row_type(rows, names[0]), _dims(rows, 2), _dims(slots, 2)
+    ready = _ready((rows, rows.dtype, (R, D)), (slots, torch.int32, (T, K)),
+                   *(() if topk_w is None else ((topk_w, torch.float32, (T, K)),)),
+                   *(() if out is None else ((out, rows.dtype, (T, D)),)))
+    if not ready:
+        _check(rows, names[0], rows.dtype, 2)
+        _check(slots, "slots", torch.int32, 2)
+        if topk_w is not None:
+            _check(topk_w, "topk_w", torch.float32, 2)
+            _shape(topk_w, "topk_w", (T, K))
+    if out is None:
+        with _pool(stream):
+            out = torch.empty((T, D), dtype=rows.dtype, device=rows.device)
+    if not ready:
+        _check(out, names[1], rows.dtype, 2)
+        _shape(out, names[1], (T, D))
+        _on_current_device(**_given(**{names[0]: rows, "slots": slots, "topk_w": topk_w, names[1]: out}))
+    lib, s = _lib.load(), _raw_stream(stream, rows)
+    if topk_w is None:
+        st = lib.beam_moe_gather_backward(s, rows.data_ptr(), slots.data_ptr(), T, _c_int(K), R, _c_int(D), kind,
+                                          out.data_ptr())
+    else:
+        st = lib.beam_moe_combine(s, rows.data_ptr(), slots.data_ptr(), topk_w.data_ptr(), T, _c_int(K), R, _c_int(D),
+                                  kind, out.data_ptr())
+    if st != 0:
+        raise BeamError(st, call)
+    return out
+
+
+def moe_gather_backward(drows, slots, dx=None, stream=None):
+    """Gradient of ``moe_gather`` for x: dx[t] = sum over k of drows[slots[t, k]].
+
+    drows: [R, D] bfloat16 or float32, D a multiple of 8; slots: [T, topk] int32. FP32 sums in the order
+    of the choices, rounded once. Returns dx [T, D] of drows' type (0 for a token without choices).
+    """
+    return _sum_rows(drows, slots, None, dx, stream, ("drows", "dx"), "beam_moe_gather_backward")
+
+
+def moe_combine(rows, slots, topk_w, out=None, stream=None):
+    """The experts' outputs back to their tokens: out[t] = sum over k of topk_w[t, k] rows[slots[t, k]].
+
+    rows: [R, D] bfloat16 or float32, D a multiple of 8; slots: [T, topk] int32 as ``moe_sort`` gives
+    them; topk_w: [T, topk] float32. FP32 multiply-adds in the order of the choices, rounded once, as
+    ``moe_combine_boundary`` makes its x: ``boundary_fused`` on the result gives the same bits.
+    Returns out [T, D] of the rows' type (0 for a token without choices). Gradients come from
+    ``moe_combine_backward``.
+    """
+    if topk_w is None:
+        raise TypeError("topk_w must be a torch.Tensor")
+    return _sum_rows(rows, slots, topk_w, out, stream, ("rows", "out"), "beam_moe_combine")
+
+
+def moe_combine_backward(dx, rows, slots, topk_w, drows=None, dw=None, stream=None):
+    """Gradients of ``moe_combine`` for the gradient dx [T, D] of its result.
+
+    Returns (drows [R, D] of the rows' type: topk_w[t, k] dx[t] at slots[t, k], rows that no choice has
+    left as they were; dw float32 [T, topk]: the product of dx[t] with the choice's row, 0 for none).
+    """
+    import torch
+    kind, (R, D), (T, K) = _row_type(rows, "rows"), _dims(rows, 2), _dims(slots, 2)
+    dtype = rows.dtype
+    ready = _ready((dx, dtype, (T, D)), (rows, dtype, (R, D)), (slots, torch.int32, (T, K)),
+                   (topk_w, torch.float32, (T, K)), *(() if drows is None else ((drows, dtype, (R, D)),)),
+                   *(() if dw is None else ((dw, torch.float32, (T, K)),)))
+    if not ready:
+        _check(rows, "rows", dtype, 2)
+        _check(slots, "slots", torch.int32, 2)
+        _check(dx, "dx", dtype, 2)
+        _check(topk_w, "topk_w", torch.float32, 2)
+        _shape(dx, "dx", (T, D))
+        _shape(topk_w, "topk_w", (T, K))
+    with _pool(stream):
+        if drows is None:
+            drows = torch.empty_like(rows)
+        if dw is None:
+            dw = torch.empty((T, K), dtype=torch.float32, device=rows.device)
+    if not ready:
+        _check(drows, "drows", dtype, 2)
+        _check(dw, "dw", torch.float32, 2)
+        _shape(drows, "drows", (R, D))
+        _shape(dw, "dw", (T, K))
+        _on_current_device(dx=dx, rows=rows, slots=slots, topk_w=topk_w, drows=drows, dw=dw)
+    st = _lib.load().beam_moe_combine_backward(
+        _raw_stream(stream, rows), dx.data_ptr(), rows.data_ptr(), slots.data_ptr(), topk_w.data_ptr(), T, _c_int(K), R,
+        _c_int(D), kind, drows.data_ptr(), dw.data_ptr())
+    if st != 0:
+        raise BeamError(st, "beam_moe_combine_backward")
+    return drows, dw
 
 
 def moe_route(logits, bias, n_group: int = 8, topk_group: int = 4, topk: int = 8,

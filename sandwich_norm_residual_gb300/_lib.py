@@ -31,6 +31,7 @@ BEAM_OUT_FP32 = 1
 BEAM_MATMUL_MAX_K = 65536
 BEAM_MATMUL_FP8_MAX_ROWS = 0x7FFFF000
 BEAM_MOE_MAX_EXPERTS = 512
+BEAM_MOE_MAX_PAIRS = 0x7FFFF000
 BEAM_FP8_BLOCK = 128
 BEAM_OPT_FORCE_EXACT_SUM = 0x1
 BEAM_OPT_TEST_WAIT_TIMEOUT = 0x2
@@ -64,6 +65,9 @@ SIGNATURES = {
                                          _OPTS]),
     "beam_moe_combine_boundary_int8": (_i32, [_vp, _vp, _vp, _vp, _f32, _vp, _vp, _i32, _f32, _i64,
                                                _i32, _vp, _vp, _OPTS]),
+    "beam_boundary_fused_fp8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _f32, _i64, _i32, _vp, _vp, _OPTS]),
+    "beam_moe_combine_boundary_fp8": (_i32, [_vp, _vp, _vp, _vp, _f32, _vp, _vp, _i32, _f32, _i64,
+                                             _i32, _vp, _vp, _OPTS]),
     "beam_boundary_fused_host": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _f32, _i64, _i32, _vp]),
     "beam_moe_combine_boundary_host": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _f32, _i64, _i32,
                                                _vp]),
@@ -80,6 +84,13 @@ SIGNATURES = {
     "beam_matmul_fp8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _u32]),
     "beam_matmul_fp8_experts": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp,
                                        _u32]),
+    "beam_moe_sort": (_i32, [_vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _i64]),
+    "beam_moe_sort_workspace": (_i64, [_i64, _i32, _i32]),
+    "beam_moe_gather": (_i32, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _vp, _vp]),
+    "beam_moe_gather_backward": (_i32, [_vp, _vp, _vp, _i64, _i32, _i64, _i32, _i32, _vp]),
+    "beam_moe_combine": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i64, _i32, _i32, _vp]),
+    "beam_moe_combine_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i64, _i32, _i32, _vp, _vp]),
+    "beam_swiglu_fp8": (_i32, [_vp, _vp, _vp, _i64, _i32, _vp, _vp]),
     "beam_moe_balance_loss": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i64, _f32, _vp, _vp, _vp,
                                      _i64]),
     "beam_moe_balance_workspace": (_i64, [_i64, _i32, _i64]),

@@ -49,8 +49,8 @@ struct DeviceInfo {
     int sms = 0;
     long long l2_bytes = 0;
     int smem_optin = 0;                       // max dynamic + static shared memory per CTA
-    KernelFn lim_fn[96] = {};                 // kernels whose dynamic smem limit was raised
-    int lim_val[96] = {};
+    KernelFn lim_fn[128] = {};                 // kernels whose dynamic smem limit was raised
+    int lim_val[128] = {};
     int lim_n = 0;
     OccKey occ_key[128] = {};
     int occ_val[128] = {};
@@ -68,6 +68,7 @@ template <int V, int KIND, bool FULL, int OUT>
 KernelFn pick() {
     if constexpr (KIND == kDenseRing) return beam::boundary_ring_kernel<V, FULL>;
     else if constexpr (OUT == beam::kOutInt8) return beam::boundary_int8_kernel<V, KIND == kMoeRegs, FULL>;
+    else if constexpr (OUT == beam::kOutFp8) return beam::boundary_fp8_kernel<V, KIND == kMoeRegs, FULL>;
     else return beam::boundary_kernel<V, KIND == kMoeRegs, FULL, OUT == beam::kOutNvfp4>;
 }
 
@@ -105,18 +106,20 @@ KernelFn kernel_for_kind(int kind, int vpt, bool full, int out) {
     switch (out) {
     case beam::kOutNvfp4: return register_kernel<beam::kOutNvfp4>(kind, vpt, full);
     case beam::kOutInt8: return register_kernel<beam::kOutInt8>(kind, vpt, full);
+    case beam::kOutFp8: return register_kernel<beam::kOutFp8>(kind, vpt, full);
     default: return register_kernel<beam::kOutBf16>(kind, vpt, full);
     }
 }
 
 // Where y goes when it does not leave as BF16
 struct QuantOut {
-    int kind;  // kOutNvfp4: q, sf, gs; kOutInt8: yi, yis
+    int kind;  // kOutNvfp4: q, sf, gs; kOutInt8: yi, yis; kOutFp8: y8, yis
     uint8_t* q;
     uint8_t* sf;
     float gs;
     int8_t* yi;
     float* yis;
+    uint8_t* y8;
 };
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -242,7 +245,7 @@ beam_status smem_limit(DeviceInfo* d, KernelFn fn, int* out) {
         cudaGetLastError();
         return BEAM_ERR_CUDA;
     }
-    if (d->lim_n < 96) {
+    if (d->lim_n < 128) {
         d->lim_fn[d->lim_n] = fn;
         d->lim_val[d->lim_n++] = limit;
     }
@@ -399,6 +402,8 @@ beam_status launch(bool moe, beam_stream_t stream, uint16_t* h, const uint16_t* 
     p.y_gs = quant ? quant->gs : 0.0f;
     p.yi = quant ? quant->yi : nullptr;
     p.yis = quant ? quant->yis : nullptr;
+    p.y8 = quant ? quant->y8 : nullptr;
+    p.y8s = p.yis;
 
     void* args[] = {&p};
     cudaError_t err;
@@ -545,7 +550,7 @@ beam_status beam_boundary_fused_nvfp4(beam_stream_t stream, uint16_t* h, const u
         return BEAM_ERR_ALIAS;
     if ((const void*)x != (const void*)h && overlaps(h, rows, x, rows)) return BEAM_ERR_ALIAS;
     if (overlaps(h, rows, post_w, vec) || overlaps(h, rows, pre_w, vec)) return BEAM_ERR_ALIAS;
-    const QuantOut qo{beam::kOutNvfp4, y_fp4, y_scale, y_global_scale, nullptr, nullptr};
+    const QuantOut qo{beam::kOutNvfp4, y_fp4, y_scale, y_global_scale, nullptr, nullptr, nullptr};
     return launch(false, stream, h, x, nullptr, nullptr, post_w, pre_w, n, eps, T, D, nullptr, opts, 1.0f, &qo);
 }
 
@@ -567,15 +572,16 @@ beam_status beam_moe_combine_boundary_nvfp4(beam_stream_t stream, uint16_t* h, c
     if (overlaps(h, rows, expert_out, erows) || overlaps(h, rows, topk_w, wbytes) || overlaps(h, rows, post_w, vec) ||
         overlaps(h, rows, pre_w, vec))
         return BEAM_ERR_ALIAS;
-    const QuantOut qo{beam::kOutNvfp4, y_fp4, y_scale, y_global_scale, nullptr, nullptr};
+    const QuantOut qo{beam::kOutNvfp4, y_fp4, y_scale, y_global_scale, nullptr, nullptr, nullptr};
     return launch(true, stream, h, nullptr, expert_out, topk_w, post_w, pre_w, n, eps, T, D, nullptr, opts, 1.0f,
                   &qo);
 }
 
-// y's int8 buffers: both given, aligned, apart from each other and from every other operand
-static beam_status check_int8(int64_t T, int D, const int8_t* q, const float* scale, const beam_launch_opts* opts,
-                              std::initializer_list<std::pair<const void*, size_t>> others) {
-    // the register kernels alone write int8: no ring options
+// y's buffers of codes of a byte each and `blocks` FP32 scales a row: both given, aligned, apart
+// from each other and from every other operand
+static beam_status check_codes(int64_t T, int D, const void* q, const float* scale, int blocks, const beam_launch_opts* opts,
+                               std::initializer_list<std::pair<const void*, size_t>> others) {
+    // the register kernels alone write codes: no ring options
     if (opts && (opts->stages > 0 || (opts->flags & BEAM_OPT_TEST_WAIT_TIMEOUT))) return BEAM_ERR_ARG;
     if (T == 0) return BEAM_OK;
     if (!q || !scale) return BEAM_ERR_NULL;
@@ -584,7 +590,7 @@ static beam_status check_int8(int64_t T, int D, const int8_t* q, const float* sc
     if (!aligned16(q) || !aligned16(scale)) return BEAM_ERR_ALIGN;
     for (const auto& o : others)
         if (!aligned16(o.first)) return BEAM_ERR_ALIGN;
-    const size_t qb = (size_t)T * (size_t)D, sb = (size_t)T * 4u;
+    const size_t qb = (size_t)T * (size_t)D, sb = (size_t)T * (size_t)blocks * 4u;
     if (overlaps(q, qb, scale, sb)) return BEAM_ERR_ALIAS;
     for (const auto& o : others)
         if (overlaps(q, qb, o.first, o.second) || overlaps(scale, sb, o.first, o.second)) return BEAM_ERR_ALIAS;
@@ -597,11 +603,11 @@ beam_status beam_boundary_fused_int8(beam_stream_t stream, uint16_t* h, const ui
     beam_status st = check_common(n, eps, T, D, opts);
     if (st != BEAM_OK) return st;
     const size_t rows = (size_t)T * (size_t)D * 2u, vec = (size_t)D * 2u;
-    st = check_int8(T, D, y_int8, y_scale, opts, {{h, rows}, {x, rows}, {post_w, vec}, {pre_w, vec}});
+    st = check_codes(T, D, y_int8, y_scale, 1, opts, {{h, rows}, {x, rows}, {post_w, vec}, {pre_w, vec}});
     if (st != BEAM_OK || T == 0) return st;
     if ((const void*)x != (const void*)h && overlaps(h, rows, x, rows)) return BEAM_ERR_ALIAS;
     if (overlaps(h, rows, post_w, vec) || overlaps(h, rows, pre_w, vec)) return BEAM_ERR_ALIAS;
-    const QuantOut qo{beam::kOutInt8, nullptr, nullptr, 0.0f, y_int8, y_scale};
+    const QuantOut qo{beam::kOutInt8, nullptr, nullptr, 0.0f, y_int8, y_scale, nullptr};
     return launch(false, stream, h, x, nullptr, nullptr, post_w, pre_w, n, eps, T, D, nullptr, opts, 1.0f, &qo);
 }
 
@@ -614,13 +620,49 @@ beam_status beam_moe_combine_boundary_int8(beam_stream_t stream, uint16_t* h, co
     if (!std::isfinite(route_scale)) return BEAM_ERR_ARG;
     const size_t rows = (size_t)T * (size_t)D * 2u, vec = (size_t)D * 2u;
     const size_t erows = rows * BEAM_MOE_TOPK, wbytes = (size_t)T * BEAM_MOE_TOPK * 4u;
-    st = check_int8(T, D, y_int8, y_scale, opts,
+    st = check_codes(T, D, y_int8, y_scale, 1, opts,
                     {{h, rows}, {expert_out, erows}, {topk_w, wbytes}, {post_w, vec}, {pre_w, vec}});
     if (st != BEAM_OK || T == 0) return st;
     if (overlaps(h, rows, expert_out, erows) || overlaps(h, rows, topk_w, wbytes) || overlaps(h, rows, post_w, vec) ||
         overlaps(h, rows, pre_w, vec))
         return BEAM_ERR_ALIAS;
-    const QuantOut qo{beam::kOutInt8, nullptr, nullptr, 0.0f, y_int8, y_scale};
+    const QuantOut qo{beam::kOutInt8, nullptr, nullptr, 0.0f, y_int8, y_scale, nullptr};
+    return launch(true, stream, h, nullptr, expert_out, topk_w, post_w, pre_w, n, eps, T, D, nullptr, opts,
+                  route_scale, &qo);
+}
+
+static int fp8_blocks(int D) { return (D + beam::kFp8Block - 1) / beam::kFp8Block; }
+
+beam_status beam_boundary_fused_fp8(beam_stream_t stream, uint16_t* h, const uint16_t* x, const uint16_t* post_w,
+                                    const uint16_t* pre_w, int n, float eps, int64_t T, int D, uint8_t* y_fp8,
+                                    float* y_scale, const beam_launch_opts* opts) {
+    beam_status st = check_common(n, eps, T, D, opts);
+    if (st != BEAM_OK) return st;
+    const size_t rows = (size_t)T * (size_t)D * 2u, vec = (size_t)D * 2u;
+    st = check_codes(T, D, y_fp8, y_scale, fp8_blocks(D), opts, {{h, rows}, {x, rows}, {post_w, vec}, {pre_w, vec}});
+    if (st != BEAM_OK || T == 0) return st;
+    if ((const void*)x != (const void*)h && overlaps(h, rows, x, rows)) return BEAM_ERR_ALIAS;
+    if (overlaps(h, rows, post_w, vec) || overlaps(h, rows, pre_w, vec)) return BEAM_ERR_ALIAS;
+    const QuantOut qo{beam::kOutFp8, nullptr, nullptr, 0.0f, nullptr, y_scale, y_fp8};
+    return launch(false, stream, h, x, nullptr, nullptr, post_w, pre_w, n, eps, T, D, nullptr, opts, 1.0f, &qo);
+}
+
+beam_status beam_moe_combine_boundary_fp8(beam_stream_t stream, uint16_t* h, const uint16_t* expert_out,
+                                          const float* topk_w, float route_scale, const uint16_t* post_w,
+                                          const uint16_t* pre_w, int n, float eps, int64_t T, int D, uint8_t* y_fp8,
+                                          float* y_scale, const beam_launch_opts* opts) {
+    beam_status st = check_common(n, eps, T, D, opts);
+    if (st != BEAM_OK) return st;
+    if (!std::isfinite(route_scale)) return BEAM_ERR_ARG;
+    const size_t rows = (size_t)T * (size_t)D * 2u, vec = (size_t)D * 2u;
+    const size_t erows = rows * BEAM_MOE_TOPK, wbytes = (size_t)T * BEAM_MOE_TOPK * 4u;
+    st = check_codes(T, D, y_fp8, y_scale, fp8_blocks(D), opts,
+                     {{h, rows}, {expert_out, erows}, {topk_w, wbytes}, {post_w, vec}, {pre_w, vec}});
+    if (st != BEAM_OK || T == 0) return st;
+    if (overlaps(h, rows, expert_out, erows) || overlaps(h, rows, topk_w, wbytes) || overlaps(h, rows, post_w, vec) ||
+        overlaps(h, rows, pre_w, vec))
+        return BEAM_ERR_ALIAS;
+    const QuantOut qo{beam::kOutFp8, nullptr, nullptr, 0.0f, nullptr, y_scale, y_fp8};
     return launch(true, stream, h, nullptr, expert_out, topk_w, post_w, pre_w, n, eps, T, D, nullptr, opts,
                   route_scale, &qo);
 }
