@@ -157,6 +157,7 @@ beam_status product(beam_stream_t stream, const uint8_t* a, const float* a_scale
     q.n_tiles = (uint32_t)(((int64_t)N + beam::kFp8Chan * (plan.pair ? 2 : 1) - 1) / (beam::kFp8Chan * (plan.pair ? 2 : 1)));
     q.most = plan.pair ? beam::kFp8Many : beam::kFp8Few;
     q.split = plan.split;
+    q.scales16 = steps % 4 == 0 && !misaligned(a_scale, 16);
     q.wide = !f32 && N % 8 == 0 && !misaligned(out, 16);
     q.wait_ns = drop ? beam::kFp8TestWaitNs : beam::kFp8WaitNs;
     q.drop = drop;

@@ -43,6 +43,7 @@ struct Fp8Params {
     int E, N;
     uint32_t steps, n_tiles, most;  // of k; of channels; tokens of a tile at most
     int split;                 // CTAs (pairs) of a cluster, which share a tile's steps
+    int scales16;              // rows of a_scale are whole groups of 16 bytes
     int wide;                  // rows of a BF16 out start and end on 16 bytes
     uint64_t wait_ns;
     int drop;                  // test hook: every tile's second step is never loaded
@@ -57,18 +58,17 @@ struct Fp8Tile {
     static constexpr int kRows = kTokens / CG;      // of B in a CTA
     static constexpr int kSlots = CG == 1 ? 7 : 6;  // ring of operand tiles
     static constexpr int kAccs = CG == 1 ? 4 : 2;   // accumulators of a step
+    static constexpr int kHalves = CG;              // ... each in halves of the columns, which come and go apart
     static constexpr int kScales = 8;               // ring of a step's scales
-    // Warps: those that add, in groups of four (a group has all lanes, and a half or all
-    // of the columns); four that load (weights and tokens, every second slot each: a copy takes
-    // its warp longer than a step takes HBM); one that multiplies; those that bring scales.
-    static constexpr int kGroups = CG == 1 ? 1 : 2, kAddWarps = 4 * kGroups;
+    // Warps: those that add, in groups of four (a group has all lanes and a share of the
+    // columns); two that load, every second slot each; one that brings scales; one that
+    // multiplies.
+    static constexpr int kGroups = CG == 1 ? 2 : 4, kAddWarps = 4 * kGroups;
     static constexpr int kColumns = kTokens / kGroups;  // of an adding warp
-    static constexpr int kLoadWarp = kAddWarps, kMulWarp = kLoadWarp + 4, kScaleWarp = kMulWarp + 1;
-    static constexpr int kScaleWarps = CG == 1 ? 1 : 2;
-    static constexpr int kThreads = 32 * ((kScaleWarp + kScaleWarps + 3) / 4 * 4);
-    // Pairs: 128 sums and 32 values on their way leave 128 registers a thread behind; the
-    // adding warps take theirs from the others (2 x 208 + 2 x 48 = 4 x 128)
-    static constexpr int kAddRegs = 208, kOtherRegs = 48;
+    static constexpr int kLoadWarp = kAddWarps, kScaleWarp = kLoadWarp + 2, kMulWarp = kScaleWarp + 1;
+    static constexpr int kThreads = 32 * (kMulWarp + 1);
+    // Pairs: the adding warps take registers from the others (4 x 104 + 64 = 5 x 96)
+    static constexpr int kAddRegs = 104, kOtherRegs = 64;
     static constexpr uint32_t kABytes = kFp8Chan * kFp8Step;
     static constexpr uint32_t kSlotBytes = kABytes + kRows * kFp8Step;
     static constexpr uint32_t kRedAt = kSlots * kSlotBytes;                  // sums from the cluster's other CTAs
@@ -78,7 +78,7 @@ struct Fp8Tile {
     static constexpr uint32_t kStageAt = kScaleAt + kScales * kTokens * 4;
     static constexpr uint32_t kTableAt = kStageAt + kAddWarps * kStageWarp;  // experts: first tile, first row, rows
     static constexpr uint32_t kBarAt = kTableAt + (3 * kFp8MaxExperts + 4) * 4;
-    static constexpr int kBars = 2 * kSlots + 2 * kAccs + 2 * kScales + 2;
+    static constexpr int kBars = 2 * kSlots + 2 * kAccs * kHalves + 2 * kScales + 2;
     static constexpr uint32_t kSmem = kBarAt + kBars * 8 + 16;
     static constexpr uint32_t kTmem = kAccs * kTokens;
     static_assert(kTmem <= 512 && kSmem <= 232448 && kBarAt % 8 == 0, "tensor memory, shared memory of a CTA");
@@ -125,7 +125,7 @@ public:
 };
 
 // all lanes: whether every lane's wait ended
-template <int CG>
+template <int CG = 1>
 __device__ __forceinline__ bool fp8_wait(uint64_t* bar, uint32_t parity, uint64_t ns) {
     return __all_sync(0xFFFFFFFFu, mbar_wait<CG>(bar, parity, ns));
 }
@@ -147,9 +147,9 @@ __global__ void __launch_bounds__(Fp8Tile<CG>::kThreads, 1)
                              reinterpret_cast<int32_t*>(table + 2 * kFp8MaxExperts + 4)};
     uint64_t* const full = reinterpret_cast<uint64_t*>(smem + C::kBarAt);  // a slot's tiles have landed (the pair's: in its first CTA)
     uint64_t* const empty = full + C::kSlots;             // ... are multiplied
-    uint64_t* const acc_full = empty + C::kSlots;         // a step is multiplied
-    uint64_t* const acc_empty = acc_full + C::kAccs;      // ... and read, by both CTAs
-    uint64_t* const scale_full = acc_empty + C::kAccs;    // a step's scales are there
+    uint64_t* const acc_full = empty + C::kSlots;                     // half of a step's columns are multiplied
+    uint64_t* const acc_empty = acc_full + C::kAccs * C::kHalves;     // ... and read, by both CTAs
+    uint64_t* const scale_full = acc_empty + C::kAccs * C::kHalves;   // a step's scales are there
     uint64_t* const scale_empty = scale_full + C::kScales;
     uint64_t* const red_full = scale_empty + C::kScales;  // the other CTAs' sums of a tile are there
     uint64_t* const red_empty = red_full + 1;             // this CTA's are read
@@ -163,15 +163,15 @@ __global__ void __launch_bounds__(Fp8Tile<CG>::kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
-            mbar_init(&full[i], 2);
+            mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < C::kAccs; ++i) {
+        for (int i = 0; i < C::kAccs * C::kHalves; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], C::kAddWarps * CG);
+            mbar_init(&acc_empty[i], C::kAddWarps / C::kHalves * CG);
         }
         for (int i = 0; i < C::kScales; ++i) {
-            mbar_init(&scale_full[i], C::kScaleWarps);
+            mbar_init(&scale_full[i], 1);
             mbar_init(&scale_empty[i], C::kAddWarps);
         }
         mbar_init(red_full, (q.split > 1 ? q.split - 1 : 1) * C::kAddWarps);
@@ -230,9 +230,10 @@ __global__ void __launch_bounds__(Fp8Tile<CG>::kThreads, 1)
 
     if (warp < C::kAddWarps) {
         if constexpr (CG == 2) more_registers<C::kAddRegs>();
-        constexpr int kChunks = C::kColumns / 32;
-        const int group = warp >> 2, chan = 32 * (warp & 3);
-        const uint32_t lanes = tmem + ((uint32_t)chan << 16);
+        // Columns of a group: a share of one half. A half's columns are a quarter of the tile's
+        // tokens from each CTA's rows of B, so the group's are neighbouring tokens.
+        const int group = warp >> 2, half = group * C::kHalves / C::kGroups, chan = 32 * (warp & 3);
+        const uint32_t lanes = tmem + ((uint32_t)chan << 16) + half * (C::kTokens / C::kHalves);
         unsigned char* const stage = smem + C::kStageAt + warp * C::kStageWarp;
         for (int tile = 0; ok && todo.next(w); ++tile) {
             // sums[j][i]: columns 8 j + 2 (lane % 4) and the next, channel 8 i + lane / 4
@@ -241,67 +242,65 @@ __global__ void __launch_bounds__(Fp8Tile<CG>::kThreads, 1)
             for (int j = 0; j < C::kColumns / 8; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sums[j][i] = make_float2(0.f, 0.f);
-            const int mine = (int)w.n / C::kGroups, c0 = group * mine;  // this warp's columns
+            const int mine = (int)w.n / C::kGroups;  // this warp's columns
+            const int col = CG == 1 ? group * mine : (group & 1) * mine;
+            const int c0 = CG == 1 ? col : (2 * (group & 1) + half) * mine;  // its first token
+            const float* const sc = scales + c0 + 2 * (lane & 3);
             for (uint32_t k = k0; k < k1; ++k, ++it) {
-                const int a = it % C::kAccs, s = it % C::kScales;
-                ok = fp8_wait<1>(&scale_full[s], (uint32_t)(it / C::kScales) & 1, q.wait_ns) &&
-                     fp8_wait<CG>(&acc_full[a], (uint32_t)(it / C::kAccs) & 1, q.wait_ns);
+                const int a = it % C::kAccs, h = a * C::kHalves + half, s = it % C::kScales;
+                ok = fp8_wait(&scale_full[s], (uint32_t)(it / C::kScales) & 1, q.wait_ns) &&
+                     fp8_wait(&acc_full[h], (uint32_t)(it / C::kAccs) & 1, q.wait_ns);
                 if (!ok) break;
                 tmem_fence_after();
-                const uint32_t from = lanes + a * C::kTokens + c0;
-                const float* sc = scales + s * C::kTokens + c0 + 2 * (lane & 3);
-                // 32 columns at a time, the next on their way meanwhile. A last half that is
-                // not there reads columns of this accumulator that no tile stores.
-                float v[2][2][16];
-                tmem_ld_16x256b_x4(from, v[0][0]);
-                tmem_ld_16x256b_x4(from + (16u << 16), v[0][1]);
+                const uint32_t from = lanes + a * C::kTokens + col;
+                // 16 columns at a time. A second eight that are not there are columns of this
+                // accumulator that no tile stores.
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    if (32 * c < mine) {
-                        float(&now)[2][16] = v[c & 1];
-                        tmem_wait_ld(now[0]);
-                        tmem_wait_ld(now[1]);
-                        if (c + 1 < kChunks && 32 * (c + 1) < mine) {
-                            tmem_ld_16x256b_x4(from + 32 * (c + 1), v[(c + 1) & 1][0]);
-                            tmem_ld_16x256b_x4(from + (16u << 16) + 32 * (c + 1), v[(c + 1) & 1][1]);
-                        } else {
+                for (int c = 0; c < C::kColumns / 16; ++c) {
+                    if (16 * c < mine) {
+                        float v[2][8];
+                        tmem_ld_16x256b(from + 16 * c, v[0]);
+                        tmem_ld_16x256b(from + (16u << 16) + 16 * c, v[1]);
+                        float2 f[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            f[j] = *reinterpret_cast<const float2*>(sc + s * C::kTokens + 16 * c + 8 * j);
+                        tmem_wait_ld(v[0], v[1]);
+                        if (16 * (c + 1) >= mine) {
                             // all read: the accumulator may be written again
                             tmem_fence_before();
                             __syncwarp();
                             if (lane == 0) {
-                                if constexpr (CG == 2) mbar_arrive_cluster_relaxed(cluster_addr(&acc_empty[a], place & ~1u));
-                                else mbar_arrive(&acc_empty[a]);
+                                if constexpr (CG == 2) mbar_arrive_cluster_relaxed(cluster_addr(&acc_empty[h], place & ~1u));
+                                else mbar_arrive(&acc_empty[h]);
+                                mbar_arrive(&scale_empty[s]);
                             }
                         }
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 f = *reinterpret_cast<const float2*>(sc + 32 * c + 8 * j);
+                        for (int j = 0; j < 2; ++j)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const float* p = &now[i >> 1][4 * j + 2 * (i & 1)];
-                                sums[4 * c + j][i] = __ffma2_rn(make_float2(p[0], p[1]), f, sums[4 * c + j][i]);
+                                const float* p = &v[i >> 1][4 * j + 2 * (i & 1)];
+                                sums[2 * c + j][i] = __ffma2_rn(make_float2(p[0], p[1]), f[j], sums[2 * c + j][i]);
                             }
-                        }
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&scale_empty[s]);
             }
             if (!ok) break;
             if constexpr (CG == 1) {
                 // A tile that the cluster's CTAs have shares of: CTA d adds up and stores the
-                // columns 8 j .. with j % split = d, from sums that the others write to its
+                // columns of every split-th group of eight, from sums that the others write to its
                 // shared memory
                 if (q.split > 1) {
-                    const int n_groups = mine / 8, each = (C::kColumns / 8 + q.split - 1) / q.split;
+                    const int n_groups = mine / 8, each = (C::kTokens / 8 + q.split - 1) / q.split, lane128 = tid & 127;
                     if (tile > 0) ok = fp8_wait<2>(red_empty, (uint32_t)(tile - 1) & 1, q.wait_ns);
                     if (!ok) break;
 #pragma unroll
                     for (int j = 0; j < C::kColumns / 8; ++j) {
-                        const int d = j % q.split;
+                        const int d = (j * C::kGroups + group) % q.split;
                         if (j < n_groups && d != (int)share) {
                             const int from = (int)share < d ? share : share - 1;
-                            unsigned char* at = smem + C::kRedAt + ((from * each + j / q.split) * 256 + tid) * 16;
+                            unsigned char* at = smem + C::kRedAt + ((from * each + (j * C::kGroups + group) / q.split) * 256 + lane128) * 16;
                             const uint32_t there = cluster_addr(at, d);
                             st_cluster(there, make_float4(sums[j][0].x, sums[j][0].y, sums[j][1].x, sums[j][1].y));
                             st_cluster(there + 2048, make_float4(sums[j][2].x, sums[j][2].y, sums[j][3].x, sums[j][3].y));
@@ -315,10 +314,10 @@ __global__ void __launch_bounds__(Fp8Tile<CG>::kThreads, 1)
                     if (!ok) break;
 #pragma unroll
                     for (int j = 0; j < C::kColumns / 8; ++j)
-                        if (j < n_groups && j % q.split == (int)share)
+                        if (j < n_groups && (j * C::kGroups + group) % q.split == (int)share)
                             for (int from = 0; from < q.split - 1; ++from) {
                                 const float4* at = reinterpret_cast<const float4*>(smem + C::kRedAt) +
-                                                   (from * each + j / q.split) * 256 + tid;
+                                                   (from * each + (j * C::kGroups + group) / q.split) * 256 + lane128;
                                 const float4 u = at[0], v = at[128];
                                 sums[j][0].x += u.x; sums[j][0].y += u.y; sums[j][1].x += u.z; sums[j][1].y += u.w;
                                 sums[j][2].x += v.x; sums[j][2].y += v.y; sums[j][3].x += v.z; sums[j][3].y += v.w;
@@ -335,7 +334,7 @@ __global__ void __launch_bounds__(Fp8Tile<CG>::kThreads, 1)
             const int cols = (int)w.cols - c0;  // from this warp's first on
 #pragma unroll
             for (int j = 0; j < C::kColumns / 8; ++j) {
-                if (8 * j < mine && 8 * j < cols && (CG == 2 || j % q.split == (int)share)) {
+                if (8 * j < mine && 8 * j < cols && (CG == 2 || (j * C::kGroups + group) % q.split == (int)share)) {
                     if constexpr (F32) {
                         // a warp's 32 values: 4 tokens by 8 channels, whole sectors
                         const int t = 8 * j + 2 * (lane & 3);
@@ -372,27 +371,31 @@ __global__ void __launch_bounds__(Fp8Tile<CG>::kThreads, 1)
         }
     } else {
         if constexpr (CG == 2) fewer_registers<C::kOtherRegs>();
-        if (warp < C::kMulWarp) {
-            // Loads. A slot is always filled by the same two warps, one for the channels and
-            // one for the tokens, which therefore have seen every use of it.
-            const int part = warp - C::kLoadWarp, parity = part & 1;
-            const bool channels = part < 2;
+        if (warp < C::kScaleWarp) {
+            // Loads. A slot is always filled by the same warp, which therefore has seen every use
+            // of it; its lanes issue a copy each.
+            const int parity = warp - C::kLoadWarp;
             if (lane == 0) {
-                tma_prefetch_map(channels ? &wmap : &amap64);
-                if (!channels) tma_prefetch_map(&amap16);
+                tma_prefetch_map(&wmap);
+                tma_prefetch_map(&amap64);
+                tma_prefetch_map(&amap16);
             }
             const uint64_t keep = l2_evict_normal(), once = l2_evict_first();
             for (; ok && todo.next(w);) {
                 const uint32_t rows = w.n / CG;  // of B in this CTA
-                // weights that one tile of tokens reads: an expert's only
-                const uint64_t policy = channels && experts.rows[w.e] <= (int)q.most ? once : keep;
-                const uint32_t bytes = CG * (channels ? C::kABytes : rows * kFp8Step);
-                const int big = (int)rows / 64, copies = big + ((int)rows % 64) / 16;
+                // weights that one tile of tokens reads, an expert's only
+                const uint64_t policy = experts.rows[w.e] <= (int)q.most ? once : keep;
+                const uint32_t bytes = CG * (C::kABytes + rows * kFp8Step);
+                // lane 0: the channels; then 64 or 16 tokens a lane
+                const int big = (int)rows / 64, copies = 1 + big + ((int)rows % 64) / 16;
+                const bool wide = lane - 1 < big;
+                const int r = wide ? 64 * (lane - 1) : 64 * big + 16 * (lane - 1 - big);
+                const int y = w.m0 + (int)(rank * rows) + r;
                 for (uint32_t k = k0; k < k1; ++k, ++it) {
                     const int slot = it % C::kSlots;
                     if ((slot & 1) != parity) continue;
                     if (it >= C::kSlots) {
-                        ok = fp8_wait<CG>(&empty[slot], (uint32_t)(it / C::kSlots - 1) & 1, q.wait_ns);
+                        ok = fp8_wait(&empty[slot], (uint32_t)(it / C::kSlots - 1) & 1, q.wait_ns);
                         if (!ok) break;
                     }
                     if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
@@ -401,13 +404,8 @@ __global__ void __launch_bounds__(Fp8Tile<CG>::kThreads, 1)
                     unsigned char* const to = smem + slot * C::kSlotBytes;
                     const uint32_t bar = CG == 2 ? cluster_addr(&full[slot], place & ~1u) : smem_u32(&full[slot]);
                     const int x = (int)k * kFp8Step;
-                    if (channels) {
-                        if (elect_one()) tma_load_3d<CG == 2>(to, &wmap, x, w.n0, w.e, bar, policy);
-                    } else if (lane < copies) {
-                        const int r = lane < big ? 64 * lane : 64 * big + 16 * (lane - big);
-                        const int y = w.m0 + (int)(rank * rows) + r;
-                        tma_load_2d_on<CG == 2>(to + C::kABytes + r * kFp8Step, lane < big ? &amap64 : &amap16, x, y, bar, policy);
-                    }
+                    if (lane == 0) tma_load_3d<CG == 2>(to, &wmap, x, w.n0, w.e, bar, policy);
+                    else if (lane < copies) tma_load_2d_on<CG == 2>(to + C::kABytes + r * kFp8Step, wide ? &amap64 : &amap16, x, y, bar, keep);
                     __syncwarp();
                 }
             }
@@ -416,8 +414,8 @@ __global__ void __launch_bounds__(Fp8Tile<CG>::kThreads, 1)
             // the other leaves its copies the time to land.
             for (int i = max(it - C::kSlots, 0); i < it; ++i)
                 if (((i % C::kSlots) & 1) == parity) {
-                    if (rank == 0) fp8_wait<CG>(&full[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
-                    ok = ok && fp8_wait<CG>(&empty[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
+                    if (rank == 0) fp8_wait(&full[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
+                    ok = ok && fp8_wait(&empty[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
                 }
             if (!ok && rank != 0) {
                 const uint64_t t0 = global_ns();
@@ -427,66 +425,85 @@ __global__ void __launch_bounds__(Fp8Tile<CG>::kThreads, 1)
             if (rank == 0) {
                 const uint64_t a0 = umma_smem_desc(smem_u32(smem)), b0 = a0 + C::kABytes / 16;
                 for (; ok && todo.next(w);) {
-                    const uint32_t idesc = umma_e4m3_desc<kFp8Chan * CG>(w.n);
+                    const uint32_t idesc = umma_e4m3_desc<kFp8Chan * CG>(w.n / C::kHalves);
                     for (uint32_t k = k0; k < k1; ++k, ++it) {
                         const int a = it % C::kAccs, slot = it % C::kSlots;
-                        if (it >= C::kAccs) ok = fp8_wait<CG>(&acc_empty[a], (uint32_t)(it / C::kAccs - 1) & 1, q.wait_ns);
-                        ok = ok && fp8_wait<CG>(&full[slot], (uint32_t)(it / C::kSlots) & 1, q.wait_ns);
-                        if (!ok) break;
-                        tmem_fence_after();
                         // descriptors count addresses in units of 16 bytes
-                        const uint32_t at = (uint32_t)slot * (C::kSlotBytes / 16), d = tmem + a * C::kTokens;
-                        if (elect_one()) {
+                        const uint32_t at = (uint32_t)slot * (C::kSlotBytes / 16);
+                        ok = fp8_wait(&full[slot], (uint32_t)(it / C::kSlots) & 1, q.wait_ns);
 #pragma unroll
-                            for (int j = 0; j < kFp8Step / 32; ++j)
-                                umma_e4m3<CG>(d, a0 + at + 2 * j, b0 + at + 2 * j, idesc, j > 0);
-                            if constexpr (CG == 2) {
-                                umma_commit_pair(&empty[slot], 3u << place);
-                                umma_commit_pair(&acc_full[a], 3u << place);
-                            } else {
-                                umma_commit<1>(&empty[slot]);
-                                umma_commit<1>(&acc_full[a]);
+                        for (int h = 0; h < C::kHalves; ++h) {
+                            uint64_t* const done = &acc_full[a * C::kHalves + h];
+                            if (it >= C::kAccs)
+                                ok = ok && fp8_wait(&acc_empty[a * C::kHalves + h], (uint32_t)(it / C::kAccs - 1) & 1, q.wait_ns);
+                            if (!ok) break;
+                            tmem_fence_after();
+                            const uint32_t d = tmem + a * C::kTokens + h * (C::kTokens / C::kHalves);
+                            const uint64_t b = b0 + at + h * (w.n / (CG * C::kHalves)) * (kFp8Step / 16);
+                            if (elect_one()) {
+#pragma unroll
+                                for (int j = 0; j < kFp8Step / 32; ++j)
+                                    umma_e4m3<CG>(d, a0 + at + 2 * j, b + 2 * j, idesc, j > 0);
+                                if constexpr (CG == 2) umma_commit_pair(done, 3u << place);
+                                else umma_commit<1>(done);
+                                if (h == C::kHalves - 1) {
+                                    if constexpr (CG == 2) umma_commit_pair(&empty[slot], 3u << place);
+                                    else umma_commit<1>(&empty[slot]);
+                                }
                             }
+                            __syncwarp();
                         }
-                        __syncwarp();
+                        if (!ok) break;
                     }
                 }
                 // its instructions have ended, and the readers' arrivals come, before the memory goes
-                for (int i = max(it - C::kAccs, 0); i < it; ++i) {
-                    fp8_wait<CG>(&acc_full[i % C::kAccs], (uint32_t)(i / C::kAccs) & 1, q.wait_ns);
-                    ok = ok && fp8_wait<CG>(&acc_empty[i % C::kAccs], (uint32_t)(i / C::kAccs) & 1, q.wait_ns);
-                }
+                for (int i = max(it - C::kAccs, 0); i < it; ++i)
+                    for (int h = i % C::kAccs * C::kHalves, n = 0; n < C::kHalves; ++h, ++n) {
+                        fp8_wait(&acc_full[h], (uint32_t)(i / C::kAccs) & 1, q.wait_ns);
+                        ok = ok && fp8_wait(&acc_empty[h], (uint32_t)(i / C::kAccs) & 1, q.wait_ns);
+                    }
             }
-        } else if (warp < C::kScaleWarp + C::kScaleWarps) {
+        } else {
             // Scales of a step: a's of every token times w's of this CTA's channels, rounded once
-            // to FP32. The loads of eight steps fall into the same sectors.
-            constexpr int kEach = C::kTokens / (32 * C::kScaleWarps);
-            const int first = 32 * (warp - C::kScaleWarp) + lane;
+            // to FP32. Four steps' are fetched at a time: the way to L2 takes longer than a step
+            // (one step at a time: 0.96 us a step for 256 tokens, where the matrix unit takes 0.27).
+            constexpr int kEach = C::kTokens / 32;
             const uint32_t w_rows = fp8_up((uint32_t)q.N, kFp8Chan);
             for (; ok && todo.next(w);) {
-                const float* as[kEach];
-#pragma unroll
-                for (int i = 0; i < kEach; ++i) {
-                    const uint32_t c = first + 32 * C::kScaleWarps * i;
-                    as[i] = c < w.cols ? q.a_scale + (size_t)(w.m0 + c) * q.steps : nullptr;
-                }
                 const uint32_t w_row = min((uint32_t)w.n0 / kFp8Chan, w_rows - 1);
                 const float* ws = q.w_scale + ((size_t)w.e * w_rows + w_row) * q.steps;
-                for (uint32_t k = k0; k < k1; ++k, ++it) {
-                    const int s = it % C::kScales;
-                    float v[kEach];
-                    const float f = __ldg(ws + k);
+                const float* as = q.a_scale + (size_t)(w.m0 + lane) * q.steps;
+                for (uint32_t g = k0 & ~3u; ok && g < k1; g += 4) {
+                    float f[4], v[kEach][4];
 #pragma unroll
-                    for (int i = 0; i < kEach; ++i) v[i] = as[i] ? __ldg(as[i] + k) : 0.f;
-                    if (it >= C::kScales) {
-                        ok = fp8_wait<1>(&scale_empty[s], (uint32_t)(it / C::kScales - 1) & 1, q.wait_ns);
-                        if (!ok) break;
+                    for (int j = 0; j < 4; ++j) f[j] = g + j < k1 ? __ldg(ws + g + j) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < kEach; ++i) {
+                        const float* from = as + (size_t)(32 * i) * q.steps + g;
+                        const bool in = lane + 32 * i < (int)w.cols;
+                        if (q.scales16) {
+                            const float4 u = in ? __ldg(reinterpret_cast<const float4*>(from)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                            v[i][0] = u.x; v[i][1] = u.y; v[i][2] = u.z; v[i][3] = u.w;
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) v[i][j] = in && g + j < k1 ? __ldg(from + j) : 0.f;
+                        }
                     }
 #pragma unroll
-                    for (int i = 0; i < kEach; ++i)
-                        scales[s * C::kTokens + first + 32 * C::kScaleWarps * i] = as[i] ? __fmul_rn(v[i], f) : 0.f;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&scale_full[s]);
+                    for (int j = 0; j < 4; ++j) {
+                        if (g + j < k0 || g + j >= k1) continue;
+                        const int s = it % C::kScales;
+                        if (it >= C::kScales) {
+                            ok = fp8_wait(&scale_empty[s], (uint32_t)(it / C::kScales - 1) & 1, q.wait_ns);
+                            if (!ok) break;
+                        }
+                        ++it;
+#pragma unroll
+                        for (int i = 0; i < kEach; ++i)
+                            scales[s * C::kTokens + lane + 32 * i] = __fmul_rn(v[i][j], f[j]);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&scale_full[s]);
+                    }
                 }
             }
         }

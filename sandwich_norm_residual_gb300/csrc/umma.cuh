@@ -78,20 +78,11 @@ __device__ __forceinline__ void tmem_ld_16x256b(uint32_t at, float (&r)[8]) {
                  : "r"(at) : "memory");
 }
 
-// the same for 32 columns, without waiting: the values are there behind tmem_wait_ld
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t at, float (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
-          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
-        : "r"(at) : "memory");
-}
-// the wait, which the uses of r cannot be moved ahead of
-__device__ __forceinline__ void tmem_wait_ld(float (&r)[16]) {
+// the wait for such loads, which the uses of what they brought cannot be moved ahead of
+__device__ __forceinline__ void tmem_wait_ld(float (&r)[8], float (&s)[8]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
-                   "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
+                   "+f"(s[0]), "+f"(s[1]), "+f"(s[2]), "+f"(s[3]), "+f"(s[4]), "+f"(s[5]), "+f"(s[6]), "+f"(s[7])
                  :: "memory");
 }
 
