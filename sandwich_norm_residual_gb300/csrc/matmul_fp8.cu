@@ -36,37 +36,46 @@ EncodeTiled encode_tiled() {
 }
 
 // matrices of 8-bit rows of K, one behind the other, in tiles of `rows` rows of one matrix by
-// one step of k, 128-byte swizzle; dims = 2: one matrix
-bool tile_map(CUtensorMap* map, const void* base, int dims, int64_t matrices, int64_t rows_each, int K, int rows) {
+// one step of k, 128-byte swizzle
+bool tile_map(CUtensorMap* map, const void* base, int64_t matrices, int64_t rows_each, int K, int rows) {
     const EncodeTiled encode = encode_tiled();
     const cuuint64_t size[3] = {(cuuint64_t)K, (cuuint64_t)rows_each, (cuuint64_t)matrices};
     const cuuint64_t strides[2] = {(cuuint64_t)K, (cuuint64_t)K * (cuuint64_t)rows_each};
     const cuuint32_t box[3] = {beam::kFp8Step, (cuuint32_t)rows, 1}, unit[3] = {1, 1, 1};
-    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)dims, const_cast<void*>(base), size, strides, box, unit,
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), size, strides, box, unit,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CG>
+template <bool FEW>
 const void* kernel(bool f32) {
-    return f32 ? reinterpret_cast<const void*>(beam::matmul_fp8_kernel<CG, true>)
-               : reinterpret_cast<const void*>(beam::matmul_fp8_kernel<CG, false>);
+    return f32 ? reinterpret_cast<const void*>(beam::matmul_fp8_kernel<FEW, true>)
+               : reinterpret_cast<const void*>(beam::matmul_fp8_kernel<FEW, false>);
 }
 
-template <int CG>
+template <bool FEW>
 cudaLaunchConfig_t config(int workers, int split, cudaStream_t stream, cudaLaunchAttribute* attr) {
-    using C = beam::Fp8Tile<CG>;
+    using C = beam::Fp8Tile<FEW>;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(workers * split * CG));
+    cfg.gridDim = dim3((unsigned)(workers * split * C::CG));
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = stream;
     attr->id = cudaLaunchAttributeClusterDimension;
-    attr->val.clusterDim.x = (unsigned)(split * CG);
+    attr->val.clusterDim.x = (unsigned)(split * C::CG);
     attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = split * CG > 1 ? 1 : 0;
+    cfg.numAttrs = split * C::CG > 1 ? 1 : 0;
     return cfg;
+}
+
+template <bool FEW>
+bool allow_smem() {
+    for (int f32 = 0; f32 < 2; ++f32)
+        if (cudaFuncSetAttribute(kernel<FEW>(f32), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)beam::Fp8Tile<FEW>::kSmem) !=
+            cudaSuccess)
+            return false;
+    return true;
 }
 
 // Raises the kernels' shared-memory limits and asks how many clusters fit, once on each device
@@ -75,39 +84,37 @@ beam_status room(const beam::Device& dev, Fp8Room* out) {
     std::atomic<uint64_t>& slot = known[dev.ordinal & 63];
     uint64_t v = slot.load(std::memory_order_acquire);
     if (!v) {
-        for (int f32 = 0; f32 < 2; ++f32)
-            if (cudaFuncSetAttribute(kernel<1>(f32), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)beam::Fp8Tile<1>::kSmem) != cudaSuccess ||
-                cudaFuncSetAttribute(kernel<2>(f32), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)beam::Fp8Tile<2>::kSmem) != cudaSuccess) {
-                cudaGetLastError();
-                return BEAM_ERR_CUDA;
-            }
+        if (!allow_smem<true>() || !allow_smem<false>()) {
+            cudaGetLastError();
+            return BEAM_ERR_CUDA;
+        }
         cudaLaunchAttribute attr;
-        for (int i = 0; i < 5; ++i) {
+        for (int i = 0; i < 5; ++i) {  // clusters of 1, 2, 4 and 8, and pairs
             int n = dev.sms;
-            const cudaLaunchConfig_t cfg = i == 4 ? config<2>(1, 1, nullptr, &attr) : config<1>(1, 1 << i, nullptr, &attr);
-            if (i > 0 && cudaOccupancyMaxActiveClusters(&n, i == 4 ? kernel<2>(false) : kernel<1>(false), &cfg) != cudaSuccess) {
+            const cudaLaunchConfig_t cfg = i == 4 ? config<false>(1, 1, nullptr, &attr) : config<true>(1, 1 << i, nullptr, &attr);
+            if (i > 0 && cudaOccupancyMaxActiveClusters(&n, i == 4 ? kernel<false>(false) : kernel<true>(false), &cfg) != cudaSuccess) {
                 cudaGetLastError();
                 return BEAM_ERR_CUDA;
             }
-            v |= (uint64_t)(n < 1 ? 0 : n > 4095 ? 4095 : n) << (12 * i);
+            v |= (uint64_t)(n < 0 ? 0 : n > 4095 ? 4095 : n) << (12 * i);
         }
         slot.store(v, std::memory_order_release);
     }
     for (int i = 0; i < 4; ++i) out->clusters[i] = (int)(v >> (12 * i)) & 4095;
     out->pairs = (int)(v >> 48) & 4095;
-    return out->pairs < 1 ? BEAM_ERR_CUDA : BEAM_OK;
+    return out->clusters[0] < 1 || out->pairs < 1 ? BEAM_ERR_CUDA : BEAM_OK;
 }
 
-template <int CG>
-beam_status launch(const Fp8Params& q, const beam::Fp8Plan& plan, const CUtensorMap& wmap, const CUtensorMap& amap64,
-                   const CUtensorMap& amap16, bool f32, cudaStream_t stream) {
+template <bool FEW>
+beam_status launch(const Fp8Params& q, const beam::Fp8Plan& plan, const uint8_t* a, const uint8_t* w, int K, bool f32, cudaStream_t stream) {
+    CUtensorMap wmap, amap, amap16;
+    if (!tile_map(&wmap, w, q.E, q.N, K, 128) || !tile_map(&amap, a, 1, q.R, K, FEW ? 64 : 128)) return BEAM_ERR_CUDA;
+    if (!FEW) amap16 = amap;
+    else if (!tile_map(&amap16, a, 1, q.R, K, 16)) return BEAM_ERR_CUDA;
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config<CG>(plan.workers, plan.split, stream, &attr);
-    void* args[] = {const_cast<CUtensorMap*>(&wmap), const_cast<CUtensorMap*>(&amap64), const_cast<CUtensorMap*>(&amap16),
-                    const_cast<Fp8Params*>(&q)};
-    if (cudaLaunchKernelExC(&cfg, kernel<CG>(f32), args) != cudaSuccess) {
+    const cudaLaunchConfig_t cfg = config<FEW>(plan.workers, plan.split, stream, &attr);
+    void* args[] = {&wmap, &amap, &amap16, const_cast<Fp8Params*>(&q)};
+    if (cudaLaunchKernelExC(&cfg, kernel<FEW>(f32), args) != cudaSuccess) {
         cudaGetLastError();
         return BEAM_ERR_CUDA;
     }
@@ -119,7 +126,7 @@ beam_status product(beam_stream_t stream, const uint8_t* a, const float* a_scale
                     uint32_t flags) {
     if (R < 0 || R > BEAM_MATMUL_FP8_MAX_ROWS || N < 0 || N > BEAM_MATMUL_FP8_MAX_ROWS || K < 16 || (K & 15) ||
         K > BEAM_MATMUL_MAX_K || E < 1 || E > BEAM_MOE_MAX_EXPERTS || (int64_t)N * K >= (int64_t(1) << 40) ||
-        beam::fp8_most_tiles(R, E, ((int64_t)N + beam::kFp8Chan - 1) / beam::kFp8Chan, beam::kFp8Few) > 0x7FFFFFFF)
+        beam::fp8_most_tiles(R, E, beam::kFp8Few) * (((int64_t)N + 127) / 128) > 0x7FFFFFFF)
         return BEAM_ERR_SHAPE;
     if ((out_type != BEAM_OUT_BF16 && out_type != BEAM_OUT_FP32) || (flags & ~BEAM_OPT_TEST_WAIT_TIMEOUT)) return BEAM_ERR_ARG;
     if (R == 0 || N == 0) return BEAM_OK;
@@ -154,20 +161,16 @@ beam_status product(beam_stream_t stream, const uint8_t* a, const float* a_scale
     q.E = E;
     q.N = N;
     q.steps = (uint32_t)steps;
-    q.n_tiles = (uint32_t)(((int64_t)N + beam::kFp8Chan * (plan.pair ? 2 : 1) - 1) / (beam::kFp8Chan * (plan.pair ? 2 : 1)));
-    q.most = plan.pair ? beam::kFp8Many : beam::kFp8Few;
+    q.width = (uint32_t)plan.width;
+    q.n_tiles = beam::fp8_up((uint32_t)N, q.width);
     q.split = plan.split;
     q.scales16 = steps % 4 == 0 && !misaligned(a_scale, 16);
-    q.wide = !f32 && N % 8 == 0 && !misaligned(out, 16);
+    q.wide = (int64_t)N * out_size % 32 == 0 && !misaligned(out, 32);
     q.wait_ns = drop ? beam::kFp8TestWaitNs : beam::kFp8WaitNs;
     q.drop = drop;
     q.status = dev.status_word;
-    CUtensorMap wmap, amap64, amap16;
-    if (!tile_map(&wmap, w, 3, E, N, K, beam::kFp8Chan) || !tile_map(&amap64, a, 2, 1, R, K, 64) ||
-        !tile_map(&amap16, a, 2, 1, R, K, 16))
-        return BEAM_ERR_CUDA;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    return plan.pair ? launch<2>(q, plan, wmap, amap64, amap16, f32, cs) : launch<1>(q, plan, wmap, amap64, amap16, f32, cs);
+    return plan.few ? launch<true>(q, plan, a, w, K, f32, cs) : launch<false>(q, plan, a, w, K, f32, cs);
 }
 
 }  // namespace

@@ -13,29 +13,30 @@
 
 namespace beam {
 
-constexpr int kFp8Step = 128;    // k of a step: the block that shares a scale
-constexpr int kFp8Chan = 128;    // channels of a CTA: the lanes of tensor memory, a block of w_scale
-constexpr int kFp8Band = 8;      // tiles of tokens that a band of tiles is high
-constexpr int kFp8MaxSplit = 8;  // CTAs of a cluster at most
-constexpr int kFp8Few = 64;      // tokens of a tile of single CTAs (CG = 1)
-constexpr int kFp8Many = 256;    // ... of a pair of CTAs (CG = 2)
+constexpr int kFp8Step = 128;      // k of a step: the block that shares a scale
+constexpr int kFp8Block128 = 128;  // channels that share a scale
+constexpr int kFp8Few = 64;        // few tokens: tiles of 128 channels by up to 64 tokens
+constexpr int kFp8Many = 256;      // many: tiles of 256 tokens ...
+constexpr int kFp8Width = 256;     // ... by up to 256 channels
+constexpr int kFp8Band = 8;        // tiles of tokens that a band of tiles is high
+constexpr int kFp8MaxSplit = 8;    // CTAs of a cluster at most
 
 BEAM_HOST_DEVICE constexpr uint32_t fp8_up(uint32_t v, uint32_t to) { return (v + to - 1) / to; }
 
-// n rows of one expert in tiles of at most `most`: as many as needed, alike as far as
-// the matrix instruction's granularity (16 rows of B in every CTA) allows. 530 rows are 3 tiles of
-// 192, 192 and 146 and not 256, 256 and 18: a tile of few tokens still takes all of its
-// channels' loads.
+// n rows of one expert in tiles: as many as needed; few tokens alike as far as the matrix
+// instruction's columns (multiples of 16) allow
 struct Fp8Rows {
     uint32_t tiles, each;
 };
-BEAM_HOST_DEVICE inline Fp8Rows fp8_rows(uint32_t n, uint32_t most, uint32_t grain) {
-    const uint32_t tiles = fp8_up(n, most);
-    return Fp8Rows{tiles, tiles ? fp8_up(fp8_up(n, tiles), grain) * grain : 0u};
+template <bool FEW>
+BEAM_HOST_DEVICE Fp8Rows fp8_rows(uint32_t n) {
+    const uint32_t tiles = fp8_up(n, FEW ? kFp8Few : kFp8Many);
+    if (!FEW) return Fp8Rows{tiles, kFp8Many};
+    return Fp8Rows{tiles, tiles ? fp8_up(fp8_up(n, tiles), 16) * 16 : 0u};
 }
 
 // Tile `u` of an expert's m by n tiles: bands of kFp8Band tiles of tokens, in a band
-// channel by channel. The CTAs at work at a time then share about as many tiles of
+// channel by channel. The CTAs at work at a time then share about as many rows of
 // tokens as of channels, and read the fewest bytes through L2.
 BEAM_HOST_DEVICE inline void fp8_place(uint32_t u, uint32_t m_tiles, uint32_t n_tiles, uint32_t* m, uint32_t* n) {
     const uint32_t band = u / (kFp8Band * n_tiles), left = m_tiles - band * kFp8Band;
@@ -44,39 +45,40 @@ BEAM_HOST_DEVICE inline void fp8_place(uint32_t u, uint32_t m_tiles, uint32_t n_
     *m = band * kFp8Band + v % high;
 }
 
-// Tiles of a product of R rows by `experts` experts at most (which rows are whose is known
-// on the device only): every expert with rows has a tile that may not be whole.
-inline int64_t fp8_most_tiles(int64_t R, int experts, int64_t n_tiles, int most) {
+// Tiles of R rows by `experts` experts at most (which rows are whose is known on the
+// device only): every expert with rows has a tile that may not be whole.
+inline int64_t fp8_most_tiles(int64_t R, int experts, int most) {
     const int64_t live = R < experts ? R : experts;
-    return ((R - live) / most + live) * n_tiles;
+    return (R - live) / most + live;
 }
 
 struct Fp8Plan {
-    bool pair;      // pairs of CTAs on 256 channels by up to 256 tokens, else single CTAs on 128 by up to 64
-    int split;      // CTAs of a cluster, which share a tile's steps (single CTAs only)
+    bool few;
+    int width;      // channels of a tile
+    int split;      // CTAs of a cluster, which share a tile's steps (few tokens only)
     int64_t tiles;  // at most
     int workers;    // clusters
 };
 
-// How many clusters of `split` single CTAs (one an SM) the device holds at a time, for 1, 2, 4 and 8
+// How many clusters of 1, 2, 4 and 8 CTAs (one an SM) with few tokens and how many pairs the device holds at a time
 struct Fp8Room {
     int clusters[4];
     int pairs;
 };
 
-// Single CTAs up to 64 rows an expert on average, where the weights' way from memory
-// bounds it; pairs beyond, where the matrix unit does. Single CTAs share a tile's steps
-// where that evens out the waves: a wave of tiles is as long as its steps, and a tile
-// that is shared costs its join, about two steps more.
+// Few tokens' tiles up to 64 rows an expert on average, where the weights' way from memory
+// bounds the product; many tokens' beyond. Few tokens' tiles share their steps where that
+// evens out the waves: a wave of tiles is as long as its steps, and a tile that is
+// shared costs its join, about two steps more.
 inline Fp8Plan fp8_plan(int64_t R, int experts, int64_t N, int K, const Fp8Room& room) {
     const int64_t live = R < experts ? R : experts;
     Fp8Plan q{};
-    q.pair = R > live * kFp8Few;
-    const int64_t n_tiles = (N + kFp8Chan * (q.pair ? 2 : 1) - 1) / (kFp8Chan * (q.pair ? 2 : 1));
-    q.tiles = fp8_most_tiles(R, experts, n_tiles, q.pair ? kFp8Many : kFp8Few);
+    q.few = R <= live * kFp8Few;
+    q.width = q.few ? 128 : kFp8Width;
+    q.tiles = fp8_most_tiles(R, experts, q.few ? kFp8Few : kFp8Many) * ((N + q.width - 1) / q.width);
     q.split = 1;
-    int room_for = q.pair ? room.pairs : room.clusters[0];
-    if (!q.pair) {
+    int fit = q.few ? room.clusters[0] : room.pairs;
+    if (q.few) {
         const int64_t steps = (K + kFp8Step - 1) / kFp8Step;
         int64_t best = 0;
         for (int i = 0; i < 4; ++i) {
@@ -87,11 +89,11 @@ inline Fp8Plan fp8_plan(int64_t R, int experts, int64_t N, int K, const Fp8Room&
             if (i == 0 || cost < best) {
                 best = cost;
                 q.split = (int)split;
-                room_for = room.clusters[i];
+                fit = room.clusters[i];
             }
         }
     }
-    q.workers = (int)(q.tiles < room_for ? q.tiles : room_for);
+    q.workers = (int)(q.tiles < fit ? q.tiles : fit);
     return q;
 }
 

@@ -78,12 +78,15 @@ __device__ __forceinline__ void tmem_ld_16x256b(uint32_t at, float (&r)[8]) {
                  : "r"(at) : "memory");
 }
 
-// the wait for such loads, which the uses of what they brought cannot be moved ahead of
-__device__ __forceinline__ void tmem_wait_ld(float (&r)[8], float (&s)[8]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
-                   "+f"(s[0]), "+f"(s[1]), "+f"(s[2]), "+f"(s[3]), "+f"(s[4]), "+f"(s[5]), "+f"(s[6]), "+f"(s[7])
-                 :: "memory");
+// 16 columns, with the wait for them
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t at, float (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(at) : "memory");
 }
 
 // transposes the 8 x 8 matrix of 16-bit values that a warp holds, thread t two
@@ -162,11 +165,6 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
     else
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
                      :: "r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
-}
-// the same in a cluster of several pairs: `ctas` has a bit for each CTA of this pair
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint32_t ctas) {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 :: "r"(smem_u32(bar)), "h"((uint16_t)ctas) : "memory");
 }
 
 // ---------------------------------------------------------------- barriers, clusters, TMA
@@ -266,34 +264,20 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, i
         "[%0], [%1, {%2, %6, %6, %6, %3}], [%4], %5;"
         :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy), "r"(0) : "memory");
 }
-// a 3-D tile of the last dimension's slice z. PAIR: its bytes are counted on the barrier at the
-// cluster address `bar`, which may be the other CTA's of the pair; else `bar` is this CTA's.
-template <bool PAIR>
+// A 3-D tile in slice z of the last dimension, its bytes counted on the barrier at the cluster
+// address `bar`: with CG = 2 it may be the other CTA's of the pair, else it is this CTA's
+template <int CG>
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar, uint64_t policy) {
-    if constexpr (PAIR)
-        asm volatile(
-            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-            "[%0], [%1, {%2, %3, %4}], [%5], %6;"
-            :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy) : "memory");
-    else
+    if constexpr (CG == 1)
         asm volatile(
             "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
             "[%0], [%1, {%2, %3, %4}], [%5], %6;"
             :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy) : "memory");
-}
-// a 2-D tile, counted as above
-template <bool PAIR>
-__device__ __forceinline__ void tma_load_2d_on(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t policy) {
-    if constexpr (PAIR)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-            "[%0], [%1, {%2, %3}], [%4], %5;"
-            :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy) : "memory");
     else
         asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-            "[%0], [%1, {%2, %3}], [%4], %5;"
-            :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy) : "memory");
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3, %4}], [%5], %6;"
+            :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
