@@ -153,12 +153,12 @@ int choose_vpt(int nvec, bool moe) {
     return 0;
 }
 
-// The dense rows with y as int8: 4 to 6 vectors where they waste under 1/16 of
+// The dense rows with y as int8 or FP8: 4 to 6 vectors where they waste under 1/16 of
 // the slots, else 5 even where a quarter is wasted. Fewer vectors mean more
 // threads a row, and the row's three reductions then cost more than idle slots:
 // T = 8000, D = 4104: 2 vectors 96 us, 5 vectors 79 us; T = 4000, D = 8200: 3
 // vectors 108 us, 5 vectors 79 us.
-int choose_vpt_int8(int nvec) {
+int choose_vpt_codes(int nvec) {
     for (int v : {5, 4, 6}) {
         const int nt = threads_for(nvec, v);
         if (nt && (nt * v - nvec) * 16 <= nvec) return v;
@@ -304,7 +304,7 @@ beam_status launch(bool moe, beam_stream_t stream, uint16_t* h, const uint16_t* 
     const int nvec = D / 8;
     const int out = quant ? quant->kind : beam::kOutBf16;
     const int vpt = (opts && opts->vec_per_thread)        ? opts->vec_per_thread
-                    : (out == beam::kOutInt8 && !moe) ? choose_vpt_int8(nvec)
+                    : (out >= beam::kOutInt8 && !moe) ? choose_vpt_codes(nvec)
                                                       : choose_vpt(nvec, moe);
     const int nt = threads_for(nvec, vpt);
     if (!nt) return BEAM_ERR_SHAPE;

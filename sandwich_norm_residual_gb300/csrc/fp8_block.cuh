@@ -36,21 +36,36 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t bits) {
     return bits;
 }
 
+// RN32(a / 448) for 2^-100 <= a < inf in three operations instead of an IEEE division: t = RN(a c)
+// with c = RN(1 / 448) is within an ulp of a / 448, r = a - 448 t is exact in one multiply-add,
+// and t + r c rounds correctly (Markstein's theorem, for c the reciprocal rounded to nearest). Checked for every
+// significand. An infinite t is returned as it is, a NaN too.
+__device__ __forceinline__ float div448(float a) {
+    const float c = 0x1.24924ap-9f;
+    const float t = __fmul_rn(a, c);
+    const float q = __fmaf_rn(__fmaf_rn(-t, 448.0f, a), c, t);
+    return t < INFINITY ? q : t;
+}
+
 // codes of the eight values that a lane holds of a block with this amax; the block's scale
 __device__ __forceinline__ uint2 fp8_codes(const float2 (&v)[4], float amax, float* scale) {
-    *scale = __fdiv_rn(amax, 448.0f);
-    if (!(amax > 0.0f && amax < INFINITY)) return make_uint2(0u, 0u);
-    float up = 1.0f;
+    float2 q[4] = {v[0], v[1], v[2], v[3]};
+    // whatever comes out for zeros, infinities and NaN is masked
+    const uint32_t live = amax > 0.0f && amax < INFINITY ? 0xFFFFFFFFu : 0u;
     if (amax < 0x1p-100f) {
-        up = 0x1p+64f;
-        amax *= up;
+        *scale = __fdiv_rn(amax, 448.0f);
+        amax *= 0x1p+64f;
+        const float2 up = make_float2(0x1p+64f, 0x1p+64f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = mul2_rn(q[i], up);
+    } else {
+        *scale = div448(amax);
     }
     const float inv = __fdiv_rn(448.0f, amax);
-    const float2 i2 = make_float2(inv, inv), u2 = make_float2(up, up);
-    float2 q[4];
+    const float2 i2 = make_float2(inv, inv);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = mul2_rn(up == 1.0f ? v[i] : mul2_rn(v[i], u2), i2);
-    return make_uint2(f4_to_e4m3x4(q[0].x, q[0].y, q[1].x, q[1].y), f4_to_e4m3x4(q[2].x, q[2].y, q[3].x, q[3].y));
+    for (int i = 0; i < 4; ++i) q[i] = mul2_rn(q[i], i2);
+    return make_uint2(f4_to_e4m3x4(q[0].x, q[0].y, q[1].x, q[1].y) & live, f4_to_e4m3x4(q[2].x, q[2].y, q[3].x, q[3].y) & live);
 }
 
 }  // namespace beam

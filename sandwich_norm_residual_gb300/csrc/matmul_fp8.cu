@@ -54,10 +54,10 @@ const void* kernel(bool f32) {
 }
 
 template <bool FEW>
-cudaLaunchConfig_t config(int workers, int split, cudaStream_t stream, cudaLaunchAttribute* attr) {
+cudaLaunchConfig_t config(int clusters, int split, cudaStream_t stream, cudaLaunchAttribute* attr) {
     using C = beam::Fp8Tile<FEW>;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(workers * split * C::CG));
+    cfg.gridDim = dim3((unsigned)(clusters * split * C::CG));
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = stream;
@@ -112,7 +112,7 @@ beam_status launch(const Fp8Params& q, const beam::Fp8Plan& plan, const uint8_t*
     if (!FEW) amap16 = amap;
     else if (!tile_map(&amap16, a, 1, q.R, K, 16)) return BEAM_ERR_CUDA;
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config<FEW>(plan.workers, plan.split, stream, &attr);
+    const cudaLaunchConfig_t cfg = config<FEW>(plan.clusters, plan.split, stream, &attr);
     void* args[] = {&wmap, &amap, &amap16, const_cast<Fp8Params*>(&q)};
     if (cudaLaunchKernelExC(&cfg, kernel<FEW>(f32), args) != cudaSuccess) {
         cudaGetLastError();

@@ -99,20 +99,31 @@ struct Fp8Work {
     int e, n0, m0;     // expert; the tile's first channel; this CTA's first row of a and out
     int cols;          // this CTA's tokens
     uint32_t n;        // the instruction's columns: tokens (few) or channels (many), a multiple of 16
+    uint32_t k0, k1;   // this CTA's steps
+    bool shared;       // the cluster's CTAs each have some of the tile's steps
 };
 
-// The tiles worker, worker + workers, ... in order
+// Worker c of W (a CTA, or a pair) takes the tiles c, c + W, ... Where clusters share (few
+// tokens), only the tiles behind the last full wave are shared, one by a cluster at a
+// time: a join takes as long as some ten steps.
 template <bool FEW>
 class Fp8Schedule {
     const Fp8Params& q;
     const Fp8Experts& x;
-    const uint32_t rank, stride;
-    uint32_t at;
+    const uint32_t rank, worker, workers, place;
+    uint32_t at, whole;  // the next tile; the tiles that are not shared
     int e = 0;
 
 public:
-    __device__ Fp8Schedule(const Fp8Params& q_, const Fp8Experts& x_, uint32_t worker, uint32_t workers, uint32_t rank_)
-        : q(q_), x(x_), rank(rank_), stride(workers), at(worker) {}
+    // place: in the cluster
+    __device__ Fp8Schedule(const Fp8Params& q_, const Fp8Experts& x_, uint32_t place_)
+        : q(q_), x(x_), rank(FEW ? 0u : place_), worker(FEW ? blockIdx.x : blockIdx.x / 2), workers(FEW ? gridDim.x : gridDim.x / 2),
+          place(place_), at(worker), whole(0xFFFFFFFFu) {
+        if (FEW && q.split > 1) {
+            whole = x.tile[q.E] / workers * workers;
+            if (at >= whole) at = whole + worker / q.split;
+        }
+    }
     __device__ bool next(Fp8Work& w) {
         while (e < q.E && at >= x.tile[e + 1]) ++e;
         if (e >= q.E) return false;
@@ -126,7 +137,15 @@ public:
         w.m0 = x.row[e] + (int)before;
         w.cols = (int)min(FEW ? r.each : 128u, rows - min(rows, before));
         w.n = FEW ? fp8_up((uint32_t)w.cols, 16) * 16 : min(q.width, fp8_up((uint32_t)(q.N - w.n0), 16) * 16);
-        at += stride;
+        w.shared = FEW && at >= whole;
+        w.k0 = w.shared ? q.steps * place / q.split : 0u;
+        w.k1 = w.shared ? q.steps * (place + 1) / q.split : q.steps;
+        if (w.shared) {
+            at += workers / q.split;
+        } else {
+            at += workers;
+            if (FEW && at >= whole) at = whole + worker / q.split;
+        }
         return true;
     }
 };
@@ -193,9 +212,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(red_empty + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t place = !FEW || q.split > 1 ? cluster_rank() : 0u;
-    const uint32_t share = FEW ? place : 0u, rank = FEW ? 0u : place;  // of the steps; in the pair
-    const uint32_t worker = blockIdx.x / (C::CG * q.split), workers = gridDim.x / (C::CG * q.split);
-    const uint32_t k0 = q.steps * share / q.split, k1 = q.steps * (share + 1) / q.split;
+    const uint32_t rank = FEW ? 0u : place;  // in the pair
 
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
@@ -260,7 +277,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
     tmem_fence_after();
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
-    Fp8Schedule<FEW> todo(q, experts, worker, workers, rank);
+    Fp8Schedule<FEW> todo(q, experts, place);
     Fp8Work w;
     int it = 0;                // steps so far (loads and products)
     int sg = 0, sturn = 0;     // the group of scales, and how often the ring went around
@@ -271,7 +288,8 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
         const uint32_t lanes = tmem + ((uint32_t)(row & 96) << 16);
         const uint32_t leader_empty = FEW ? 0u : cluster_addr(acc_empty, 0);
         int a = 0, aturn = 0;
-        for (int tile = 0; todo.next(w); ++tile) {
+        int joins = 0;
+        while (todo.next(w)) {
             float2 sums[C::kMine / 2];
 #pragma unroll
             for (int j = 0; j < C::kMine / 2; ++j) sums[j] = make_float2(0.f, 0.f);
@@ -279,14 +297,14 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
             const int mine = FEW ? (int)w.n / C::kGroups : C::kMine, c0 = group * mine;
             const bool some = FEW || c0 < (int)w.n;
             // scales come in groups of four steps, at multiples of four
-            for (uint32_t g = k0 & ~3u; g < k1; g += 4) {
+            for (uint32_t g = w.k0 & ~3u; g < w.k1; g += 4) {
                 if (ok) ok = mbar_wait(&scale_full[sg], sturn & 1, q.wait_ns);
                 __syncwarp();
                 // many: this thread's token's in the four steps
                 const float4 own = FEW ? float4{} : scales[sg * C::kScaleRow + group * 128 + row];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (g + j < k0 || g + j >= k1) continue;
+                    if (g + j < w.k0 || g + j >= w.k1) continue;
                     // No vote on the wait: a thread that gave up goes on without waiting
                     if (ok) ok = mbar_wait(&acc_full[a], aturn & 1, q.wait_ns);
                     __syncwarp();
@@ -335,15 +353,15 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                 // A tile that the cluster's CTAs have shares of: CTA d adds up and stores every
                 // split-th group of eight columns, from sums that the others write to its shared memory
                 const int n_groups = mine / 8;
-                if (q.split > 1) {
+                if (w.shared) {
                     const int each = (C::kColumns / 8 + q.split - 1) / q.split;
-                    if (tile > 0 && ok) ok = mbar_wait<2>(red_empty, (uint32_t)(tile - 1) & 1, q.wait_ns);
+                    if (joins > 0 && ok) ok = mbar_wait(red_empty, (uint32_t)(joins - 1) & 1, q.wait_ns);
                     __syncwarp();
 #pragma unroll
                     for (int j = 0; j < C::kMine / 8; ++j) {
                         const int g = j * C::kGroups + group, d = g % q.split;
-                        if (j < n_groups && d != (int)share) {
-                            const int slot = ((int)share < d ? (int)share : (int)share - 1) * each + g / q.split;
+                        if (j < n_groups && d != (int)place) {
+                            const int slot = ((int)place < d ? (int)place : (int)place - 1) * each + g / q.split;
                             const uint32_t there = cluster_addr(smem + C::kRedAt + (slot * 256 + row) * 16, d);
                             st_cluster(there, make_float4(sums[4 * j].x, sums[4 * j].y, sums[4 * j + 1].x, sums[4 * j + 1].y));
                             st_cluster(there + 2048, make_float4(sums[4 * j + 2].x, sums[4 * j + 2].y, sums[4 * j + 3].x, sums[4 * j + 3].y));
@@ -352,13 +370,13 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0)
                         for (int d = 0; d < q.split; ++d)
-                            if (d != (int)share) mbar_arrive_cluster_release(cluster_addr(red_full, d));
-                    if (ok) ok = mbar_wait<2>(red_full, (uint32_t)tile & 1, q.wait_ns);
+                            if (d != (int)place) mbar_arrive_cluster_release(cluster_addr(red_full, d));
+                    if (ok) ok = mbar_wait<2>(red_full, (uint32_t)joins & 1, q.wait_ns);
                     __syncwarp();
 #pragma unroll
                     for (int j = 0; j < C::kMine / 8; ++j) {
                         const int g = j * C::kGroups + group;
-                        if (j < n_groups && g % q.split == (int)share)
+                        if (j < n_groups && g % q.split == (int)place)
                             for (int from = 0; from < q.split - 1; ++from) {
                                 const float4* at = reinterpret_cast<const float4*>(smem + C::kRedAt) + (from * each + g / q.split) * 256 + row;
                                 const float4 u = at[0], v = at[128];
@@ -369,7 +387,8 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0)
                         for (int d = 0; d < q.split; ++d)
-                            if (d != (int)share) mbar_arrive_cluster_release(cluster_addr(red_empty, d));
+                            if (d != (int)place) mbar_arrive_cluster_relaxed(cluster_addr(red_empty, d));
+                    ++joins;
                 }
                 // thread = channel: a warp's store is 32 neighbours of a row
                 Out* const to = out + (size_t)(w.m0 + c0) * (size_t)q.N + (size_t)(w.n0 + row);
@@ -377,7 +396,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                 if (w.n0 + row < q.N) {
 #pragma unroll
                     for (int j = 0; j < C::kMine / 2; ++j)
-                        if ((j / 4 * C::kGroups + group) % q.split == (int)share) {
+                        if (!w.shared || (j / 4 * C::kGroups + group) % q.split == (int)place) {
                             if (2 * j < cols && 2 * j < mine) to[(size_t)(2 * j) * (size_t)q.N] = fp8_round<F32>(sums[j].x);
                             if (2 * j + 1 < cols && 2 * j < mine) to[(size_t)(2 * j + 1) * (size_t)q.N] = fp8_round<F32>(sums[j].y);
                         }
@@ -449,7 +468,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                 const int y = channels ? w.n0 + (int)(rank * (w.n / 2)) : w.m0 + r;
                 const uint32_t bytes = FEW ? C::kABytes + w.n * kFp8Step : 2 * C::kSlotBytes;
                 const uint32_t off = lane == 0 ? 0u : C::kABytes + (uint32_t)r * kFp8Step;
-                for (uint32_t k = k0; k < k1; ++k, ++it) {
+                for (uint32_t k = w.k0; k < w.k1; ++k, ++it) {
                     const int slot = it % C::kSlots;
                     if ((slot & 1) != parity) continue;
                     if (it >= C::kSlots) {
@@ -458,7 +477,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                     }
                     if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&full[slot], bytes);
                     __syncwarp();
-                    if (q.drop && k == k0 + 1) continue;
+                    if (q.drop && k == w.k0 + 1) continue;
                     const uint32_t bar = FEW ? smem_u32(&full[slot]) : cluster_addr(&full[slot], 0);
                     unsigned char* const to = smem + slot * C::kSlotBytes + off;
                     const int x = (int)k * kFp8Step;
@@ -488,7 +507,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                 const uint64_t a0 = umma_smem_desc(smem_u32(smem));
                 for (; ok && todo.next(w);) {
                     const uint32_t idesc = umma_e4m3_desc<128 * C::CG>(w.n);
-                    for (uint32_t k = k0; k < k1; ++k, ++it) {
+                    for (uint32_t k = w.k0; k < w.k1; ++k, ++it) {
                         const int slot = it % C::kSlots, a = it % C::kAccs;
                         ok = mbar_wait(&full[slot], (uint32_t)(it / C::kSlots) & 1, q.wait_ns);
                         if (it >= C::kAccs) ok = ok && mbar_wait(&acc_empty[a], (uint32_t)(it / C::kAccs - 1) & 1, q.wait_ns);
@@ -522,12 +541,12 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                 for (int b = 0; b < kBlocks; ++b)
                     ws[b] = q.w_scale + ((size_t)w.e * w_rows + min((uint32_t)w.n0 / kFp8Block128 + b, w_rows - 1)) * q.steps;
                 const float* as = q.a_scale + (size_t)(w.m0 + lane) * q.steps;
-                for (uint32_t g = k0 & ~3u; g < k1; g += 4) {
+                for (uint32_t g = w.k0 & ~3u; g < w.k1; g += 4) {
                     float f[kBlocks][4], v[kEach][4];
 #pragma unroll
                     for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) f[b][j] = g + j < k1 ? __ldg(ws[b] + g + j) : 0.f;
+                        for (int j = 0; j < 4; ++j) f[b][j] = g + j < w.k1 ? __ldg(ws[b] + g + j) : 0.f;
 #pragma unroll
                     for (int i = 0; i < kEach; ++i) {
                         const float* from = as + (size_t)(32 * i) * q.steps + g;
@@ -537,7 +556,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                             v[i][0] = u.x; v[i][1] = u.y; v[i][2] = u.z; v[i][3] = u.w;
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) v[i][j] = in && g + j < k1 ? __ldg(from + j) : 0.f;
+                            for (int j = 0; j < 4; ++j) v[i][j] = in && g + j < w.k1 ? __ldg(from + j) : 0.f;
                         }
                     }
                     if (sturn > 0) {

@@ -55,9 +55,9 @@ inline int64_t fp8_most_tiles(int64_t R, int experts, int most) {
 struct Fp8Plan {
     bool few;
     int width;      // channels of a tile
-    int split;      // CTAs of a cluster, which share a tile's steps (few tokens only)
+    int split;      // CTAs of a cluster, which share the steps of some tiles (few tokens only)
     int64_t tiles;  // at most
-    int workers;    // clusters
+    int clusters;   // (many tokens: pairs)
 };
 
 // How many clusters of 1, 2, 4 and 8 CTAs (one an SM) with few tokens and how many pairs the device holds at a time
@@ -66,10 +66,11 @@ struct Fp8Room {
     int pairs;
 };
 
+constexpr int kFp8JoinSteps = 4;  // what a join takes in steps
+
 // Few tokens' tiles up to 64 rows an expert on average, where the weights' way from memory
-// bounds the product; many tokens' beyond. Few tokens' tiles share their steps where that
-// evens out the waves: a wave of tiles is as long as its steps, and a tile that is
-// shared costs its join, about two steps more.
+// bounds the product; many tokens' beyond. Few tokens' tiles behind the last full wave
+// are shared by clusters where that ends sooner, counted in steps.
 inline Fp8Plan fp8_plan(int64_t R, int experts, int64_t N, int K, const Fp8Room& room) {
     const int64_t live = R < experts ? R : experts;
     Fp8Plan q{};
@@ -77,23 +78,23 @@ inline Fp8Plan fp8_plan(int64_t R, int experts, int64_t N, int K, const Fp8Room&
     q.width = q.few ? 128 : kFp8Width;
     q.tiles = fp8_most_tiles(R, experts, q.few ? kFp8Few : kFp8Many) * ((N + q.width - 1) / q.width);
     q.split = 1;
-    int fit = q.few ? room.clusters[0] : room.pairs;
+    int64_t fit = q.few ? room.clusters[0] : room.pairs;
     if (q.few) {
         const int64_t steps = (K + kFp8Step - 1) / kFp8Step;
-        int64_t best = 0;
-        for (int i = 0; i < 4; ++i) {
-            const int64_t split = 1 << i;
-            if (room.clusters[i] < 1 || split > steps) break;
-            const int64_t waves = (q.tiles + room.clusters[i] - 1) / room.clusters[i];
-            const int64_t cost = waves * ((steps + split - 1) / split + (i ? 2 : 0));
-            if (i == 0 || cost < best) {
+        int64_t best = (q.tiles + fit - 1) / fit * steps;
+        for (int i = 1; i < 4; ++i) {
+            const int64_t split = 1 << i, clusters = room.clusters[i];
+            if (clusters < 1 || split > steps) break;
+            const int64_t waves = q.tiles / (clusters * split), rest = q.tiles - waves * clusters * split;
+            const int64_t cost = waves * steps + (rest + clusters - 1) / clusters * ((steps + split - 1) / split + kFp8JoinSteps);
+            if (cost < best) {
                 best = cost;
                 q.split = (int)split;
-                fit = room.clusters[i];
+                fit = clusters;
             }
         }
     }
-    q.workers = (int)(q.tiles < fit ? q.tiles : fit);
+    q.clusters = (int)(q.tiles < fit ? q.tiles : fit);
     return q;
 }
 

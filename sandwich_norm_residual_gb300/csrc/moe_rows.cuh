@@ -270,8 +270,18 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const RowsPara
     const int slot = row_slot(p, t, lane);
     const float weight = lane < p.K ? (p.w ? __ldg(p.w + t * p.K + lane) : 1.0f) : 0.0f;
     const uint4* rows = static_cast<const uint4*>(p.rows);
+    // Eight loads a thread do not cover HBM's latency with the 28 warps that an SM holds: the lines
+    // of a few passes ahead are asked for, four of each of the first eight rows, one a lane.
+    const int ahead = __shfl_sync(0xFFFFFFFFu, slot, lane >> 2);
+    const uint4* const line = rows + (size_t)max(ahead, 0) * (size_t)p.vecs + 8 * (lane & 3);
+    auto ask = [&](int base) {
+        if (ahead >= 0 && base + 8 * (lane & 3) < hi) asm volatile("prefetch.global.L2 [%0];" :: "l"(line + base));
+    };
+    constexpr int kAhead = 4;
+    for (int i = 1; i < kAhead; ++i) ask(lo + 32 * i);
     for (int base = lo; base < hi; base += 32) {
         const int v = base + lane;
+        ask(base + 32 * kAhead);
         float2 acc[X::kPairs];
 #pragma unroll
         for (int i = 0; i < X::kPairs; ++i) acc[i] = make_float2(0.f, 0.f);

@@ -1,10 +1,11 @@
 // The experts' activation, written as the FP8 operand of the product behind it:
 //   y = g / (1 + e^-g) * u,  then E4M3 codes with a scale for each 128 (fp8_block.cuh)
 // Half a warp has a block, 8 values a lane, 16 bytes of gate and of up each. Bound by HBM: 4
-// bytes read and 1.03 written for a value. e^-g and the quotient are the special-function
-// unit's base-2 exponential and reciprocal (2 units of 2^-24 and the argument's rounding, 1.44 |g| units): the
-// library's expf and division are 30 more instructions a value, which at HBM's rate do
-// not fit in.
+// bytes read and 1.03 written for a value, if not by the instructions. e^-g and the quotient are the
+// special-function unit's base-2 exponential and reciprocal (2 units of 2^-24 each and the
+// argument's rounding, 1.44 |g| units): the library's expf and division are 30 more
+// instructions a value. What they flush to 0, e^-g below 2^-126, is added to 1; the reciprocal of
+// more than 2^126 is 0.
 #pragma once
 
 #include "fp8_block.cuh"
@@ -23,11 +24,23 @@ struct SwigluParams {
     unsigned int* status;
 };
 
-__device__ __forceinline__ float swiglu(float g, float u) {
-    float t, r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(t) : "f"(__fmul_rn(g, -1.4426950408889634f)));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, t)));
-    return __fmul_rn(__fmul_rn(g, r), u);
+// read once
+__device__ __forceinline__ uint4 ld_swiglu(const uint16_t* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
+// two values; packed products, none of which feeds a packed sum
+__device__ __forceinline__ float2 swiglu2(float2 g, float2 u) {
+    const float2 x = mul2_rn(g, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    float2 t, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t.x) : "f"(x.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t.y) : "f"(x.y));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(__fadd_rn(1.0f, t.x)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(__fadd_rn(1.0f, t.y)));
+    return mul2_rn(mul2_rn(g, r), u);
 }
 
 __global__ void __launch_bounds__(kSwigluThreads) swiglu_fp8_kernel(const SwigluParams p) {
@@ -40,24 +53,27 @@ __global__ void __launch_bounds__(kSwigluThreads) swiglu_fp8_kernel(const Swiglu
             rows = rows < 0 ? 0 : p.R;
         }
     }
-    const long long todo = rows * p.chunks, stride = (long long)gridDim.x * (kSwigluThreads / 32);
-    for (long long w = (long long)blockIdx.x * (kSwigluThreads / 32) + (threadIdx.x >> 5); w < todo; w += stride) {
-        const long long row = w / p.chunks;
-        const int at = (int)(w - row * p.chunks) * 256 + lane * 8;
+    // Pieces of 256 values: warp w takes w, w + warps, ... Row and piece go on by steps that are
+    // divided out once (a 64-bit division for every piece took half of the time).
+    const uint32_t first = blockIdx.x * (kSwigluThreads / 32) + (threadIdx.x >> 5), warps = gridDim.x * (kSwigluThreads / 32);
+    const uint32_t row_step = warps / p.chunks, chunk_step = warps % p.chunks;
+    long long row = first / p.chunks;
+    uint32_t chunk = first % p.chunks;
+    for (; row < rows;) {
+        const int at = (int)chunk * 256 + lane * 8;
         const bool in = at < p.F;
         uint4 g = make_uint4(0, 0, 0, 0), u = g;
         if (in) {
             const uint16_t* x = p.x + (size_t)row * (size_t)(2 * (long long)p.F) + at;
-            g = __ldg(reinterpret_cast<const uint4*>(x));
-            u = __ldg(reinterpret_cast<const uint4*>(x + p.F));
+            g = ld_swiglu(x);
+            u = ld_swiglu(x + p.F);
         }
         const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
         float2 y[4];
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 a = bf2_to_f2(gw[i]), b = bf2_to_f2(uw[i]);
-            y[i] = make_float2(swiglu(a.x, b.x), swiglu(a.y, b.y));
+            y[i] = swiglu2(bf2_to_f2(gw[i]), bf2_to_f2(uw[i]));
             top = max(top, max(__float_as_uint(y[i].x) & 0x7FFFFFFFu, __float_as_uint(y[i].y) & 0x7FFFFFFFu));
         }
         float scale;
@@ -65,6 +81,12 @@ __global__ void __launch_bounds__(kSwigluThreads) swiglu_fp8_kernel(const Swiglu
         if (in) {
             *reinterpret_cast<uint2*>(p.y + (size_t)row * (size_t)p.F + at) = c;
             if ((lane & 15) == 0) p.scale[(size_t)row * (size_t)p.blocks + at / 128] = scale;
+        }
+        row += row_step;
+        chunk += chunk_step;
+        if (chunk >= (uint32_t)p.chunks) {
+            chunk -= p.chunks;
+            ++row;
         }
     }
 }
