@@ -1,6 +1,6 @@
 // Host side of the 8-bit floating-point product: argument checks (before any CUDA
 // call), the choice of the kernel and the launch.
-#include "matmul_fp8.cuh"
+#include "matmul_fp8_dot.cuh"
 
 #include <atomic>
 
@@ -36,13 +36,13 @@ EncodeTiled encode_tiled() {
 }
 
 // matrices of 8-bit rows of K, one behind the other, in tiles of `rows` rows of one matrix by
-// one step of k, 128-byte swizzle
-bool tile_map(CUtensorMap* map, const void* base, int64_t matrices, int64_t rows_each, int K, int rows) {
+// one step of k, 128-byte swizzle; dims = 2: one matrix
+bool tile_map(CUtensorMap* map, const void* base, int dims, int64_t matrices, int64_t rows_each, int K, int rows) {
     const EncodeTiled encode = encode_tiled();
     const cuuint64_t size[3] = {(cuuint64_t)K, (cuuint64_t)rows_each, (cuuint64_t)matrices};
     const cuuint64_t strides[2] = {(cuuint64_t)K, (cuuint64_t)K * (cuuint64_t)rows_each};
     const cuuint32_t box[3] = {beam::kFp8Step, (cuuint32_t)rows, 1}, unit[3] = {1, 1, 1};
-    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), size, strides, box, unit,
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)dims, const_cast<void*>(base), size, strides, box, unit,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -57,24 +57,30 @@ template <bool FEW>
 cudaLaunchConfig_t config(int clusters, int split, cudaStream_t stream, cudaLaunchAttribute* attr) {
     using C = beam::Fp8Tile<FEW>;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(clusters * split * C::CG));
+    cfg.gridDim = dim3((unsigned)(clusters * split));
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = stream;
     attr->id = cudaLaunchAttributeClusterDimension;
-    attr->val.clusterDim.x = (unsigned)(split * C::CG);
+    attr->val.clusterDim.x = (unsigned)(split);
     attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = split * C::CG > 1 ? 1 : 0;
+    cfg.numAttrs = split > 1 ? 1 : 0;
     return cfg;
 }
 
+// Also that the adding warps' registers are there: a request for more than the launch has would wait forever
 template <bool FEW>
 bool allow_smem() {
-    for (int f32 = 0; f32 < 2; ++f32)
+    using C = beam::Fp8Tile<FEW>;
+    for (int f32 = 0; f32 < 2; ++f32) {
+        cudaFuncAttributes attr;
+        if (cudaFuncGetAttributes(&attr, kernel<FEW>(f32)) != cudaSuccess) return false;
+        if (!FEW && attr.numRegs * C::kThreads < 32 * (C::kAddWarps * C::kAddRegs + 4 * C::kOtherRegs)) return false;
         if (cudaFuncSetAttribute(kernel<FEW>(f32), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)beam::Fp8Tile<FEW>::kSmem) !=
             cudaSuccess)
             return false;
+    }
     return true;
 }
 
@@ -89,32 +95,47 @@ beam_status room(const beam::Device& dev, Fp8Room* out) {
             return BEAM_ERR_CUDA;
         }
         cudaLaunchAttribute attr;
-        for (int i = 0; i < 5; ++i) {  // clusters of 1, 2, 4 and 8, and pairs
+        for (int i = 0; i < 4; ++i) {  // both kernels fill an SM
             int n = dev.sms;
-            const cudaLaunchConfig_t cfg = i == 4 ? config<false>(1, 1, nullptr, &attr) : config<true>(1, 1 << i, nullptr, &attr);
-            if (i > 0 && cudaOccupancyMaxActiveClusters(&n, i == 4 ? kernel<false>(false) : kernel<true>(false), &cfg) != cudaSuccess) {
+            const cudaLaunchConfig_t cfg = config<true>(1, 1 << i, nullptr, &attr);
+            if (i > 0 && cudaOccupancyMaxActiveClusters(&n, kernel<true>(false), &cfg) != cudaSuccess) {
                 cudaGetLastError();
                 return BEAM_ERR_CUDA;
             }
-            v |= (uint64_t)(n < 0 ? 0 : n > 4095 ? 4095 : n) << (12 * i);
+            v |= (uint64_t)(n < 0 ? 0 : n > 0xFFFF ? 0xFFFF : n) << (16 * i);
         }
         slot.store(v, std::memory_order_release);
     }
-    for (int i = 0; i < 4; ++i) out->clusters[i] = (int)(v >> (12 * i)) & 4095;
-    out->pairs = (int)(v >> 48) & 4095;
-    return out->clusters[0] < 1 || out->pairs < 1 ? BEAM_ERR_CUDA : BEAM_OK;
+    for (int i = 0; i < 4; ++i) out->clusters[i] = (int)(v >> (16 * i)) & 0xFFFF;
+    return BEAM_OK;
 }
 
 template <bool FEW>
 beam_status launch(const Fp8Params& q, const beam::Fp8Plan& plan, const uint8_t* a, const uint8_t* w, int K, bool f32, cudaStream_t stream) {
     CUtensorMap wmap, amap, amap16;
-    if (!tile_map(&wmap, w, q.E, q.N, K, 128) || !tile_map(&amap, a, 1, q.R, K, FEW ? 64 : 128)) return BEAM_ERR_CUDA;
+    if (!tile_map(&wmap, w, 3, q.E, q.N, K, 128) || !tile_map(&amap, a, 2, 1, q.R, K, FEW ? 64 : 128)) return BEAM_ERR_CUDA;
     if (!FEW) amap16 = amap;
-    else if (!tile_map(&amap16, a, 1, q.R, K, 16)) return BEAM_ERR_CUDA;
+    else if (!tile_map(&amap16, a, 2, 1, q.R, K, 16)) return BEAM_ERR_CUDA;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config<FEW>(plan.clusters, plan.split, stream, &attr);
     void* args[] = {&wmap, &amap, &amap16, const_cast<Fp8Params*>(&q)};
     if (cudaLaunchKernelExC(&cfg, kernel<FEW>(f32), args) != cudaSuccess) {
+        cudaGetLastError();
+        return BEAM_ERR_CUDA;
+    }
+    return BEAM_OK;
+}
+
+// A warp takes two channels, and four where there are enough of them: N = 6144, 8.3 and 9.6 us; N =
+// 20480, 22.0 and 21.4; eight experts of 5120, 45 and 41.
+template <int CH, int BLOCKS>
+beam_status launch_dot(const beam::Fp8DotParams& p, bool f32, int groups, cudaStream_t stream) {
+    const void* fn = f32 ? reinterpret_cast<const void*>(beam::matmul_fp8_dot_kernel<CH, BLOCKS, true>)
+                         : reinterpret_cast<const void*>(beam::matmul_fp8_dot_kernel<CH, BLOCKS, false>);
+    const int64_t per_block = CH * beam::kFp8DotWarps;
+    void* args[] = {const_cast<beam::Fp8DotParams*>(&p)};
+    if (cudaLaunchKernel(fn, dim3((unsigned)((p.q.N + per_block - 1) / per_block), (unsigned)groups), dim3(32 * beam::kFp8DotWarps),
+                         args, 0, stream) != cudaSuccess) {
         cudaGetLastError();
         return BEAM_ERR_CUDA;
     }
@@ -147,11 +168,26 @@ beam_status product(beam_stream_t stream, const uint8_t* a, const float* a_scale
     beam::Device dev;
     beam_status st = beam::device(&dev);
     if (st != BEAM_OK) return st;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const bool drop = (flags & BEAM_OPT_TEST_WAIT_TIMEOUT) != 0;
+    if (!drop && beam::fp8_dot(R, E)) {
+        beam::Fp8DotParams p{a, w, {}, K};
+        p.q.a_scale = a_scale;
+        p.q.w_scale = w_scale;
+        p.q.out = out;
+        p.q.offsets = offsets;
+        p.q.R = R;
+        p.q.E = E;
+        p.q.N = N;
+        p.q.steps = (uint32_t)steps;
+        p.q.status = dev.status_word;
+        const int groups = (int)(R < E ? R : E);
+        return (int64_t)N * groups >= 16384 ? launch_dot<4, 3>(p, f32, groups, cs) : launch_dot<2, 4>(p, f32, groups, cs);
+    }
     Fp8Room fits;
     st = room(dev, &fits);
     if (st != BEAM_OK) return st;
     const beam::Fp8Plan plan = beam::fp8_plan(R, E, N, K, fits);
-    const bool drop = (flags & BEAM_OPT_TEST_WAIT_TIMEOUT) != 0;
     Fp8Params q{};
     q.a_scale = a_scale;
     q.w_scale = w_scale;
@@ -169,7 +205,6 @@ beam_status product(beam_stream_t stream, const uint8_t* a, const float* a_scale
     q.wait_ns = drop ? beam::kFp8TestWaitNs : beam::kFp8WaitNs;
     q.drop = drop;
     q.status = dev.status_word;
-    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     return plan.few ? launch<true>(q, plan, a, w, K, f32, cs) : launch<false>(q, plan, a, w, K, f32, cs);
 }
 

@@ -16,12 +16,14 @@
 //     Few tokens: lanes are channels, columns tokens (the instruction's columns are any
 //     multiple of 16, its lanes are not); every column's scale is read from shared memory by
 //     all lanes at once, and a warp stores 32 neighbours of a row of out.
-//   - An SM takes 64 bytes a clock from L2. 128 tokens by 256 channels on one SM bring 48 KB
-//     a step, 768 clocks, where its products take 512; a pair of SMs on 256 by 256 brings 32 KB
-//     to each (M = 2048, N = 4864, K = 20480: 194 and 152 us).
+//   - Tiles of one CTA. Pairs of CTAs on 256 by 256 bring a third less through L2 but free their
+//     accumulators through the cluster's network: M = 16384, N = 20480, K = 5120 took 1322 us
+//     in pairs, 1326 in single CTAs, and experts fill tiles of 128 rows better (16384 tokens to
+//     8 of 256, N = K = 5120: 3390 and 3204 us).
 //   - What the adding warps do beside reading, multiplying and adding counts twice: their
 //     waits end with no vote, scales come four steps at a time, the barriers' places are
-//     kept, not computed (200 -> 152 us; without any reading and adding 122 us).
+//     kept, not computed (M = 2048, N = 4864, K = 20480: 200 -> 152 us; without any reading
+//     and adding 122 us).
 #pragma once
 
 #include <type_traits>
@@ -53,14 +55,16 @@ struct Fp8Params {
     unsigned int* status;
 };
 
-// Few tokens: a CTA with 128 channels and up to 64 tokens. Many: a pair of CTAs on one tensor
-// tile, 128 tokens each, that share up to 256 channels: either loads half of them.
+// A CTA's tile. Few tokens: 128 channels and up to 64 tokens; many: 128 tokens and up to 256
+// channels.
 template <bool FEW>
 struct Fp8Tile {
-    static constexpr int CG = FEW ? 1 : 2;
     static constexpr int kColumns = FEW ? kFp8Few : kFp8Width;  // of an accumulator
-    static constexpr int kSlots = FEW ? 7 : 6;       // ring of operand tiles
-    static constexpr int kAccs = FEW ? 4 : 2;        // accumulators of a step
+    static constexpr int kSlots = FEW ? 7 : 4;       // ring of operand tiles
+    // Accumulators of a step. Few tokens: one for every slot, so that a slot that has been read
+    // and an accumulator that may be written again are one barrier, and the multiplying
+    // thread waits once a step.
+    static constexpr int kAccs = FEW ? kSlots : 2;
     static constexpr int kScales = 8;                // ring of steps' scales, in groups of four
     // FP32 of four steps in units of 16 bytes: of a step's tokens side by side; of a token's four
     // steps, the CTA's tokens for either block of channels
@@ -77,16 +81,17 @@ struct Fp8Tile {
     // these 0.47.
     static constexpr int kAddRegs = 216, kOtherRegs = 72;
     static constexpr uint32_t kABytes = 128 * kFp8Step;  // rows of the lanes
-    static constexpr uint32_t kSlotBytes = kABytes + kColumns / CG * kFp8Step;
-    static constexpr uint32_t kRedAt = kSlots * kSlotBytes;                  // sums from the cluster's other CTAs
-    static constexpr uint32_t kRedBytes = FEW ? (kFp8MaxSplit - 1) * 4096 : 0;
-    static constexpr uint32_t kScaleAt = kRedAt + kRedBytes;                 // FP32 [kScales][kScaleRow]
+    static constexpr uint32_t kSlotBytes = kABytes + kColumns * kFp8Step;
+    static constexpr uint32_t kRedAt = FEW ? kSlots * kSlotBytes : 0;        // sums from the cluster's other CTAs
+    static constexpr uint32_t kRedBytes = (kFp8MaxSplit - 1) * kColumns / kFp8MaxSplit * 512;
+    static constexpr uint32_t kScaleAt = kSlots * kSlotBytes + (FEW ? kRedBytes : 0);  // FP32 [kScales][kScaleRow]
     static constexpr uint32_t kTableAt = kScaleAt + kScales * kScaleRow * 4; // experts: first tile, first row, rows
     static constexpr uint32_t kBarAt = kTableAt + (3 * kFp8MaxExperts + 4) * 4;
     static constexpr int kBars = 2 * kSlots + 2 * kAccs + 2 * (kScales / 4) + 2;
     static constexpr uint32_t kSmem = kBarAt + kBars * 8 + 16;
-    static constexpr uint32_t kTmem = kAccs * kColumns;
-    static_assert(kTmem <= 512 && kSmem <= 232448 && kBarAt % 8 == 0, "tensor memory, shared memory of a CTA");
+    static constexpr uint32_t kTmem = 512;
+    static_assert(FEW || kRedBytes <= kSlots * kSlotBytes, "the join fits the ring");
+    static_assert(kAccs * kColumns <= 512 && kSmem <= 232448 && kBarAt % 8 == 0, "tensor memory, shared memory of a CTA");
 };
 
 // Which rows and tiles an expert has, in shared memory
@@ -96,32 +101,35 @@ struct Fp8Experts {
 };
 
 struct Fp8Work {
-    int e, n0, m0;     // expert; the tile's first channel; this CTA's first row of a and out
-    int cols;          // this CTA's tokens
+    int e, n0, m0;     // expert; the tile's first channel; its first row of a and out
+    int cols;          // its tokens
     uint32_t n;        // the instruction's columns: tokens (few) or channels (many), a multiple of 16
     uint32_t k0, k1;   // this CTA's steps
     bool shared;       // the cluster's CTAs each have some of the tile's steps
 };
 
-// Worker c of W (a CTA, or a pair) takes the tiles c, c + W, ... Where clusters share (few
-// tokens), only the tiles behind the last full wave are shared, one by a cluster at a
-// time: a join takes as long as some ten steps.
+// CTA c of W takes the tiles c, c + W, ... Where there are clusters, the tiles behind the last
+// full wave are shared, one by a cluster at a time.
 template <bool FEW>
 class Fp8Schedule {
     const Fp8Params& q;
     const Fp8Experts& x;
-    const uint32_t rank, worker, workers, place;
-    uint32_t at, whole;  // the next tile; the tiles that are not shared
+    const uint32_t place;  // in the cluster
+    uint32_t at, whole;    // the next tile; the tiles that are not shared
     int e = 0;
 
+    __device__ uint32_t first_shared() const { return whole + blockIdx.x / q.split; }
+
 public:
-    // place: in the cluster
     __device__ Fp8Schedule(const Fp8Params& q_, const Fp8Experts& x_, uint32_t place_)
-        : q(q_), x(x_), rank(FEW ? 0u : place_), worker(FEW ? blockIdx.x : blockIdx.x / 2), workers(FEW ? gridDim.x : gridDim.x / 2),
-          place(place_), at(worker), whole(0xFFFFFFFFu) {
-        if (FEW && q.split > 1) {
-            whole = x.tile[q.E] / workers * workers;
-            if (at >= whole) at = whole + worker / q.split;
+        : q(q_), x(x_), place(place_), at(blockIdx.x), whole(0xFFFFFFFFu) {
+        if (q.split > 1) {
+            const uint32_t all = x.tile[q.E], rest = all % gridDim.x;
+            // many tokens' joins go through the ring, so a cluster has one at most, its last tile
+            if (FEW || rest <= gridDim.x / q.split) {
+                whole = all - rest;
+                if (at >= whole) at = first_shared();
+            }
         }
     }
     __device__ bool next(Fp8Work& w) {
@@ -133,18 +141,17 @@ public:
         fp8_place(at - x.tile[e], r.tiles, q.n_tiles, &m, &n);
         w.e = e;
         w.n0 = (int)(n * q.width);
-        const uint32_t before = m * r.each + rank * 128;
-        w.m0 = x.row[e] + (int)before;
-        w.cols = (int)min(FEW ? r.each : 128u, rows - min(rows, before));
+        w.m0 = x.row[e] + (int)(m * r.each);
+        w.cols = (int)min(r.each, rows - m * r.each);
         w.n = FEW ? fp8_up((uint32_t)w.cols, 16) * 16 : min(q.width, fp8_up((uint32_t)(q.N - w.n0), 16) * 16);
-        w.shared = FEW && at >= whole;
+        w.shared = at >= whole;
         w.k0 = w.shared ? q.steps * place / q.split : 0u;
         w.k1 = w.shared ? q.steps * (place + 1) / q.split : q.steps;
         if (w.shared) {
-            at += workers / q.split;
+            at += gridDim.x / q.split;
         } else {
-            at += workers;
-            if (FEW && at >= whole) at = whole + worker / q.split;
+            at += gridDim.x;
+            if (at >= whole) at = first_shared();
         }
         return true;
     }
@@ -202,36 +209,35 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
     const Fp8Experts experts{table, reinterpret_cast<int32_t*>(table + kFp8MaxExperts + 4),
                              reinterpret_cast<int32_t*>(table + 2 * kFp8MaxExperts + 4)};
     uint64_t* const full = reinterpret_cast<uint64_t*>(smem + C::kBarAt);  // a slot's tiles have landed
-    uint64_t* const empty = full + C::kSlots;                 // ... are multiplied
-    uint64_t* const acc_full = empty + C::kSlots;             // a step is multiplied
+    uint64_t* const acc_full = full + C::kSlots;              // a step is multiplied
     uint64_t* const acc_empty = acc_full + C::kAccs;          // ... and read
-    uint64_t* const scale_full = acc_empty + C::kAccs;        // four steps' scales are there
+    uint64_t* const empty = FEW ? acc_empty : acc_empty + C::kAccs;  // a slot's tiles may be written again
+    uint64_t* const scale_full = empty + C::kSlots;           // four steps' scales are there
     uint64_t* const scale_empty = scale_full + C::kScales / 4;
     uint64_t* const red_full = scale_empty + C::kScales / 4;  // the other CTAs' sums of a tile are there
-    uint64_t* const red_empty = red_full + 1;                 // this CTA's are read
-    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(red_empty + 1);
+    uint64_t* const red_ready = red_full + 1;                 // they let this CTA write theirs
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(red_ready + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t place = !FEW || q.split > 1 ? cluster_rank() : 0u;
-    const uint32_t rank = FEW ? 0u : place;  // in the pair
+    const uint32_t place = q.split > 1 ? cluster_rank() : 0u;
 
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            if (!FEW) mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < C::kAccs; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], C::kAddWarps * C::CG);
+            mbar_init(&acc_empty[i], C::kAddWarps);
         }
         for (int i = 0; i < C::kScales / 4; ++i) {
             mbar_init(&scale_full[i], 1);
             mbar_init(&scale_empty[i], C::kAddWarps);
         }
         mbar_init(red_full, (q.split > 1 ? q.split - 1 : 1) * C::kAddWarps);
-        mbar_init(red_empty, (q.split > 1 ? q.split - 1 : 1) * C::kAddWarps);
+        mbar_init(red_ready, (q.split > 1 ? q.split - 1 : 1) * C::kAddWarps);
         mbar_fence_init();
     }
-    if (warp == C::kMulWarp) tmem_alloc<C::CG, C::kTmem>(tmem_slot);
+    if (warp == C::kMulWarp) tmem_alloc<1, C::kTmem>(tmem_slot);
     // Experts' rows. Offsets that decrease or leave [0, R] are held within: what they
     // make of out is not said, but nothing outside of it is touched.
     bool bad = false;
@@ -273,7 +279,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
     }
     tmem_fence_before();
     __syncthreads();
-    if (!FEW || q.split > 1) cluster_sync();  // the other CTAs' barriers are ready too
+    if (q.split > 1) cluster_sync();  // the other CTAs' barriers are ready too
     tmem_fence_after();
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
@@ -286,7 +292,6 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
         if constexpr (!FEW) more_registers<C::kAddRegs>();
         const int group = warp >> 2, row = tid & 127;  // row: this thread's lane of tensor memory
         const uint32_t lanes = tmem + ((uint32_t)(row & 96) << 16);
-        const uint32_t leader_empty = FEW ? 0u : cluster_addr(acc_empty, 0);
         int a = 0, aturn = 0;
         int joins = 0;
         while (todo.next(w)) {
@@ -331,10 +336,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                     // all read: the accumulator may be written again
                     tmem_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (FEW) mbar_arrive(&acc_empty[a]);
-                        else mbar_arrive_cluster_relaxed(leader_empty + a * 8);
-                    }
+                    if (lane == 0) mbar_arrive(&acc_empty[a]);
                     if (++a == C::kAccs) {
                         a = 0;
                         ++aturn;
@@ -349,54 +351,64 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
             }
             using Out = Fp8Out<F32>;
             Out* const out = static_cast<Out*>(q.out);
-            if constexpr (FEW) {
-                // A tile that the cluster's CTAs have shares of: CTA d adds up and stores every
-                // split-th group of eight columns, from sums that the others write to its shared memory
-                const int n_groups = mine / 8;
-                if (w.shared) {
-                    const int each = (C::kColumns / 8 + q.split - 1) / q.split;
-                    if (joins > 0 && ok) ok = mbar_wait(red_empty, (uint32_t)(joins - 1) & 1, q.wait_ns);
-                    __syncwarp();
+            // A tile that the cluster's CTAs have shares of: CTA d adds up and stores every split-th
+            // piece of the columns, from sums that the others write to its shared memory: few
+            // tokens' to a place of their own, many tokens' to the ring, which by then is done with.
+            constexpr int kPiece = FEW ? 8 : 32, kPieces = C::kMine / kPiece;
+            auto owner = [&](int j) { return (j * C::kGroups + group) % q.split; };
+            if (w.shared) {
+                const int each = (C::kColumns / kPiece + q.split - 1) / q.split;
+                const auto place_of = [&](int from, int j) {
+                    return smem + C::kRedAt + (((from * each + (j * C::kGroups + group) / q.split) * (kPiece / 4)) * 128 + row) * 16;
+                };
+                // the others may write to this CTA's, and this one to theirs
+                __syncwarp();
+                if (lane == 0)
+                    for (int d = 0; d < q.split; ++d)
+                        if (d != (int)place) mbar_arrive_cluster_relaxed(cluster_addr(red_ready, d));
+                if (ok) ok = mbar_wait(red_ready, joins & 1, q.wait_ns);
+                __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < C::kMine / 8; ++j) {
-                        const int g = j * C::kGroups + group, d = g % q.split;
-                        if (j < n_groups && d != (int)place) {
-                            const int slot = ((int)place < d ? (int)place : (int)place - 1) * each + g / q.split;
-                            const uint32_t there = cluster_addr(smem + C::kRedAt + (slot * 256 + row) * 16, d);
-                            st_cluster(there, make_float4(sums[4 * j].x, sums[4 * j].y, sums[4 * j + 1].x, sums[4 * j + 1].y));
-                            st_cluster(there + 2048, make_float4(sums[4 * j + 2].x, sums[4 * j + 2].y, sums[4 * j + 3].x, sums[4 * j + 3].y));
+                for (int j = 0; j < kPieces; ++j) {
+                    const int d = owner(j);
+                    if ((!FEW || kPiece * j < mine) && d != (int)place) {
+                        const uint32_t there = cluster_addr(place_of((int)place < d ? (int)place : (int)place - 1, j), d);
+#pragma unroll
+                        for (int i = 0; i < kPiece / 4; ++i) {
+                            const float2 u = sums[kPiece / 2 * j + 2 * i], v = sums[kPiece / 2 * j + 2 * i + 1];
+                            st_cluster(there + i * 2048, make_float4(u.x, u.y, v.x, v.y));
                         }
                     }
-                    __syncwarp();
-                    if (lane == 0)
-                        for (int d = 0; d < q.split; ++d)
-                            if (d != (int)place) mbar_arrive_cluster_release(cluster_addr(red_full, d));
-                    if (ok) ok = mbar_wait<2>(red_full, (uint32_t)joins & 1, q.wait_ns);
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < C::kMine / 8; ++j) {
-                        const int g = j * C::kGroups + group;
-                        if (j < n_groups && g % q.split == (int)place)
-                            for (int from = 0; from < q.split - 1; ++from) {
-                                const float4* at = reinterpret_cast<const float4*>(smem + C::kRedAt) + (from * each + g / q.split) * 256 + row;
-                                const float4 u = at[0], v = at[128];
-                                sums[4 * j].x += u.x; sums[4 * j].y += u.y; sums[4 * j + 1].x += u.z; sums[4 * j + 1].y += u.w;
-                                sums[4 * j + 2].x += v.x; sums[4 * j + 2].y += v.y; sums[4 * j + 3].x += v.z; sums[4 * j + 3].y += v.w;
-                            }
-                    }
-                    __syncwarp();
-                    if (lane == 0)
-                        for (int d = 0; d < q.split; ++d)
-                            if (d != (int)place) mbar_arrive_cluster_relaxed(cluster_addr(red_empty, d));
-                    ++joins;
                 }
+                __syncwarp();
+                if (lane == 0)
+                    for (int d = 0; d < q.split; ++d)
+                        if (d != (int)place) mbar_arrive_cluster_release(cluster_addr(red_full, d));
+                if (ok) ok = mbar_wait<2>(red_full, joins & 1, q.wait_ns);
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < kPieces; ++j)
+                    if ((!FEW || kPiece * j < mine) && owner(j) == (int)place)
+                        for (int from = 0; from < q.split - 1; ++from) {
+                            const float4* at = reinterpret_cast<const float4*>(place_of(from, j));
+#pragma unroll
+                            for (int i = 0; i < kPiece / 4; ++i) {
+                                const float4 v = at[i * 128];
+                                float2(&t)[2] = reinterpret_cast<float2(&)[2]>(sums[kPiece / 2 * j + 2 * i]);
+                                t[0].x += v.x; t[0].y += v.y; t[1].x += v.z; t[1].y += v.w;
+                            }
+                        }
+                ++joins;
+            }
+            auto stored = [&](int j) { return !w.shared || owner(j) == (int)place; };
+            if constexpr (FEW) {
                 // thread = channel: a warp's store is 32 neighbours of a row
                 Out* const to = out + (size_t)(w.m0 + c0) * (size_t)q.N + (size_t)(w.n0 + row);
                 const int cols = w.cols - c0;  // from this warp's first on
                 if (w.n0 + row < q.N) {
 #pragma unroll
                     for (int j = 0; j < C::kMine / 2; ++j)
-                        if (!w.shared || (j / 4 * C::kGroups + group) % q.split == (int)place) {
+                        if (stored(j / 4)) {
                             if (2 * j < cols && 2 * j < mine) to[(size_t)(2 * j) * (size_t)q.N] = fp8_round<F32>(sums[j].x);
                             if (2 * j + 1 < cols && 2 * j < mine) to[(size_t)(2 * j + 1) * (size_t)q.N] = fp8_round<F32>(sums[j].y);
                         }
@@ -410,7 +422,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                     if (row < w.cols) {
 #pragma unroll
                         for (int j = 0; j < C::kMine / kBatch; ++j) {
-                            if (kBatch * j < left) {
+                            if (kBatch * j < left && stored(kBatch * j / 32)) {
                                 uint32_t v[8];
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
@@ -425,7 +437,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                     // rows that do not start on a sector: transposed, 32 neighbours of a row a store
 #pragma unroll
                     for (int c = 0; c < C::kMine / 32; ++c) {
-                        {
+                        if (stored(c)) {
                             float v[32];
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
@@ -459,14 +471,15 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
             const uint64_t keep = l2_evict_normal(), once = l2_evict_first();
             for (; ok && todo.next(w);) {
                 // weights that one tile of tokens reads, an expert's only
-                const uint64_t policy = experts.rows[w.e] <= (FEW ? kFp8Few : kFp8Many) ? once : keep;
-                // few: lane 0 the channels, then 64 or 16 tokens a lane; many: lane 0 the tokens, lane 1
-                // this CTA's half of the channels
-                const int big = FEW ? (int)w.n / 64 : 1, copies = 1 + big + (FEW ? (int)w.n % 64 / 16 : 0);
+                const uint64_t policy = experts.rows[w.e] <= (int)fp8_most(FEW) ? once : keep;
+                // few: lane 0 the channels, then 64 or 16 tokens a lane; many: lane 0 the tokens, then 128
+                // channels a lane
+                const int big = FEW ? (int)w.n / 64 : (int)(w.n + 127) / 128;
+                const int copies = 1 + big + (FEW ? (int)w.n % 64 / 16 : 0);
                 const bool whole = lane - 1 < big, channels = FEW == (lane == 0);
-                const int r = lane == 0 || !FEW ? 0 : whole ? 64 * (lane - 1) : 64 * big + 16 * (lane - 1 - big);
-                const int y = channels ? w.n0 + (int)(rank * (w.n / 2)) : w.m0 + r;
-                const uint32_t bytes = FEW ? C::kABytes + w.n * kFp8Step : 2 * C::kSlotBytes;
+                const int r = lane == 0 ? 0 : !FEW ? 128 * (lane - 1) : whole ? 64 * (lane - 1) : 64 * big + 16 * (lane - 1 - big);
+                const int y = r + (channels ? w.n0 : w.m0);
+                const uint32_t bytes = C::kABytes + (FEW ? w.n : 128u * big) * kFp8Step;
                 const uint32_t off = lane == 0 ? 0u : C::kABytes + (uint32_t)r * kFp8Step;
                 for (uint32_t k = w.k0; k < w.k1; ++k, ++it) {
                     const int slot = it % C::kSlots;
@@ -475,51 +488,44 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                         ok = fp8_wait(&empty[slot], (uint32_t)(it / C::kSlots - 1) & 1, q.wait_ns);
                         if (!ok) break;
                     }
-                    if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&full[slot], bytes);
+                    if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
                     __syncwarp();
                     if (q.drop && k == w.k0 + 1) continue;
-                    const uint32_t bar = FEW ? smem_u32(&full[slot]) : cluster_addr(&full[slot], 0);
                     unsigned char* const to = smem + slot * C::kSlotBytes + off;
                     const int x = (int)k * kFp8Step;
                     if (lane < copies) {
-                        if (channels) tma_load_3d<C::CG>(to, &wmap, x, y, w.e, bar, policy);
-                        else tma_load_3d<C::CG>(to, FEW && !whole ? &amap16 : &amap, x, y, 0, bar, keep);
+                        if (channels) tma_load_3d(to, &wmap, x, y, w.e, &full[slot], policy);
+                        else tma_load_2d(to, FEW && !whole ? &amap16 : &amap, x, y, &full[slot], keep);
                     }
                     __syncwarp();
                 }
             }
-            // Every copy has landed, and every arrival on these barriers come, before the shared memory
-            // goes. The pair's first CTA counts both CTAs' copies; where it gave up, the other
-            // leaves its copies the time to land.
+            // every copy has landed, and every arrival on these barriers come, before the shared memory goes
             for (int i = max(it - C::kSlots, 0); i < it; ++i)
                 if (((i % C::kSlots) & 1) == parity) {
-                    if (rank == 0) fp8_wait(&full[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
+                    fp8_wait(&full[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
                     ok = ok && fp8_wait(&empty[i % C::kSlots], (uint32_t)(i / C::kSlots) & 1, q.wait_ns);
                 }
-            if (!ok && rank != 0) {
-                const uint64_t t0 = global_ns();
-                while (global_ns() - t0 < 1000000ull) __nanosleep(1000);
-            }
         } else if (warp == C::kMulWarp) {
             // One thread: a vote after every wait and a choice of the thread for every step took
             // a third of a step
-            if (rank == 0 && elect_one()) {
+            if (elect_one()) {
                 const uint64_t a0 = umma_smem_desc(smem_u32(smem));
                 for (; ok && todo.next(w);) {
-                    const uint32_t idesc = umma_e4m3_desc<128 * C::CG>(w.n);
+                    const uint32_t idesc = umma_e4m3_desc<128>(w.n);
                     for (uint32_t k = w.k0; k < w.k1; ++k, ++it) {
                         const int slot = it % C::kSlots, a = it % C::kAccs;
                         ok = mbar_wait(&full[slot], (uint32_t)(it / C::kSlots) & 1, q.wait_ns);
-                        if (it >= C::kAccs) ok = ok && mbar_wait(&acc_empty[a], (uint32_t)(it / C::kAccs - 1) & 1, q.wait_ns);
+                        if (!FEW && it >= C::kAccs) ok = ok && mbar_wait(&acc_empty[a], (uint32_t)(it / C::kAccs - 1) & 1, q.wait_ns);
                         if (!ok) break;
                         tmem_fence_after();
                         // descriptors count addresses in units of 16 bytes
                         const uint64_t at = a0 + (uint32_t)slot * (C::kSlotBytes / 16), b = at + C::kABytes / 16;
 #pragma unroll
                         for (int j = 0; j < kFp8Step / 32; ++j)
-                            umma_e4m3<C::CG>(tmem + a * C::kColumns, at + 2 * j, b + 2 * j, idesc, j > 0);
-                        umma_commit<C::CG>(&acc_full[a]);
-                        umma_commit<C::CG>(&empty[slot]);
+                            umma_e4m3(tmem + a * C::kColumns, at + 2 * j, b + 2 * j, idesc, j > 0);
+                        umma_commit<1>(&acc_full[a]);
+                        if (!FEW) umma_commit<1>(&empty[slot]);
                     }
                 }
                 // its instructions have ended, and the readers' arrivals come, before the memory goes, also
@@ -592,10 +598,10 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
-    if (!FEW || q.split > 1) cluster_sync();  // nobody leaves while another CTA works with its memory
+    if (q.split > 1) cluster_sync();  // nobody leaves while another CTA works with its memory
     if (warp == C::kMulWarp) {
         tmem_fence_after();
-        tmem_dealloc<C::CG, C::kTmem>(tmem);
+        tmem_dealloc<1, C::kTmem>(tmem);
     }
 }
 

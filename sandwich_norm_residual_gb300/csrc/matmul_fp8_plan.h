@@ -16,12 +16,15 @@ namespace beam {
 constexpr int kFp8Step = 128;      // k of a step: the block that shares a scale
 constexpr int kFp8Block128 = 128;  // channels that share a scale
 constexpr int kFp8Few = 64;        // few tokens: tiles of 128 channels by up to 64 tokens
-constexpr int kFp8Many = 256;      // many: tiles of 256 tokens ...
+constexpr int kFp8Many = 128;      // many: tiles of 128 tokens
 constexpr int kFp8Width = 256;     // ... by up to 256 channels
 constexpr int kFp8Band = 8;        // tiles of tokens that a band of tiles is high
 constexpr int kFp8MaxSplit = 8;    // CTAs of a cluster at most
 
 BEAM_HOST_DEVICE constexpr uint32_t fp8_up(uint32_t v, uint32_t to) { return (v + to - 1) / to; }
+
+// tokens of a tile at most
+BEAM_HOST_DEVICE constexpr uint32_t fp8_most(bool few) { return few ? kFp8Few : kFp8Many; }
 
 // n rows of one expert in tiles: as many as needed; few tokens alike as far as the matrix
 // instruction's columns (multiples of 16) allow
@@ -30,7 +33,7 @@ struct Fp8Rows {
 };
 template <bool FEW>
 BEAM_HOST_DEVICE Fp8Rows fp8_rows(uint32_t n) {
-    const uint32_t tiles = fp8_up(n, FEW ? kFp8Few : kFp8Many);
+    const uint32_t tiles = fp8_up(n, fp8_most(FEW));
     if (!FEW) return Fp8Rows{tiles, kFp8Many};
     return Fp8Rows{tiles, tiles ? fp8_up(fp8_up(n, tiles), 16) * 16 : 0u};
 }
@@ -52,50 +55,57 @@ inline int64_t fp8_most_tiles(int64_t R, int experts, int most) {
     return (R - live) / most + live;
 }
 
+// Whether the plain cores do it: a single token, which may have up to 16 experts
+inline bool fp8_dot(int64_t R, int experts) { return R <= (experts == 1 ? 1 : 16); }
+
+// How many clusters of 1, 2, 4 and 8 CTAs (one an SM) the device holds at a time
+struct Fp8Room {
+    int clusters[4];
+};
+
 struct Fp8Plan {
     bool few;
     int width;      // channels of a tile
-    int split;      // CTAs of a cluster, which share the steps of some tiles (few tokens only)
-    int64_t tiles;  // at most
-    int clusters;   // (many tokens: pairs)
+    int split;      // CTAs of a cluster, which share the steps of the tiles behind the last full wave
+    int clusters;   // of the launch
+    double ns;
 };
 
-// How many clusters of 1, 2, 4 and 8 CTAs (one an SM) with few tokens and how many pairs the device holds at a time
-struct Fp8Room {
-    int clusters[4];
-    int pairs;
-};
+// What a step takes with all SMs at work, and a join
+constexpr double kFp8StepNs[2] = {470, 400}, kFp8JoinNs[2] = {3000, 1600};  // many, few tokens
 
-constexpr int kFp8JoinSteps = 4;  // what a join takes in steps
-
-// Few tokens' tiles up to 64 rows an expert on average, where the weights' way from memory
-// bounds the product; many tokens' beyond. Few tokens' tiles behind the last full wave
-// are shared by clusters where that ends sooner, counted in steps.
-inline Fp8Plan fp8_plan(int64_t R, int experts, int64_t N, int K, const Fp8Room& room) {
-    const int64_t live = R < experts ? R : experts;
-    Fp8Plan q{};
-    q.few = R <= live * kFp8Few;
-    q.width = q.few ? 128 : kFp8Width;
-    q.tiles = fp8_most_tiles(R, experts, q.few ? kFp8Few : kFp8Many) * ((N + q.width - 1) / q.width);
-    q.split = 1;
-    int64_t fit = q.few ? room.clusters[0] : room.pairs;
-    if (q.few) {
-        const int64_t steps = (K + kFp8Step - 1) / kFp8Step;
-        int64_t best = (q.tiles + fit - 1) / fit * steps;
-        for (int i = 1; i < 4; ++i) {
-            const int64_t split = 1 << i, clusters = room.clusters[i];
-            if (clusters < 1 || split > steps) break;
-            const int64_t waves = q.tiles / (clusters * split), rest = q.tiles - waves * clusters * split;
-            const int64_t cost = waves * steps + (rest + clusters - 1) / clusters * ((steps + split - 1) / split + kFp8JoinSteps);
-            if (cost < best) {
-                best = cost;
-                q.split = (int)split;
-                fit = clusters;
-            }
+// The split of tiles of one kind that ends first. Many tokens' shared tiles have one round at
+// most; with offsets on the device the number of tiles is only known within bounds, so there
+// clusters of two, which leave no SM out.
+inline Fp8Plan fp8_plan_of(bool few, int64_t R, int experts, int64_t N, int K, const Fp8Room& room) {
+    Fp8Plan best{};
+    best.few = few;
+    best.width = few ? 128 : kFp8Width;
+    const int64_t tiles = fp8_most_tiles(R, experts, (int)fp8_most(few)) * ((N + best.width - 1) / best.width);
+    const int64_t steps = (K + kFp8Step - 1) / kFp8Step;
+    for (int i = 0; i < 4; ++i) {
+        const int64_t split = 1 << i, clusters = tiles < room.clusters[i] ? tiles : room.clusters[i];
+        if (clusters < 1 || split > steps) continue;
+        const int64_t waves = tiles / (clusters * split), rest = tiles % (clusters * split);
+        if (i > 0 && !few && (rest > clusters || (experts > 1 && i > 1))) continue;
+        double ns = waves * steps * kFp8StepNs[few];
+        if (rest && i == 0) ns += steps * kFp8StepNs[few];
+        else if (rest) ns += (rest + clusters - 1) / clusters * ((steps + split - 1) / split * kFp8StepNs[few] + kFp8JoinNs[few]);
+        if (best.clusters == 0 || ns < best.ns) {
+            best.split = (int)split;
+            best.clusters = (int)clusters;
+            best.ns = ns;
         }
     }
-    q.clusters = (int)(q.tiles < fit ? q.tiles : fit);
-    return q;
+    return best;
+}
+
+// Few tokens' tiles or many tokens', whichever end first. Up to 32 rows always the first: a copy
+// of 128 rows of which the tensor has fewer than 32 takes twice as long (N = 20480, K = 5120, many
+// tokens' tiles: 52 us for 1 to 16 rows, 24 us for 32 to 64).
+inline Fp8Plan fp8_plan(int64_t R, int experts, int64_t N, int K, const Fp8Room& room) {
+    const Fp8Plan few = fp8_plan_of(true, R, experts, N, K, room), many = fp8_plan_of(false, R, experts, N, K, room);
+    return R <= 32 || few.ns <= 1.05 * many.ns ? few : many;
 }
 
 }  // namespace beam

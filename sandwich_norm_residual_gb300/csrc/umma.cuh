@@ -137,22 +137,16 @@ __device__ __forceinline__ void umma_f16(uint32_t d, uint32_t a, uint64_t b, uin
 }
 
 // kind::f8f6f4 on E4M3 operands, K-major both, FP32 accumulators: M rows of A by n (a
-// multiple of 16) rows of B, both in shared memory (CG = 2: half of either in each CTA)
+// multiple of 16) rows of B, both in shared memory
 template <uint32_t M>
 __device__ __forceinline__ uint32_t umma_e4m3_desc(uint32_t n) {
     return (1u << 4) | ((n >> 3) << 17) | ((M >> 4) << 24);
 }
-// D += A B^T over 32 k, or D = where add is 0; one thread (of the pair's first CTA)
-template <int CG>
+// D += A B^T over 32 k, or D = where add is 0; one thread
 __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-    if constexpr (CG == 1)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
 }
 
 // one arrival on `bar` (CG = 2: on that barrier of both CTAs) when every matrix
@@ -264,20 +258,12 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, i
         "[%0], [%1, {%2, %6, %6, %6, %3}], [%4], %5;"
         :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy), "r"(0) : "memory");
 }
-// A 3-D tile in slice z of the last dimension, its bytes counted on the barrier at the cluster
-// address `bar`: with CG = 2 it may be the other CTA's of the pair, else it is this CTA's
-template <int CG>
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar, uint64_t policy) {
-    if constexpr (CG == 1)
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-            "[%0], [%1, {%2, %3, %4}], [%5], %6;"
-            :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy) : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-            "[%0], [%1, {%2, %3, %4}], [%5], %6;"
-            :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy) : "memory");
+// the same for a 3-D tensor, in slice z of the last dimension
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3, %4}], [%5], %6;"
+        :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
