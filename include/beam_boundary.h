@@ -498,7 +498,7 @@ BEAM_API beam_status beam_swiglu_fp8(beam_stream_t stream, const uint16_t* gate_
  * infinite those that it scales (0 * inf).
  * flags: 0, or BEAM_OPT_TEST_WAIT_TIMEOUT, a test hook for the bounded waits: the copies of every
  * tile's second 128 k are never issued, the waits for them give up after 1 ms, out holds
- * anything and beam_sync_status returns BEAM_ERR_TIMEOUT.
+ * anything and beam_sync_status returns BEAM_ERR_TIMEOUT (needs K > 128).
  */
 BEAM_API beam_status beam_matmul_fp8(beam_stream_t stream, const uint8_t* a, const float* a_scale,
                                      const uint8_t* w, const float* w_scale, int64_t M, int N, int K,

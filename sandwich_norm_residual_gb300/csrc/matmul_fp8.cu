@@ -149,7 +149,9 @@ beam_status product(beam_stream_t stream, const uint8_t* a, const float* a_scale
         K > BEAM_MATMUL_MAX_K || E < 1 || E > BEAM_MOE_MAX_EXPERTS || (int64_t)N * K >= (int64_t(1) << 40) ||
         beam::fp8_most_tiles(R, E, beam::kFp8Few) * (((int64_t)N + 127) / 128) > 0x7FFFFFFF)
         return BEAM_ERR_SHAPE;
-    if ((out_type != BEAM_OUT_BF16 && out_type != BEAM_OUT_FP32) || (flags & ~BEAM_OPT_TEST_WAIT_TIMEOUT)) return BEAM_ERR_ARG;
+    if ((out_type != BEAM_OUT_BF16 && out_type != BEAM_OUT_FP32) || (flags & ~BEAM_OPT_TEST_WAIT_TIMEOUT) ||
+        ((flags & BEAM_OPT_TEST_WAIT_TIMEOUT) && K <= beam::kFp8Step))
+        return BEAM_ERR_ARG;
     if (R == 0 || N == 0) return BEAM_OK;
     if (!a || !a_scale || !w || !w_scale || !out || (grouped && !offsets)) return BEAM_ERR_NULL;
     const bool f32 = out_type == BEAM_OUT_FP32;

@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                     }
                     if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
                     __syncwarp();
-                    if (q.drop && k == w.k0 + 1) continue;
+                    if (q.drop && k == 1) continue;
                     unsigned char* const to = smem + slot * C::kSlotBytes + off;
                     const int x = (int)k * kFp8Step;
                     if (lane < copies) {

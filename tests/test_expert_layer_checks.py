@@ -71,6 +71,7 @@ def test_product_argument_errors(lib):
         assert call(**{rows: _lib.BEAM_MATMUL_FP8_MAX_ROWS}, N=1 << 14, K=16) == _lib.BEAM_ERR_SHAPE
         assert call(ty=2) == _lib.BEAM_ERR_ARG
         assert call(flags=_lib.BEAM_OPT_PDL) == _lib.BEAM_ERR_ARG
+        assert call(flags=_lib.BEAM_OPT_TEST_WAIT_TIMEOUT) == _lib.BEAM_ERR_ARG  # K = 64: no second 128
         assert call(**{rows: 0}, a=None) == _lib.BEAM_OK
         assert call(N=0, w=None) == _lib.BEAM_OK
         for name in ("a", "sa", "w", "sw", "o"):
