@@ -28,12 +28,12 @@ void split(int64_t pairs, SortParams* p) {
     p->blocks = (int)((pairs + p->chunk - 1) / p->chunk);
 }
 
-beam_status launch(const void* fn, int64_t blocks, int threads, size_t smem, void* p, cudaStream_t stream, bool pdl = false) {
+beam_status launch(const void* fn, dim3 blocks, int threads, size_t smem, void* p, cudaStream_t stream, bool pdl = false) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.gridDim = blocks;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -82,13 +82,20 @@ void share(RowsParams* p, int sms) {
 
 beam_status launch_rows(const void* fn, const RowsParams& p, cudaStream_t stream) {
     const int64_t warps = p.T * p.parts, each = beam::kRowThreads / 32, blocks = (warps + each - 1) / each;
-    return launch(fn, blocks, beam::kRowThreads, 0, const_cast<RowsParams*>(&p), stream);
+    return launch(fn, dim3((unsigned)blocks), beam::kRowThreads, 0, const_cast<RowsParams*>(&p), stream);
 }
 
 template <class V>
 const void* gather_kernel(bool scale16) {
     return scale16 ? reinterpret_cast<const void*>(beam::moe_gather_kernel<V, uint4>)
                    : reinterpret_cast<const void*>(beam::moe_gather_kernel<V, uint32_t>);
+}
+
+template <bool F32>
+const void* combine_kernel(int topk) {
+    return topk <= 2   ? reinterpret_cast<const void*>(beam::moe_combine_kernel<F32, 2>)
+           : topk <= 4 ? reinterpret_cast<const void*>(beam::moe_combine_kernel<F32, 4>)
+                       : reinterpret_cast<const void*>(beam::moe_combine_kernel<F32, 8>);
 }
 
 // the shared end of combine and gather's backward
@@ -114,16 +121,19 @@ beam_status combine(beam_stream_t stream, const void* rows, const int32_t* slots
     p.rows = rows;
     p.out = out;
     p.status = dev.status_word;
-    share(&p, dev.sms);
-    return launch_rows(type == BEAM_OUT_FP32 ? reinterpret_cast<const void*>(beam::moe_combine_kernel<true>)
-                                             : reinterpret_cast<const void*>(beam::moe_combine_kernel<false>),
-                       p, reinterpret_cast<cudaStream_t>(stream));
+    const int threads = p.vecs >= beam::kCombineThreads ? beam::kCombineThreads : (p.vecs + 31) / 32 * 32;
+    // fewer tokens than the device holds blocks: several share one
+    const int64_t room = (int64_t)dev.sms * 8, parts = T < room ? room / T : 1, most = (p.vecs + threads - 1) / threads;
+    return launch(type == BEAM_OUT_FP32 ? combine_kernel<true>(topk) : combine_kernel<false>(topk),
+                  dim3((unsigned)T, (unsigned)(parts < most ? parts : most)), threads, 0, &p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 template <bool F32>
 const void* backward_kernel(int topk) {
-    return topk <= 8 ? reinterpret_cast<const void*>(beam::moe_combine_backward_kernel<F32, 8>)
-                     : reinterpret_cast<const void*>(beam::moe_combine_backward_kernel<F32, 16>);
+    return topk <= 2   ? reinterpret_cast<const void*>(beam::moe_combine_backward_kernel<F32, 2>)
+           : topk <= 4 ? reinterpret_cast<const void*>(beam::moe_combine_backward_kernel<F32, 4>)
+           : topk <= 8 ? reinterpret_cast<const void*>(beam::moe_combine_backward_kernel<F32, 8>)
+                       : reinterpret_cast<const void*>(beam::moe_combine_backward_kernel<F32, 16>);
 }
 
 }  // namespace
@@ -237,8 +247,9 @@ beam_status beam_moe_combine_backward(beam_stream_t stream, const void* dx, cons
     p.drows = drows;
     p.dw = dw;
     p.status = dev.status_word;
-    return launch(type == BEAM_OUT_FP32 ? backward_kernel<true>(topk) : backward_kernel<false>(topk), T, beam::kBackThreads, 0,
-                  &p, reinterpret_cast<cudaStream_t>(stream));
+    const int threads = p.vecs >= beam::kBackThreads ? beam::kBackThreads : (p.vecs + 31) / 32 * 32;
+    return launch(type == BEAM_OUT_FP32 ? backward_kernel<true>(topk) : backward_kernel<false>(topk), dim3((unsigned)T), threads, 0, &p,
+                  reinterpret_cast<cudaStream_t>(stream));
 }
 
 beam_status beam_swiglu_fp8(beam_stream_t stream, const uint16_t* gate_up, const int32_t* live_rows, int64_t R, int F,
@@ -267,7 +278,7 @@ beam_status beam_swiglu_fp8(beam_stream_t stream, const uint16_t* gate_up, const
     const int64_t warps = R * p.chunks, each = beam::kSwigluThreads / 32, most = (int64_t)dev.sms * 8;
     int64_t grid = (warps + each - 1) / each;
     if (grid > most) grid = most;
-    return launch(reinterpret_cast<const void*>(beam::swiglu_fp8_kernel), grid, beam::kSwigluThreads, 0, &p,
+    return launch(reinterpret_cast<const void*>(beam::swiglu_fp8_kernel), dim3((unsigned)grid), beam::kSwigluThreads, 0, &p,
                   reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -259,64 +259,77 @@ struct Vec {
 };
 
 // x[t] = sum over k in order of w rows, one FP32 multiply-add each; a choice that is none adds
-// nothing. Up to eight rows are on their way at a time.
-template <bool F32>
-__global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const RowsParams p) {
+// nothing. A block has a token, or (few tokens) a share of its row; eight loads a thread are on their
+// way at a time, KB choices of 8 / KB vectors.
+// Eight loads do not cover HBM's latency with the 28 warps that an SM holds: L2 is asked for the
+// next pass's lines, one a lane (T = 16384, D = 5120, BF16, K = 8: 258 us without, 216 us; two
+// passes ahead 236 us). A warp for each token took 246 us.
+constexpr int kCombineThreads = 128;  // fewer where a row has fewer vectors
+
+template <bool F32, int KB>
+__global__ void __launch_bounds__(kCombineThreads, KB == 2 ? 5 : 7) moe_combine_kernel(const RowsParams p) {
     using X = Vec<F32>;
-    const int lane = threadIdx.x & 31;
-    long long t;
-    int lo, hi;
-    if (!row_share(p, &t, &lo, &hi)) return;
+    constexpr int VU = 8 / KB;
+    const int tid = threadIdx.x, lane = tid & 31, nt = blockDim.x;
+    const long long t = blockIdx.x;
+    const int each = (p.vecs + gridDim.y - 1) / gridDim.y, lo = min((int)blockIdx.y * each, p.vecs), hi = min(lo + each, p.vecs);
     const int slot = row_slot(p, t, lane);
     const float weight = lane < p.K ? (p.w ? __ldg(p.w + t * p.K + lane) : 1.0f) : 0.0f;
     const uint4* rows = static_cast<const uint4*>(p.rows);
-    // Eight loads a thread do not cover HBM's latency with the 28 warps that an SM holds: the lines
-    // of a few passes ahead are asked for, four of each of the first eight rows, one a lane.
-    const int ahead = __shfl_sync(0xFFFFFFFFu, slot, lane >> 2);
-    const uint4* const line = rows + (size_t)max(ahead, 0) * (size_t)p.vecs + 8 * (lane & 3);
-    auto ask = [&](int base) {
-        if (ahead >= 0 && base + 8 * (lane & 3) < hi) asm volatile("prefetch.global.L2 [%0];" :: "l"(line + base));
-    };
-    constexpr int kAhead = 4;
-    for (int i = 1; i < kAhead; ++i) ask(lo + 32 * i);
-    for (int base = lo; base < hi; base += 32) {
-        const int v = base + lane;
-        ask(base + 32 * kAhead);
-        float2 acc[X::kPairs];
+    // four lines of each of a pass's KB rows and VU places
+    const int ahead = __shfl_sync(0xFFFFFFFFu, slot, lane / (4 * VU));
+    const int line = nt * (VU + lane / 4 % VU) + 8 * (lane & 3);
+    const uint4* const ahead_row = rows + (size_t)max(ahead, 0) * (size_t)p.vecs;
+    for (int base = lo; base < hi; base += nt * VU) {
+        const int v = base + tid, asked = v - lane + line;
+        if (ahead >= 0 && asked < hi) asm volatile("prefetch.global.L2 [%0];" :: "l"(ahead_row + asked));
+        float2 acc[VU][X::kPairs];
 #pragma unroll
-        for (int i = 0; i < X::kPairs; ++i) acc[i] = make_float2(0.f, 0.f);
-        for (int k0 = 0; k0 < p.K; k0 += 8) {
-            uint4 r[8];
+        for (int j = 0; j < VU; ++j)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int i = 0; i < X::kPairs; ++i) acc[j][i] = make_float2(0.f, 0.f);
+        for (int k0 = 0; k0 < p.K; k0 += KB) {
+            uint4 r[KB][VU];
+#pragma unroll
+            for (int k = 0; k < KB; ++k) {
                 const int s = __shfl_sync(0xFFFFFFFFu, slot, k0 + k);
-                if (s >= 0 && v < hi) r[k] = ld_once(rows + (size_t)s * (size_t)p.vecs + v);
+                const uint4* row = rows + (size_t)max(s, 0) * (size_t)p.vecs + v;
+#pragma unroll
+                for (int j = 0; j < VU; ++j)
+                    if (s >= 0 && v + nt * j < hi) r[k][j] = ld_once(row + nt * j);
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < KB; ++k) {
                 const int s = __shfl_sync(0xFFFFFFFFu, slot, k0 + k);
                 const float w = __shfl_sync(0xFFFFFFFFu, weight, k0 + k);
-                if (s >= 0 && v < hi) {
-                    float2 f[X::kPairs];
-                    X::unpack(r[k], f);
 #pragma unroll
-                    for (int i = 0; i < X::kPairs; ++i) acc[i] = __ffma2_rn(make_float2(w, w), f[i], acc[i]);
-                }
+                for (int j = 0; j < VU; ++j)
+                    if (s >= 0 && v + nt * j < hi) {
+                        float2 f[X::kPairs];
+                        X::unpack(r[k][j], f);
+#pragma unroll
+                        for (int i = 0; i < X::kPairs; ++i) acc[j][i] = __ffma2_rn(make_float2(w, w), f[i], acc[j][i]);
+                    }
             }
         }
-        if (v < hi) static_cast<uint4*>(p.out)[(size_t)t * (size_t)p.vecs + v] = X::pack(acc);
+#pragma unroll
+        for (int j = 0; j < VU; ++j)
+            if (v + nt * j < hi) static_cast<uint4*>(p.out)[(size_t)t * (size_t)p.vecs + v + nt * j] = X::pack(acc[j]);
     }
 }
 
 // One block a token: drows = w dx, and the products of dx with the token's rows, added in FP32 by
-// thread, then over the warp, then over the warps.
-constexpr int kBackThreads = 128;
+// thread, then over the warp, then over the warps. Eight rows' loads a thread on their way (two for
+// each of 8, one for each of 16 choices), as above.
+// T = 16384, D = 5120, BF16, K = 8: 421 us (6773 GB/s).
+constexpr int kBackThreads = 128;  // fewer where a row has fewer vectors
 
 template <bool F32, int CHOICES>
 __global__ void __launch_bounds__(kBackThreads) moe_combine_backward_kernel(const RowsParams p) {
     using X = Vec<F32>;
+    constexpr int VU = CHOICES < 8 ? 8 / CHOICES : 1;
     __shared__ float part[kBackThreads / 32][CHOICES];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nt = blockDim.x;
     const long long t = blockIdx.x;
     const int slot = row_slot(p, t, lane);
     const float weight = lane < p.K ? __ldg(p.w + t * p.K + lane) : 0.0f;
@@ -326,33 +339,38 @@ __global__ void __launch_bounds__(kBackThreads) moe_combine_backward_kernel(cons
     float2 dot[CHOICES];
 #pragma unroll
     for (int k = 0; k < CHOICES; ++k) dot[k] = make_float2(0.f, 0.f);
-    for (int base = 0; base < p.vecs; base += kBackThreads) {
-        const int v = base + tid;
-        const bool in = v < p.vecs;
-        float2 d[X::kPairs];
-        uint4 r[CHOICES];
-        uint4 dv = make_uint4(0, 0, 0, 0);
-        if (in) dv = __ldg(dx + v);
+    for (int v = tid; v - tid < p.vecs; v += nt * VU) {
+        float2 d[VU][X::kPairs];
+        uint4 r[CHOICES][VU], dv[VU];
+#pragma unroll
+        for (int j = 0; j < VU; ++j) dv[j] = v + nt * j < p.vecs ? __ldg(dx + v + nt * j) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int k = 0; k < CHOICES; ++k) {
             const int s = __shfl_sync(0xFFFFFFFFu, slot, k);
-            if (s >= 0 && in) r[k] = ld_once(rows + (size_t)s * (size_t)p.vecs + v);
+            const uint4* row = rows + (size_t)max(s, 0) * (size_t)p.vecs + v;
+#pragma unroll
+            for (int j = 0; j < VU; ++j)
+                if (s >= 0 && v + nt * j < p.vecs) r[k][j] = ld_once(row + nt * j);
         }
-        X::unpack(dv, d);
+#pragma unroll
+        for (int j = 0; j < VU; ++j) X::unpack(dv[j], d[j]);
 #pragma unroll
         for (int k = 0; k < CHOICES; ++k) {
             const int s = __shfl_sync(0xFFFFFFFFu, slot, k);
             const float w = __shfl_sync(0xFFFFFFFFu, weight, k);
-            if (s >= 0 && in) {
-                float2 f[X::kPairs], o[X::kPairs];
-                X::unpack(r[k], f);
+            uint4* to = drows + (size_t)max(s, 0) * (size_t)p.vecs + v;
 #pragma unroll
-                for (int i = 0; i < X::kPairs; ++i) {
-                    dot[k] = __ffma2_rn(d[i], f[i], dot[k]);
-                    o[i] = mul2_rn(make_float2(w, w), d[i]);
+            for (int j = 0; j < VU; ++j)
+                if (s >= 0 && v + nt * j < p.vecs) {
+                    float2 f[X::kPairs], o[X::kPairs];
+                    X::unpack(r[k][j], f);
+#pragma unroll
+                    for (int i = 0; i < X::kPairs; ++i) {
+                        dot[k] = __ffma2_rn(d[j][i], f[i], dot[k]);
+                        o[i] = mul2_rn(make_float2(w, w), d[j][i]);
+                    }
+                    to[nt * j] = X::pack(o);
                 }
-                drows[(size_t)s * (size_t)p.vecs + v] = X::pack(o);
-            }
         }
     }
 #pragma unroll
@@ -365,7 +383,7 @@ __global__ void __launch_bounds__(kBackThreads) moe_combine_backward_kernel(cons
     __syncthreads();
     if (tid < p.K) {
         float v = part[0][tid];
-        for (int w = 1; w < kBackThreads / 32; ++w) v = __fadd_rn(v, part[w][tid]);
+        for (int w = 1; w < nt >> 5; ++w) v = __fadd_rn(v, part[w][tid]);
         p.dw[t * p.K + tid] = slot >= 0 ? v : 0.0f;
     }
 }

@@ -43,8 +43,11 @@ def test_single_token_products_keep_their_blocks(kernels, shape, blocks, f32):  
 
 
 @pytest.mark.parametrize("pattern,regs,spilled", [
-    ("moe_combine_kernel<false>", 64, 0), ("moe_combine_kernel<true>", 64, 64),
+    ("moe_combine_kernel<false, 8>", 72, 0), ("moe_combine_kernel<true, 8>", 72, 0),
+    ("moe_combine_kernel<false, 4>", 72, 0), ("moe_combine_kernel<true, 4>", 72, 0),
+    ("moe_combine_kernel<false, 2>", 102, 0), ("moe_combine_kernel<true, 2>", 102, 0),
     ("moe_combine_backward_kernel<false, 8>", 80, 0), ("moe_combine_backward_kernel<true, 8>", 80, 0),
+    ("moe_combine_backward_kernel<false, 2>", 96, 0), ("moe_combine_backward_kernel<true, 2>", 96, 0),
     ("moe_combine_backward_kernel<false, 16>", 128, 0), ("moe_combine_backward_kernel<true, 16>", 128, 0),
     ("moe_gather_kernel<uint4, uint4>", 40, 0), ("moe_gather_kernel<unsigned int, unsigned int>", 40, 0),
     ("moe_place_kernel", 64, 0), ("moe_count_kernel", 32, 0), ("swiglu_fp8_kernel", 32, 0)])
