@@ -112,13 +112,11 @@ beam_status room(const beam::Device& dev, Fp8Room* out) {
 
 template <bool FEW>
 beam_status launch(const Fp8Params& q, const beam::Fp8Plan& plan, const uint8_t* a, const uint8_t* w, int K, bool f32, cudaStream_t stream) {
-    CUtensorMap wmap, amap, amap16;
-    if (!tile_map(&wmap, w, 3, q.E, q.N, K, 128) || !tile_map(&amap, a, 2, 1, q.R, K, FEW ? 64 : 128)) return BEAM_ERR_CUDA;
-    if (!FEW) amap16 = amap;
-    else if (!tile_map(&amap16, a, 2, 1, q.R, K, 16)) return BEAM_ERR_CUDA;
+    CUtensorMap wmap, amap;
+    if (!tile_map(&wmap, w, 3, q.E, q.N, K, 128) || !tile_map(&amap, a, 2, 1, q.R, K, FEW ? 16 : 128)) return BEAM_ERR_CUDA;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config<FEW>(plan.clusters, plan.split, stream, &attr);
-    void* args[] = {&wmap, &amap, &amap16, const_cast<Fp8Params*>(&q)};
+    void* args[] = {&wmap, &amap, const_cast<Fp8Params*>(&q)};
     if (cudaLaunchKernelExC(&cfg, kernel<FEW>(f32), args) != cudaSuccess) {
         cudaGetLastError();
         return BEAM_ERR_CUDA;

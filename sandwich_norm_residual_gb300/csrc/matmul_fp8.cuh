@@ -56,7 +56,7 @@ struct Fp8Params {
 };
 
 // A CTA's tile. Few tokens: 128 channels and up to 64 tokens; many: 128 tokens and up to 256
-// channels.
+// channels, or up to 128.
 template <bool FEW>
 struct Fp8Tile {
     static constexpr int kColumns = FEW ? kFp8Few : kFp8Width;  // of an accumulator
@@ -201,7 +201,7 @@ __device__ __forceinline__ void transpose32(float (&r)[32], int lane) {
 template <bool FEW, bool F32>
 __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
     matmul_fp8_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
-                      const __grid_constant__ CUtensorMap amap16, const __grid_constant__ Fp8Params q) {
+                      const __grid_constant__ Fp8Params q) {
     using C = Fp8Tile<FEW>;
     extern __shared__ __align__(1024) unsigned char smem[];
     float4* const scales = reinterpret_cast<float4*>(smem + C::kScaleAt);
@@ -299,14 +299,14 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < C::kMine / 2; ++j) sums[j] = make_float2(0.f, 0.f);
             // this warp's columns: a share of the tokens, or of the tile's channels (within a block of 128)
-            const int mine = FEW ? (int)w.n / C::kGroups : C::kMine, c0 = group * mine;
+            const int mine = (int)(FEW ? w.n : q.width) / C::kGroups, c0 = group * mine;
             const bool some = FEW || c0 < (int)w.n;
             // scales come in groups of four steps, at multiples of four
             for (uint32_t g = w.k0 & ~3u; g < w.k1; g += 4) {
                 if (ok) ok = mbar_wait(&scale_full[sg], sturn & 1, q.wait_ns);
                 __syncwarp();
                 // many: this thread's token's in the four steps
-                const float4 own = FEW ? float4{} : scales[sg * C::kScaleRow + group * 128 + row];
+                const float4 own = FEW ? float4{} : scales[sg * C::kScaleRow + (c0 & 128) + row];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (g + j < w.k0 || g + j >= w.k1) continue;
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                         for (int c = 0; c < C::kMine / 16; ++c) {
                             // few: a second eight columns that are not there are columns of this
                             // accumulator that no tile stores
-                            if (!FEW || 16 * c < mine) {
+                            if (FEW ? 16 * c < mine : c < C::kMine / 32 || mine == C::kMine) {
                                 float v[16];
                                 tmem_ld16_wait(from + 16 * c, v);
 #pragma unroll
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < kPieces; ++j) {
                     const int d = owner(j);
-                    if ((!FEW || kPiece * j < mine) && d != (int)place) {
+                    if (kPiece * j < mine && d != (int)place) {
                         const uint32_t there = cluster_addr(place_of((int)place < d ? (int)place : (int)place - 1, j), d);
 #pragma unroll
                         for (int i = 0; i < kPiece / 4; ++i) {
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < kPieces; ++j)
-                    if ((!FEW || kPiece * j < mine) && owner(j) == (int)place)
+                    if (kPiece * j < mine && owner(j) == (int)place)
                         for (int from = 0; from < q.split - 1; ++from) {
                             const float4* at = reinterpret_cast<const float4*>(place_of(from, j));
 #pragma unroll
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                     if (row < w.cols) {
 #pragma unroll
                         for (int j = 0; j < C::kMine / kBatch; ++j) {
-                            if (kBatch * j < left && stored(kBatch * j / 32)) {
+                            if (kBatch * j < mine && kBatch * j < left && stored(kBatch * j / 32)) {
                                 uint32_t v[8];
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                     // rows that do not start on a sector: transposed, 32 neighbours of a row a store
 #pragma unroll
                     for (int c = 0; c < C::kMine / 32; ++c) {
-                        if (stored(c)) {
+                        if (32 * c < mine && stored(c)) {
                             float v[32];
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
@@ -466,20 +466,19 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
             if (lane == 0) {
                 tma_prefetch_map(&wmap);
                 tma_prefetch_map(&amap);
-                if (FEW) tma_prefetch_map(&amap16);
             }
             const uint64_t keep = l2_evict_normal(), once = l2_evict_first();
             for (; ok && todo.next(w);) {
                 // weights that one tile of tokens reads, an expert's only
                 const uint64_t policy = experts.rows[w.e] <= (int)fp8_most(FEW) ? once : keep;
-                // few: lane 0 the channels, then 64 or 16 tokens a lane; many: lane 0 the tokens, then 128
+                // few: lane 0 the channels, then 16 tokens a lane; many: lane 0 the tokens, then 128
                 // channels a lane
-                const int big = FEW ? (int)w.n / 64 : (int)(w.n + 127) / 128;
-                const int copies = 1 + big + (FEW ? (int)w.n % 64 / 16 : 0);
-                const bool whole = lane - 1 < big, channels = FEW == (lane == 0);
-                const int r = lane == 0 ? 0 : !FEW ? 128 * (lane - 1) : whole ? 64 * (lane - 1) : 64 * big + 16 * (lane - 1 - big);
+                constexpr int kBox = FEW ? 16 : 128;
+                const int copies = 1 + (int)(w.n + kBox - 1) / kBox;
+                const bool channels = FEW == (lane == 0);
+                const int r = lane == 0 ? 0 : kBox * (lane - 1);
                 const int y = r + (channels ? w.n0 : w.m0);
-                const uint32_t bytes = C::kABytes + (FEW ? w.n : 128u * big) * kFp8Step;
+                const uint32_t bytes = C::kABytes + (uint32_t)((copies - 1) * kBox * kFp8Step);
                 const uint32_t off = lane == 0 ? 0u : C::kABytes + (uint32_t)r * kFp8Step;
                 for (uint32_t k = w.k0; k < w.k1; ++k, ++it) {
                     const int slot = it % C::kSlots;
@@ -495,7 +494,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                     const int x = (int)k * kFp8Step;
                     if (lane < copies) {
                         if (channels) tma_load_3d(to, &wmap, x, y, w.e, &full[slot], policy);
-                        else tma_load_2d(to, FEW && !whole ? &amap16 : &amap, x, y, &full[slot], keep);
+                        else tma_load_2d(to, &amap, x, y, &full[slot], keep);
                     }
                     __syncwarp();
                 }

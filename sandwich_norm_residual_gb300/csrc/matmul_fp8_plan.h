@@ -71,26 +71,34 @@ struct Fp8Plan {
     double ns;
 };
 
-// What a step takes with all SMs at work, and a join
-constexpr double kFp8StepNs[2] = {470, 400}, kFp8JoinNs[2] = {3000, 1600};  // many, few tokens
+// What a step takes with all SMs at work, and a join, in ns: few tokens' tiles, many tokens' with 128
+// and with 256 channels. Measured at M = 64, N = 19456, K = 10240 and M = 16384, N = 20480, K = 5120 (a
+// step: 0.36 us and 1913 us / 5390, 1326 us / 2695); the joins and the choice were held against all
+// three kinds forced at 16 sizes from M = 128, N = K = 5120 to 4096 tokens to 8 of 256 experts:
+// the choice is within 3% of the best at 14 of them (M = N = 1000, K = 2000: 15.0 us where few tokens'
+// tiles take 12.9; M = 128, N = K = 5120: 16.0 and 15.3).
+struct Fp8Cost {
+    double step, join;
+};
+constexpr Fp8Cost kFp8FewCost{400, 1600}, kFp8NarrowCost{350, 2000}, kFp8WideCost{470, 3000};
 
 // The split of tiles of one kind that ends first. Many tokens' shared tiles have one round at
 // most; with offsets on the device the number of tiles is only known within bounds, so there
 // clusters of two, which leave no SM out.
-inline Fp8Plan fp8_plan_of(bool few, int64_t R, int experts, int64_t N, int K, const Fp8Room& room) {
+inline Fp8Plan fp8_plan_of(bool few, int width, const Fp8Cost& cost, int64_t R, int experts, int64_t N, int K, const Fp8Room& room) {
     Fp8Plan best{};
     best.few = few;
-    best.width = few ? 128 : kFp8Width;
-    const int64_t tiles = fp8_most_tiles(R, experts, (int)fp8_most(few)) * ((N + best.width - 1) / best.width);
+    best.width = width;
+    const int64_t tiles = fp8_most_tiles(R, experts, (int)fp8_most(few)) * ((N + width - 1) / width);
     const int64_t steps = (K + kFp8Step - 1) / kFp8Step;
     for (int i = 0; i < 4; ++i) {
         const int64_t split = 1 << i, clusters = tiles < room.clusters[i] ? tiles : room.clusters[i];
         if (clusters < 1 || split > steps) continue;
         const int64_t waves = tiles / (clusters * split), rest = tiles % (clusters * split);
         if (i > 0 && !few && (rest > clusters || (experts > 1 && i > 1))) continue;
-        double ns = waves * steps * kFp8StepNs[few];
-        if (rest && i == 0) ns += steps * kFp8StepNs[few];
-        else if (rest) ns += (rest + clusters - 1) / clusters * ((steps + split - 1) / split * kFp8StepNs[few] + kFp8JoinNs[few]);
+        double ns = waves * steps * cost.step;
+        if (rest && i == 0) ns += steps * cost.step;
+        else if (rest) ns += (rest + clusters - 1) / clusters * ((steps + split - 1) / split * cost.step + cost.join);
         if (best.clusters == 0 || ns < best.ns) {
             best.split = (int)split;
             best.clusters = (int)clusters;
@@ -104,7 +112,10 @@ inline Fp8Plan fp8_plan_of(bool few, int64_t R, int experts, int64_t N, int K, c
 // of 128 rows of which the tensor has fewer than 32 takes twice as long (N = 20480, K = 5120, many
 // tokens' tiles: 52 us for 1 to 16 rows, 24 us for 32 to 64).
 inline Fp8Plan fp8_plan(int64_t R, int experts, int64_t N, int K, const Fp8Room& room) {
-    const Fp8Plan few = fp8_plan_of(true, R, experts, N, K, room), many = fp8_plan_of(false, R, experts, N, K, room);
+    const Fp8Plan few = fp8_plan_of(true, 128, kFp8FewCost, R, experts, N, K, room);
+    const Fp8Plan narrow = fp8_plan_of(false, 128, kFp8NarrowCost, R, experts, N, K, room);
+    const Fp8Plan wide = fp8_plan_of(false, kFp8Width, kFp8WideCost, R, experts, N, K, room);
+    const Fp8Plan& many = narrow.ns < wide.ns ? narrow : wide;
     return R <= 32 || few.ns <= 1.05 * many.ns ? few : many;
 }
 

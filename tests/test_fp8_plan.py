@@ -80,12 +80,12 @@ def test_plans_fit_the_device_and_take_every_step(lib, room):
         index = {1: 0, 2: 1, 4: 2, 8: 3}[q["split"]]
         assert 1 <= q["clusters"] <= room[index]
         assert q["split"] <= -(-K // 128)  # a share has a step at least
-        assert q["width"] == (128 if q["few"] else 256)
+        assert q["width"] == 128 or (q["width"] == 256 and not q["few"])
         if R <= 32:
             assert q["few"]
         if not q["few"] and q["split"] > 1 and E == 1:
             # many tokens' shared tiles have one round at most
-            tiles = -(-R // 128) * -(-N // 256)
+            tiles = -(-R // 128) * -(-N // q["width"])
             assert tiles % (q["clusters"] * q["split"]) <= q["clusters"]
 
 
