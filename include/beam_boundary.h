@@ -512,8 +512,8 @@ BEAM_API beam_status beam_matmul_fp8(beam_stream_t stream, const uint8_t* a, con
  *           the device. Rows of no expert (before the first, behind the last) are not read
  *           for a result, whatever they hold, and out keeps there what it held.
  *   w [E, N, K] E4M3; w_scale [E, ceil(N / 128), ceil(K / 128)]; E in [1, BEAM_MOE_MAX_EXPERTS]
- * Offsets that decrease or leave [0, R] make out unspecified (no address outside the operands
- * is touched); beam_sync_status then returns BEAM_ERR_ARG.
+ * Where an offset decreases or leaves [0, R] no row has an expert: out keeps what it held, and
+ * beam_sync_status returns BEAM_ERR_ARG.
  */
 BEAM_API beam_status beam_matmul_fp8_experts(beam_stream_t stream, const uint8_t* a, const float* a_scale,
                                              const int32_t* offsets, const uint8_t* w,

@@ -28,7 +28,8 @@ __all__ = ["boundary_fused", "moe_combine_boundary", "boundary_fused_host",
            "moe_combine_boundary_nvfp4", "boundary_fused_int8", "moe_combine_boundary_int8",
            "boundary_fused_fp8", "moe_combine_boundary_fp8",
            "matmul_int8", "matmul_fp8", "matmul_fp8_experts", "swiglu_fp8",
-           "moe_sort", "moe_gather", "moe_gather_backward", "moe_combine", "moe_combine_backward", "moe_route", "moe_balance_loss", "moe_balance_loss_backward",
+           "moe_sort", "moe_gather", "moe_gather_backward", "moe_combine", "moe_combine_backward",
+           "moe_route", "moe_balance_loss", "moe_balance_loss_backward",
            "router_sigmoid", "qk_norm", "sync_status",
            "exact_sum_count",
            "version", "BeamError", "LaunchOpts", "library"]

@@ -49,7 +49,7 @@ struct DeviceInfo {
     int sms = 0;
     long long l2_bytes = 0;
     int smem_optin = 0;                       // max dynamic + static shared memory per CTA
-    KernelFn lim_fn[128] = {};                 // kernels whose dynamic smem limit was raised
+    KernelFn lim_fn[128] = {};                // kernels whose dynamic smem limit was raised
     int lim_val[128] = {};
     int lim_n = 0;
     OccKey occ_key[128] = {};

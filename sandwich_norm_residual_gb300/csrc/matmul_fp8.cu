@@ -8,6 +8,8 @@
 #include "device.h"
 #include "host.h"
 
+static_assert(BEAM_MOE_MAX_EXPERTS <= beam::kFp8MaxExperts, "the table of experts");
+
 namespace {
 
 using beam::Fp8Params;

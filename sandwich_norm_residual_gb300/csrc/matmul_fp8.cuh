@@ -158,9 +158,8 @@ public:
 };
 
 // all lanes: whether every lane's wait ended
-template <int CG = 1>
 __device__ __forceinline__ bool fp8_wait(uint64_t* bar, uint32_t parity, uint64_t ns) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait<CG>(bar, parity, ns));
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, ns));
 }
 
 template <int REGS>
@@ -238,22 +237,24 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
         mbar_fence_init();
     }
     if (warp == C::kMulWarp) tmem_alloc<1, C::kTmem>(tmem_slot);
-    // Experts' rows. Offsets that decrease or leave [0, R] are held within: what they
-    // make of out is not said, but nothing outside of it is touched.
+    // Experts' rows. Where an offset decreases or leaves [0, R] nobody has any: rows counted twice
+    // could be more tiles than 32 bits number.
     bool bad = false;
     for (int e = tid; e < q.E; e += C::kThreads) {
         long long lo = 0, hi = q.R;
         if (q.offsets) {
-            const long long a = __ldg(q.offsets + e), b = __ldg(q.offsets + e + 1);
-            lo = min(max(a, 0ll), q.R);
-            hi = min(max(b, lo), q.R);
-            bad |= lo != a || hi != b;
+            lo = __ldg(q.offsets + e);
+            hi = __ldg(q.offsets + e + 1);
+            bad |= lo < 0 || hi < lo || hi > q.R;
         }
         experts.row[e] = (int32_t)lo;
         experts.rows[e] = (int32_t)(hi - lo);
     }
     if (bad && blockIdx.x == 0) atomicOr(q.status, 2u);
-    __syncthreads();
+    if (__syncthreads_or(bad)) {
+        for (int e = tid; e < q.E; e += C::kThreads) experts.rows[e] = 0;
+        __syncthreads();
+    }
     if (warp == 0) {
         constexpr int kEach = kFp8MaxExperts / 32;
         uint32_t sum = 0;

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(32 * kFp8DotWarps, BLOCKS) matmul_fp8_dot_kern
     int e = 0;
     long long lo = 0, hi = q.R;
     if (q.offsets) {
-        // blocks [., y] have the y-th expert that has rows; offsets are held within [0, R]
+        // blocks [., y] have the y-th expert that has rows; nobody where an offset decreases or leaves [0, R]
         int left = blockIdx.y;
         bool bad = false;
         e = -1;
@@ -62,10 +62,9 @@ __global__ void __launch_bounds__(32 * kFp8DotWarps, BLOCKS) matmul_fp8_dot_kern
             const int i = base + lane;
             long long b = 0, c = 0;
             if (i < q.E) {
-                const long long x = __ldg(q.offsets + i), y = __ldg(q.offsets + i + 1);
-                b = min(max(x, 0ll), q.R);
-                c = min(max(y, b), q.R);
-                bad |= b != x || c != y;
+                b = __ldg(q.offsets + i);
+                c = __ldg(q.offsets + i + 1);
+                bad |= b < 0 || c < b || c > q.R;
             }
             const unsigned some = __ballot_sync(0xFFFFFFFFu, c > b);
             const int n = __popc(some);
@@ -78,7 +77,7 @@ __global__ void __launch_bounds__(32 * kFp8DotWarps, BLOCKS) matmul_fp8_dot_kern
             left -= n;
         }
         if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(q.status, 2u);
-        if (e < 0) return;
+        if (__any_sync(0xFFFFFFFFu, bad) || e < 0) return;
     }
     if (n0 >= q.N) return;
     const uint8_t* wr[CH];

@@ -9,6 +9,10 @@
 #include "device.h"
 #include "host.h"
 
+static_assert(BEAM_MOE_MAX_EXPERTS <= beam::kSortMaxExperts && beam::kSortMaxExperts <= beam::kSortThreads &&
+                  BEAM_ROUTE_MAX_TOPK <= 16,
+              "an expert a thread, the choices of a token in half a warp");
+
 namespace {
 
 using beam::misaligned;

@@ -147,7 +147,6 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const SortParam
 // ---------------------------------------------------------------- rows
 
 constexpr int kRowThreads = 256;
-constexpr int kMaxChoices = 16;
 
 struct RowsParams {
     const int32_t* slots;  // [T, K]

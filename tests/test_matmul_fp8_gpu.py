@@ -238,18 +238,18 @@ def test_a_dense_product_is_one_expert():
 
 
 @pytest.mark.parametrize("R", [10, 40, 500])
-def test_bad_offsets_are_reported_and_touch_nothing_outside(R):
+def test_bad_offsets_are_reported_and_touch_nothing(R):
     N, K, E = 150, 256, 4
     a, sa, w, sw = inputs(R, N, K, 1, E)
     buf = torch.full((R + 200, N), 5.0, device="cuda")
     for off in ([0, R + 50, R + 90, R + 100, R + 150], [-5, 2, 1, R, R], [5, 3, 2, 1, 0], [2 ** 31 - 1] * 5,
-                [-2 ** 31] * 5, [0, 2, 2 ** 31 - 1, -2 ** 31, R]):
+                [-2 ** 31] * 5, [0, 2, 2 ** 31 - 1, -2 ** 31, R], [0, R, 0, R, R]):
         out = buf[100:100 + R]
         snr.matmul_fp8_experts(a, sa, torch.tensor(off, dtype=torch.int32, device="cuda"), w, sw, out=out)
         with pytest.raises(snr.BeamError) as e:
             snr.sync_status()
         assert e.value.status == _lib.BEAM_ERR_ARG
-        assert (buf[:100] == 5).all() and (buf[100 + R:] == 5).all()
+        assert (buf == 5).all()
     # and the next call is whole
     check_experts([3, 0, R - 3], N, K)
 
