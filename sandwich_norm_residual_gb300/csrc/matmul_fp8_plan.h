@@ -71,16 +71,19 @@ struct Fp8Plan {
     double ns;
 };
 
-// What a step takes with all SMs at work, and a join, in ns: few tokens' tiles, many tokens' with 128
-// and with 256 channels. Measured at M = 64, N = 19456, K = 10240 and M = 16384, N = 20480, K = 5120 (a
-// step: 0.36 us and 1913 us / 5390, 1326 us / 2695); the joins and the choice were held against all
-// three kinds forced at 16 sizes from M = 128, N = K = 5120 to 4096 tokens to 8 of 256 experts:
-// the choice is within 3% of the best at 14 of them (M = N = 1000, K = 2000: 15.0 us where few tokens'
-// tiles take 12.9; M = 128, N = K = 5120: 16.0 and 15.3).
+// What tiles of a kind take, in ns: a step that waits for nothing but its own chain of loads,
+// products and additions; a step with all SMs at work, which share the way to memory (in
+// proportion for fewer); sharing a tile in a cluster: its launch, the sums' way, the wait for the
+// last CTA. Fitted to all kinds and splits at 319 sizes (M from 2 to 3000, N from 640 to 20480, K
+// from 256 to 20480, operands not in L2): the choice takes 0.9% more than the best on average, 14% at
+// most but for one size, and over 5% at 19; a step without the first part, joins of 1600 to
+// 3000 ns, 11% on average and up to 62%. M = 64, N = 6144, K = 1280: 11.3 -> 8.3 us; M = 128, N =
+// 2565, K = 5120: 19.7 -> 13.4; M = 517, N = 640, K = 5120: 18.6 -> 12.9.
 struct Fp8Cost {
-    double step, join;
+    double alone, all, join;
+    double step(int64_t ctas, int sms) const { return all * ctas > alone * sms ? all * ctas / sms : alone; }
 };
-constexpr Fp8Cost kFp8FewCost{400, 1600}, kFp8NarrowCost{350, 2000}, kFp8WideCost{470, 3000};
+constexpr Fp8Cost kFp8FewCost{200, 420, 3500}, kFp8NarrowCost{260, 350, 3500}, kFp8WideCost{380, 420, 5000};
 
 // The split of tiles of one kind that ends first. Many tokens' shared tiles have one round at
 // most; with offsets on the device the number of tiles is only known within bounds, so there
@@ -94,11 +97,12 @@ inline Fp8Plan fp8_plan_of(bool few, int width, const Fp8Cost& cost, int64_t R, 
     for (int i = 0; i < 4; ++i) {
         const int64_t split = 1 << i, clusters = tiles < room.clusters[i] ? tiles : room.clusters[i];
         if (clusters < 1 || split > steps) continue;
-        const int64_t waves = tiles / (clusters * split), rest = tiles % (clusters * split);
+        const int64_t ctas = clusters * split, waves = tiles / ctas, rest = tiles % ctas;
         if (i > 0 && !few && (rest > clusters || (experts > 1 && i > 1))) continue;
-        double ns = waves * steps * cost.step;
-        if (rest && i == 0) ns += steps * cost.step;
-        else if (rest) ns += (rest + clusters - 1) / clusters * ((steps + split - 1) / split * cost.step + cost.join);
+        const double step = cost.step(ctas, room.clusters[0]);
+        double ns = waves * steps * step;
+        if (rest && i == 0) ns += steps * step;
+        else if (rest) ns += (rest + clusters - 1) / clusters * ((steps + split - 1) / split * step + cost.join);
         if (best.clusters == 0 || ns < best.ns) {
             best.split = (int)split;
             best.clusters = (int)clusters;
@@ -116,7 +120,7 @@ inline Fp8Plan fp8_plan(int64_t R, int experts, int64_t N, int K, const Fp8Room&
     const Fp8Plan narrow = fp8_plan_of(false, 128, kFp8NarrowCost, R, experts, N, K, room);
     const Fp8Plan wide = fp8_plan_of(false, kFp8Width, kFp8WideCost, R, experts, N, K, room);
     const Fp8Plan& many = narrow.ns < wide.ns ? narrow : wide;
-    return R <= 32 || few.ns <= 1.05 * many.ns ? few : many;
+    return R <= 32 || few.ns <= many.ns ? few : many;
 }
 
 }  // namespace beam
