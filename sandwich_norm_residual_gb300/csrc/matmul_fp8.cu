@@ -1,6 +1,6 @@
 // Host side of the 8-bit floating-point product: argument checks (before any CUDA
 // call), the choice of the kernel and the launch.
-#include "matmul_fp8_dot.cuh"
+#include "matmul_fp8_small.cuh"
 
 #include <atomic>
 
@@ -126,16 +126,15 @@ beam_status launch(const Fp8Params& q, const beam::Fp8Plan& plan, const uint8_t*
     return BEAM_OK;
 }
 
-// A warp takes two channels, and four where there are enough of them: N = 6144, 8.3 and 9.6 us; N =
-// 20480, 22.0 and 21.4; eight experts of 5120, 45 and 41.
-template <int CH, int BLOCKS>
-beam_status launch_dot(const beam::Fp8DotParams& p, bool f32, int groups, cudaStream_t stream) {
-    const void* fn = f32 ? reinterpret_cast<const void*>(beam::matmul_fp8_dot_kernel<CH, BLOCKS, true>)
-                         : reinterpret_cast<const void*>(beam::matmul_fp8_dot_kernel<CH, BLOCKS, false>);
-    const int64_t per_block = CH * beam::kFp8DotWarps;
-    void* args[] = {const_cast<beam::Fp8DotParams*>(&p)};
-    if (cudaLaunchKernel(fn, dim3((unsigned)((p.q.N + per_block - 1) / per_block), (unsigned)groups), dim3(32 * beam::kFp8DotWarps),
-                         args, 0, stream) != cudaSuccess) {
+// Eight warps share a block's k, and four where there are channels enough for 13 blocks on every SM
+// (N = 20480, 8 and 4 warps: 21.4 and 21.9 us; N = 40960: 38.6 and 36.2; sixteen experts of N = 5120:
+// 84 and 74)
+template <int WARPS, int BLOCKS>
+beam_status launch_small(const beam::Fp8SmallParams& p, bool f32, dim3 grid, cudaStream_t stream) {
+    const void* fn = f32 ? reinterpret_cast<const void*>(beam::matmul_fp8_small_kernel<WARPS, BLOCKS, true>)
+                         : reinterpret_cast<const void*>(beam::matmul_fp8_small_kernel<WARPS, BLOCKS, false>);
+    void* args[] = {const_cast<beam::Fp8SmallParams*>(&p)};
+    if (cudaLaunchKernel(fn, grid, dim3(32 * WARPS), args, 0, stream) != cudaSuccess) {
         cudaGetLastError();
         return BEAM_ERR_CUDA;
     }
@@ -172,8 +171,8 @@ beam_status product(beam_stream_t stream, const uint8_t* a, const float* a_scale
     if (st != BEAM_OK) return st;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const bool drop = (flags & BEAM_OPT_TEST_WAIT_TIMEOUT) != 0;
-    if (!drop && beam::fp8_dot(R, E)) {
-        beam::Fp8DotParams p{a, w, {}, K};
+    if (!drop && beam::fp8_small(R, E)) {
+        beam::Fp8SmallParams p{a, w, {}, K};
         p.q.a_scale = a_scale;
         p.q.w_scale = w_scale;
         p.q.out = out;
@@ -183,8 +182,9 @@ beam_status product(beam_stream_t stream, const uint8_t* a, const float* a_scale
         p.q.N = N;
         p.q.steps = (uint32_t)steps;
         p.q.status = dev.status_word;
-        const int groups = (int)(R < E ? R : E);
-        return (int64_t)N * groups >= 16384 ? launch_dot<4, 3>(p, f32, groups, cs) : launch_dot<2, 4>(p, f32, groups, cs);
+        const int64_t groups = R < E ? R : E, blocks = ((int64_t)N + beam::kFp8SmallChannels - 1) / beam::kFp8SmallChannels;
+        const dim3 grid((unsigned)blocks, (unsigned)groups);
+        return blocks * groups >= 13 * (int64_t)dev.sms ? launch_small<4, 6>(p, f32, grid, cs) : launch_small<8, 3>(p, f32, grid, cs);
     }
     Fp8Room fits;
     st = room(dev, &fits);

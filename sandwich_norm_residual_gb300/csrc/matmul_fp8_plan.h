@@ -55,8 +55,11 @@ inline int64_t fp8_most_tiles(int64_t R, int experts, int most) {
     return (R - live) / most + live;
 }
 
-// Whether the plain cores do it: a single token, which may have up to 16 experts
-inline bool fp8_dot(int64_t R, int experts) { return R <= (experts == 1 ? 1 : 16); }
+// Whether rows go straight to registers, 8 tokens at a time: up to 8 tokens, and up to 32 rows of
+// experts, which seldom have more than 8 of them each (K = 5120: M = 9, N = 6144, twice through the
+// weights, 13.5 us and 14.6 in tiles, but M = 16, N = 20480 37 and 28.5; 32 rows of 31 experts with N
+// = 5120 128 us either way, 64 of 57 experts 225 and 214; 24 of 8 experts 35 and 49)
+inline bool fp8_small(int64_t R, int experts) { return R <= (experts == 1 ? 8 : 32); }
 
 // How many clusters of 1, 2, 4 and 8 CTAs (one an SM) the device holds at a time
 struct Fp8Room {

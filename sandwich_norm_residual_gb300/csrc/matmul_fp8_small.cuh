@@ -1,0 +1,145 @@
+// The product of matmul_fp8.cuh for up to 8 tokens at a time: warp matrix instructions on rows of
+// channels that go from memory straight to registers.
+//
+// It is the weights' way from HBM that counts, and the time until it is in full flow: no tensor
+// maps, no ring, no tensor memory to set up. A block has 16 channels and up to 8 tokens; its
+// warps take the blocks of 128 k in turn, two of each warp's on their way, and add up at the
+// end, in the order of the warps. The instruction wants 4 neighbours of k in a register; which k they
+// are is free as long as channels and tokens agree, so a lane loads 16 neighbours of a row and uses
+// them in two instructions.
+//   P_b = four instructions' sum from 0, times RN(a_scale w_scale), added to the warp's sum
+// M = 1 to 8, K = 5120: N = 6144 8.7 us and N = 20480 21 to 22 us (4.8 TB/s), where the tiles of 128
+// channels take 14.9 and 28; M = 5, N = 2560, K = 1280: 3.5 and 7.9 us. Plain FP32 multiply-adds of
+// a single token took 9.8 and 22.7 us: turning codes into FP32 takes as long as their way. What is left
+// over the floor is the way in and out of blocks that live 5 to 10 us; asking L2 ahead made it
+// slower by a tenth, a third block of k on its way no faster.
+#pragma once
+
+#include "matmul_fp8.cuh"
+
+namespace beam {
+
+constexpr int kFp8SmallChannels = 16, kFp8SmallTokens = 8;
+
+// c += 16 channels by 8 tokens over 32 k, E4M3 with FP32 sums. Lane l: channels l / 4 (a0, a2)
+// and l / 4 + 8 (a1, a3), token l / 4; c: channels l / 4 and l / 4 + 8 by tokens 2 (l % 4) and the next
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 ld_fp8_weights(const uint8_t* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p), "l"(l2_evict_first()));
+    return r;
+}
+
+struct Fp8SmallParams {
+    const uint8_t* a;
+    const uint8_t* w;
+    Fp8Params q;
+    int K;
+};
+
+template <int WARPS, int BLOCKS, bool F32>
+__global__ void __launch_bounds__(32 * WARPS, BLOCKS) matmul_fp8_small_kernel(const __grid_constant__ Fp8SmallParams p) {
+    constexpr int U = 2;
+    __shared__ float part[WARPS][kFp8SmallTokens][kFp8SmallChannels];
+    const Fp8Params& q = p.q;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int n0 = (int)blockIdx.x * kFp8SmallChannels;
+    int e = 0, lo = 0, hi = (int)q.R;  // few rows: fp8_small
+    if (q.offsets) {
+        // blocks [., y] have the y-th expert that has rows; nobody where an offset decreases or leaves [0, R]
+        int left = blockIdx.y;
+        bool bad = false;
+        e = -1;
+        for (int base = 0; base < q.E; base += 32) {
+            const int i = base + lane;
+            int b = 0, c = 0;
+            if (i < q.E) {
+                b = __ldg(q.offsets + i);
+                c = __ldg(q.offsets + i + 1);
+                bad |= b < 0 || c < b || c > q.R;
+            }
+            const unsigned some = __ballot_sync(0xFFFFFFFFu, c > b);
+            const int n = __popc(some);
+            if (e < 0 && left < n) {
+                const int at = __fns(some, 0, left + 1);
+                e = base + at;
+                lo = __shfl_sync(0xFFFFFFFFu, b, at);
+                hi = __shfl_sync(0xFFFFFFFFu, c, at);
+            }
+            left -= n;
+        }
+        if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(q.status, 2u);
+        if (__any_sync(0xFFFFFFFFu, bad) || e < 0) return;  // every warp alike
+    }
+    const int c0 = min(n0 + g, q.N - 1), c1 = min(n0 + g + 8, q.N - 1);  // channels behind the last are not stored
+    const uint8_t* const w0 = p.w + ((size_t)e * (size_t)q.N + (size_t)c0) * (size_t)p.K;
+    const uint32_t w1 = (uint32_t)(c1 - c0) * (uint32_t)p.K;
+    const float* const ws = q.w_scale + ((size_t)e * fp8_up((uint32_t)q.N, kFp8Block128) + (size_t)(n0 / kFp8Block128)) * q.steps;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const int steps = (int)q.steps;
+    for (int m = lo; m < hi; m += kFp8SmallTokens) {
+        const int cols = min(kFp8SmallTokens, hi - m);
+        const uint8_t* const ar = p.a + (size_t)(m + g) * (size_t)p.K;  // read for g < cols
+        const float* const as = q.a_scale + (size_t)(m + 2 * t) * (size_t)steps;
+        float sums[4] = {};
+        for (int b0 = warp; b0 < steps; b0 += WARPS * U) {
+            uint4 wv[U][4], av[U][2];
+            float ws_b[U], as_b[U][2];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = (b0 + u * WARPS) * kFp8Step + t * 16;
+                const bool in0 = k < p.K, in1 = k + 64 < p.K;
+                wv[u][0] = in0 ? ld_fp8_weights(w0 + k) : zero;
+                wv[u][1] = in0 ? ld_fp8_weights(w0 + w1 + k) : zero;
+                wv[u][2] = in1 ? ld_fp8_weights(w0 + k + 64) : zero;
+                wv[u][3] = in1 ? ld_fp8_weights(w0 + w1 + k + 64) : zero;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int b = b0 + u * WARPS, k = b * kFp8Step + t * 16;
+                av[u][0] = g < cols && k < p.K ? __ldg(reinterpret_cast<const uint4*>(ar + k)) : zero;
+                av[u][1] = g < cols && k + 64 < p.K ? __ldg(reinterpret_cast<const uint4*>(ar + k + 64)) : zero;
+                const bool live = b < steps;
+                ws_b[u] = live ? __ldg(ws + b) : 0.f;
+                as_b[u][0] = live && 2 * t < cols ? __ldg(as + b) : 0.f;
+                as_b[u][1] = live && 2 * t + 1 < cols ? __ldg(as + steps + b) : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (b0 + u * WARPS >= steps) continue;
+                float c[4] = {};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 &x = wv[u][2 * h], &y = wv[u][2 * h + 1], &z = av[u][h];
+                    mma_e4m3(c, x.x, y.x, x.y, y.y, z.x, z.y);
+                    mma_e4m3(c, x.z, y.z, x.w, y.w, z.z, z.w);
+                }
+                const float s0 = __fmul_rn(as_b[u][0], ws_b[u]), s1 = __fmul_rn(as_b[u][1], ws_b[u]);
+                sums[0] = __fmaf_rn(s0, c[0], sums[0]);
+                sums[1] = __fmaf_rn(s1, c[1], sums[1]);
+                sums[2] = __fmaf_rn(s0, c[2], sums[2]);
+                sums[3] = __fmaf_rn(s1, c[3], sums[3]);
+            }
+        }
+        part[warp][2 * t][g] = sums[0];
+        part[warp][2 * t + 1][g] = sums[1];
+        part[warp][2 * t][g + 8] = sums[2];
+        part[warp][2 * t + 1][g + 8] = sums[3];
+        __syncthreads();
+        const int col = threadIdx.x / kFp8SmallChannels, row = threadIdx.x % kFp8SmallChannels;
+        if (col < cols && n0 + row < q.N) {
+            float v = part[0][col][row];
+#pragma unroll
+            for (int i = 1; i < WARPS; ++i) v = __fadd_rn(v, part[i][col][row]);
+            static_cast<Fp8Out<F32>*>(q.out)[(size_t)(m + col) * (size_t)q.N + (size_t)(n0 + row)] = fp8_round<F32>(v);
+        }
+        __syncthreads();  // before the next eight tokens' sums
+    }
+}
+
+}  // namespace beam

@@ -36,10 +36,10 @@ def test_product_tiles_fit_an_sm(kernels, f32):  # noqa: F811
 
 
 @pytest.mark.parametrize("f32", ["false", "true"])
-@pytest.mark.parametrize("shape,blocks", [("2, 4", 4), ("4, 3", 3)])
-def test_single_token_products_keep_their_blocks(kernels, shape, blocks, f32):  # noqa: F811
-    regs, spilled = find(kernels, f"matmul_fp8_dot_kernel<{shape}, {f32}>")
-    assert ctas_per_sm(regs, 256) >= blocks and spilled <= 32
+@pytest.mark.parametrize("warps,blocks", [(8, 3), (4, 6)])
+def test_products_of_a_few_tokens_keep_their_blocks(kernels, warps, blocks, f32):  # noqa: F811
+    regs, spilled = find(kernels, f"matmul_fp8_small_kernel<{warps}, {blocks}, {f32}>")
+    assert ctas_per_sm(regs, 32 * warps) >= blocks and spilled <= 64
 
 
 @pytest.mark.parametrize("pattern,regs,spilled", [

@@ -89,6 +89,6 @@ def test_plans_fit_the_device_and_take_every_step(lib, room):
             assert tiles % (q["clusters"] * q["split"]) <= q["clusters"]
 
 
-def test_single_tokens_go_to_the_plain_cores(lib):
-    assert [lib.plan_dot(ctypes.c_int64(r), 1) for r in (1, 2, 8)] == [1, 0, 0]
-    assert [lib.plan_dot(ctypes.c_int64(r), 256) for r in (8, 16, 17)] == [1, 1, 0]
+def test_a_few_tokens_go_straight_to_registers(lib):
+    assert [lib.plan_small(ctypes.c_int64(r), 1) for r in (1, 8, 9, 64)] == [1, 1, 0, 0]
+    assert [lib.plan_small(ctypes.c_int64(r), 256) for r in (8, 32, 33)] == [1, 1, 0]
