@@ -129,10 +129,10 @@ beam_status launch(const Fp8Params& q, const beam::Fp8Plan& plan, const uint8_t*
 // Eight warps share a block's k, and four where there are channels enough for 13 blocks on every SM
 // (N = 20480, 8 and 4 warps: 21.4 and 21.9 us; N = 40960: 38.6 and 36.2; sixteen experts of N = 5120:
 // 84 and 74)
-template <int WARPS, int BLOCKS>
+template <int WARPS, int BLOCKS, int NT>
 beam_status launch_small(const beam::Fp8SmallParams& p, bool f32, dim3 grid, cudaStream_t stream) {
-    const void* fn = f32 ? reinterpret_cast<const void*>(beam::matmul_fp8_small_kernel<WARPS, BLOCKS, true>)
-                         : reinterpret_cast<const void*>(beam::matmul_fp8_small_kernel<WARPS, BLOCKS, false>);
+    const void* fn = f32 ? reinterpret_cast<const void*>(beam::matmul_fp8_small_kernel<WARPS, BLOCKS, NT, true>)
+                         : reinterpret_cast<const void*>(beam::matmul_fp8_small_kernel<WARPS, BLOCKS, NT, false>);
     void* args[] = {const_cast<beam::Fp8SmallParams*>(&p)};
     if (cudaLaunchKernel(fn, grid, dim3(32 * WARPS), args, 0, stream) != cudaSuccess) {
         cudaGetLastError();
@@ -171,7 +171,7 @@ beam_status product(beam_stream_t stream, const uint8_t* a, const float* a_scale
     if (st != BEAM_OK) return st;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const bool drop = (flags & BEAM_OPT_TEST_WAIT_TIMEOUT) != 0;
-    if (!drop && beam::fp8_small(R, E)) {
+    if (!drop && beam::fp8_small(R, E, N, K)) {
         beam::Fp8SmallParams p{a, w, {}, K};
         p.q.a_scale = a_scale;
         p.q.w_scale = w_scale;
@@ -184,7 +184,8 @@ beam_status product(beam_stream_t stream, const uint8_t* a, const float* a_scale
         p.q.status = dev.status_word;
         const int64_t groups = R < E ? R : E, blocks = ((int64_t)N + beam::kFp8SmallChannels - 1) / beam::kFp8SmallChannels;
         const dim3 grid((unsigned)blocks, (unsigned)groups);
-        return blocks * groups >= 13 * (int64_t)dev.sms ? launch_small<4, 6>(p, f32, grid, cs) : launch_small<8, 3>(p, f32, grid, cs);
+        if (E == 1 && R > 8) return launch_small<8, 3, 2>(p, f32, grid, cs);
+        return blocks * groups >= 13 * (int64_t)dev.sms ? launch_small<4, 6, 1>(p, f32, grid, cs) : launch_small<8, 3, 1>(p, f32, grid, cs);
     }
     Fp8Room fits;
     st = room(dev, &fits);

@@ -55,11 +55,16 @@ inline int64_t fp8_most_tiles(int64_t R, int experts, int most) {
     return (R - live) / most + live;
 }
 
-// Whether rows go straight to registers, 8 tokens at a time: up to 8 tokens, and up to 32 rows of
-// experts, which seldom have more than 8 of them each (K = 5120: M = 9, N = 6144, twice through the
-// weights, 13.5 us and 14.6 in tiles, but M = 16, N = 20480 37 and 28.5; 32 rows of 31 experts with N
-// = 5120 128 us either way, 64 of 57 experts 225 and 214; 24 of 8 experts 35 and 49)
-inline bool fp8_small(int64_t R, int experts) { return R <= (experts == 1 ? 8 : 32); }
+// Whether rows go straight to registers. Up to 8 tokens, unless few channels' long rows are better
+// shared by clusters (M = 4: N = 2560, K = 20480 17.3 us and 19.4 in tiles, K = 65536 48.8 and 40.7, but N
+// = 5120 64.7 and 70.7); up to 16 on up to 8192 channels (M = 16: N = 6144, K = 5120 10.8 and 14.7, K = 10240
+// 18.6 and 20.1, but N = 12800, K = 5120 18.6 and 17.4; N = 2560, K = 20480 25.8 and 19.5); up to 32 rows of
+// experts, which seldom have more than 8 of them each (N = K = 5120: 32 rows of 31 experts 122 and 128, 64
+// of 57 experts 225 and 214; 24 of 8 experts 35 and 49).
+inline bool fp8_small(int64_t R, int experts, int64_t N, int K) {
+    if (experts > 1) return R <= 32;
+    return R <= 8 ? K <= 20480 || N >= 4096 : R <= 16 && N <= 8192 && K <= 10240;
+}
 
 // How many clusters of 1, 2, 4 and 8 CTAs (one an SM) the device holds at a time
 struct Fp8Room {

@@ -1,10 +1,10 @@
-// The product of matmul_fp8.cuh for up to 8 tokens at a time: warp matrix instructions on rows of
+// The product of matmul_fp8.cuh for 8 or 16 tokens at a time: warp matrix instructions on rows of
 // channels that go from memory straight to registers.
 //
 // It is the weights' way from HBM that counts, and the time until it is in full flow: no tensor
-// maps, no ring, no tensor memory to set up. A block has 16 channels and up to 8 tokens; its
-// warps take the blocks of 128 k in turn, two of each warp's on their way, and add up at the
-// end, in the order of the warps. The instruction wants 4 neighbours of k in a register; which k they
+// maps, no ring, no tensor memory to set up. A block has 16 channels and up to 8 or 16 tokens; its
+// warps take the blocks of 128 k in turn, two of each warp's on their way (one for 16 tokens), and
+// add up at the end, in the order of the warps. The instruction wants 4 neighbours of k in a register; which k they
 // are is free as long as channels and tokens agree, so a lane loads 16 neighbours of a row and uses
 // them in two instructions.
 //   P_b = four instructions' sum from 0, times RN(a_scale w_scale), added to the warp's sum
@@ -12,14 +12,15 @@
 // channels take 14.9 and 28; M = 5, N = 2560, K = 1280: 3.5 and 7.9 us. Plain FP32 multiply-adds of
 // a single token took 9.8 and 22.7 us: turning codes into FP32 takes as long as their way. What is left
 // over the floor is the way in and out of blocks that live 5 to 10 us; asking L2 ahead made it
-// slower by a tenth, a third block of k on its way no faster.
+// slower by a tenth, the next block of k ahead of the present one's products no faster.
+// 16 tokens: N = 6144 10.6 and 14.9 us, N = 2560, K = 1280 4.2 and 7.9; 32 at a time took 17.6 and 15.4.
 #pragma once
 
 #include "matmul_fp8.cuh"
 
 namespace beam {
 
-constexpr int kFp8SmallChannels = 16, kFp8SmallTokens = 8;
+constexpr int kFp8SmallChannels = 16;
 
 // c += 16 channels by 8 tokens over 32 k, E4M3 with FP32 sums. Lane l: channels l / 4 (a0, a2)
 // and l / 4 + 8 (a1, a3), token l / 4; c: channels l / 4 and l / 4 + 8 by tokens 2 (l % 4) and the next
@@ -42,10 +43,11 @@ struct Fp8SmallParams {
     int K;
 };
 
-template <int WARPS, int BLOCKS, bool F32>
+// NT: eights of tokens
+template <int WARPS, int BLOCKS, int NT, bool F32>
 __global__ void __launch_bounds__(32 * WARPS, BLOCKS) matmul_fp8_small_kernel(const __grid_constant__ Fp8SmallParams p) {
-    constexpr int U = 2;
-    __shared__ float part[WARPS][kFp8SmallTokens][kFp8SmallChannels];
+    constexpr int U = NT == 1 ? 2 : 1, kTok = 8 * NT;  // blocks of k on their way; tokens at a time
+    __shared__ float part[WARPS][kTok][kFp8SmallChannels];
     const Fp8Params& q = p.q;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int n0 = (int)blockIdx.x * kFp8SmallChannels;
@@ -82,14 +84,14 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) matmul_fp8_small_kernel(co
     const float* const ws = q.w_scale + ((size_t)e * fp8_up((uint32_t)q.N, kFp8Block128) + (size_t)(n0 / kFp8Block128)) * q.steps;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     const int steps = (int)q.steps;
-    for (int m = lo; m < hi; m += kFp8SmallTokens) {
-        const int cols = min(kFp8SmallTokens, hi - m);
+    for (int m = lo; m < hi; m += kTok) {
+        const int cols = min(kTok, hi - m);
         const uint8_t* const ar = p.a + (size_t)(m + g) * (size_t)p.K;  // read for g < cols
         const float* const as = q.a_scale + (size_t)(m + 2 * t) * (size_t)steps;
-        float sums[4] = {};
+        float sums[NT][4] = {};
         for (int b0 = warp; b0 < steps; b0 += WARPS * U) {
-            uint4 wv[U][4], av[U][2];
-            float ws_b[U], as_b[U][2];
+            uint4 wv[U][4], av[U][NT][2];
+            float ws_b[U], as_b[U][NT][2];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int k = (b0 + u * WARPS) * kFp8Step + t * 16;
@@ -102,43 +104,56 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) matmul_fp8_small_kernel(co
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int b = b0 + u * WARPS, k = b * kFp8Step + t * 16;
-                av[u][0] = g < cols && k < p.K ? __ldg(reinterpret_cast<const uint4*>(ar + k)) : zero;
-                av[u][1] = g < cols && k + 64 < p.K ? __ldg(reinterpret_cast<const uint4*>(ar + k + 64)) : zero;
                 const bool live = b < steps;
                 ws_b[u] = live ? __ldg(ws + b) : 0.f;
-                as_b[u][0] = live && 2 * t < cols ? __ldg(as + b) : 0.f;
-                as_b[u][1] = live && 2 * t + 1 < cols ? __ldg(as + steps + b) : 0.f;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const uint8_t* const from = ar + (size_t)(8 * i) * (size_t)p.K + k;
+                    av[u][i][0] = g + 8 * i < cols && k < p.K ? __ldg(reinterpret_cast<const uint4*>(from)) : zero;
+                    av[u][i][1] = g + 8 * i < cols && k + 64 < p.K ? __ldg(reinterpret_cast<const uint4*>(from + 64)) : zero;
+                    const float* const sf = as + (size_t)(8 * i) * (size_t)steps + b;
+                    as_b[u][i][0] = live && 2 * t + 8 * i < cols ? __ldg(sf) : 0.f;
+                    as_b[u][i][1] = live && 2 * t + 8 * i + 1 < cols ? __ldg(sf + steps) : 0.f;
+                }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (b0 + u * WARPS >= steps) continue;
-                float c[4] = {};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint4 &x = wv[u][2 * h], &y = wv[u][2 * h + 1], &z = av[u][h];
-                    mma_e4m3(c, x.x, y.x, x.y, y.y, z.x, z.y);
-                    mma_e4m3(c, x.z, y.z, x.w, y.w, z.z, z.w);
+                for (int i = 0; i < NT; ++i) {
+                    if (8 * i >= cols) break;
+                    float c[4] = {};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 &x = wv[u][2 * h], &y = wv[u][2 * h + 1], &z = av[u][i][h];
+                        mma_e4m3(c, x.x, y.x, x.y, y.y, z.x, z.y);
+                        mma_e4m3(c, x.z, y.z, x.w, y.w, z.z, z.w);
+                    }
+                    const float s0 = __fmul_rn(as_b[u][i][0], ws_b[u]), s1 = __fmul_rn(as_b[u][i][1], ws_b[u]);
+                    sums[i][0] = __fmaf_rn(s0, c[0], sums[i][0]);
+                    sums[i][1] = __fmaf_rn(s1, c[1], sums[i][1]);
+                    sums[i][2] = __fmaf_rn(s0, c[2], sums[i][2]);
+                    sums[i][3] = __fmaf_rn(s1, c[3], sums[i][3]);
                 }
-                const float s0 = __fmul_rn(as_b[u][0], ws_b[u]), s1 = __fmul_rn(as_b[u][1], ws_b[u]);
-                sums[0] = __fmaf_rn(s0, c[0], sums[0]);
-                sums[1] = __fmaf_rn(s1, c[1], sums[1]);
-                sums[2] = __fmaf_rn(s0, c[2], sums[2]);
-                sums[3] = __fmaf_rn(s1, c[3], sums[3]);
             }
         }
-        part[warp][2 * t][g] = sums[0];
-        part[warp][2 * t + 1][g] = sums[1];
-        part[warp][2 * t][g + 8] = sums[2];
-        part[warp][2 * t + 1][g + 8] = sums[3];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            part[warp][8 * i + 2 * t][g] = sums[i][0];
+            part[warp][8 * i + 2 * t + 1][g] = sums[i][1];
+            part[warp][8 * i + 2 * t][g + 8] = sums[i][2];
+            part[warp][8 * i + 2 * t + 1][g + 8] = sums[i][3];
+        }
         __syncthreads();
-        const int col = threadIdx.x / kFp8SmallChannels, row = threadIdx.x % kFp8SmallChannels;
-        if (col < cols && n0 + row < q.N) {
+        for (int i = threadIdx.x; i < cols * kFp8SmallChannels; i += 32 * WARPS) {
+            const int col = i / kFp8SmallChannels, row = i % kFp8SmallChannels;
+            if (n0 + row >= q.N) continue;
             float v = part[0][col][row];
 #pragma unroll
-            for (int i = 1; i < WARPS; ++i) v = __fadd_rn(v, part[i][col][row]);
+            for (int j = 1; j < WARPS; ++j) v = __fadd_rn(v, part[j][col][row]);
             static_cast<Fp8Out<F32>*>(q.out)[(size_t)(m + col) * (size_t)q.N + (size_t)(n0 + row)] = fp8_round<F32>(v);
         }
-        __syncthreads();  // before the next eight tokens' sums
+        __syncthreads();  // before the next tokens' sums
     }
 }
 

@@ -15,7 +15,7 @@ void plan_fields(int64_t R, int experts, int64_t N, int K, const int* clusters, 
     out[3] = q.clusters;
 }
 
-int plan_small(int64_t R, int experts) { return fp8_small(R, experts); }
+int plan_small(int64_t R, int experts, int64_t N, int K) { return fp8_small(R, experts, N, K); }
 
 int64_t plan_most_tiles(int64_t R, int experts, int most) { return fp8_most_tiles(R, experts, most); }
 

@@ -36,9 +36,9 @@ def test_product_tiles_fit_an_sm(kernels, f32):  # noqa: F811
 
 
 @pytest.mark.parametrize("f32", ["false", "true"])
-@pytest.mark.parametrize("warps,blocks", [(8, 3), (4, 6)])
-def test_products_of_a_few_tokens_keep_their_blocks(kernels, warps, blocks, f32):  # noqa: F811
-    regs, spilled = find(kernels, f"matmul_fp8_small_kernel<{warps}, {blocks}, {f32}>")
+@pytest.mark.parametrize("warps,blocks,eights", [(8, 3, 1), (4, 6, 1), (8, 3, 2)])
+def test_products_of_a_few_tokens_keep_their_blocks(kernels, warps, blocks, eights, f32):  # noqa: F811
+    regs, spilled = find(kernels, f"matmul_fp8_small_kernel<{warps}, {blocks}, {eights}, {f32}>")
     assert ctas_per_sm(regs, 32 * warps) >= blocks and spilled <= 64
 
 

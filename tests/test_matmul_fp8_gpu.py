@@ -71,9 +71,9 @@ def check(ops, dtype=torch.float32, **kw):
 
 
 SHAPES = [
-    # up to eight tokens: odd channels, one step, a k that ends inside a step, warps with a step more than others
+    # up to 8 and 16 tokens: odd channels, one step, a k that ends inside a step, warps with a step more than others
     (1, 1, 16), (1, 129, 144), (1, 2565, 5120), (1, 20480, 528), (8, 17, 48), (5, 2565, 2576), (7, 16, 1152), (8, 40000, 640),
-    (3, 33000, 80), (6, 15, 65536), (9, 2565, 528),
+    (3, 33000, 80), (6, 15, 65536), (9, 2565, 528), (16, 33, 5120), (13, 8192, 1680), (16, 8193, 1664), (4, 1000, 20496),
     # few tokens: odd counts around the instruction's 16 and the tile's 64, channels around 128
     (2, 7, 5120), (3, 130, 272), (15, 127, 128), (16, 384, 1040), (17, 1, 32), (33, 130, 96), (48, 257, 2064),
     (63, 640, 400), (64, 5120, 1024), (64, 129, 20480), (65, 257, 528),
@@ -109,7 +109,7 @@ def test_every_code_times_one(M):
     assert torch.equal(out, w[:, 0].float()[None, :].expand(M, N))
 
 
-@pytest.mark.parametrize("M", [1, 8, 20, 300])
+@pytest.mark.parametrize("M", [1, 8, 12, 20, 300])
 @pytest.mark.parametrize("kind", ["like signs", "far apart", "far apart, largest last"])
 def test_sums_of_like_signs_and_far_apart(M, kind):
     """Where sums that are cut lose most: all of one sign, and one large product among many that it cuts."""
