@@ -38,14 +38,14 @@ WORKLOAD = (f"layer boundary pair, T={T_TOKENS} tokens per GPU, D={D}: dense bou
 # DRAM traffic per launch from one ncu capture (dram__bytes_read.sum +
 # dram__bytes_write.sum), valid only for the kernel source it was taken on.
 NCU_TRAFFIC = {
-    "moe": {"bytes_per_launch": 1_511_286_784 + 300_368_128, "source_sha": "0bac5777e84e45f3"},
-    "dense": {"bytes_per_launch": 335_712_256 + 265_319_936, "source_sha": "0bac5777e84e45f3"},
+    "moe": {"bytes_per_launch": 1_511_441_152 + 300_543_232, "source_sha": "2d971eb4a43ff9e6"},
+    "dense": {"bytes_per_launch": 335_653_376 + 264_097_536, "source_sha": "2d971eb4a43ff9e6"},
 }
 
 # Routing is bound by instruction issue, not HBM: its warp-instructions per
 # launch at T = 16384 (ncu smsp__inst_executed.sum) give its issue roofline,
 # valid while the kernel source matches.
-ROUTE_ISSUE = {"warp_instructions_per_launch": 11_201_646, "source_sha": "0bac5777e84e45f3"}
+ROUTE_ISSUE = {"warp_instructions_per_launch": 11_224_712, "source_sha": "2d971eb4a43ff9e6"}
 
 
 # the sources of the kernels that those captures are of
