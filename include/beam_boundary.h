@@ -484,7 +484,7 @@ BEAM_API beam_status beam_swiglu_fp8(beam_stream_t stream, const uint16_t* gate_
  * each step of the sum one FP32 multiply-add, the last rounding to BF16 or, when out is
  * FP32, nothing. The matrix unit adds the exact products of P_b 16 or 32 at a time, each and the sum
  * so far cut to 2^-25 of the largest, the result to 24 bits: P_b is off by at most 2^-17 sum |a w|
- * (measured: 2^-20.4 for random codes of one sign, 2^-21.5 of both). Up to 16 tokens, or 32 rows of
+ * (measured: 2^-20.4 for random codes of one sign, 2^-21.5 of both). Up to 16 tokens, or 512 rows of
  * experts, and in tiles of the last wave, warps or CTAs share a sum: there the FP32 parts are
  * added in another order. Every run gives the same bits, but they can change with M, N, K and E.
  *   a       [M, K] E4M3 codes; w [N, K] (one row per output channel); 16-byte aligned

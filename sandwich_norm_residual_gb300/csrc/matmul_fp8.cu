@@ -170,8 +170,13 @@ beam_status product(beam_stream_t stream, const uint8_t* a, const float* a_scale
     beam_status st = beam::device(&dev);
     if (st != BEAM_OK) return st;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const bool sectors = (int64_t)N * out_size % 32 == 0 && !misaligned(out, 32);
     const bool drop = (flags & BEAM_OPT_TEST_WAIT_TIMEOUT) != 0;
-    if (!drop && beam::fp8_small(R, E, N, K)) {
+    Fp8Room fits;
+    st = room(dev, &fits);
+    if (st != BEAM_OK) return st;
+    const beam::Fp8Plan plan = beam::fp8_plan(R, E, N, K, sectors, fits);
+    if (!drop && beam::fp8_small(R, E, N, K, plan)) {
         beam::Fp8SmallParams p{a, w, {}, K};
         p.q.a_scale = a_scale;
         p.q.w_scale = w_scale;
@@ -187,10 +192,6 @@ beam_status product(beam_stream_t stream, const uint8_t* a, const float* a_scale
         if (E == 1 && R > 8) return launch_small<8, 3, 2>(p, f32, grid, cs);
         return blocks * groups >= 13 * (int64_t)dev.sms ? launch_small<4, 6, 1>(p, f32, grid, cs) : launch_small<8, 3, 1>(p, f32, grid, cs);
     }
-    Fp8Room fits;
-    st = room(dev, &fits);
-    if (st != BEAM_OK) return st;
-    const beam::Fp8Plan plan = beam::fp8_plan(R, E, N, K, fits);
     Fp8Params q{};
     q.a_scale = a_scale;
     q.w_scale = w_scale;
@@ -204,7 +205,7 @@ beam_status product(beam_stream_t stream, const uint8_t* a, const float* a_scale
     q.n_tiles = beam::fp8_up((uint32_t)N, q.width);
     q.split = plan.split;
     q.scales16 = steps % 4 == 0 && !misaligned(a_scale, 16);
-    q.wide = (int64_t)N * out_size % 32 == 0 && !misaligned(out, 32);
+    q.wide = sectors;
     q.wait_ns = drop ? beam::kFp8TestWaitNs : beam::kFp8WaitNs;
     q.drop = drop;
     q.status = dev.status_word;

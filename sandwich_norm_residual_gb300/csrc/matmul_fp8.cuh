@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                             }
                         }
                     }
-                } else {
+                } else if ((row & 96) < w.cols) {
                     // rows that do not start on a sector: transposed, 32 neighbours of a row a store
 #pragma unroll
                     for (int c = 0; c < C::kMine / 32; ++c) {

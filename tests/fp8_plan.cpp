@@ -8,14 +8,18 @@ extern "C" {
 void plan_fields(int64_t R, int experts, int64_t N, int K, const int* clusters, int64_t* out) {
     Fp8Room room;
     for (int i = 0; i < 4; ++i) room.clusters[i] = clusters[i];
-    const Fp8Plan q = fp8_plan(R, experts, N, K, room);
+    const Fp8Plan q = fp8_plan(R, experts, N, K, N % 16 == 0, room);
     out[0] = q.few;
     out[1] = q.width;
     out[2] = q.split;
     out[3] = q.clusters;
 }
 
-int plan_small(int64_t R, int experts, int64_t N, int K) { return fp8_small(R, experts, N, K); }
+int plan_small(int64_t R, int experts, int64_t N, int K, const int* clusters) {
+    Fp8Room room;
+    for (int i = 0; i < 4; ++i) room.clusters[i] = clusters[i];
+    return fp8_small(R, experts, N, K, fp8_plan(R, experts, N, K, N % 16 == 0, room));
+}
 
 int64_t plan_most_tiles(int64_t R, int experts, int most) { return fp8_most_tiles(R, experts, most); }
 

@@ -90,9 +90,11 @@ def test_plans_fit_the_device_and_take_every_step(lib, room):
 
 
 def test_a_few_tokens_go_straight_to_registers(lib):
-    small = lambda r, e, n, k: lib.plan_small(ctypes.c_int64(r), e, ctypes.c_int64(n), k)  # noqa: E731
+    room = (ctypes.c_int * 4)(*ROOM)
+    small = lambda r, e, n, k: lib.plan_small(ctypes.c_int64(r), e, ctypes.c_int64(n), k, room)  # noqa: E731
     assert [small(r, 1, 6144, 5120) for r in (1, 8, 9, 16, 17, 64)] == [1, 1, 1, 1, 0, 0]
     assert [small(r, 1, 20480, 5120) for r in (1, 8, 9, 16)] == [1, 1, 0, 0]
     assert [small(8, 1, n, k) for n, k in ((640, 20480), (640, 20496), (4096, 65536))] == [1, 0, 1]
     assert [small(16, 1, n, k) for n, k in ((8192, 10240), (8193, 10240), (8192, 10256))] == [1, 0, 0]
-    assert [small(r, 256, 5120, 5120) for r in (8, 32, 33)] == [1, 1, 0]
+    # experts: a token's choices, a few tokens' of many; not an expert's hundred rows, nor more rows than the kernel counts
+    assert [small(*c) for c in ((8, 256, 5120, 5120), (55, 211, 1383, 1152), (300, 3, 1000, 640), (513, 256, 128, 128))] == [1, 1, 0, 0]
