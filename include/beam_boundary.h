@@ -486,7 +486,8 @@ BEAM_API beam_status beam_swiglu_fp8(beam_stream_t stream, const uint16_t* gate_
  * so far cut to 2^-25 of the largest, the result to 24 bits: P_b is off by at most 2^-17 sum |a w|
  * (measured: 2^-20.4 for random codes of one sign, 2^-21.5 of both). Up to 16 tokens, or 512 rows of
  * experts, and in tiles of the last wave, warps or CTAs share a sum: there the FP32 parts are
- * added in another order. Every run gives the same bits, but they can change with M, N, K and E.
+ * added in another order. Every run gives the same bits, but they can change with M, N, K, E, the
+ * offsets and the alignment of out.
  *   a       [M, K] E4M3 codes; w [N, K] (one row per output channel); 16-byte aligned
  *   a_scale [M, ceil(K / 128)] FP32; w_scale [ceil(N / 128), ceil(K / 128)] FP32; 4-byte aligned
  *   K       a multiple of 16, 16 <= K <= BEAM_MATMUL_MAX_K

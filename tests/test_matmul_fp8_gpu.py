@@ -82,7 +82,7 @@ SHAPES = [
     (517, 2565, 2576), (1000, 777, 336), (700, 24, 2560),
     # whole waves and shared tiles, in clusters of two, four and eight
     (256, 5120, 1024), (128, 5120, 2064), (1030, 5110, 1040), (16, 20480, 1040), (150, 300, 20480), (2100, 2600, 400),
-    (40, 6144, 5120), (2048, 4864, 256),
+    (40, 6144, 5120), (2048, 4864, 256), (2000, 257, 4112), (520, 257, 4112), (900, 5120, 4112), (1500, 5120, 1040),
 ]
 
 
@@ -230,6 +230,10 @@ def check_experts(counts, N, K, R=None, before=0, dtype=torch.float32, seed=0):
     ([17, 0, 1, 40, 64, 65, 3], 515, 1040), ([3] * 40, 200, 256), ([0] * 30 + [200] + [0] * 30, 300, 400),
     # many: around 128 rows
     ([127, 128, 129, 1, 0, 300, 256], 513, 272), ([1000, 0, 0, 7], 1000, 640), ([90] * 30, 768, 128),
+    # more rows than go straight to registers: each kind of tile, alone and shared, rows of whole sectors and not
+    ([200] + [0] * 5 + [32] * 10, 2565, 4112), ([200] + [0] * 5 + [32] * 10, 2560, 4112), ([1971, 29], 257, 4112),
+    ([9, 121] + [57] * 10 + [0] * 4, 1500, 528), ([100, 1] + [35] * 14 + [9], 5120, 4112), ([60] * 14 + [0, 60], 640, 528),
+    ([1, 0, 999, 0, 500, 255, 128, 117], 5110, 528),
 ])
 def test_experts(counts, N, K, dtype):
     check_experts(counts, N, K, dtype=dtype, seed=sum(counts))
