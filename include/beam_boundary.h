@@ -455,8 +455,8 @@ BEAM_API beam_status beam_moe_combine_backward(beam_stream_t stream, const void*
  *   y = (g * (1 / (1 + e^-g))) * u,  g = gate_up[r, j], u = gate_up[r, F + j],
  * then codes and scales as beam_boundary_fused_fp8 makes them, from the FP32 y (no rounding to
  * BF16 between).
- * e^x and the reciprocal are the hardware's: y is within (6 + 2 |g|) units of 2^-24, relative; where
- * e^-g overflows (g < -88.7) it is 0.
+ * e^x and the reciprocal are the hardware's: y is within (8 + 2 |g|) units of 2^-24, relative (below
+ * 2^-126 silu and y are multiples of 2^-149); where e^-g overflows (g < -88.7, the BF16 gates from -89 on) it is 0.
  *   gate_up   [R, 2 F] BF16, 16-byte aligned; F a multiple of 16, 16 <= F <= BEAM_MATMUL_MAX_K
  *   live_rows device int32, or NULL: rows from *live_rows on are neither read nor written (the last of
  *             beam_moe_sort's offsets). Outside [0, R] it counts as 0 or R and beam_sync_status

@@ -2,10 +2,13 @@
 //   y = g / (1 + e^-g) * u,  then E4M3 codes with a scale for each 128 (fp8_block.cuh)
 // Half a warp has a block, 8 values a lane, 16 bytes of gate and of up each. Bound by HBM: 4
 // bytes read and 1.03 written for a value, if not by the instructions. e^-g and the quotient are the
-// special-function unit's base-2 exponential and reciprocal (2 units of 2^-24 each and the
-// argument's rounding, 1.44 |g| units): the library's expf and division are 30 more
-// instructions a value. What they flush to 0, e^-g below 2^-126, is added to 1; the reciprocal of
-// more than 2^126 is 0.
+// special-function unit's base-2 exponential and reciprocal (within 2^-22 and 2^-23, relative): the library's
+// expf and division are 30 more instructions a value. In units of 2^-24, with w = 1 / (1 + e^g): the argument's
+// rounding and its constant's 1.22 |g| w, the exponential 4 w, 1 + e^-g 1, the reciprocal 2, two products 1 each, in all at
+// most 8 + 2 |g|.
+// The reciprocal unit flushes results below 2^-126, that is from g = -87.4 down. So it is given (1 + e^-g) 2^-32, one
+// multiply-add, and its result brought back down by a product that rounds below 2^-126 to a multiple of 2^-149 (up to 4
+// units more). From g = -88.73 down e^-g is infinite and y 0. The exponential flushes e^-g below 2^-126, which is added to 1.
 #pragma once
 
 #include "fp8_block.cuh"
@@ -32,15 +35,17 @@ __device__ __forceinline__ uint4 ld_swiglu(const uint16_t* p) {
     return r;
 }
 
-// two values; packed products, none of which feeds a packed sum
+// two values
 __device__ __forceinline__ float2 swiglu2(float2 g, float2 u) {
+    const float2 down = make_float2(0x1p-32f, 0x1p-32f);
     const float2 x = mul2_rn(g, make_float2(-1.4426950408889634f, -1.4426950408889634f));
     float2 t, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t.x) : "f"(x.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t.y) : "f"(x.y));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(__fadd_rn(1.0f, t.x)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(__fadd_rn(1.0f, t.y)));
-    return mul2_rn(mul2_rn(g, r), u);
+    const float2 d = __ffma2_rn(t, down, down);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+    return mul2_rn(mul2_rn(g, mul2_rn(r, down)), u);
 }
 
 __global__ void __launch_bounds__(kSwigluThreads) swiglu_fp8_kernel(const SwigluParams p) {
