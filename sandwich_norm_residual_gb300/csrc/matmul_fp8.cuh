@@ -362,12 +362,13 @@ __global__ void __launch_bounds__(Fp8Tile<FEW>::kThreads, 1)
                 const auto place_of = [&](int from, int j) {
                     return smem + C::kRedAt + (((from * each + (j * C::kGroups + group) / q.split) * (kPiece / 4)) * 128 + row) * 16;
                 };
-                // the others may write to this CTA's, and this one to theirs
+                // The others may write to this CTA's, and this one to theirs: released, since it was read until now (few
+                // tokens: the join before; many: operands, whose products have ended)
                 __syncwarp();
                 if (lane == 0)
                     for (int d = 0; d < q.split; ++d)
-                        if (d != (int)place) mbar_arrive_cluster_relaxed(cluster_addr(red_ready, d));
-                if (ok) ok = mbar_wait(red_ready, joins & 1, q.wait_ns);
+                        if (d != (int)place) mbar_arrive_cluster_release(cluster_addr(red_ready, d));
+                if (ok) ok = mbar_wait<2>(red_ready, joins & 1, q.wait_ns);
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < kPieces; ++j) {
