@@ -188,7 +188,7 @@ beam_status product(beam_stream_t stream, const uint8_t* a, const float* a_scale
         p.q.steps = (uint32_t)steps;
         p.q.status = dev.status_word;
         const int64_t groups = R < E ? R : E, blocks = ((int64_t)N + beam::kFp8SmallChannels - 1) / beam::kFp8SmallChannels;
-        const dim3 grid((unsigned)blocks, (unsigned)groups);
+        const dim3 grid((unsigned)blocks, (unsigned)(E == 1 ? 1 : beam::fp8_most_tiles(R, E, beam::kFp8SmallPart)));
         if (E == 1 && R > 8) return launch_small<8, 3, 2>(p, f32, grid, cs);
         return blocks * groups >= 13 * (int64_t)dev.sms ? launch_small<4, 6, 1>(p, f32, grid, cs) : launch_small<8, 3, 1>(p, f32, grid, cs);
     }

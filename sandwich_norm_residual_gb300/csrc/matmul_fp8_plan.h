@@ -22,6 +22,7 @@ constexpr int kFp8Width = 256;     // ... by up to 256 channels
 constexpr int kFp8Band = 8;        // tiles of tokens that a band of tiles is high
 constexpr int kFp8MaxSplit = 8;    // CTAs of a cluster at most
 constexpr int kFp8SmallRows = 512; // of experts whose rows go straight to registers, at most
+constexpr int kFp8SmallPart = 8;   // ... of an expert's that a block has
 
 BEAM_HOST_DEVICE constexpr uint32_t fp8_up(uint32_t v, uint32_t to) { return (v + to - 1) / to; }
 
@@ -77,8 +78,8 @@ struct Fp8Plan {
 // sectors and where they are.
 // Fitted, with the cost of rows that go straight to registers, to all kinds and splits at 702 sizes
 // (dense: M from 2 to 3000, N from 640 to 20480, K from 256 to 20480; 382 products of 1 to 256
-// experts with 0.1 to 3000 rows for each; operands not in L2): the choice takes 0.8% more than the
-// best on average, over 5% at 20 and 19% at most, but for one (165 rows of 210 experts, N = 2432, K = 384: 59
+// experts with 0.1 to 3000 rows for each; operands not in L2): at these the choice takes 0.8% more than the
+// best on average, over 5% at 20 and 19% at most, but for one (165 rows of 210 experts, N = 2432, K = 384: 52
 // us and 41). With one cost a step, joins of 1600 to 3000 ns and, for experts, the most tiles that there can be,
 // it was 11% for the dense ones, up to 62%, and 25% for experts, up to three times: M = 64, N =
 // 6144, K = 1280: 11.3 -> 8.3 us; M = 128, N = 2565, K = 5120: 19.7 -> 13.4; 55 rows of 211 experts, N = 1383, K =
@@ -148,7 +149,9 @@ inline Fp8Plan fp8_plan(int64_t R, int experts, int64_t N, int K, bool sectors, 
 // 18.6 and 20.1, but N = 12800, K = 5120 18.6 and 17.4; N = 2560, K = 20480 25.8 and 19.5). Experts: where the
 // weights' way from memory, or a warp's blocks of k one after the other, and the further eights of an
 // expert's rows end before the tiles do, less the 1.3 us by which those start later (55 rows of 211
-// experts, N = 1383, K = 1152: 23 us and 29 in tiles; 252 of 18, N = 3601, K = 656: 24 and 20).
+// experts, N = 1383, K = 1152: 21 us and 29 in tiles; 252 of 18, N = 3601, K = 656: 24 and 20). Fitted while the
+// eights of an expert followed one another in its blocks; they now have blocks of their own, which cost a tenth to a
+// quarter less, and no more where rows do not fall alike.
 inline bool fp8_small(int64_t R, int experts, int64_t N, int K, const Fp8Plan& tiles) {
     if (experts == 1) return R <= 8 ? K <= 20480 || N >= 4096 : R <= 16 && N <= 8192 && K <= 10240;
     if (R > kFp8SmallRows) return false;
