@@ -6,17 +6,13 @@
 
 #include "beam_boundary.h"
 #include "device.h"
+#include "host.h"
 
 namespace {
 
 using beam::BalanceParams;
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return na && nb && a0 < b0 + nb && b0 < a0 + na;
-}
-
-bool misaligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1u)) != 0; }
+using beam::misaligned;
+using beam::overlaps;
 
 bool bad_shape(int64_t T, int E, int K, int64_t S, const void* off) {
     return T < 0 || T > 0x7FFFFFFF || E < 4 || (E & 3) || E > BEAM_BALANCE_MAX_EXPERTS || K < 1 ||

@@ -16,12 +16,14 @@
 
 #include "boundary_kernels.cuh"
 #include "device.h"
+#include "host.h"
 #include "route.cuh"
 #include "qk_norm.cuh"
 
 namespace {
 
 using beam::BoundaryParams;
+using beam::overlaps;
 using KernelFn = void (*)(BoundaryParams);
 
 constexpr int kMaxDevices = 64;
@@ -123,11 +125,6 @@ struct QuantOut {
 };
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-    uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return na && nb && a0 < b0 + nb && b0 < a0 + na;
-}
 
 int round_up32(int v) { return (v + 31) & ~31; }
 
@@ -403,7 +400,6 @@ beam_status launch(bool moe, beam_stream_t stream, uint16_t* h, const uint16_t* 
     p.yi = quant ? quant->yi : nullptr;
     p.yis = quant ? quant->yis : nullptr;
     p.y8 = quant ? quant->y8 : nullptr;
-    p.y8s = p.yis;
 
     void* args[] = {&p};
     cudaError_t err;

@@ -48,9 +48,8 @@ struct BoundaryParams {
     uint8_t* ysf;           // NVFP4 y: [T, D/16] E4M3 block scales
     float y_gs;             // NVFP4 y: global scale
     int8_t* yi;             // [T, D] int8 codes of y (y as int8)
-    float* yis;             // [T] their scales
     uint8_t* y8;            // [T, D] E4M3 codes of y (y as FP8)
-    float* y8s;             // [T, ceil(D/128)] their scales
+    float* yis;             // the codes' scales: int8 [T], FP8 [T, ceil(D/128)]
 };
 
 constexpr unsigned kFlagForceExact = 1u;
@@ -354,7 +353,7 @@ __device__ __forceinline__ void store_fp8(const BoundaryParams& p, long long row
     const uint2 c = fp8_codes(f, amax, &scale);
     if (valid) {
         st_stream_u64(p.y8 + (size_t)row * (size_t)p.D + (size_t)vi * 8, c);
-        if (!(vi & 15)) p.y8s[(size_t)row * (size_t)((p.nvec + 15) / 16) + (size_t)(vi / 16)] = scale;
+        if (!(vi & 15)) p.yis[(size_t)row * (size_t)((p.nvec + 15) / 16) + (size_t)(vi / 16)] = scale;
     }
 }
 

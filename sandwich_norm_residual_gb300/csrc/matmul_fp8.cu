@@ -7,35 +7,18 @@
 #include "beam_boundary.h"
 #include "device.h"
 #include "host.h"
+#include "tensor_map.h"
 
 static_assert(BEAM_MOE_MAX_EXPERTS <= beam::kFp8MaxExperts, "the table of experts");
 
 namespace {
 
+using beam::encode_tiled;
+using beam::EncodeTiled;
 using beam::Fp8Params;
 using beam::Fp8Room;
 using beam::misaligned;
 using beam::overlaps;
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-    static std::atomic<void*> cached{nullptr};
-    void* fn = cached.load(std::memory_order_acquire);
-    if (!fn) {
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
-                cudaSuccess ||
-            found != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            return nullptr;
-        }
-        cached.store(fn, std::memory_order_release);
-    }
-    return reinterpret_cast<EncodeTiled>(fn);
-}
 
 // matrices of 8-bit rows of K, one behind the other, in tiles of `rows` rows of one matrix by
 // one step of k, 128-byte swizzle; dims = 2: one matrix

@@ -6,18 +6,17 @@
 
 #include "beam_boundary.h"
 #include "device.h"
+#include "host.h"
+#include "tensor_map.h"
 
 namespace {
 
+using beam::encode_tiled;
+using beam::EncodeTiled;
 using beam::MatmulParams;
+using beam::misaligned;
+using beam::overlaps;
 using beam::Shape;
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return na && nb && a0 < b0 + nb && b0 < a0 + na;
-}
-
-bool misaligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1u)) != 0; }
 
 // Kernel for up to 8 tokens, and its channels a warp. At N = 6144, K = 5120 the
 // shapes below take 6.5, 7.4, 9.0 and 11.2 us for 1, 2, 4 and 8 tokens; two
@@ -61,26 +60,6 @@ beam_status launch(const void* fn, dim3 grid, dim3 block, void** args, size_t sm
         return BEAM_ERR_CUDA;
     }
     return BEAM_OK;
-}
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-    static std::atomic<void*> cached{nullptr};
-    void* fn = cached.load(std::memory_order_acquire);
-    if (!fn) {
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
-                cudaSuccess ||
-            found != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            return nullptr;
-        }
-        cached.store(fn, std::memory_order_release);
-    }
-    return reinterpret_cast<EncodeTiled>(fn);
 }
 
 // int8 rows of K in tiles of `rows` by one step of k, 128-byte swizzle
