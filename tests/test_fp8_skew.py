@@ -40,5 +40,6 @@ def test_every_pass_has_a_block(lib, R, E):  # noqa: F811
 def test_the_skewed_cases_go_straight_to_registers(lib):  # noqa: F811
     """Those that tests/test_fp8_skew_gpu.py runs."""
     room = (ctypes.c_int * 4)(*ROOM)
-    for R, E, N, K in ((512, 256, 1383, 1152), (512, 256, 520, 400), (300, 40, 700, 528), (64, 256, 2565, 272)):
+    experts = (31, 32, 33, 255, 256, 257, 300, 511, 512)
+    for R, E, N, K in (*((r, e, 130, 144) for e in experts for r in (e // 2 + 2, 400)), (512, 256, 1383, 1152), (512, 256, 520, 400), (300, 40, 700, 528), (64, 256, 2565, 272)):
         assert lib.plan_small(ctypes.c_int64(R), E, ctypes.c_int64(N), K, room)

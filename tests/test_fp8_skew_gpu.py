@@ -1,6 +1,7 @@
 """Few rows of experts that do not fall alike, straight to registers: right, and not slower by the largest expert's rows."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
@@ -26,6 +27,19 @@ def built():
 ])
 def test_rows_that_do_not_fall_alike(counts, N, K, dtype):
     check_experts(counts, N, K, dtype=dtype, seed=len(counts))
+
+
+@pytest.mark.parametrize("E", [31, 32, 33, 255, 256, 257, 300, 511, 512])
+def test_any_number_of_experts(E):
+    """A lane looks at 1, 8 or 16 of them."""
+    rng = np.random.default_rng(E)
+    few = rng.integers(0, 2, E)
+    few[-1] = 3
+    check_experts(few.tolist(), 130, 144, seed=E)
+    many = np.zeros(E, dtype=np.int64)
+    many[rng.integers(0, E, 5)] += rng.integers(1, 60, 5)
+    many[0], many[-1] = 9, 25
+    check_experts(many.tolist(), 130, 144, R=400, before=7, seed=E)
 
 
 def test_rows_before_and_behind_the_experts():
