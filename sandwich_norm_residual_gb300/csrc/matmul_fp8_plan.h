@@ -84,6 +84,8 @@ struct Fp8Plan {
 // it was 11% for the dense ones, up to 62%, and 25% for experts, up to three times: M = 64, N =
 // 6144, K = 1280: 11.3 -> 8.3 us; M = 128, N = 2565, K = 5120: 19.7 -> 13.4; 55 rows of 211 experts, N = 1383, K =
 // 1152: 50 -> 23; 3045 of 166, N = 314, K = 336: 34 -> 21.
+// Joins have since come to take 0.3 (few tokens) to 0.7 us more, at the cluster's scope. With that in the constants the
+// choice would be another at 54 of 3000 random dense sizes, near ties all.
 struct Fp8Cost {
     double alone, shared, once, join, tile, tile_of_sectors;
     double step(double ctas, int sms, double m_tiles) const {
